@@ -63,7 +63,7 @@ def draw(rng):
     while E * K * N > 1.2e9:
         K, N = max(256, K // 16 * 8), max(128, N // 16 * 8)
     k = rng.randint(1, min(E, 16))
-    T = max(1, min(_log(rng, 1, 8192), 120000 // k, int(4e11 / (k * K * N))))
+    T = max(1, min(_log(rng, 1, 8192), 120000 // k, int(2.3e11 / (k * K * N))))
     return {"op": op, "T": T, "E": E, "k": k, "K": K, "N": N, "skew": rng.random() < 0.3 and E <= 64}
 
 
