@@ -280,6 +280,97 @@ lmoe_status lmoe_forward_block(const uint16_t *x_h, const uint16_t *W_in, const 
                                int32_t hidden, uint16_t *out, uint16_t *lat, uint16_t *y, int32_t *topk_idx,
                                float *topk_w, float *logits, void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- norms around the block ------------------------------------------------ */
+
+/* Element type of a tensor that may be either. */
+typedef enum { LMOE_BF16 = 0, LMOE_F32 = 1 } lmoe_fmt;
+
+/* out[t][c] = bf16( x[t][c] * rsqrt(mean_c x[t][c]^2 + eps) * w[c] ): the norm
+ * before a block.  x [T][H] of type x_fmt (the residual stream), w fp32 [H],
+ * fp32 arithmetic.  H % 8 == 0, H <= 32768, eps >= 0. */
+lmoe_status lmoe_rms_norm(const void *x, int32_t x_fmt, const float *w, float eps, int64_t T, int32_t H, uint16_t *out,
+                          void *stream);
+
+/* What the block's output is multiplied by before the residual add: nothing;
+ * an fp32 factor per channel [H]; an fp32 factor per token [T]; a bf16 factor
+ * per element [T][H]. */
+typedef enum {
+    LMOE_GATE_NONE = 0,
+    LMOE_GATE_CHANNEL = 1,
+    LMOE_GATE_TOKEN = 2,
+    LMOE_GATE_FULL = 3
+} lmoe_gate_kind;
+
+/* After a block, in one pass over its output y (bf16 [T][H]) and the residual
+ * stream res ([T][H], bf16 or fp32 by res_fmt):
+ *   s  = post_w ? y * rsqrt(mean(y^2) + eps) * post_w : y
+ *   res_out  = res + scale * gate * s             (rounded to the type of res)
+ *   next_out = bf16( res_out * rsqrt(mean(res_out^2) + eps) * next_w )
+ * with res_out as stored in the last line.  post_w and next_w fp32 [H] or
+ * NULL (next_w NULL: next_out is not written and may be NULL); gate by
+ * gate_kind (NULL for LMOE_GATE_NONE).  fp32 arithmetic.  res_out may be res
+ * and next_out may be y; otherwise outputs overlap no input.  Limits as for
+ * lmoe_rms_norm; scale finite. */
+lmoe_status lmoe_residual_norm(const uint16_t *y, const void *res, int32_t res_fmt, const float *post_w,
+                               const void *gate, int32_t gate_kind, float scale, float eps, const float *next_w,
+                               int64_t T, int32_t H, void *res_out, uint16_t *next_out, void *stream);
+
+/* ---- MXFP4 linear on bf16 rows ---------------------------------------------- */
+
+/* out[r][n] = bf16( sum_c x[r][c] * W[n][c] ): x bf16 [rows][K], W one MXFP4
+ * matrix of N x K in LMOE_LAYOUT_TC (lmoe_quant_mxfp4 or lmoe_repack_mxfp4
+ * with nmat = 1; q 32-byte, s 16-byte aligned), fp32 accumulation.  Unlike
+ * the expert GEMMs the activations are not rounded to MXFP8: the products use
+ * x as it is (see below).  K % 32 == 0, any N >= 1.  Made for the
+ * hidden <-> latent projections of decode batches, whose time is the weight
+ * stream (0.53 bytes per weight, against 2 of lmoe_linear_bf16); it holds for
+ * any number of rows.  This call and the grouped products below leave the
+ * workspace's status word alone unless they find an error, and one found
+ * stays until it is cleared: clear it once before the workspace's first use
+ * (lmoe_clear_device_status).  Calls that may overlap on the GPU, captured
+ * graphs among them, need a workspace each. */
+size_t lmoe_linear_mxfp4_workspace_size(int64_t rows, int32_t K, int32_t N);
+lmoe_status lmoe_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int32_t K, int32_t N,
+                              uint16_t *out, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- bf16 products grouped by expert ----------------------------------------- */
+
+/* The rows of a grouped product: row q of expert e for q in [offsets[e],
+ * offsets[e+1]) (offsets [E+1], from lmoe_permute: offsets[0] >= 0, not
+ * decreasing, offsets[E] <= P), ragged groups, empty ones among them.  perm
+ * [P] gives each row's pair p = t*k + j (NULL: p = q, k = 1). */
+typedef struct {
+    const int32_t *offsets;
+    const int32_t *perm;
+    int64_t P;
+    int32_t E, k;
+} lmoe_groups;
+
+/* Workspace of the two calls below: the status word alone. */
+size_t lmoe_grouped_workspace_size(void);
+
+/* out[q][n] = w(q) * sum_c x[src(q)][c] * W[e(q)][n][c], for every row q of a
+ * group: x bf16 [x_rows][K], W bf16 [E][N][K], fp32 accumulation; src(q) =
+ * perm[q] / k with gather != 0, else q; w(q) = row_w[perm[q]] (row_w [P]), or 1 without
+ * row_w; out [P][N] bf16 or fp32 (out_fmt), rounded once.  Rows of out that
+ * belong to no group are left as they were.  With fp32 out and the gate
+ * weights as row_w, out is the yp that lmoe_combine takes.
+ * K % 8 == 0, any N >= 1, 1 <= E <= 2048, E * N <= INT32_MAX, 1 <= k,
+ * P <= INT32_MAX; without gather x_rows >= P.
+ * Offsets that break the rule above and source rows outside [0, x_rows) are
+ * recorded as LMOE_ERR_DEVICE_CHECK; the call then reads and writes nothing
+ * out of bounds, and what the groups concerned hold is undefined. */
+lmoe_status lmoe_grouped_linear_bf16(const uint16_t *x, int64_t x_rows, const uint16_t *W, const lmoe_groups *groups,
+                                     int32_t gather, const float *row_w, int32_t K, int32_t N, int32_t out_fmt,
+                                     void *out, void *workspace, size_t ws_bytes, void *stream);
+
+/* h[q][i] = bf16( silu(g) * u ), g = sum_c x[src(q)][c] * Wg[e(q)][i][c],
+ * u = sum_c x[src(q)][c] * Wu[e(q)][i][c]: both products and the gating in
+ * one kernel; Wg, Wu bf16 [E][I][K], h [P][I].  The rest as above. */
+lmoe_status lmoe_grouped_swiglu_bf16(const uint16_t *x, int64_t x_rows, const uint16_t *Wg, const uint16_t *Wu,
+                                     const lmoe_groups *groups, int32_t gather, int32_t K, int32_t I, uint16_t *h,
+                                     void *workspace, size_t ws_bytes, void *stream);
+
 /* ---- helpers --------------------------------------------------------------- */
 
 /* Reads (synchronously, after all prior work on the device) the status word

@@ -1,6 +1,7 @@
 // C ABI of the lmoe library: argument checks, workspace carving, launches.
 // Every entry point validates before it enqueues anything, so an argument
 // error leaves all outputs untouched.
+#include <math.h>
 #include <stdio.h>
 
 #include "lmoe_internal.cuh"
@@ -114,6 +115,51 @@ FwdLayout fwd_layout(const lmoe_dims *d)
     L.yp = take(size_t((ffn_layout(P, d->d, int(E), d->I).fused ? T : P) * d->d * 4));
     L.total = off;
     return L;
+}
+
+WaitArgs wait_args()
+{
+    WaitArgs w;
+    w.limit = g_wait_limit;
+    w.stall_first_fill = g_stall;
+    return w;
+}
+
+bool norm_ok(int64_t T, int32_t H, float eps, int32_t fmt)
+{
+    return T >= 0 && T <= INT32_MAX && H > 0 && H % 8 == 0 && H <= 32768 && eps >= 0.f && isfinite(eps) &&
+           (fmt == LMOE_BF16 || fmt == LMOE_F32);
+}
+
+// The checks the two grouped products share; fills all of `a` but the weights,
+// row weights and output type.
+lmoe_status grouped_args(const uint16_t *x, int64_t x_rows, const lmoe_groups *g, int32_t gather, int32_t K, int32_t N,
+                         void *out, void *workspace, size_t ws_bytes, GroupedArgs &a)
+{
+    if (!g || g->P < 0 || g->P > INT32_MAX || g->E <= 0 || g->E > 2048 || g->k <= 0 || K <= 0 || K % 8 != 0 || N <= 0 ||
+        x_rows < 0 || x_rows > INT32_MAX || int64_t(g->E) * N > INT32_MAX)
+        return LMOE_ERR_INVALID_ARG;
+    if (gather && (!g->perm || x_rows == 0) && g->P > 0) return LMOE_ERR_INVALID_ARG;
+    if (!gather && x_rows < g->P) return LMOE_ERR_INVALID_ARG;
+    a.P = g->P;
+    if (g->P == 0) return LMOE_OK;
+    if (!x || !g->offsets || !out || !aligned(x, 16) || !aligned(g->offsets, 4) || !aligned(g->perm, 4) ||
+        !aligned(out, 16))
+        return LMOE_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < size_t(kStatusBytes) || !aligned(workspace, 256)) return LMOE_ERR_WORKSPACE;
+    a.x = x;
+    a.x_rows = x_rows;
+    a.offsets = g->offsets;
+    a.perm = g->perm;
+    a.E = g->E;
+    a.k = g->k;
+    a.K = K;
+    a.N = N;
+    a.gather = gather != 0;
+    a.out = out;
+    a.status = static_cast<int32_t *>(workspace);
+    a.wait = wait_args();
+    return LMOE_OK;
 }
 
 }  // namespace
@@ -437,6 +483,83 @@ lmoe_status lmoe_forward_block(const uint16_t *x_h, const uint16_t *W_in, const 
                                  ws_bytes - 2 * latb, stream);
     if (s != LMOE_OK) return s;
     return cuda_status(launch_linear_bf16(y_buf, W_out, dims->T, dims->d, hidden, out, nullptr, nullptr, st));
+}
+
+lmoe_status lmoe_rms_norm(const void *x, int32_t x_fmt, const float *w, float eps, int64_t T, int32_t H, uint16_t *out,
+                          void *stream)
+{
+    if (!norm_ok(T, H, eps, x_fmt)) return LMOE_ERR_INVALID_ARG;
+    if (T == 0) return LMOE_OK;
+    if (!x || !w || !out || !aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16)) return LMOE_ERR_INVALID_ARG;
+    NormArgs a{nullptr, x, x_fmt, nullptr, nullptr, LMOE_GATE_NONE, 1.f, eps, w, T, H, nullptr, out};
+    return cuda_status(launch_residual_norm(a, cudaStream_t(stream)));
+}
+
+lmoe_status lmoe_residual_norm(const uint16_t *y, const void *res, int32_t res_fmt, const float *post_w,
+                               const void *gate, int32_t gate_kind, float scale, float eps, const float *next_w,
+                               int64_t T, int32_t H, void *res_out, uint16_t *next_out, void *stream)
+{
+    if (!norm_ok(T, H, eps, res_fmt) || !isfinite(scale)) return LMOE_ERR_INVALID_ARG;
+    if (gate_kind < LMOE_GATE_NONE || gate_kind > LMOE_GATE_FULL) return LMOE_ERR_INVALID_ARG;
+    if (T == 0) return LMOE_OK;
+    if (!y || !res || !res_out || (gate_kind != LMOE_GATE_NONE) != (gate != nullptr) || (next_w && !next_out))
+        return LMOE_ERR_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(res, 16) || !aligned(res_out, 16) || !aligned(post_w, 16) || !aligned(gate, 16) ||
+        !aligned(next_w, 16) || !aligned(next_out, 16))
+        return LMOE_ERR_INVALID_ARG;
+    NormArgs a{y, res, res_fmt, post_w, gate, gate_kind, scale, eps, next_w, T, H, res_out, next_w ? next_out : nullptr};
+    return cuda_status(launch_residual_norm(a, cudaStream_t(stream)));
+}
+
+size_t lmoe_linear_mxfp4_workspace_size(int64_t rows, int32_t K, int32_t N)
+{
+    if (rows < 0 || rows > INT32_MAX || K <= 0 || K % 32 != 0 || N <= 0) return 0;
+    return kStatusBytes + linear_mxfp4_scratch_bytes(rows, K, N);
+}
+
+lmoe_status lmoe_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int32_t K, int32_t N,
+                              uint16_t *out, void *workspace, size_t ws_bytes, void *stream)
+{
+    if (rows < 0 || rows > INT32_MAX || K <= 0 || K % 32 != 0 || N <= 0) return LMOE_ERR_INVALID_ARG;
+    if (rows == 0) return LMOE_OK;
+    if (!x || !q || !s || !out || !aligned(x, 16) || !aligned(q, 32) || !aligned(s, 16) || !aligned(out, 16))
+        return LMOE_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < lmoe_linear_mxfp4_workspace_size(rows, K, N) || !aligned(workspace, 256))
+        return LMOE_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    return cuda_status(launch_linear_mxfp4(x, q, s, rows, K, N, out, ws + kStatusBytes,
+                                           reinterpret_cast<int32_t *>(ws), wait_args(), cudaStream_t(stream)));
+}
+
+size_t lmoe_grouped_workspace_size(void) { return kStatusBytes; }
+
+lmoe_status lmoe_grouped_linear_bf16(const uint16_t *x, int64_t x_rows, const uint16_t *W, const lmoe_groups *groups,
+                                     int32_t gather, const float *row_w, int32_t K, int32_t N, int32_t out_fmt,
+                                     void *out, void *workspace, size_t ws_bytes, void *stream)
+{
+    if (out_fmt != LMOE_BF16 && out_fmt != LMOE_F32) return LMOE_ERR_INVALID_ARG;
+    GroupedArgs a{};
+    const lmoe_status c = grouped_args(x, x_rows, groups, gather, K, N, out, workspace, ws_bytes, a);
+    if (c != LMOE_OK || a.P == 0) return c;
+    if (!W || !aligned(W, 16) || !aligned(row_w, 4)) return LMOE_ERR_INVALID_ARG;
+    a.W = W;
+    a.row_w = row_w;
+    a.out_fmt = out_fmt;
+    return cuda_status(launch_grouped(a, cudaStream_t(stream)));
+}
+
+lmoe_status lmoe_grouped_swiglu_bf16(const uint16_t *x, int64_t x_rows, const uint16_t *Wg, const uint16_t *Wu,
+                                     const lmoe_groups *groups, int32_t gather, int32_t K, int32_t I, uint16_t *h,
+                                     void *workspace, size_t ws_bytes, void *stream)
+{
+    GroupedArgs a{};
+    const lmoe_status c = grouped_args(x, x_rows, groups, gather, K, I, h, workspace, ws_bytes, a);
+    if (c != LMOE_OK || a.P == 0) return c;
+    if (!Wg || !Wu || !aligned(Wg, 16) || !aligned(Wu, 16)) return LMOE_ERR_INVALID_ARG;
+    a.W = Wg;
+    a.W2 = Wu;
+    a.out_fmt = LMOE_BF16;
+    return cuda_status(launch_grouped(a, cudaStream_t(stream)));
 }
 
 int32_t lmoe_forward_kernel_count(const lmoe_dims *dims)

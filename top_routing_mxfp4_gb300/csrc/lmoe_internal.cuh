@@ -50,6 +50,13 @@ __device__ __forceinline__ void set_status(int32_t *status, int32_t code)
     if (status) atomicCAS(status, 0, code);
 }
 
+// Bounded waits of a kernel: the limit in SM clocks (0: the default, about
+// 2 s) and the failure-path test's withheld first stage (lmoe_set_wait_test).
+struct WaitArgs {
+    long long limit = 0;
+    int stall_first_fill = 0;
+};
+
 // ---- small numeric helpers ----------------------------------------------------------
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
@@ -332,5 +339,47 @@ cudaError_t launch_combine(const float *yp, const int32_t *inv, int T, int d, in
                            bool inv_early);
 // y = bf16(acc), n elements (n % 4 == 0)
 cudaError_t launch_acc_to_bf16(const float *acc, int64_t n, uint16_t *y, cudaStream_t st);
+
+
+// ---- norms around a block (k_norm.cu) -------------------------------------------------
+// y == null: only the norm of the stream (res -> next_out).  res_out may be
+// res, next_out may be y: each thread reads its elements before it writes them.
+struct NormArgs {
+    const uint16_t *y;
+    const void *res;
+    int res_fmt;
+    const float *post_w;
+    const void *gate;
+    int gate_kind;
+    float scale, eps;
+    const float *next_w;
+    int64_t T;
+    int H;
+    void *res_out;
+    uint16_t *next_out;
+};
+cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t st);
+
+// ---- MXFP4 linear on bf16 rows (k_linear_mxfp4.cu) -------------------------------------
+size_t linear_mxfp4_scratch_bytes(int64_t rows, int K, int N);
+cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int K, int N,
+                                uint16_t *out, void *scratch, int32_t *status, const WaitArgs &wait, cudaStream_t st);
+
+// ---- bf16 products grouped by expert (k_grouped.cu) ------------------------------------
+struct GroupedArgs {
+    const uint16_t *x;
+    int64_t x_rows;
+    const uint16_t *W, *W2;  // W2: the up matrices (swiglu), else null
+    const int32_t *offsets, *perm;
+    const float *row_w;
+    int64_t P;
+    int E, k, K, N;
+    bool gather;  // row q reads x row perm[q] / k, else x row q
+    int out_fmt;
+    void *out;
+    int32_t *status;
+    WaitArgs wait;
+};
+cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st);
 
 }  // namespace lmoe

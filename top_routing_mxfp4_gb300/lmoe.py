@@ -89,6 +89,28 @@ _set_events = _sig("lmoe_set_stage_events", ctypes.c_int, ctypes.POINTER(_vp), _
 _kernel_count = _sig("lmoe_forward_kernel_count", _i32, _DP)
 
 
+_rms_norm = _sig("lmoe_rms_norm", ctypes.c_int, _vp, _i32, _vp, ctypes.c_float, _i64, _i32, _vp, _vp)
+_residual_norm = _sig("lmoe_residual_norm", ctypes.c_int, _vp, _vp, _i32, _vp, _vp, _i32, ctypes.c_float,
+                      ctypes.c_float, _vp, _i64, _i32, _vp, _vp, _vp)
+_linear_mx_ws = _sig("lmoe_linear_mxfp4_workspace_size", _sz, _i64, _i32, _i32)
+_linear_mx = _sig("lmoe_linear_mxfp4", ctypes.c_int, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _sz, _vp)
+
+
+class Groups(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("perm", ctypes.c_void_p), ("P", ctypes.c_int64), ("E", ctypes.c_int32),
+                ("k", ctypes.c_int32)]
+
+
+_GP = ctypes.POINTER(Groups)
+_grouped_ws = _sig("lmoe_grouped_workspace_size", _sz)
+_grouped_linear = _sig("lmoe_grouped_linear_bf16", ctypes.c_int, _vp, _i64, _vp, _GP, _i32, _vp, _i32, _i32, _i32, _vp,
+                       _vp, _sz, _vp)
+_grouped_swiglu = _sig("lmoe_grouped_swiglu_bf16", ctypes.c_int, _vp, _i64, _vp, _vp, _GP, _i32, _i32, _i32, _vp, _vp,
+                       _sz, _vp)
+BF16, F32 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+
 class FfnViews(ctypes.Structure):
     _fields_ = [("xq", _i64), ("xs", _i64), ("hq", _i64), ("hs", _i64), ("dst_row", _i64), ("rows", _i64),
                 ("tile_tokens", _i32), ("slot_rows", _i32), ("path", _i32), ("code_row", _i64), ("ksplit", _i64)]
@@ -482,6 +504,196 @@ def linear_bf16(x, W, out=None, stream=None):
     _need(W, torch.bfloat16, (N, K), "W")
     out = _empty((rows, N), torch.bfloat16, x.device) if out is None else out
     _check(_linear(_ptr(x), _ptr(W), rows, K, N, _ptr(out), _stream(stream)), "lmoe_linear_bf16")
+    return out
+
+
+# ---- norms, MXFP4 linear and grouped products around the layer ----------------------------
+
+def _on(x, stream, *tensors):
+    """Checks that the call's other tensors are on x's device; returns the stream
+    (x's device's current one by default) and its handle."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError(f"CUDA tensors expected, got one on {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"stream on {s.device}, tensors on {dev}")
+    return s, ctypes.c_void_p(s.cuda_stream)
+
+
+def _call(dev, what, fn, *args):
+    """A library call with `dev` as the current device."""
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args), what)
+
+
+def _scratch(nbytes, s, dev):
+    """A workspace for one call, its status word cleared, in `s`'s order."""
+    with torch.cuda.stream(s):
+        return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+
+
+def _result(shape, dtype, s, dev):
+    """An output allocated in `s`'s order."""
+    if s == torch.cuda.current_stream(dev):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _fmt(t, name):
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return BF16 if t.dtype == torch.bfloat16 else F32
+
+
+def rms_norm(x, w, eps: float = 1e-5, out=None, stream=None):
+    """The norm before a block: x [T, H] bf16 or fp32, w fp32 [H] -> bf16 [T, H] (lmoe_rms_norm)."""
+    T, H = x.shape
+    fmt = _fmt(x, "x")
+    _need(x, x.dtype, (T, H), "x")
+    _need(w, torch.float32, (H,), "w")
+    s, sp = _on(x, stream, w, out)
+    if out is None:
+        out = _result((T, H), torch.bfloat16, s, x.device)
+    _need(out, torch.bfloat16, (T, H), "out")
+    _call(x.device, "lmoe_rms_norm", _rms_norm, x.data_ptr(), fmt, w.data_ptr(), eps, T, H, out.data_ptr(), sp)
+    return out
+
+
+def residual_norm(y, res, post_w=None, gate=None, scale: float = 1.0, next_w=None, eps: float = 1e-5, res_out=None,
+                  next_out=None, stream=None):
+    """After a block (lmoe_residual_norm): res + scale * gate * norm(y; post_w)
+    and, with next_w, its norm.  y bf16 [T, H]; res [T, H] bf16 or fp32; gate
+    fp32 [H] or [1, H] (per channel), fp32 [T, 1] (per token) or bf16 [T, H].
+    Returns (res_out, next_out or None)."""
+    T, H = y.shape
+    fmt = _fmt(res, "res")
+    _need(y, torch.bfloat16, (T, H), "y")
+    _need(res, res.dtype, (T, H), "res")
+    for t, name in ((post_w, "post_w"), (next_w, "next_w")):
+        if t is not None:
+            _need(t, torch.float32, (H,), name)
+    kind = GATE_NONE
+    if gate is not None:
+        if gate.dtype == torch.bfloat16:
+            kind = GATE_FULL
+            _need(gate, torch.bfloat16, (T, H), "gate")
+        elif tuple(gate.shape) == (T, 1) and H != 1:
+            kind = GATE_TOKEN
+            _need(gate, torch.float32, (T, 1), "gate")
+        else:
+            kind = GATE_CHANNEL
+            _need(gate, torch.float32, (H,) if gate.dim() == 1 else (1, H), "gate")
+    s, sp = _on(y, stream, res, post_w, gate, next_w, res_out, next_out)
+    if res_out is None:
+        res_out = _result((T, H), res.dtype, s, y.device)
+    _need(res_out, res.dtype, (T, H), "res_out")
+    if next_w is not None:
+        if next_out is None:
+            next_out = _result((T, H), torch.bfloat16, s, y.device)
+        _need(next_out, torch.bfloat16, (T, H), "next_out")
+    elif next_out is not None:
+        raise ValueError("next_out without next_w")
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _call(y.device, "lmoe_residual_norm", _residual_norm, y.data_ptr(), res.data_ptr(), fmt, ptr(post_w), ptr(gate),
+          kind, scale, eps, ptr(next_w), T, H, res_out.data_ptr(), ptr(next_out), sp)
+    return res_out, next_out
+
+
+def linear_mxfp4_workspace_size(rows: int, K: int, N: int) -> int:
+    return int(_linear_mx_ws(rows, K, N))
+
+
+def linear_mxfp4(x, q, s, N: int, out=None, ws=None, stream=None):
+    """out = bf16(x W^T): x bf16 [rows, K], W one MXFP4 matrix [N, K] in the
+    tensor-core layout (q, s of quant_mxfp4 or repack_mxfp4).  `ws`: a zeroed
+    workspace of linear_mxfp4_workspace_size bytes, kept by the caller; one is
+    made for the call without it."""
+    rows, K = x.shape
+    _need(x, torch.bfloat16, (rows, K), "x")
+    qb, sb = mxfp4_bytes(1, N, K, LAYOUT_TC) if K % 32 == 0 and K > 0 and N > 0 else (0, 0)
+    if qb == 0:
+        raise ValueError(f"weights [{N}, {K}]: K must be a multiple of 32")
+    _need(q, torch.uint8, (qb,), "q")
+    _need(s, torch.uint8, (sb,), "s")
+    st, sp = _on(x, stream, q, s, out, ws)
+    if out is None:
+        out = _result((rows, N), torch.bfloat16, st, x.device)
+    _need(out, torch.bfloat16, (rows, N), "out")
+    if ws is None:
+        ws = _scratch(linear_mxfp4_workspace_size(rows, K, N), st, x.device)
+    _call(x.device, "lmoe_linear_mxfp4", _linear_mx, x.data_ptr(), q.data_ptr(), s.data_ptr(), rows, K, N,
+          out.data_ptr(), ws.data_ptr(), ws.numel(), sp)
+    return out
+
+
+def grouped_workspace_size() -> int:
+    return int(_grouped_ws())
+
+
+def _groups(offsets, perm, k, P, E):
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    if perm is not None:
+        _need(perm, torch.int32, (P,), "perm")
+    return Groups(offsets.data_ptr(), None if perm is None else perm.data_ptr(), P, E, k)
+
+
+def grouped_linear_bf16(x, W, offsets, perm=None, k: int = 1, gather=None, row_w=None, out=None, ws=None, stream=None):
+    """Products grouped by expert (lmoe_grouped_linear_bf16): row q of expert e
+    (offsets[e] <= q < offsets[e + 1]) is x[perm[q] // k] (gather, the default
+    with perm) or x[q], times W[e]^T, W bf16 [E, N, K].  Without row_w: bf16
+    [P, N].  With row_w (fp32, P values in pair order): fp32 [P, N], row q
+    times row_w[perm[q]].  `out` may be given in either type; rows in no group
+    are not written.  `ws`: a zeroed workspace kept by the caller."""
+    E, N, K = W.shape
+    gather = perm is not None if gather is None else bool(gather)
+    P = x.shape[0] if perm is None else perm.shape[0]
+    _need(x, torch.bfloat16, (x.shape[0], K), "x")
+    _need(W, torch.bfloat16, (E, N, K), "W")
+    G = _groups(offsets, perm, k, P, E)
+    if row_w is not None:
+        _need(row_w, torch.float32, row_w.shape, "row_w")
+        if row_w.numel() != P:
+            raise ValueError(f"row_w: {P} values expected, got {row_w.numel()}")
+    s, sp = _on(x, stream, W, offsets, perm, row_w, out, ws)
+    if out is None:
+        out = _result((P, N), torch.float32 if row_w is not None else torch.bfloat16, s, x.device)
+    fmt = _fmt(out, "out")
+    _need(out, out.dtype, (P, N), "out")
+    if ws is None:
+        ws = _scratch(256, s, x.device)
+    _call(x.device, "lmoe_grouped_linear_bf16", _grouped_linear, x.data_ptr(), x.shape[0], W.data_ptr(),
+          ctypes.byref(G), int(gather), None if row_w is None else row_w.data_ptr(), K, N, fmt, out.data_ptr(),
+          ws.data_ptr(), ws.numel(), sp)
+    return out
+
+
+def grouped_swiglu_bf16(x, Wg, Wu, offsets, perm=None, k: int = 1, gather=None, out=None, ws=None, stream=None):
+    """bf16 [P, I] rows silu(x Wg[e]^T) * (x Wu[e]^T), both products and the
+    gating in one kernel (lmoe_grouped_swiglu_bf16); arguments as for
+    grouped_linear_bf16."""
+    E, I, K = Wg.shape
+    gather = perm is not None if gather is None else bool(gather)
+    P = x.shape[0] if perm is None else perm.shape[0]
+    _need(x, torch.bfloat16, (x.shape[0], K), "x")
+    _need(Wg, torch.bfloat16, (E, I, K), "Wg")
+    _need(Wu, torch.bfloat16, (E, I, K), "Wu")
+    G = _groups(offsets, perm, k, P, E)
+    s, sp = _on(x, stream, Wg, Wu, offsets, perm, out, ws)
+    if out is None:
+        out = _result((P, I), torch.bfloat16, s, x.device)
+    _need(out, torch.bfloat16, (P, I), "out")
+    if ws is None:
+        ws = _scratch(256, s, x.device)
+    _call(x.device, "lmoe_grouped_swiglu_bf16", _grouped_swiglu, x.data_ptr(), x.shape[0], Wg.data_ptr(),
+          Wu.data_ptr(), ctypes.byref(G), int(gather), K, I, out.data_ptr(), ws.data_ptr(), ws.numel(), sp)
     return out
 
 
