@@ -53,21 +53,6 @@ struct DCfg {
     static_assert(STAGES >= 2, "pipeline depth");
 };
 
-// kind::f16 instruction descriptor: fp32 accumulator, A and B bf16, both
-// K-major, M = 128, N given.
-__device__ __forceinline__ uint32_t idesc_bf16(uint32_t N)
-{
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((128u >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
 template <int NPARTS, int NB, int OUT>
 __global__ void __launch_bounds__(192, 1)
     k_gemm_bf16(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const DenseArgs p)

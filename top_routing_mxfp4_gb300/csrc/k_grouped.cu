@@ -1,95 +1,516 @@
 // bf16 products grouped by expert, ragged groups:
 //   out[q][n] = w(q) * sum_c x[src(q)][c] * W[e(q)][n][c]
-// and the gated pair h[q][i] = bf16( silu(g) * u ).
+// and the gated pair h[q][i] = bf16( silu(g) * u ), on the tensor cores
+// (tcgen05.mma kind::f16, fp32 accumulation in TMEM).
 //
-// First, plain form: a block owns 32 rows of one group and 32 output columns,
-// both operands' 32-column slices in shared memory, fp32 products and sums.
+// The weight rows are the M = 128 operand (A), the expert's rows the N operand
+// (B, both K-major, 64 columns = one 128-byte swizzle row a chunk), so N
+// follows the group's rows (16..NT in steps of 16) and a short group costs no
+// tensor work on padding.  For the gated pair an A tile holds 64 features:
+// of each TMEM lane quarter's 32 rows, 16 of the gate matrix and the same 16
+// of the up matrix, so both products of a feature meet in one warp and the
+// accumulator is no larger than a plain one.
+//
+// Work items (expert, row tile of NT, weight tile), row tile fastest, so an A
+// tile is read from HBM once and the row tiles that share it run side by side
+// out of L2.  The item list is never written down: every CTA scans the offsets
+// into per-expert tile counts in shared memory and finds its items by a warp
+// search.
+//
+// Persistent CTA, 256 threads: warp 0 streams A (TMA), warp 1 issues the MMAs,
+// warps 2-5 are the epilogue (TMEM lane quarter = warp % 4), warp 6 brings B:
+// boxes of 16 or 32 rows where a group's rows are consecutive, or gather4
+// copies of four rows each where they come through the permutation.
+// Where the host can tell that the items cannot fill the GPU, a cluster of KS
+// CTAs shares an item along K, and rank 0 adds the others' accumulators, which
+// they store into its shared memory, in rank order.
+// Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "lmoe_internal.cuh"
+#include "schedule.cuh"
+#include "tc_ptx.cuh"
 
 namespace lmoe {
 namespace {
 
-constexpr int BT = 32;
+using namespace tc;
 
-// Offsets of a group, checked: false (and the status word) unless
-// 0 <= o0 <= o1 <= P.
-__device__ __forceinline__ bool group_ok(const GroupedArgs &p, int o0, int o1)
-{
-    if (o0 >= 0 && o0 <= o1 && o1 <= p.P) return true;
-    set_status(p.status, LMOE_ERR_DEVICE_CHECK);
-    return false;
-}
+constexpr int THREADS = 256;
+constexpr uint32_t A_TILE = 128 * 128;  // 128 rows x 64 bf16
 
-__global__ void __launch_bounds__(256) k_grouped_plain(const GroupedArgs p)
+template <int NT, int KS>
+struct GCfg {
+    static constexpr uint32_t B_TILE = NT * 128;
+    static constexpr uint32_t STAGE = A_TILE + B_TILE;
+    static constexpr int BOX = NT < 32 ? 16 : 32;  // rows of a B box
+    static constexpr uint32_t RED = (KS - 1) * 128 * NT * 4;  // the other ranks' accumulators
+    static constexpr int S_RAW = int((200 * 1024 - RED) / STAGE);
+    static constexpr int S = S_RAW > 10 ? 10 : S_RAW;
+    static constexpr int ACC = 2;  // accumulators: an item's epilogue overlaps the next one's MMAs
+    static constexpr uint32_t TMEM_COLS = ACC * NT < 32 ? 32 : ACC * NT;
+    static constexpr int LANE_ROWS = (NT + 31) / 32;  // gathered: rows a lane of warp 6 holds the ids of / 4
+};
+
+struct GArgs {
+    const int32_t *offsets, *perm;
+    const float *row_w;
+    int64_t P, x_rows;
+    int E, k, N, MT, KC;
+    int max_items;  // no valid groups have more
+    int out_f32;
+    void *out;
+    int32_t *status;
+    long long limit;
+    int stall;
+};
+
+struct GItem {
+    int e, m, row0, nv;  // expert, weight tile, first row, rows
+};
+
+// Walks a CTA's items in order; every lane of a warp calls next().
+template <int NT>
+struct Walk {
+    const int32_t *s_tiles, *s_off;
+    int E, MT, e = 0;
+    __device__ GItem at(int it)
+    {
+        const int t = it / MT;  // s_tiles[e] * MT <= it < s_tiles[e + 1] * MT
+        const int lane = threadIdx.x & 31;
+        for (;;) {
+            const int c = e + 1 + lane;
+            const unsigned b = __ballot_sync(0xFFFFFFFFu, c < E && s_tiles[c] <= t);
+            const int n = __popc(b);
+            e += n;
+            if (n < 32) break;
+        }
+        const int nt = s_tiles[e + 1] - s_tiles[e], l = it - s_tiles[e] * MT;
+        GItem r;
+        r.e = e;
+        r.m = l / nt;
+        const int n = l - r.m * nt;
+        r.row0 = s_off[e] + n * NT;
+        r.nv = min(NT, s_off[e + 1] - r.row0);
+        return r;
+    }
+};
+
+template <int NT, bool SWIGLU, bool GATHER, int KS>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_grouped(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
+              const __grid_constant__ CUtensorMap tmB, const GArgs p)
 {
-    __shared__ float xs[BT][BT + 1], ws[BT][BT + 1], us[BT][BT + 1];
-    __shared__ int src[BT];
+    using C = GCfg<NT, KS>;
+    constexpr int S = C::S;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // KS > 1: [KS - 1][NT][128]
+    uint64_t *full = reinterpret_cast<uint64_t *>(red + (KS - 1) * 128 * NT);
+    uint64_t *empty = full + S;
+    uint64_t *acc_full = empty + S;
+    uint64_t *acc_empty = acc_full + C::ACC;
+    uint64_t *drain = acc_empty + C::ACC;
+    uint64_t *red_full = drain + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(red_full + 1);
+    int32_t *warp_tot = reinterpret_cast<int32_t *>(tmem_slot + 2);
+    int32_t *s_off = warp_tot + 8;
+    int32_t *s_tiles = s_off + p.E + 1;
+    int32_t *s_cnt = s_tiles + p.E + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 2);  // the A and the B producer
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < C::ACC; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], 128);
+        }
+        mbar_init(drain, 1);
+        mbar_init(red_full, (KS - 1) * 128 > 0 ? (KS - 1) * 128 : 1);
+        mbar_init_fence();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmA);
+        if (SWIGLU) prefetch_tensormap(&tmA2);
+    }
+    if (warp == 6 && lane == 0) prefetch_tensormap(&tmB);
+    if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
     pdl_enter();
-    const int n0 = blockIdx.x * BT, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    for (int e = blockIdx.y; e < p.E; e += gridDim.y) {
-        const int o0 = p.offsets[e], o1 = p.offsets[e + 1];
-        if (!group_ok(p, o0, o1)) continue;
-        for (int r0 = o0; r0 < o1; r0 += BT) {
-            __syncthreads();
-            if (threadIdx.x < BT) {
-                int sr = -1;
-                if (r0 + tx < o1) {
-                    sr = p.gather ? p.perm[r0 + tx] / p.k : r0 + tx;
-                    if (sr < 0 || sr >= p.x_rows) {
-                        set_status(p.status, LMOE_ERR_DEVICE_CHECK);
-                        sr = -1;
-                    }
-                }
-                src[tx] = sr;
-            }
-            __syncthreads();
-            float a[4] = {}, b[4] = {};
-            for (int c0 = 0; c0 < p.K; c0 += BT) {
-                for (int i = ty; i < BT; i += 8) {
-                    const bool in = c0 + tx < p.K;
-                    xs[i][tx] = in && src[i] >= 0 ? bf16_bits_to_f32(p.x[int64_t(src[i]) * p.K + c0 + tx]) : 0.f;
-                    const int64_t wr = (int64_t(e) * p.N + n0 + i) * p.K + c0 + tx;
-                    const bool wi = in && n0 + i < p.N;
-                    ws[i][tx] = wi ? bf16_bits_to_f32(p.W[wr]) : 0.f;
-                    us[i][tx] = wi && p.W2 ? bf16_bits_to_f32(p.W2[wr]) : 0.f;
-                }
-                __syncthreads();
-                for (int c = 0; c < BT; ++c)
+    // row tiles per expert, scanned; a group that breaks 0 <= o0 <= o1 <= P is empty and reported
+    bool bad = false;
+    for (int e = threadIdx.x; e < p.E; e += THREADS) {
+        const int o0 = __ldg(p.offsets + e), o1 = __ldg(p.offsets + e + 1);
+        const bool ok = o0 >= 0 && o0 <= o1 && o1 <= p.P;
+        bad |= !ok;
+        s_off[e] = o0;
+        if (e == p.E - 1) s_off[p.E] = o1;
+        s_cnt[e] = ok ? (o1 - o0 + NT - 1) / NT : 0;
+    }
+    tc_fence_before();
+    bad = __syncthreads_or(bad);
+    tc_fence_after();
+    block_scan<THREADS>(s_cnt, p.E, s_tiles, warp_tot);
+    if (KS > 1) cluster_sync();  // the cluster's barriers are initialised
+    const uint32_t tmem = *tmem_slot;
+    // Around a bad group others may overlap, so that there are more tiles than
+    // any valid groups have: no more than those are worked off, and none where
+    // the tile counts may have wrapped.
+    int total = s_tiles[p.E] * p.MT;
+    if (bad) {
+        if (threadIdx.x == 0) set_status(p.status, LMOE_ERR_DEVICE_CHECK);
+        const int64_t most = int64_t(p.E) * ceil_div(p.P, NT) * p.MT;
+        total = most > INT32_MAX ? 0 : min(total, p.max_items);
+    }
+    const int rank = KS > 1 ? int(cluster_rank()) : 0;
+    const int first = int(blockIdx.x) / KS, step = int(gridDim.x) / KS;
+    // this rank's K chunks
+    const int k0 = KS > 1 ? rank * p.KC / KS : 0, k1 = KS > 1 ? (rank + 1) * p.KC / KS : p.KC;
+    Walk<NT> walk{s_tiles, s_off, p.E, p.MT};
+
+    // Copies still in flight after a timeout land before the CTA ends (bounded).
+    auto settle = [&](int fills) {
+        for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
+    };
+
+    if (warp == 0 || warp == 6) {
+        // ---------------- producers: A (warp 0), B (warp 6) ----------------
+        int stage = 0, fills = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int it = first; it < total && ok; it += step) {
+            const GItem w = walk.at(it);
+            [[maybe_unused]] int4 rows[C::LANE_ROWS > 1 ? 2 : 1];
+            const int nb = GATHER ? (w.nv + 3) / 4 : (w.nv + C::BOX - 1) / C::BOX;  // copies of B a chunk
+            if (GATHER && warp == 6) {
+#pragma unroll
+                for (int i = 0; i < (C::LANE_ROWS > 1 ? 2 : 1); ++i) {
+                    int r[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        a[j] = fmaf(xs[ty + 8 * j][c], ws[tx][c], a[j]);
-                        b[j] = fmaf(xs[ty + 8 * j][c], us[tx][c], b[j]);
+                        const int l = 4 * (lane + 32 * i) + j;
+                        r[j] = 0;
+                        if (l < w.nv) {
+                            const int pr = __ldg(p.perm + w.row0 + l);
+                            r[j] = pr / p.k;
+                            if (pr < 0 || r[j] >= p.x_rows) {
+                                set_status(p.status, LMOE_ERR_DEVICE_CHECK);
+                                r[j] = 0;
+                            }
+                        }
                     }
-                __syncthreads();
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t qr = r0 + ty + 8 * j;
-                if (qr >= o1 || n0 + tx >= p.N) continue;
-                float v = p.W2 ? a[j] / (1.f + __expf(-a[j])) * b[j] : a[j];
-                if (p.row_w) {
-                    const int64_t pr = p.perm ? p.perm[qr] : qr;
-                    if (pr >= 0 && pr < p.P)
-                        v *= p.row_w[pr];
-                    else
-                        set_status(p.status, LMOE_ERR_DEVICE_CHECK);
+                    rows[i] = make_int4(r[0], r[1], r[2], r[3]);
                 }
-                if (p.out_fmt == LMOE_F32)
-                    static_cast<float *>(p.out)[qr * p.N + n0 + tx] = v;
-                else
-                    static_cast<__nv_bfloat16 *>(p.out)[qr * p.N + n0 + tx] = __float2bfloat16_rn(v);
+            }
+            for (int kc = k0; kc < k1; ++kc) {
+                ok = mbar_wait(&empty[stage], phase ^ 1, p.limit);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                uint8_t *sb = stages + stage * C::STAGE;
+                if (warp == 0) {
+                    if (lane == 0 && !(p.stall && it == first && kc == k0)) {
+                        mbar_arrive_expect_tx(&full[stage], A_TILE);
+                        if (SWIGLU) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                tma_load_2d(sb + j * 4096, &tmA, kc * 64, w.e * p.N + w.m * 64 + 16 * j, &full[stage]);
+                                tma_load_2d(sb + j * 4096 + 2048, &tmA2, kc * 64, w.e * p.N + w.m * 64 + 16 * j,
+                                            &full[stage]);
+                            }
+                        } else {
+                            tma_load_2d(sb, &tmA, kc * 64, w.e * p.N + w.m * 128, &full[stage]);
+                        }
+                    }
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], uint32_t(nb) * (GATHER ? 512u : C::BOX * 128u));
+                    __syncwarp();
+                    if (GATHER) {
+#pragma unroll
+                        for (int i = 0; i < (C::LANE_ROWS > 1 ? 2 : 1); ++i)
+                            if (lane + 32 * i < nb)
+                                tma_gather4(sb + A_TILE + (lane + 32 * i) * 512, &tmB, kc * 64, rows[i], &full[stage]);
+                    } else if (lane < nb) {
+                        tma_load_2d(sb + A_TILE + lane * C::BOX * 128, &tmB, kc * 64, w.row0 + lane * C::BOX,
+                                    &full[stage]);
+                    }
+                }
+                ++fills;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok) settle(fills);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (int it = first; it < total && ok; it += step) {
+            const GItem w = walk.at(it);
+            const uint32_t id = idesc_bf16(uint32_t((w.nv + 15) & ~15));
+            ok = mbar_wait(&acc_empty[acc], acc_phase ^ 1, p.limit);
+            tc_fence_after();
+            const uint32_t d = tmem + uint32_t(acc * NT);
+            for (int kc = k0; kc < k1 && ok; ++kc) {
+                ok = mbar_wait(&full[stage], phase, p.limit);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint8_t *sb = stages + stage * C::STAGE;
+                    const uint64_t ad = sdesc_k128(smem_u32(sb)), bd = sdesc_k128(smem_u32(sb + A_TILE));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)  // 4 x K = 16 per 128-byte row
+                        mma_bf16(d, ad + 2 * kk, bd + 2 * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
+                    tc_commit(&empty[stage]);
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (lane == 0) tc_commit(&acc_full[acc]);
+            __syncwarp();
+            if (++acc == C::ACC) {
+                acc = 0;
+                acc_phase ^= 1;
+            }
+        }
+        if (!ok) {
+            if (lane == 0) {
+                set_status(p.status, LMOE_ERR_TIMEOUT);
+                tc_commit(drain);  // this CTA's MMAs in flight end before the tensor memory is freed
+                mbar_wait(drain, 0, p.limit);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 2 && warp < 6) {
+        // ---------------- epilogue ----------------
+        const int q = warp & 3;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int it = first; it < total; it += step) {
+            const GItem w = walk.at(it);
+            const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.limit);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
+            if (KS > 1 && rank > 0) {
+                // this rank's sums into rank 0's shared memory, [NT][128]
+                const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * 128 * NT + 32 * q + lane), 0);
+                for (int c0 = 0; c0 < w.nv; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tb + c0, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) cluster_store(dst + (c0 + j) * 512, __uint_as_float(v[j]));
+                }
+                cluster_arrive(cluster_map(smem_u32(red_full), 0));
+            } else {
+                if (KS > 1) {
+                    const bool in = mbar_wait_cluster(red_full, 0, p.limit);
+                    if (!__all_sync(0xFFFFFFFFu, in)) {
+                        if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                        break;
+                    }
+                }
+                // plain: lane = output column; gated: lanes 0-15 gate, 16-31 up of 16 features
+                const int n = SWIGLU ? w.m * 64 + 16 * q + (lane & 15) : w.m * 128 + 32 * q + lane;
+                const bool mine = n < p.N && (!SWIGLU || lane < 16);
+                for (int c0 = 0; c0 < w.nv; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tb + c0, v);
+                    float rw = 1.f;  // lane j: the weight of row c0 + j
+                    if (!SWIGLU && p.row_w && lane < 16 && c0 + lane < w.nv) {
+                        const int64_t pr = p.perm ? __ldg(p.perm + w.row0 + c0 + lane) : w.row0 + c0 + lane;
+                        if (pr >= 0 && pr < p.P)
+                            rw = __ldg(p.row_w + pr);
+                        else
+                            set_status(p.status, LMOE_ERR_DEVICE_CHECK);
+                    }
+                    tmem_ld_wait();
+                    float y[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]);
+                    if (KS > 1) {
+                        const float *part = red + c0 * 128 + 32 * q + lane;
+#pragma unroll
+                        for (int r = 0; r < KS - 1; ++r)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) y[j] += part[(r * NT + j) * 128];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (SWIGLU) {
+                            const float u = __shfl_down_sync(0xFFFFFFFFu, y[j], 16);
+                            y[j] = __fdividef(y[j], 1.f + expf(-y[j])) * u;
+                        } else if (p.row_w) {
+                            y[j] *= __shfl_sync(0xFFFFFFFFu, rw, j);
+                        }
+                    }
+                    if (mine) {
+                        const int64_t o = int64_t(w.row0 + c0) * p.N + n;
+                        if (!SWIGLU && p.out_f32) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (c0 + j < w.nv) static_cast<float *>(p.out)[o + int64_t(j) * p.N] = y[j];
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (c0 + j < w.nv)
+                                    static_cast<__nv_bfloat16 *>(p.out)[o + int64_t(j) * p.N] =
+                                        __float2bfloat16_rn(y[j]);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&acc_empty[acc]);
+            if (++acc == C::ACC) {
+                acc = 0;
+                acc_phase ^= 1;
             }
         }
     }
+    tc_fence_before();
+    __syncthreads();
+    if (KS > 1) cluster_sync();  // nobody's shared memory goes while another rank may store into it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool bf16_map(CUtensorMap *m, const void *base, int64_t K, int64_t rows, int box_rows)
+{
+    static const EncodeTiledFn fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(K) * 2};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
+    const cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count()
+{
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+template <int NT, bool SWIGLU, bool GATHER, int KS>
+cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms, cudaStream_t st)
+{
+    using C = GCfg<NT, KS>;
+    CUtensorMap ma, ma2, mb;
+    if (!bf16_map(&ma, a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
+        !bf16_map(&ma2, SWIGLU ? a.W2 : a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
+        !bf16_map(&mb, a.x, a.K, a.x_rows, GATHER ? 1 : C::BOX))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + size_t(C::S) * C::STAGE + size_t(KS - 1) * 128 * NT * 4 + (2 * C::S + 2 * C::ACC + 2) * 8 +
+                        16 + 32 + size_t(3 * a.E + 2) * 4;
+    auto *kern = k_grouped<NT, SWIGLU, GATHER, KS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t slots = sms / KS;
+    const unsigned grid = unsigned((items < slots ? items : slots) * KS);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = KS;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = KS > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, ma, ma2, mb, g);
+}
+
+template <int NT, int KS>
+cudaError_t pick(const GroupedArgs &a, const GArgs &g, int64_t items, int sms, cudaStream_t st)
+{
+    if (a.W2)
+        return a.gather ? launch<NT, true, true, KS>(a, g, items, sms, st)
+                        : launch<NT, true, false, KS>(a, g, items, sms, st);
+    return a.gather ? launch<NT, false, true, KS>(a, g, items, sms, st)
+                    : launch<NT, false, false, KS>(a, g, items, sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st)
 {
-    return launch_pdl(k_grouped_plain, dim3(unsigned(ceil_div(a.N, BT)), unsigned(a.E)), dim3(256), 0, st, a);
+    GArgs g{};
+    g.offsets = a.offsets;
+    g.perm = a.perm;
+    g.row_w = a.row_w;
+    g.P = a.P;
+    g.x_rows = a.x_rows;
+    g.E = a.E;
+    g.k = a.k;
+    g.N = a.N;
+    g.MT = int(ceil_div(a.N, a.W2 ? 64 : 128));
+    g.KC = int(ceil_div(a.K, 64));
+    g.out_f32 = a.out_fmt == LMOE_F32;
+    g.out = a.out;
+    g.status = a.status;
+    g.limit = a.wait.limit > 0 ? a.wait.limit : 4000000000LL;  // about 2 s of SM clocks
+    g.stall = a.wait.stall_first_fill;
+    // Row tile: the smallest that holds a group of average size and a quarter
+    // more, so that most groups are one tile.
+    const int64_t active = a.P < a.E ? a.P : a.E;
+    const int64_t rows = ceil_div(a.P * 5, active * 4);
+    const int NT = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    // most tiles there can be, whatever the groups are
+    const int64_t by_rows = (a.P + active * (NT - 1)) / NT;
+    const int64_t items = (by_rows < a.P ? by_rows : a.P) * g.MT;
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    g.max_items = int(items);
+    const int sms = sm_count();
+    if (NT == 16) {
+        // Items that cannot fill the GPU: several CTAs along K an item, each at least 4 chunks.
+        if (items * 8 <= sms && g.KC >= 32) return pick<16, 8>(a, g, items, sms, st);
+        if (items * 4 <= sms && g.KC >= 16) return pick<16, 4>(a, g, items, sms, st);
+        if (items * 2 <= sms && g.KC >= 8) return pick<16, 2>(a, g, items, sms, st);
+        return pick<16, 1>(a, g, items, sms, st);
+    }
+    switch (NT) {
+    case 32: return pick<32, 1>(a, g, items, sms, st);
+    case 64: return pick<64, 1>(a, g, items, sms, st);
+    case 128: return pick<128, 1>(a, g, items, sms, st);
+    default: return pick<256, 1>(a, g, items, sms, st);
+    }
 }
 
 }  // namespace lmoe

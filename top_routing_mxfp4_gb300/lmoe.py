@@ -509,61 +509,84 @@ def linear_bf16(x, W, out=None, stream=None):
 
 # ---- norms, MXFP4 linear and grouped products around the layer ----------------------------
 
-def _on(x, stream, *tensors):
-    """Checks that the call's other tensors are on x's device; returns the stream
-    (x's device's current one by default) and its handle."""
-    dev = x.device
-    if dev.type != "cuda":
-        raise ValueError(f"CUDA tensors expected, got one on {dev}")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"stream on {s.device}, tensors on {dev}")
-    return s, ctypes.c_void_p(s.cuda_stream)
+# These calls run on the device of their first tensor and, by default, on that
+# device's current stream.  The checks are written for short calls: a call of a
+# few microseconds on the GPU is launched by a few on the host.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_cur_device = torch._C._cuda_getDevice
+_empty_on = torch.empty
 
 
-def _call(dev, what, fn, *args):
-    """A library call with `dev` as the current device."""
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args), what)
+def _bad(t, dtype, shape, name):
+    raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)} on "
+                     f"{t.device}, strides {t.stride()}")
+
+
+def _arg(t, dtype, shape, name, di):
+    """Checks one tensor (contiguous, on CUDA device `di`); returns its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != di or di < 0 or not t.is_contiguous():
+        if di >= 0 and t.is_cuda and t.get_device() != di:
+            raise ValueError(f"{name}: on {t.device}, the call's first tensor on cuda:{di}")
+        _bad(t, dtype, shape, name)
+    return t.data_ptr()
+
+
+def _make(make, shape, dtype, x, stream):
+    """A tensor for the call's result or scratch, allocated in the order of the call's stream."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=x.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=x.device)
+
+
+def _handle(stream, di):
+    if stream is None:
+        return _raw_stream(di)
+    if stream.device.index != di:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{di}")
+    return stream.cuda_stream
+
+
+def _run(di, what, fn, *args):
+    """A library call with device `di` current."""
+    if _cur_device() == di:
+        code = fn(*args)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args), what)
-
-
-def _scratch(nbytes, s, dev):
-    """A workspace for one call, its status word cleared, in `s`'s order."""
-    with torch.cuda.stream(s):
-        return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
-
-
-def _result(shape, dtype, s, dev):
-    """An output allocated in `s`'s order."""
-    if s == torch.cuda.current_stream(dev):
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        with torch.cuda.device(di):
+            code = fn(*args)
+    if code != OK:
+        raise LmoeError(code, what)
 
 
 def _fmt(t, name):
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
-    return BF16 if t.dtype == torch.bfloat16 else F32
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+
+
+def _ws_arg(ws, di):
+    if ws.dtype is not torch.uint8 or ws.get_device() != di or not ws.is_contiguous():
+        _bad(ws, torch.uint8, ws.shape, "ws")
+    return ws.data_ptr()
 
 
 def rms_norm(x, w, eps: float = 1e-5, out=None, stream=None):
     """The norm before a block: x [T, H] bf16 or fp32, w fp32 [H] -> bf16 [T, H] (lmoe_rms_norm)."""
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
+    di = x.get_device()
     fmt = _fmt(x, "x")
-    _need(x, x.dtype, (T, H), "x")
-    _need(w, torch.float32, (H,), "w")
-    s, sp = _on(x, stream, w, out)
+    xp = _arg(x, x.dtype, shape, "x", di)
+    wp = _arg(w, torch.float32, (H,), "w", di)
+    sp = _handle(stream, di)
     if out is None:
-        out = _result((T, H), torch.bfloat16, s, x.device)
-    _need(out, torch.bfloat16, (T, H), "out")
-    _call(x.device, "lmoe_rms_norm", _rms_norm, x.data_ptr(), fmt, w.data_ptr(), eps, T, H, out.data_ptr(), sp)
+        out = _make(_empty_on, shape, torch.bfloat16, x, stream)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, torch.bfloat16, shape, "out", di)
+    _run(di, "lmoe_rms_norm", _rms_norm, xp, fmt, wp, eps, T, H, op, sp)
     return out
 
 
@@ -573,37 +596,39 @@ def residual_norm(y, res, post_w=None, gate=None, scale: float = 1.0, next_w=Non
     and, with next_w, its norm.  y bf16 [T, H]; res [T, H] bf16 or fp32; gate
     fp32 [H] or [1, H] (per channel), fp32 [T, 1] (per token) or bf16 [T, H].
     Returns (res_out, next_out or None)."""
-    T, H = y.shape
+    shape = y.shape
+    T, H = shape
+    di = y.get_device()
     fmt = _fmt(res, "res")
-    _need(y, torch.bfloat16, (T, H), "y")
-    _need(res, res.dtype, (T, H), "res")
-    for t, name in ((post_w, "post_w"), (next_w, "next_w")):
-        if t is not None:
-            _need(t, torch.float32, (H,), name)
-    kind = GATE_NONE
+    yp = _arg(y, torch.bfloat16, shape, "y", di)
+    rp = _arg(res, res.dtype, shape, "res", di)
+    pp = None if post_w is None else _arg(post_w, torch.float32, (H,), "post_w", di)
+    kind, gp = GATE_NONE, None
     if gate is not None:
-        if gate.dtype == torch.bfloat16:
-            kind = GATE_FULL
-            _need(gate, torch.bfloat16, (T, H), "gate")
-        elif tuple(gate.shape) == (T, 1) and H != 1:
-            kind = GATE_TOKEN
-            _need(gate, torch.float32, (T, 1), "gate")
+        gs = gate.shape
+        if gate.dtype is torch.bfloat16:
+            kind, gp = GATE_FULL, _arg(gate, torch.bfloat16, shape, "gate", di)
+        elif gs == (T, 1):
+            kind, gp = GATE_TOKEN, _arg(gate, torch.float32, gs, "gate", di)
         else:
-            kind = GATE_CHANNEL
-            _need(gate, torch.float32, (H,) if gate.dim() == 1 else (1, H), "gate")
-    s, sp = _on(y, stream, res, post_w, gate, next_w, res_out, next_out)
+            kind, gp = GATE_CHANNEL, _arg(gate, torch.float32, (1, H) if len(gs) == 2 else (H,), "gate", di)
+    sp = _handle(stream, di)
     if res_out is None:
-        res_out = _result((T, H), res.dtype, s, y.device)
-    _need(res_out, res.dtype, (T, H), "res_out")
+        res_out = _make(_empty_on, shape, res.dtype, y, stream)
+        rop = res_out.data_ptr()
+    else:
+        rop = _arg(res_out, res.dtype, shape, "res_out", di)
+    np_ = nop = None
     if next_w is not None:
+        np_ = _arg(next_w, torch.float32, (H,), "next_w", di)
         if next_out is None:
-            next_out = _result((T, H), torch.bfloat16, s, y.device)
-        _need(next_out, torch.bfloat16, (T, H), "next_out")
+            next_out = _make(_empty_on, shape, torch.bfloat16, y, stream)
+            nop = next_out.data_ptr()
+        else:
+            nop = _arg(next_out, torch.bfloat16, shape, "next_out", di)
     elif next_out is not None:
         raise ValueError("next_out without next_w")
-    ptr = lambda t: None if t is None else t.data_ptr()
-    _call(y.device, "lmoe_residual_norm", _residual_norm, y.data_ptr(), res.data_ptr(), fmt, ptr(post_w), ptr(gate),
-          kind, scale, eps, ptr(next_w), T, H, res_out.data_ptr(), ptr(next_out), sp)
+    _run(di, "lmoe_residual_norm", _residual_norm, yp, rp, fmt, pp, gp, kind, scale, eps, np_, T, H, rop, nop, sp)
     return res_out, next_out
 
 
@@ -617,20 +642,22 @@ def linear_mxfp4(x, q, s, N: int, out=None, ws=None, stream=None):
     workspace of linear_mxfp4_workspace_size bytes, kept by the caller; one is
     made for the call without it."""
     rows, K = x.shape
-    _need(x, torch.bfloat16, (rows, K), "x")
-    qb, sb = mxfp4_bytes(1, N, K, LAYOUT_TC) if K % 32 == 0 and K > 0 and N > 0 else (0, 0)
-    if qb == 0:
+    di = x.get_device()
+    if K <= 0 or K % 32 or N <= 0:
         raise ValueError(f"weights [{N}, {K}]: K must be a multiple of 32")
-    _need(q, torch.uint8, (qb,), "q")
-    _need(s, torch.uint8, (sb,), "s")
-    st, sp = _on(x, stream, q, s, out, ws)
+    KC = (K + 127) >> 7
+    xp = _arg(x, torch.bfloat16, (rows, K), "x", di)
+    qp = _arg(q, torch.uint8, (N * KC * 64,), "q", di)
+    spp = _arg(s, torch.uint8, (((N + 127) >> 7) * KC * 512,), "s", di)
+    sp = _handle(stream, di)
     if out is None:
-        out = _result((rows, N), torch.bfloat16, st, x.device)
-    _need(out, torch.bfloat16, (rows, N), "out")
+        out = _make(_empty_on, (rows, N), torch.bfloat16, x, stream)
+        op = out.data_ptr()
+    else:
+        op = _arg(out, torch.bfloat16, (rows, N), "out", di)
     if ws is None:
-        ws = _scratch(linear_mxfp4_workspace_size(rows, K, N), st, x.device)
-    _call(x.device, "lmoe_linear_mxfp4", _linear_mx, x.data_ptr(), q.data_ptr(), s.data_ptr(), rows, K, N,
-          out.data_ptr(), ws.data_ptr(), ws.numel(), sp)
+        ws = _make(torch.zeros, (linear_mxfp4_workspace_size(rows, K, N) or 256,), torch.uint8, x, stream)
+    _run(di, "lmoe_linear_mxfp4", _linear_mx, xp, qp, spp, rows, K, N, op, _ws_arg(ws, di), ws.numel(), sp)
     return out
 
 
@@ -638,11 +665,43 @@ def grouped_workspace_size() -> int:
     return int(_grouped_ws())
 
 
-def _groups(offsets, perm, k, P, E):
-    _need(offsets, torch.int32, (E + 1,), "offsets")
-    if perm is not None:
-        _need(perm, torch.int32, (P,), "perm")
-    return Groups(offsets.data_ptr(), None if perm is None else perm.data_ptr(), P, E, k)
+def _grouped_call(name, x, W, Wu, offsets, perm, k, gather, row_w, out, out_dtype, ws, stream):
+    E, N, K = W.shape
+    di = x.get_device()
+    rows = x.shape[0]
+    xp = _arg(x, torch.bfloat16, (rows, K), "x", di)
+    wp = _arg(W, torch.bfloat16, (E, N, K), "W", di)
+    offp = _arg(offsets, torch.int32, (E + 1,), "offsets", di)
+    if perm is None:
+        P, pp, ga = rows, None, 1 if gather else 0
+    else:
+        P = perm.shape[0]
+        pp, ga = _arg(perm, torch.int32, (P,), "perm", di), 0 if gather is False else 1
+    sp = _handle(stream, di)
+    if out is None:
+        out = _make(_empty_on, (P, N), out_dtype, x, stream)
+        fmt, op = _fmt(out, "out"), out.data_ptr()
+    else:
+        fmt = _fmt(out, "out")
+        op = _arg(out, out.dtype, (P, N), "out", di)
+    if ws is None:
+        ws = _make(torch.zeros, (256,), torch.uint8, x, stream)
+    G = Groups(offp, pp, P, E, k)
+    if Wu is None:
+        rp = None
+        if row_w is not None:
+            if row_w.numel() != P:
+                raise ValueError(f"row_w: {P} values expected, got {row_w.numel()}")
+            rp = _arg(row_w, torch.float32, row_w.shape, "row_w", di)
+        _run(di, name, _grouped_linear, xp, rows, wp, ctypes.byref(G), ga, rp, K, N, fmt, op, _ws_arg(ws, di),
+             ws.numel(), sp)
+    else:
+        if fmt != BF16:
+            raise ValueError("out: expected bfloat16")
+        up = _arg(Wu, torch.bfloat16, (E, N, K), "Wu", di)
+        _run(di, name, _grouped_swiglu, xp, rows, wp, up, ctypes.byref(G), ga, K, N, op, _ws_arg(ws, di), ws.numel(),
+             sp)
+    return out
 
 
 def grouped_linear_bf16(x, W, offsets, perm=None, k: int = 1, gather=None, row_w=None, out=None, ws=None, stream=None):
@@ -652,49 +711,16 @@ def grouped_linear_bf16(x, W, offsets, perm=None, k: int = 1, gather=None, row_w
     [P, N].  With row_w (fp32, P values in pair order): fp32 [P, N], row q
     times row_w[perm[q]].  `out` may be given in either type; rows in no group
     are not written.  `ws`: a zeroed workspace kept by the caller."""
-    E, N, K = W.shape
-    gather = perm is not None if gather is None else bool(gather)
-    P = x.shape[0] if perm is None else perm.shape[0]
-    _need(x, torch.bfloat16, (x.shape[0], K), "x")
-    _need(W, torch.bfloat16, (E, N, K), "W")
-    G = _groups(offsets, perm, k, P, E)
-    if row_w is not None:
-        _need(row_w, torch.float32, row_w.shape, "row_w")
-        if row_w.numel() != P:
-            raise ValueError(f"row_w: {P} values expected, got {row_w.numel()}")
-    s, sp = _on(x, stream, W, offsets, perm, row_w, out, ws)
-    if out is None:
-        out = _result((P, N), torch.float32 if row_w is not None else torch.bfloat16, s, x.device)
-    fmt = _fmt(out, "out")
-    _need(out, out.dtype, (P, N), "out")
-    if ws is None:
-        ws = _scratch(256, s, x.device)
-    _call(x.device, "lmoe_grouped_linear_bf16", _grouped_linear, x.data_ptr(), x.shape[0], W.data_ptr(),
-          ctypes.byref(G), int(gather), None if row_w is None else row_w.data_ptr(), K, N, fmt, out.data_ptr(),
-          ws.data_ptr(), ws.numel(), sp)
-    return out
+    return _grouped_call("lmoe_grouped_linear_bf16", x, W, None, offsets, perm, k, gather, row_w, out,
+                         torch.bfloat16 if row_w is None else torch.float32, ws, stream)
 
 
 def grouped_swiglu_bf16(x, Wg, Wu, offsets, perm=None, k: int = 1, gather=None, out=None, ws=None, stream=None):
     """bf16 [P, I] rows silu(x Wg[e]^T) * (x Wu[e]^T), both products and the
     gating in one kernel (lmoe_grouped_swiglu_bf16); arguments as for
     grouped_linear_bf16."""
-    E, I, K = Wg.shape
-    gather = perm is not None if gather is None else bool(gather)
-    P = x.shape[0] if perm is None else perm.shape[0]
-    _need(x, torch.bfloat16, (x.shape[0], K), "x")
-    _need(Wg, torch.bfloat16, (E, I, K), "Wg")
-    _need(Wu, torch.bfloat16, (E, I, K), "Wu")
-    G = _groups(offsets, perm, k, P, E)
-    s, sp = _on(x, stream, Wg, Wu, offsets, perm, out, ws)
-    if out is None:
-        out = _result((P, I), torch.bfloat16, s, x.device)
-    _need(out, torch.bfloat16, (P, I), "out")
-    if ws is None:
-        ws = _scratch(256, s, x.device)
-    _call(x.device, "lmoe_grouped_swiglu_bf16", _grouped_swiglu, x.data_ptr(), x.shape[0], Wg.data_ptr(),
-          Wu.data_ptr(), ctypes.byref(G), int(gather), K, I, out.data_ptr(), ws.data_ptr(), ws.numel(), sp)
-    return out
+    return _grouped_call("lmoe_grouped_swiglu_bf16", x, Wg, Wu, offsets, perm, k, gather, None, out, torch.bfloat16,
+                         ws, stream)
 
 
 class Block:
