@@ -17,10 +17,11 @@
 // into per-expert tile counts in shared memory and finds its items by a warp
 // search.
 //
-// Persistent CTA, 256 threads: warp 0 streams A (TMA), warp 1 issues the MMAs,
-// warps 2-5 are the epilogue (TMEM lane quarter = warp % 4), warp 6 brings B:
-// boxes of 16 or 32 rows where a group's rows are consecutive, or gather4
-// copies of four rows each where they come through the permutation.
+// Persistent CTA: warp 0 streams A (TMA; gated: another warp the up rows), warp
+// 1 issues the MMAs, warps 2-5 are the epilogue (TMEM lane quarter = warp % 4),
+// warps 6.. bring B: boxes of 16 or 32 rows where a group's rows are
+// consecutive, or gather4 copies of four rows each where they come through the
+// permutation.
 // Where the host can tell that the items cannot fill the GPU, a cluster of KS
 // CTAs shares an item along K, and rank 0 adds the others' accumulators, which
 // they store into its shared memory, in rank order.
@@ -37,11 +38,19 @@ namespace {
 
 using namespace tc;
 
-constexpr int THREADS = 256;
 constexpr uint32_t A_TILE = 128 * 128;  // 128 rows x 64 bf16
 
-template <int NT, int KS>
+template <int NT, bool SWIGLU, bool GATHER, int KS>
 struct GCfg {
+    // Warps that bring B.  A warp issues an asynchronous copy only every 75
+    // cycles or so, however many lanes ask: eight warps for the 64 gather4
+    // copies of a 256-row chunk (a gate/up pass of 8192 tokens over 896
+    // experts took 3.78 ms with one, 2.12 ms with two).
+    static constexpr int BW = !GATHER ? 1 : NT <= 32 ? 1 : NT == 64 ? 4 : 8;
+    static constexpr int THREADS = BW > 1 ? 512 : 256;
+    static constexpr int A2 = 6 + BW;  // the second A warp (SWIGLU: the up rows)
+    static_assert(A2 < THREADS / 32, "warps");
+    static constexpr int LANE_COPIES = NT / 4 > 32 * BW ? 2 : 1;  // gather4 copies a lane issues a chunk, at most
     static constexpr uint32_t B_TILE = NT * 128;
     static constexpr uint32_t STAGE = A_TILE + B_TILE;
     static constexpr int BOX = NT < 32 ? 16 : 32;  // rows of a B box
@@ -50,7 +59,6 @@ struct GCfg {
     static constexpr int S = S_RAW > 10 ? 10 : S_RAW;
     static constexpr int ACC = 2;  // accumulators: an item's epilogue overlaps the next one's MMAs
     static constexpr uint32_t TMEM_COLS = ACC * NT < 32 ? 32 : ACC * NT;
-    static constexpr int LANE_ROWS = (NT + 31) / 32;  // gathered: rows a lane of warp 6 holds the ids of / 4
 };
 
 struct GArgs {
@@ -98,12 +106,12 @@ struct Walk {
 };
 
 template <int NT, bool SWIGLU, bool GATHER, int KS>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     k_grouped(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
               const __grid_constant__ CUtensorMap tmB, const GArgs p)
 {
-    using C = GCfg<NT, KS>;
-    constexpr int S = C::S;
+    using C = GCfg<NT, SWIGLU, GATHER, KS>;
+    constexpr int S = C::S, THREADS = C::THREADS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // KS > 1: [KS - 1][NT][128]
@@ -115,14 +123,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint64_t *red_full = drain + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(red_full + 1);
     int32_t *warp_tot = reinterpret_cast<int32_t *>(tmem_slot + 2);
-    int32_t *s_off = warp_tot + 8;
+    int32_t *s_off = warp_tot + 16;
     int32_t *s_tiles = s_off + p.E + 1;
     int32_t *s_cnt = s_tiles + p.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 2);  // the A and the B producer
+            mbar_init(&full[s], C::BW + (SWIGLU ? 2 : 1));  // one arrival of each producer warp
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < C::ACC; ++a) {
@@ -176,22 +184,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
     };
 
-    if (warp == 0 || warp == 6) {
-        // ---------------- producers: A (warp 0), B (warp 6) ----------------
+    if (warp == 0 || (warp >= 6 && warp < C::A2 + (SWIGLU ? 1 : 0))) {
+        // ---------------- producers: A (warp 0 and, gated, warp A2), B (warps 6 ..) ----------------
+        const bool isA = warp == 0 || warp == C::A2;
+        const int bw = warp - 6;  // B: this warp's copies are bw, bw + BW, ...
         int stage = 0, fills = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int it = first; it < total && ok; it += step) {
             const GItem w = walk.at(it);
-            [[maybe_unused]] int4 rows[C::LANE_ROWS > 1 ? 2 : 1];
-            const int nb = GATHER ? (w.nv + 3) / 4 : (w.nv + C::BOX - 1) / C::BOX;  // copies of B a chunk
-            if (GATHER && warp == 6) {
+            const int copies = GATHER ? (w.nv + 3) / 4 : (w.nv + C::BOX - 1) / C::BOX;  // of B a chunk, all warps
+            const int mine = copies > bw ? (copies - bw + C::BW - 1) / C::BW : 0;
+            [[maybe_unused]] int4 rows[C::LANE_COPIES];
+            if (GATHER && !isA) {
 #pragma unroll
-                for (int i = 0; i < (C::LANE_ROWS > 1 ? 2 : 1); ++i) {
+                for (int i = 0; i < C::LANE_COPIES; ++i) {
                     int r[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int l = 4 * (lane + 32 * i) + j;
+                        const int l = 4 * (bw + C::BW * (lane + 32 * i)) + j;
                         r[j] = 0;
                         if (l < w.nv) {
                             const int pr = __ldg(p.perm + w.row0 + l);
@@ -213,31 +224,36 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 }
                 uint8_t *sb = stages + stage * C::STAGE;
-                if (warp == 0) {
+                if (isA) {
                     if (lane == 0 && !(p.stall && it == first && kc == k0)) {
-                        mbar_arrive_expect_tx(&full[stage], A_TILE);
                         if (SWIGLU) {
+                            mbar_arrive_expect_tx(&full[stage], A_TILE / 2);
+                            const CUtensorMap *tm = warp == 0 ? &tmA : &tmA2;
+                            uint8_t *dst = sb + (warp == 0 ? 0 : 2048);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                tma_load_2d(sb + j * 4096, &tmA, kc * 64, w.e * p.N + w.m * 64 + 16 * j, &full[stage]);
-                                tma_load_2d(sb + j * 4096 + 2048, &tmA2, kc * 64, w.e * p.N + w.m * 64 + 16 * j,
-                                            &full[stage]);
-                            }
+                            for (int j = 0; j < 4; ++j)
+                                tma_load_2d(dst + j * 4096, tm, kc * 64, w.e * p.N + w.m * 64 + 16 * j, &full[stage]);
                         } else {
+                            mbar_arrive_expect_tx(&full[stage], A_TILE);
                             tma_load_2d(sb, &tmA, kc * 64, w.e * p.N + w.m * 128, &full[stage]);
                         }
                     }
                 } else {
-                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], uint32_t(nb) * (GATHER ? 512u : C::BOX * 128u));
+                    if (lane == 0) {
+                        if (mine > 0)
+                            mbar_arrive_expect_tx(&full[stage], uint32_t(mine) * (GATHER ? 512u : C::BOX * 128u));
+                        else
+                            mbar_arrive(&full[stage]);
+                    }
                     __syncwarp();
-                    if (GATHER) {
 #pragma unroll
-                        for (int i = 0; i < (C::LANE_ROWS > 1 ? 2 : 1); ++i)
-                            if (lane + 32 * i < nb)
-                                tma_gather4(sb + A_TILE + (lane + 32 * i) * 512, &tmB, kc * 64, rows[i], &full[stage]);
-                    } else if (lane < nb) {
-                        tma_load_2d(sb + A_TILE + lane * C::BOX * 128, &tmB, kc * 64, w.row0 + lane * C::BOX,
-                                    &full[stage]);
+                    for (int i = 0; i < C::LANE_COPIES; ++i) {
+                        const int c = bw + C::BW * (lane + 32 * i);
+                        if (lane + 32 * i >= mine) break;
+                        if (GATHER)
+                            tma_gather4(sb + A_TILE + c * 512, &tmB, kc * 64, rows[i], &full[stage]);
+                        else
+                            tma_load_2d(sb + A_TILE + c * C::BOX * 128, &tmB, kc * 64, w.row0 + c * C::BOX, &full[stage]);
                     }
                 }
                 ++fills;
@@ -428,14 +444,14 @@ int sm_count()
 template <int NT, bool SWIGLU, bool GATHER, int KS>
 cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms, cudaStream_t st)
 {
-    using C = GCfg<NT, KS>;
+    using C = GCfg<NT, SWIGLU, GATHER, KS>;
     CUtensorMap ma, ma2, mb;
     if (!bf16_map(&ma, a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
         !bf16_map(&ma2, SWIGLU ? a.W2 : a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
         !bf16_map(&mb, a.x, a.K, a.x_rows, GATHER ? 1 : C::BOX))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + size_t(C::S) * C::STAGE + size_t(KS - 1) * 128 * NT * 4 + (2 * C::S + 2 * C::ACC + 2) * 8 +
-                        16 + 32 + size_t(3 * a.E + 2) * 4;
+                        16 + 64 + size_t(3 * a.E + 2) * 4;
     auto *kern = k_grouped<NT, SWIGLU, GATHER, KS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
@@ -443,7 +459,7 @@ cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms,
     const unsigned grid = unsigned((items < slots ? items : slots) * KS);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
