@@ -18,12 +18,18 @@
 // Bounded by the weight stream (17/32 byte a weight) up to about a hundred
 // rows, then by the tensor cores at half their 8-bit rate (two parts).
 //
-// k_split_rows writes the two parts and their scale atoms; k_linear_mx is a
-// persistent kernel over items (weight tile of 128, row tile of NB), its warps:
-// 0 weight tiles and their scale atoms (TMA), 1 MMA issuer, 2-5 epilogue, 6
-// the rows' two parts, 7 their scale atoms.  With few items a cluster of KS
-// CTAs shares an item along K: ranks 1.. store their accumulators into rank
-// 0's shared memory, which adds them in rank order.
+// The two parts of a tile of NB rows are one operand of 2 NB rows, hi above lo,
+// with accumulator columns of their own that the epilogue adds: a chunk of 128
+// columns is four MMAs.
+//
+// k_linear_mx is a persistent kernel over items (weight tile of 128, row tile),
+// its warps: 0 weight tiles and their scale atoms (TMA), 1 MMA issuer, 2-5
+// epilogue, 6.. the rows.  Up to 32 rows, warps 6-9 split the rows themselves
+// as they go (each weight tile's CTAs repeat it, which costs less than a
+// kernel before this one); beyond, k_split_rows has written the parts and warp
+// 6 copies them.  With few items a cluster of KS CTAs shares an item along K:
+// ranks 1.. store their sums into rank 0's shared memory, which adds them in
+// rank order.
 // Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -69,6 +75,12 @@ __device__ __forceinline__ void split8(const uint32_t (&w)[4], int b, uint2 &hi,
     lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
 }
 
+// Byte of (row r, block b of the chunk) in the row operand's scale atoms, 128 rows an atom.
+__device__ __forceinline__ int sf_off(int r, int b)
+{
+    return (r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + b;
+}
+
 __device__ __forceinline__ uint32_t amax8(const uint32_t (&w)[4])
 {
     uint32_t m = 0;
@@ -80,8 +92,9 @@ __device__ __forceinline__ uint32_t amax8(const uint32_t (&w)[4])
     return m;
 }
 
-// x[rows][K] -> codes [2][rows][Kp] (hi, lo), scale atoms [2][tiles][KC][512];
-// eight columns a thread, four threads a block of 32.
+// x[rows][K] -> codes [tiles][2 NB][Kp] (hi rows, then lo rows, of a tile of NB
+// rows) and scale atoms [tiles][KC][2 NB / 128][512]; eight columns a thread,
+// four threads a block of 32.
 template <int NB>
 __global__ void __launch_bounds__(256) k_split_rows(const uint16_t *__restrict__ x, int64_t rows, int K, int KC,
                                                     uint8_t *__restrict__ codes, uint8_t *__restrict__ atoms)
@@ -89,7 +102,6 @@ __global__ void __launch_bounds__(256) k_split_rows(const uint16_t *__restrict__
     pdl_enter();
     const int per = KC * 16;  // threads a row
     const int64_t n = rows * per;
-    const int64_t atom_bytes = ceil_div(rows, NB) * KC * 512;
     // whole warps: four lanes share a block
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < round_up(n, 32); i += int64_t(gridDim.x) * 256) {
         const int64_t r = i / per;
@@ -104,54 +116,68 @@ __global__ void __launch_bounds__(256) k_split_rows(const uint16_t *__restrict__
         const int b = split_byte(m);
         uint2 hi, lo;
         split8(w, b, hi, lo);
-        uint8_t *row = codes + r * (KC * 128) + c;
+        const int64_t tile = r / NB;
+        const int rr = int(r - tile * NB);
+        uint8_t *row = codes + (tile * 2 * NB + rr) * (KC * 128) + c;
         *reinterpret_cast<uint2 *>(row) = hi;
-        *reinterpret_cast<uint2 *>(row + rows * (KC * 128)) = lo;
+        *reinterpret_cast<uint2 *>(row + int64_t(NB) * (KC * 128)) = lo;
         if ((c & 31) == 0) {
-            const int64_t o = tile_atom_off(r, c >> 5, KC, NB);
-            atoms[o] = uint8_t(b);
-            atoms[atom_bytes + o] = uint8_t(b - 5);
+            uint8_t *at = atoms + (tile * KC + (c >> 7)) * (2 * NB / 128 * 512);
+            at[sf_off(rr, (c >> 5) & 3)] = uint8_t(b);
+            at[sf_off(NB + rr, (c >> 5) & 3)] = uint8_t(b - 5);
         }
     }
 }
 
 // ---- the product ---------------------------------------------------------------------------
 
-constexpr int THREADS = 256;
 constexpr uint32_t A_TILE = 128 * 128;  // 128 weight rows x 128 columns, one byte each once expanded
+constexpr int MAX_KS = 8;
 
-template <int NB, int KS>
+// FUSED: the kernel splits the rows itself.
+template <int NB, bool FUSED>
 struct LCfg {
-    static constexpr uint32_t B_TILE = NB * 128;  // one part
-    static constexpr uint32_t SF_OFF = A_TILE + 2 * B_TILE;  // scale atoms: weights, hi, lo
-    static constexpr uint32_t STAGE = (SF_OFF + 3 * 512 + 1023) / 1024 * 1024;
-    static constexpr uint32_t RED = (KS - 1) * 128 * NB * 4;
-    static constexpr int S_RAW = int((210 * 1024 - RED) / STAGE);
-    static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
-    static constexpr int ACC = 2;
-    static constexpr int SF_COLS = 12;  // TMEM columns of a stage's scales
-    static constexpr int SF_BASE = ACC * NB;
-    static constexpr int COLS = SF_BASE + S * SF_COLS;
+    static constexpr int NC = 2 * NB;  // rows of the B operand, columns of an accumulator
+    static constexpr int NAT = (NC + 127) / 128;  // its scale atoms a chunk
+    static constexpr uint32_t B_TILE = NC * 128;
+    static constexpr uint32_t SF_OFF = A_TILE + B_TILE;  // scale atoms: weights, rows
+    static constexpr uint32_t STAGE = (SF_OFF + (1 + NAT) * 512 + 1023) / 1024 * 1024;
+    static constexpr int BW = FUSED ? 4 : 1;  // warps that bring B
+    static constexpr int THREADS = 32 * (6 + BW);
+    static constexpr int ACC = NC <= 128 ? 2 : 1;
+    static constexpr int SF_COLS = 4 + 4 * NAT;  // TMEM columns of a stage's scales
+    static constexpr int SF_BASE = ACC * NC;
+    static constexpr int MAX_S_RAW = (512 - SF_BASE) / SF_COLS;
+    static constexpr int MAX_S = MAX_S_RAW > 12 ? 12 : MAX_S_RAW;
+    static constexpr int COLS = SF_BASE + MAX_S * SF_COLS;
     static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static_assert(COLS <= 512 && S >= 2, "pipeline");
+    static constexpr uint32_t RED = 128 * NB * 4;  // one rank's sums
+    static constexpr uint32_t TAIL = (2 * MAX_S + 2 * ACC + 2) * 8 + 16;
+    static constexpr int UNITS = FUSED ? NB / 2 : 1;  // fused: 8-column pieces a lane splits a chunk
+    static int stages(int ks)
+    {
+        const int s = (212 * 1024 - (ks - 1) * int(RED)) / int(STAGE);
+        return s > MAX_S ? MAX_S : s;
+    }
 };
 
 struct LArgs {
-    const uint8_t *sfa, *sfb;  // weight scale atoms [MT][KC][512], row scale atoms [2][NT][KC][512]
-    int64_t sfb_lo;            // bytes from the hi atoms to the lo ones
-    int rows, N, MT, NTL, KC;
+    const uint16_t *x;         // fused: the rows
+    const uint8_t *sfa, *sfb;  // weight scale atoms [MT][KC][512], row scale atoms [NTL][KC][NAT][512]
+    int rows, K, N, MT, NTL, KC;
+    int KS, stages;
     uint16_t *out;
     int32_t *status;
     long long limit;
     int stall;
 };
 
-template <int NB, int KS>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int NB, bool FUSED>
+__global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
     k_linear_mx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LArgs p)
 {
-    using C = LCfg<NB, KS>;
-    constexpr int S = C::S;
+    using C = LCfg<NB, FUSED>;
+    const int S = p.stages, KS = p.KS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // [KS - 1][NB][128]
@@ -173,10 +199,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // the first weight tiles on their way to L2 while the previous kernel ends
         for (int kc = k0; kc < k1 && kc < k0 + S; ++kc) tma_prefetch_2d(&tmA, kc * 128, first % p.MT * 128);
     }
-    if (warp == 6 && lane == 0) prefetch_tensormap(&tmB);
+    if (!FUSED && warp == 6 && lane == 0) prefetch_tensormap(&tmB);
     if (threadIdx.x == 64) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 3);  // the three producer warps
+            mbar_init(&full[s], 2);  // the weights' producer and the rows'
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < C::ACC; ++a) {
@@ -195,8 +221,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_enter();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0 || warp >= 6) {
-        // ---------------- producers ----------------
+    if (warp == 0 || (!FUSED && warp == 6)) {
+        // ---------------- copies: the weights (warp 0), the split rows (warp 6) ----------------
         int stage = 0, fills = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -217,15 +243,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tma_load_2d(sb, &tmA, kc * 128, mt * 128, &full[stage]);
                             bulk_load(sb + C::SF_OFF, p.sfa + (int64_t(mt) * p.KC + kc) * 512, 512, &full[stage]);
                         }
-                    } else if (warp == 6) {
-                        mbar_arrive_expect_tx(&full[stage], 2 * C::B_TILE);
-                        tma_load_2d(sb + A_TILE, &tmB, kc * 128, nt * NB, &full[stage]);
-                        tma_load_2d(sb + A_TILE + C::B_TILE, &tmB, kc * 128, p.rows + nt * NB, &full[stage]);
                     } else {
-                        const uint8_t *src = p.sfb + (int64_t(nt) * p.KC + kc) * 512;
-                        mbar_arrive_expect_tx(&full[stage], 1024);
-                        bulk_load(sb + C::SF_OFF + 512, src, 512, &full[stage]);
-                        bulk_load(sb + C::SF_OFF + 1024, src + p.sfb_lo, 512, &full[stage]);
+                        mbar_arrive_expect_tx(&full[stage], C::B_TILE + C::NAT * 512);
+                        tma_load_2d(sb + A_TILE, &tmB, kc * 128, nt * C::NC, &full[stage]);
+                        bulk_load(sb + C::SF_OFF + 512, p.sfb + (int64_t(nt) * p.KC + kc) * (C::NAT * 512),
+                                  C::NAT * 512, &full[stage]);
                     }
                 }
                 __syncwarp();
@@ -238,16 +260,64 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!ok)  // copies still in flight land before the CTA ends (bounded)
             for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
+    } else if (FUSED && warp >= 6) {
+        // ---------------- the rows, split here: warp w takes chunks w, w + 4, .. ----------------
+        const int per = k1 - k0, mine = total > first ? (total - first + step - 1) / step : 0;
+        const int64_t fills = int64_t(per) * mine;
+        uint4 u[C::UNITS];
+        auto fetch = [&](int64_t f) {  // the chunk of fill f: 16 pieces of 8 columns a row
+            const int nt = (first + int(f / per) * step) / p.MT;
+            const int c = (k0 + int(f % per)) * 128 + (lane & 15) * 8;
+#pragma unroll
+            for (int i = 0; i < C::UNITS; ++i) {
+                const int r = nt * NB + 2 * i + (lane >> 4);
+                u[i] = r < p.rows && c < p.K ? *reinterpret_cast<const uint4 *>(p.x + int64_t(r) * p.K + c)
+                                             : make_uint4(0, 0, 0, 0);
+            }
+        };
+        int64_t f = warp - 6;
+        if (f < fills) fetch(f);
+        for (; f < fills; f += C::BW) {
+            const int stage = int(f % S);
+            const bool ok = mbar_wait(&empty[stage], uint32_t(f / S + 1) & 1, p.limit);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                break;
+            }
+            uint8_t *bt = stages + stage * C::STAGE + A_TILE, *sf = stages + stage * C::STAGE + C::SF_OFF + 512;
+#pragma unroll
+            for (int i = 0; i < C::UNITS; ++i) {
+                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                uint32_t m = amax8(w);
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                const int b = split_byte(m), r = 2 * i + (lane >> 4), c16 = (lane & 15) >> 1;
+                uint2 hi, lo;
+                split8(w, b, hi, lo);
+                // 128-byte rows, 16-byte units swizzled by the row
+                *reinterpret_cast<uint2 *>(bt + r * 128 + ((c16 ^ (r & 7)) << 4) + (lane & 1) * 8) = hi;
+                *reinterpret_cast<uint2 *>(bt + (NB + r) * 128 + ((c16 ^ ((NB + r) & 7)) << 4) + (lane & 1) * 8) = lo;
+                if ((lane & 3) == 0) {
+                    sf[sf_off(r, (lane & 15) >> 2)] = uint8_t(b);
+                    sf[sf_off(NB + r, (lane & 15) >> 2)] = uint8_t(b - 5);
+                }
+            }
+            fence_async_shared();  // the tensor core reads these stores
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[stage]);
+            if (f + C::BW < fills) fetch(f + C::BW);
+        }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
         for (int it = first; it < total && ok; it += step) {
-            const uint32_t N = uint32_t((min(NB, p.rows - it / p.MT * NB) + 15) & ~15);
+            const int nv = min(NB, p.rows - it / p.MT * NB);
+            const uint32_t N = uint32_t((NB + nv + 15) & ~15);  // hi rows, padding, lo rows
             ok = mbar_wait(&acc_empty[acc], acc_phase ^ 1, p.limit);
             tc_fence_after();
-            const uint32_t d = tmem + uint32_t(acc * NB);
+            const uint32_t d = tmem + uint32_t(acc * C::NC);
             for (int kc = k0; kc < k1 && ok; ++kc) {
                 ok = mbar_wait(&full[stage], phase, p.limit);
                 if (!ok) break;
@@ -256,16 +326,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint8_t *sb = stages + stage * C::STAGE;
                     const uint32_t sfa = tmem + uint32_t(C::SF_BASE + stage * C::SF_COLS);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) tc_cp_sf(sfa + 4 * i, sdesc_sf(smem_u32(sb + C::SF_OFF + 512 * i)));
-                    const uint64_t ad = sdesc_k128(smem_u32(sb));
+                    for (int i = 0; i < 1 + C::NAT; ++i)
+                        tc_cp_sf(sfa + 4 * i, sdesc_sf(smem_u32(sb + C::SF_OFF + 512 * i)));
+                    const uint64_t ad = sdesc_k128(smem_u32(sb)), bd = sdesc_k128(smem_u32(sb + A_TILE));
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        const uint64_t bd = sdesc_k128(smem_u32(sb + A_TILE + part * C::B_TILE));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_mxf8f6f4(d, ad + 2 * kk, bd + 2 * kk, idesc_mxf4_e4m3(N, uint32_t(kk)), sfa,
-                                         sfa + 4 + 4 * part, (kc > k0 || part > 0 || kk > 0) ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_mxf8f6f4(d, ad + 2 * kk, bd + 2 * kk, idesc_mxf4_e4m3(N, uint32_t(kk)), sfa, sfa + 4,
+                                     (kc > k0 || kk > 0) ? 1u : 0u);
                     tc_commit(&empty[stage]);
                 }
                 __syncwarp();
@@ -293,6 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         // ---------------- epilogue ----------------
+        constexpr int CW = NB < 16 ? NB : 16;  // rows of x a step
         const int q = warp & 3;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -305,15 +373,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NB);
-            if (KS > 1 && rank > 0) {
-                const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * 128 * NB + 32 * q + lane), 0);
-                for (int c0 = 0; c0 < nv; c0 += 16) {
+            const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * C::NC);
+            auto sums = [&](int c0, float (&y)[CW]) {  // hi part + lo part of rows c0 ..
+                if constexpr (NB == 8) {
                     uint32_t v[16];
-                    tmem_ld16(tb + c0, v);
+                    tmem_ld16(tb, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) cluster_store(dst + (c0 + j) * 512, __uint_as_float(v[j]));
+                    for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(v[j]) + __uint_as_float(v[8 + j]);
+                } else {
+                    uint32_t v[16], l[16];
+                    tmem_ld16(tb + c0, v);
+                    tmem_ld16(tb + NB + c0, l);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]) + __uint_as_float(l[j]);
+                }
+            };
+            if (KS > 1 && rank > 0) {
+                const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * 128 * NB + 32 * q + lane), 0);
+                for (int c0 = 0; c0 < nv; c0 += CW) {
+                    float y[CW];
+                    sums(c0, y);
+#pragma unroll
+                    for (int j = 0; j < CW; ++j)
+                        if (c0 + j < nv) cluster_store(dst + (c0 + j) * 512, y[j]);
                 }
                 cluster_arrive(cluster_map(smem_u32(red_full), 0));
             } else {
@@ -325,25 +409,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 const int n = mt * 128 + 32 * q + lane;
-                for (int c0 = 0; c0 < nv; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(tb + c0, v);
-                    tmem_ld_wait();
-                    float y[16];
+                for (int c0 = 0; c0 < nv; c0 += CW) {
+                    float y[CW];
+                    sums(c0, y);
+                    const float *part = red + c0 * 128 + 32 * q + lane;
+                    for (int r = 0; r < KS - 1; ++r, part += NB * 128)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]);
-                    if (KS > 1) {
-                        const float *part = red + c0 * 128 + 32 * q + lane;
-#pragma unroll
-                        for (int r = 0; r < KS - 1; ++r)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] += part[(r * NB + j) * 128];
-                    }
+                        for (int j = 0; j < CW; ++j)
+                            if (c0 + j < nv) y[j] += part[j * 128];
                     if (n < p.N) {
-                        __nv_bfloat16 *o =
-                            reinterpret_cast<__nv_bfloat16 *>(p.out) + int64_t(row0 + c0) * p.N + n;
+                        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + int64_t(row0 + c0) * p.N + n;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
+                        for (int j = 0; j < CW; ++j)
                             if (c0 + j < nv) o[int64_t(j) * p.N] = __float2bfloat16_rn(y[j]);
                     }
                 }
@@ -399,49 +476,45 @@ int sm_count()
     return n > 0 ? n : 148;
 }
 
-int row_tile(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Rows of a tile; up to 32 the kernel splits the rows itself.
+int row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
-template <int NB, int KS>
-cudaError_t launch(const LArgs &a, const uint8_t *q, const uint8_t *codes, int sms, cudaStream_t st)
+template <int NB, bool FUSED>
+cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t st)
 {
-    using C = LCfg<NB, KS>;
+    using C = LCfg<NB, FUSED>;
     CUtensorMap ma, mb;
-    if (!byte_map(&ma, q, true, int64_t(a.KC) * 128, a.N, 128) ||
-        !byte_map(&mb, codes, false, int64_t(a.KC) * 128, 2 * int64_t(a.rows), NB))
+    if (!byte_map(&ma, q, true, int64_t(a.KC) * 128, a.N, 128)) return cudaErrorInvalidValue;
+    if (FUSED)
+        mb = ma;  // not used
+    else if (!byte_map(&mb, codes, false, int64_t(a.KC) * 128, int64_t(a.NTL) * C::NC, C::NC))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::RED + (2 * C::S + 2 * C::ACC + 2) * 8 + 16;
-    auto *kern = k_linear_mx<NB, KS>;
+    const int sms = sm_count();
+    const int64_t items = int64_t(a.MT) * a.NTL;
+    // With few items, the most ranks (1, 2, 4 or 8) an item with which all run
+    // at once, two chunks a rank at least.
+    a.KS = 1;
+    while (a.KS < MAX_KS && items * a.KS * 2 <= sms && a.KC >= 4 * a.KS && C::stages(2 * a.KS) >= 4) a.KS *= 2;
+    a.stages = C::stages(a.KS);
+    const size_t smem = 1024 + size_t(a.stages) * C::STAGE + size_t(a.KS - 1) * C::RED + C::TAIL;
+    auto *kern = k_linear_mx<NB, FUSED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    const int64_t items = int64_t(a.MT) * a.NTL, slots = sms / KS;
+    const int64_t slots = sms / a.KS;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((items < slots ? items : slots) * KS));
-    cfg.blockDim = dim3(THREADS);
+    cfg.gridDim = dim3(unsigned((items < slots ? items : slots) * a.KS));
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = KS;
+    attr[1].val.clusterDim.x = unsigned(a.KS);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = KS > 1 ? 2 : 1;
+    cfg.numAttrs = a.KS > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
-}
-
-// The most ranks (1, 2, 4 or 8) with which every item still has a cluster of
-// its own and every rank at least four chunks.
-template <int NB>
-cudaError_t pick(const LArgs &a, const uint8_t *q, const uint8_t *codes, int sms, cudaStream_t st)
-{
-    const int64_t items = int64_t(a.MT) * a.NTL;
-    if constexpr (NB <= 32)
-        if (items * 8 <= sms && a.KC >= 32) return launch<NB, 8>(a, q, codes, sms, st);
-    if constexpr (NB <= 64)
-        if (items * 4 <= sms && a.KC >= 16) return launch<NB, 4>(a, q, codes, sms, st);
-    if (items * 2 <= sms && a.KC >= 8) return launch<NB, 2>(a, q, codes, sms, st);
-    return launch<NB, 1>(a, q, codes, sms, st);
 }
 
 }  // namespace
@@ -450,7 +523,8 @@ size_t linear_mxfp4_scratch_bytes(int64_t rows, int K, int N)
 {
     (void)N;
     const int64_t KC = ceil_div(K, 128), NB = row_tile(rows);
-    return size_t(round_up(2 * rows * KC * 128, 256) + 2 * ceil_div(rows, NB) * KC * 512);
+    if (NB <= 32) return 0;
+    return size_t(ceil_div(rows, NB) * KC * (2 * NB * 128 + 2 * NB / 128 * 512));
 }
 
 cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int K, int N,
@@ -458,33 +532,31 @@ cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8
 {
     const int NB = row_tile(rows);
     LArgs a{};
+    a.x = x;
     a.rows = int(rows);
+    a.K = K;
     a.N = N;
     a.MT = int(ceil_div(N, 128));
     a.NTL = int(ceil_div(rows, NB));
     a.KC = int(ceil_div(K, 128));
     if (int64_t(a.MT) * a.NTL > INT32_MAX) return cudaErrorInvalidValue;
-    uint8_t *codes = static_cast<uint8_t *>(scratch);
-    uint8_t *atoms = codes + round_up(2 * rows * a.KC * 128, 256);
     a.sfa = s;
-    a.sfb = atoms;
-    a.sfb_lo = int64_t(a.NTL) * a.KC * 512;
     a.out = out;
     a.status = status;
     a.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
     a.stall = wait.stall_first_fill;
-    const int sms = sm_count();
-    const int64_t blocks = ceil_div(rows * a.KC * 16, 256);
-    const dim3 grid(unsigned(blocks < int64_t(sms) * 8 ? blocks : int64_t(sms) * 8)), block(256);
-    auto *split = NB == 16 ? k_split_rows<16> : NB == 32 ? k_split_rows<32> : NB == 64 ? k_split_rows<64> : k_split_rows<128>;
-    const cudaError_t e = launch_pdl(split, grid, block, 0, st, x, rows, K, a.KC, codes, atoms);
+    if (NB == 8) return launch<8, true>(a, q, nullptr, st);
+    if (NB == 16) return launch<16, true>(a, q, nullptr, st);
+    if (NB == 32) return launch<32, true>(a, q, nullptr, st);
+    uint8_t *codes = static_cast<uint8_t *>(scratch);
+    uint8_t *atoms = codes + int64_t(a.NTL) * a.KC * (2 * NB * 128);
+    a.sfb = atoms;
+    const int64_t blocks = ceil_div(rows * a.KC * 16, 256), most = int64_t(sm_count()) * 8;
+    const cudaError_t e = launch_pdl(NB == 64 ? k_split_rows<64> : k_split_rows<128>,
+                                     dim3(unsigned(blocks < most ? blocks : most)), dim3(256), 0, st, x, rows, K, a.KC,
+                                     codes, atoms);
     if (e != cudaSuccess) return e;
-    switch (NB) {
-    case 16: return pick<16>(a, q, codes, sms, st);
-    case 32: return pick<32>(a, q, codes, sms, st);
-    case 64: return pick<64>(a, q, codes, sms, st);
-    default: return pick<128>(a, q, codes, sms, st);
-    }
+    return NB == 64 ? launch<64, false>(a, q, codes, st) : launch<128, false>(a, q, codes, st);
 }
 
 }  // namespace lmoe
