@@ -23,12 +23,12 @@
 // consecutive, or gather4 copies of four rows each where they come through the
 // permutation.
 // Where the host can tell that the items cannot fill the GPU, a cluster of KS
-// CTAs shares an item along K, and rank 0 adds the others' accumulators, which
-// they store into its shared memory, in rank order.
+// CTAs shares an item along K (cluster_sum.cuh).
 // Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "cluster_sum.cuh"
 #include "lmoe_internal.cuh"
 #include "schedule.cuh"
 #include "tc_ptx.cuh"
@@ -50,11 +50,11 @@ struct GCfg {
     static constexpr int THREADS = BW > 1 ? 512 : 256;
     static constexpr int A2 = 6 + BW;  // the second A warp (SWIGLU: the up rows)
     static_assert(A2 < THREADS / 32, "warps");
-    static constexpr int LANE_COPIES = NT / 4 > 32 * BW ? 2 : 1;  // gather4 copies a lane issues a chunk, at most
+    static constexpr int COPIES = (NT / 4 + BW - 1) / BW;  // gather4 copies a warp issues a chunk, at most
     static constexpr uint32_t B_TILE = NT * 128;
     static constexpr uint32_t STAGE = A_TILE + B_TILE;
     static constexpr int BOX = NT < 32 ? 16 : 32;  // rows of a B box
-    static constexpr uint32_t RED = (KS - 1) * 128 * NT * 4;  // the other ranks' accumulators
+    static constexpr uint32_t RED = KS > 1 ? ClusterSum::red_bytes(NT) : 0;
     static constexpr int S_RAW = int((200 * 1024 - RED) / STAGE);
     static constexpr int S = S_RAW > 10 ? 10 : S_RAW;
     static constexpr int ACC = 2;  // accumulators: an item's epilogue overlaps the next one's MMAs
@@ -114,8 +114,8 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     constexpr int S = C::S, THREADS = C::THREADS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // KS > 1: [KS - 1][NT][128]
-    uint64_t *full = reinterpret_cast<uint64_t *>(red + (KS - 1) * 128 * NT);
+    float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // KS > 1 only
+    uint64_t *full = reinterpret_cast<uint64_t *>(red + C::RED / 4);
     uint64_t *empty = full + S;
     uint64_t *acc_full = empty + S;
     uint64_t *acc_empty = acc_full + C::ACC;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             mbar_init(&acc_empty[a], 128);
         }
         mbar_init(drain, 1);
-        mbar_init(red_full, (KS - 1) * 128 > 0 ? (KS - 1) * 128 : 1);
+        mbar_init(red_full, 1);
         mbar_init_fence();
     }
     if (warp == 0 && lane == 0) {
@@ -186,8 +186,10 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
 
     if (warp == 0 || (warp >= 6 && warp < C::A2 + (SWIGLU ? 1 : 0))) {
         // ---------------- producers: A (warp 0 and, gated, warp A2), B (warps 6 ..) ----------------
+        __shared__ int4 s_ids[GATHER ? C::BW : 1][C::COPIES];  // the rows of the warps' gather4 copies
         const bool isA = warp == 0 || warp == C::A2;
         const int bw = warp - 6;  // B: this warp's copies are bw, bw + BW, ...
+        [[maybe_unused]] int4 *ids = s_ids[GATHER && !isA ? bw : 0];
         int stage = 0, fills = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -195,14 +197,13 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             const GItem w = walk.at(it);
             const int copies = GATHER ? (w.nv + 3) / 4 : (w.nv + C::BOX - 1) / C::BOX;  // of B a chunk, all warps
             const int mine = copies > bw ? (copies - bw + C::BW - 1) / C::BW : 0;
-            [[maybe_unused]] int4 rows[C::LANE_COPIES];
             if (GATHER && !isA) {
-#pragma unroll
-                for (int i = 0; i < C::LANE_COPIES; ++i) {
+                __syncwarp();
+                for (int i = lane; i < mine; i += 32) {
                     int r[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int l = 4 * (bw + C::BW * (lane + 32 * i)) + j;
+                        const int l = 4 * (bw + C::BW * i) + j;
                         r[j] = 0;
                         if (l < w.nv) {
                             const int pr = __ldg(p.perm + w.row0 + l);
@@ -213,8 +214,9 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                             }
                         }
                     }
-                    rows[i] = make_int4(r[0], r[1], r[2], r[3]);
+                    ids[i] = make_int4(r[0], r[1], r[2], r[3]);
                 }
+                __syncwarp();
             }
             for (int kc = k0; kc < k1; ++kc) {
                 ok = mbar_wait(&empty[stage], phase ^ 1, p.limit);
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 }
                 uint8_t *sb = stages + stage * C::STAGE;
                 if (isA) {
-                    if (lane == 0 && !(p.stall && it == first && kc == k0)) {
+                    if (elect_one() && !(p.stall && it == first && kc == k0)) {
                         if (SWIGLU) {
                             mbar_arrive_expect_tx(&full[stage], A_TILE / 2);
                             const CUtensorMap *tm = warp == 0 ? &tmA : &tmA2;
@@ -239,23 +241,22 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                         }
                     }
                 } else {
-                    if (lane == 0) {
+                    if (elect_one()) {
                         if (mine > 0)
                             mbar_arrive_expect_tx(&full[stage], uint32_t(mine) * (GATHER ? 512u : C::BOX * 128u));
                         else
                             mbar_arrive(&full[stage]);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < C::LANE_COPIES; ++i) {
-                        const int c = bw + C::BW * (lane + 32 * i);
-                        if (lane + 32 * i >= mine) break;
-                        if (GATHER)
-                            tma_gather4(sb + A_TILE + c * 512, &tmB, kc * 64, rows[i], &full[stage]);
-                        else
-                            tma_load_2d(sb + A_TILE + c * C::BOX * 128, &tmB, kc * 64, w.row0 + c * C::BOX, &full[stage]);
+                        for (int i = 0; i < mine; ++i) {
+                            const int c = bw + C::BW * i;
+                            if (GATHER)
+                                tma_gather4(sb + A_TILE + c * 512, &tmB, kc * 64, ids[i], &full[stage]);
+                            else
+                                tma_load_2d(sb + A_TILE + c * C::BOX * 128, &tmB, kc * 64, w.row0 + c * C::BOX,
+                                            &full[stage]);
+                        }
                     }
                 }
+                __syncwarp();
                 ++fills;
                 if (++stage == S) {
                     stage = 0;
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 ok = mbar_wait(&full[stage], phase, p.limit);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint8_t *sb = stages + stage * C::STAGE;
                     const uint64_t ad = sdesc_k128(smem_u32(sb)), bd = sdesc_k128(smem_u32(sb + A_TILE));
 #pragma unroll
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            if (lane == 0) tc_commit(&acc_full[acc]);
+            if (elect_one()) tc_commit(&acc_full[acc]);
             __syncwarp();
             if (++acc == C::ACC) {
                 acc = 0;
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
         }
         if (!ok) {
-            if (lane == 0) {
+            if (elect_one()) {
                 set_status(p.status, LMOE_ERR_TIMEOUT);
                 tc_commit(drain);  // this CTA's MMAs in flight end before the tensor memory is freed
                 mbar_wait(drain, 0, p.limit);
@@ -324,73 +325,70 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
             tc_fence_after();
             const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
-            if (KS > 1 && rank > 0) {
-                // this rank's sums into rank 0's shared memory, [NT][128]
-                const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * 128 * NT + 32 * q + lane), 0);
-                for (int c0 = 0; c0 < w.nv; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(tb + c0, v);
-                    tmem_ld_wait();
+            // plain: lane = output column; gated: lanes 0-15 gate, 16-31 up of 16 features
+            const int n = SWIGLU ? w.m * 64 + 16 * q + (lane & 15) : w.m * 128 + 32 * q + lane;
+            const bool mine = n < p.N && (!SWIGLU || lane < 16);
+            // 16 rows from c0 on (rows [c0, c1) of them wanted) of the tile: weight or gate, round, store
+            auto finish = [&](int c0, int c1, float (&y)[16]) {
+                if (SWIGLU) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) cluster_store(dst + (c0 + j) * 512, __uint_as_float(v[j]));
-                }
-                cluster_arrive(cluster_map(smem_u32(red_full), 0));
-            } else {
-                if (KS > 1) {
-                    const bool in = mbar_wait_cluster(red_full, 0, p.limit);
-                    if (!__all_sync(0xFFFFFFFFu, in)) {
-                        if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-                        break;
+                    for (int j = 0; j < 16; ++j) {
+                        const float u = __shfl_down_sync(0xFFFFFFFFu, y[j], 16);
+                        y[j] = __fdividef(y[j], 1.f + expf(-y[j])) * u;
                     }
-                }
-                // plain: lane = output column; gated: lanes 0-15 gate, 16-31 up of 16 features
-                const int n = SWIGLU ? w.m * 64 + 16 * q + (lane & 15) : w.m * 128 + 32 * q + lane;
-                const bool mine = n < p.N && (!SWIGLU || lane < 16);
-                for (int c0 = 0; c0 < w.nv; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(tb + c0, v);
+                } else if (p.row_w) {
                     float rw = 1.f;  // lane j: the weight of row c0 + j
-                    if (!SWIGLU && p.row_w && lane < 16 && c0 + lane < w.nv) {
+                    if (lane < 16 && c0 + lane < c1) {
                         const int64_t pr = p.perm ? __ldg(p.perm + w.row0 + c0 + lane) : w.row0 + c0 + lane;
                         if (pr >= 0 && pr < p.P)
                             rw = __ldg(p.row_w + pr);
                         else
                             set_status(p.status, LMOE_ERR_DEVICE_CHECK);
                     }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] *= __shfl_sync(0xFFFFFFFFu, rw, j);
+                }
+                if (!mine) return;
+                const int64_t o = int64_t(w.row0 + c0) * p.N + n;
+                if (!SWIGLU && p.out_f32) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + j < c1) static_cast<float *>(p.out)[o + int64_t(j) * p.N] = y[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + j < c1)
+                            static_cast<__nv_bfloat16 *>(p.out)[o + int64_t(j) * p.N] = __float2bfloat16_rn(y[j]);
+                }
+            };
+            if (KS > 1) {
+                static_assert(KS == 1 || NT == 16, "one chunk of columns");
+                const ClusterSum cs{KS, rank, w.nv, reinterpret_cast<float *>(stages), red, red_full};
+                uint32_t v[16];
+                tmem_ld16(tb, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < w.nv) cs.stage[j * 128 + 32 * q + lane] = __uint_as_float(v[j]);
+                const bool in = cs.exchange(p.limit);
+                if (!__all_sync(0xFFFFFFFFu, in)) {
+                    if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                    break;
+                }
+                const int c0 = cs.begin(rank), c1 = cs.begin(rank + 1);  // this rank's rows
+                float y[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = c0 + j < c1 ? cs.at(c0 + j, 32 * q + lane) : 0.f;
+                finish(c0, c1, y);
+            } else {
+                for (int c0 = 0; c0 < w.nv; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tb + c0, v);
                     tmem_ld_wait();
                     float y[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]);
-                    if (KS > 1) {
-                        const float *part = red + c0 * 128 + 32 * q + lane;
-#pragma unroll
-                        for (int r = 0; r < KS - 1; ++r)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) y[j] += part[(r * NT + j) * 128];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (SWIGLU) {
-                            const float u = __shfl_down_sync(0xFFFFFFFFu, y[j], 16);
-                            y[j] = __fdividef(y[j], 1.f + expf(-y[j])) * u;
-                        } else if (p.row_w) {
-                            y[j] *= __shfl_sync(0xFFFFFFFFu, rw, j);
-                        }
-                    }
-                    if (mine) {
-                        const int64_t o = int64_t(w.row0 + c0) * p.N + n;
-                        if (!SWIGLU && p.out_f32) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (c0 + j < w.nv) static_cast<float *>(p.out)[o + int64_t(j) * p.N] = y[j];
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (c0 + j < w.nv)
-                                    static_cast<__nv_bfloat16 *>(p.out)[o + int64_t(j) * p.N] =
-                                        __float2bfloat16_rn(y[j]);
-                        }
-                    }
+                    finish(c0, w.nv, y);
                 }
             }
             tc_fence_before();
@@ -450,7 +448,7 @@ cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms,
         !bf16_map(&ma2, SWIGLU ? a.W2 : a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
         !bf16_map(&mb, a.x, a.K, a.x_rows, GATHER ? 1 : C::BOX))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + size_t(C::S) * C::STAGE + size_t(KS - 1) * 128 * NT * 4 + (2 * C::S + 2 * C::ACC + 2) * 8 +
+    const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::RED + (2 * C::S + 2 * C::ACC + 2) * 8 +
                         16 + 64 + size_t(3 * a.E + 2) * 4;
     auto *kern = k_grouped<NT, SWIGLU, GATHER, KS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));

@@ -27,13 +27,13 @@
 // epilogue, 6.. the rows.  Up to 32 rows, warps 6-9 split the rows themselves
 // as they go (each weight tile's CTAs repeat it, which costs less than a
 // kernel before this one); beyond, k_split_rows has written the parts and warp
-// 6 copies them.  With few items a cluster of KS CTAs shares an item along K:
-// ranks 1.. store their sums into rank 0's shared memory, which adds them in
-// rank order.
+// 6 copies them.  With few items a cluster of KS CTAs shares an item along K
+// (cluster_sum.cuh).
 // Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "cluster_sum.cuh"
 #include "lmoe_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -142,30 +142,34 @@ struct LCfg {
     static constexpr uint32_t B_TILE = NC * 128;
     static constexpr uint32_t SF_OFF = A_TILE + B_TILE;  // scale atoms: weights, rows
     static constexpr uint32_t STAGE = (SF_OFF + (1 + NAT) * 512 + 1023) / 1024 * 1024;
-    static constexpr int BW = FUSED ? 4 : 1;  // warps that bring B
+    // Fused: teams of TW warps take the chunks in turn, a warp 8 rows of one
+    // (four 8-column pieces a lane).
+    static constexpr int TW = FUSED ? NB / 8 : 1;
+    static constexpr int TEAMS = FUSED ? (NB <= 16 ? 4 : 2) : 1;
+    static constexpr int BW = TW * TEAMS;  // warps that bring B
     static constexpr int THREADS = 32 * (6 + BW);
+    static constexpr int UNITS = 4;
+    // Small row tiles leave room for two CTAs an SM: the next call's start up
+    // beside the last ones of this call, and the items spread more evenly.
+    static constexpr int CTAS = NB <= 32 ? 2 : 1;
     static constexpr int ACC = NC <= 128 ? 2 : 1;
     static constexpr int SF_COLS = 4 + 4 * NAT;  // TMEM columns of a stage's scales
     static constexpr int SF_BASE = ACC * NC;
-    static constexpr int MAX_S_RAW = (512 - SF_BASE) / SF_COLS;
-    static constexpr int MAX_S = MAX_S_RAW > 12 ? 12 : MAX_S_RAW;
-    static constexpr int COLS = SF_BASE + MAX_S * SF_COLS;
+    static constexpr uint32_t TAIL = 1024 + (2 * 12 + 2 * ACC + 2) * 8 + 16;
+    static constexpr uint32_t RED = ClusterSum::red_bytes(NB);
+    static constexpr int S_RAW = int(((227 * 1024) / CTAS - 1024 - TAIL - RED) / STAGE);
+    static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
+    static constexpr int COLS = SF_BASE + S * SF_COLS;
     static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static constexpr uint32_t RED = 128 * NB * 4;  // one rank's sums
-    static constexpr uint32_t TAIL = (2 * MAX_S + 2 * ACC + 2) * 8 + 16;
-    static constexpr int UNITS = FUSED ? NB / 2 : 1;  // fused: 8-column pieces a lane splits a chunk
-    static int stages(int ks)
-    {
-        const int s = (212 * 1024 - (ks - 1) * int(RED)) / int(STAGE);
-        return s > MAX_S ? MAX_S : s;
-    }
+    static_assert(COLS <= 512 && int(TMEM_COLS) * CTAS <= 512 && S >= 3, "pipeline");
+    static constexpr size_t SMEM = size_t(S) * STAGE + RED + TAIL;
 };
 
 struct LArgs {
     const uint16_t *x;         // fused: the rows
     const uint8_t *sfa, *sfb;  // weight scale atoms [MT][KC][512], row scale atoms [NTL][KC][NAT][512]
     int rows, K, N, MT, NTL, KC;
-    int KS, stages;
+    int KS;
     uint16_t *out;
     int32_t *status;
     long long limit;
@@ -173,15 +177,16 @@ struct LArgs {
 };
 
 template <int NB, bool FUSED>
-__global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
+__global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::CTAS))
     k_linear_mx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LArgs p)
 {
     using C = LCfg<NB, FUSED>;
-    const int S = p.stages, KS = p.KS;
+    constexpr int S = C::S;
+    const int KS = p.KS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // [KS - 1][NB][128]
-    uint64_t *full = reinterpret_cast<uint64_t *>(red + (KS - 1) * 128 * NB);
+    float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // [KS - 1][columns of this rank][128]
+    uint64_t *full = reinterpret_cast<uint64_t *>(red + C::RED / 4);
     uint64_t *empty = full + S;
     uint64_t *acc_full = empty + S;
     uint64_t *acc_empty = acc_full + C::ACC;
@@ -194,15 +199,11 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
     const int first = int(blockIdx.x) / KS, step = int(gridDim.x) / KS;
     const int total = p.MT * p.NTL;
     const int k0 = rank * p.KC / KS, k1 = (rank + 1) * p.KC / KS;  // this rank's chunks of 128 columns
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmA);
-        // the first weight tiles on their way to L2 while the previous kernel ends
-        for (int kc = k0; kc < k1 && kc < k0 + S; ++kc) tma_prefetch_2d(&tmA, kc * 128, first % p.MT * 128);
-    }
+    if (warp == 0 && lane == 0) prefetch_tensormap(&tmA);
     if (!FUSED && warp == 6 && lane == 0) prefetch_tensormap(&tmB);
     if (threadIdx.x == 64) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 2);  // the weights' producer and the rows'
+            mbar_init(&full[s], 1 + C::TW);  // the weights' producer and the rows'
             mbar_init(&empty[s], 1);
         }
         for (int a = 0; a < C::ACC; ++a) {
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
             mbar_init(&acc_empty[a], 128);
         }
         mbar_init(drain, 1);
-        mbar_init(red_full, KS > 1 ? (KS - 1) * 128 : 1);
+        mbar_init(red_full, 1);
         mbar_init_fence();
     }
     if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
                     break;
                 }
                 uint8_t *sb = stages + stage * C::STAGE;
-                if (lane == 0) {
+                if (elect_one()) {
                     if (warp == 0) {
                         if (!(p.stall && it == first && kc == k0)) {
                             mbar_arrive_expect_tx(&full[stage], 128 * 64 + 512);  // packed FP4: 64 bytes a row
@@ -261,42 +262,41 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
         if (!ok)  // copies still in flight land before the CTA ends (bounded)
             for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
     } else if (FUSED && warp >= 6) {
-        // ---------------- the rows, split here: warp w takes chunks w, w + 4, .. ----------------
+        // ---------------- the rows, split here: team t takes chunks t, t + TEAMS, .. ----------------
         const int per = k1 - k0, mine = total > first ? (total - first + step - 1) / step : 0;
-        const int64_t fills = int64_t(per) * mine;
-        uint4 u[C::UNITS];
-        auto fetch = [&](int64_t f) {  // the chunk of fill f: 16 pieces of 8 columns a row
-            const int nt = (first + int(f / per) * step) / p.MT;
-            const int c = (k0 + int(f % per)) * 128 + (lane & 15) * 8;
+        const int fills = per * mine, r0 = (warp - 6) % C::TW * 8, c16 = (lane & 15) >> 1;
+        // the pieces of the chunk of fill f: lanes 0-15 one row, lanes 16-31 the next
+        auto fetch = [&](int f, uint4 (&u)[C::UNITS]) {
+            const int i = f / per, nt = (first + i * step) / p.MT;
+            const int c = (k0 + f - i * per) * 128 + (lane & 15) * 8;
 #pragma unroll
-            for (int i = 0; i < C::UNITS; ++i) {
-                const int r = nt * NB + 2 * i + (lane >> 4);
-                u[i] = r < p.rows && c < p.K ? *reinterpret_cast<const uint4 *>(p.x + int64_t(r) * p.K + c)
-                                             : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < C::UNITS; ++j) {
+                const int r = nt * NB + r0 + 2 * j + (lane >> 4);
+                u[j] = f < fills && r < p.rows && c < p.K ? *reinterpret_cast<const uint4 *>(p.x + int64_t(r) * p.K + c)
+                                                          : make_uint4(0, 0, 0, 0);
             }
         };
-        int64_t f = warp - 6;
-        if (f < fills) fetch(f);
-        for (; f < fills; f += C::BW) {
-            const int stage = int(f % S);
+        auto split = [&](int f, const uint4 (&u)[C::UNITS]) -> bool {
+            const int stage = f % S;
             const bool ok = mbar_wait(&empty[stage], uint32_t(f / S + 1) & 1, p.limit);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-                break;
+                return false;
             }
             uint8_t *bt = stages + stage * C::STAGE + A_TILE, *sf = stages + stage * C::STAGE + C::SF_OFF + 512;
 #pragma unroll
-            for (int i = 0; i < C::UNITS; ++i) {
-                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            for (int j = 0; j < C::UNITS; ++j) {
+                const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
                 uint32_t m = amax8(w);
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                const int b = split_byte(m), r = 2 * i + (lane >> 4), c16 = (lane & 15) >> 1;
+                const int b = split_byte(m), r = r0 + 2 * j + (lane >> 4);
                 uint2 hi, lo;
                 split8(w, b, hi, lo);
                 // 128-byte rows, 16-byte units swizzled by the row
-                *reinterpret_cast<uint2 *>(bt + r * 128 + ((c16 ^ (r & 7)) << 4) + (lane & 1) * 8) = hi;
-                *reinterpret_cast<uint2 *>(bt + (NB + r) * 128 + ((c16 ^ ((NB + r) & 7)) << 4) + (lane & 1) * 8) = lo;
+                const int at = r * 128 + ((c16 ^ (r & 7)) << 4) + (lane & 1) * 8;
+                *reinterpret_cast<uint2 *>(bt + at) = hi;
+                *reinterpret_cast<uint2 *>(bt + NB * 128 + at) = lo;  // NB % 8 == 0: the same swizzle
                 if ((lane & 3) == 0) {
                     sf[sf_off(r, (lane & 15) >> 2)] = uint8_t(b);
                     sf[sf_off(NB + r, (lane & 15) >> 2)] = uint8_t(b - 5);
@@ -305,7 +305,18 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
             fence_async_shared();  // the tensor core reads these stores
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[stage]);
-            if (f + C::BW < fills) fetch(f + C::BW);
+            return true;
+        };
+        // two chunks ahead, so that a chunk's load latency passes under the work on two others
+        uint4 u0[C::UNITS], u1[C::UNITS];
+        int f = (warp - 6) / C::TW;
+        fetch(f, u0);
+        fetch(f + C::TEAMS, u1);
+        for (; f < fills; f += 2 * C::TEAMS) {
+            if (!split(f, u0)) break;
+            fetch(f + 2 * C::TEAMS, u0);
+            if (f + C::TEAMS >= fills || !split(f + C::TEAMS, u1)) break;
+            fetch(f + 3 * C::TEAMS, u1);
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer ----------------
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
                 ok = mbar_wait(&full[stage], phase, p.limit);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint8_t *sb = stages + stage * C::STAGE;
                     const uint32_t sfa = tmem + uint32_t(C::SF_BASE + stage * C::SF_COLS);
 #pragma unroll
@@ -343,7 +354,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            if (lane == 0) tc_commit(&acc_full[acc]);
+            if (elect_one()) tc_commit(&acc_full[acc]);
             __syncwarp();
             if (++acc == C::ACC) {
                 acc = 0;
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
             }
         }
         if (!ok) {
-            if (lane == 0) {
+            if (elect_one()) {
                 set_status(p.status, LMOE_ERR_TIMEOUT);
                 tc_commit(drain);  // MMAs in flight end before the tensor memory is freed
                 mbar_wait(drain, 0, p.limit);
@@ -390,39 +401,33 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), 1)
                     for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]) + __uint_as_float(l[j]);
                 }
             };
-            if (KS > 1 && rank > 0) {
-                const uint32_t dst = cluster_map(smem_u32(red + (rank - 1) * 128 * NB + 32 * q + lane), 0);
+            const int n = mt * 128 + 32 * q + lane;
+            __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + int64_t(row0) * p.N + n;
+            if (KS > 1) {
+                const ClusterSum cs{KS, rank, nv, reinterpret_cast<float *>(stages), red, red_full};
                 for (int c0 = 0; c0 < nv; c0 += CW) {
                     float y[CW];
                     sums(c0, y);
 #pragma unroll
                     for (int j = 0; j < CW; ++j)
-                        if (c0 + j < nv) cluster_store(dst + (c0 + j) * 512, y[j]);
+                        if (c0 + j < nv) cs.stage[(c0 + j) * 128 + 32 * q + lane] = y[j];
                 }
-                cluster_arrive(cluster_map(smem_u32(red_full), 0));
+                const bool in = cs.exchange(p.limit);
+                if (!__all_sync(0xFFFFFFFFu, in)) {
+                    if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                    break;
+                }
+                if (n < p.N)
+                    for (int c = cs.begin(rank); c < cs.begin(rank + 1); ++c)
+                        o[int64_t(c) * p.N] = __float2bfloat16_rn(cs.at(c, 32 * q + lane));
             } else {
-                if (KS > 1) {
-                    const bool in = mbar_wait_cluster(red_full, 0, p.limit);
-                    if (!__all_sync(0xFFFFFFFFu, in)) {
-                        if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-                        break;
-                    }
-                }
-                const int n = mt * 128 + 32 * q + lane;
                 for (int c0 = 0; c0 < nv; c0 += CW) {
                     float y[CW];
                     sums(c0, y);
-                    const float *part = red + c0 * 128 + 32 * q + lane;
-                    for (int r = 0; r < KS - 1; ++r, part += NB * 128)
+                    if (n < p.N)
 #pragma unroll
                         for (int j = 0; j < CW; ++j)
-                            if (c0 + j < nv) y[j] += part[j * 128];
-                    if (n < p.N) {
-                        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + int64_t(row0 + c0) * p.N + n;
-#pragma unroll
-                        for (int j = 0; j < CW; ++j)
-                            if (c0 + j < nv) o[int64_t(j) * p.N] = __float2bfloat16_rn(y[j]);
-                    }
+                            if (c0 + j < nv) o[int64_t(c0 + j) * p.N] = __float2bfloat16_rn(y[j]);
                 }
             }
             tc_fence_before();
@@ -491,16 +496,20 @@ cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t
         return cudaErrorInvalidValue;
     const int sms = sm_count();
     const int64_t items = int64_t(a.MT) * a.NTL;
-    // With few items, the most ranks (1, 2, 4 or 8) an item with which all run
-    // at once, two chunks a rank at least.
+    // With items for fewer CTAs than run at once, as many ranks an item as
+    // make the longest SM's share of the chunks shortest (fewest ranks among
+    // equals).
     a.KS = 1;
-    while (a.KS < MAX_KS && items * a.KS * 2 <= sms && a.KC >= 4 * a.KS && C::stages(2 * a.KS) >= 4) a.KS *= 2;
-    a.stages = C::stages(a.KS);
-    const size_t smem = 1024 + size_t(a.stages) * C::STAGE + size_t(a.KS - 1) * C::RED + C::TAIL;
+    int64_t best = items <= int64_t(sms) * C::CTAS ? ceil_div(items, sms) * a.KC : 0;
+    for (int ks = 2; ks <= MAX_KS && items * ks <= int64_t(sms) * C::CTAS && ks * 2 <= a.KC; ++ks) {
+        const int64_t cost = ceil_div(items * ks, sms) * ceil_div(a.KC, ks);
+        if (cost < best) best = cost, a.KS = ks;
+    }
+    const size_t smem = C::SMEM;
     auto *kern = k_linear_mx<NB, FUSED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    const int64_t slots = sms / a.KS;
+    const int64_t slots = int64_t(sms) * C::CTAS / a.KS;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((items < slots ? items : slots) * a.KS));
     cfg.blockDim = dim3(C::THREADS);
