@@ -50,8 +50,12 @@ struct GCfg {
     static constexpr int THREADS = BW > 1 ? 512 : 256;
     static constexpr int A2 = 6 + BW;  // the second A warp (SWIGLU: the up rows)
     static_assert(A2 < THREADS / 32, "warps");
-    static constexpr int COPIES = (NT / 4 + BW - 1) / BW;  // gather4 copies a warp issues a chunk, at most
-    static constexpr uint32_t B_TILE = NT * 128;
+    // The largest row tile is shared by a pair of CTAs (cta_group::2): 256
+    // weight rows, each CTA bringing 128 of them and half of B.
+    static constexpr bool PAIR = NT == 256;
+    static constexpr int CL = PAIR ? 2 : KS;  // CTAs of a cluster
+    static constexpr uint32_t B_TILE = (PAIR ? NT / 2 : NT) * 128;
+    static constexpr int COPIES = (int(B_TILE) / 512 + BW - 1) / BW;  // gather4 copies a warp issues a chunk, at most
     static constexpr uint32_t STAGE = A_TILE + B_TILE;
     static constexpr int BOX = NT < 32 ? 16 : 32;  // rows of a B box
     static constexpr uint32_t RED = KS > 1 ? ClusterSum::red_bytes(NT) : 0;
@@ -112,6 +116,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
 {
     using C = GCfg<NT, SWIGLU, GATHER, KS>;
     constexpr int S = C::S, THREADS = C::THREADS;
+    constexpr bool PAIR = C::PAIR;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *red = reinterpret_cast<float *>(stages + S * C::STAGE);  // KS > 1 only
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         }
         for (int a = 0; a < C::ACC; ++a) {
             mbar_init(&acc_full[a], 1);
-            mbar_init(&acc_empty[a], 128);
+            mbar_init(&acc_empty[a], PAIR ? 256 : 128);
         }
         mbar_init(drain, 1);
         mbar_init(red_full, 1);
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         if (SWIGLU) prefetch_tensormap(&tmA2);
     }
     if (warp == 6 && lane == 0) prefetch_tensormap(&tmB);
-    if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+    if (warp == 1) PAIR ? tmem_alloc_pair(tmem_slot, C::TMEM_COLS) : tmem_alloc(tmem_slot, C::TMEM_COLS);
     pdl_enter();
     // row tiles per expert, scanned; a group that breaks 0 <= o0 <= o1 <= P is empty and reported
     bool bad = false;
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     bad = __syncthreads_or(bad);
     tc_fence_after();
     block_scan<THREADS>(s_cnt, p.E, s_tiles, warp_tot);
-    if (KS > 1) cluster_sync();  // the cluster's barriers are initialised
+    if (C::CL > 1) cluster_sync();  // the cluster's barriers are initialised
     const uint32_t tmem = *tmem_slot;
     // Around a bad group others may overlap, so that there are more tiles than
     // any valid groups have: no more than those are worked off, and none where
@@ -173,14 +178,16 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         const int64_t most = int64_t(p.E) * ceil_div(p.P, NT) * p.MT;
         total = most > INT32_MAX ? 0 : min(total, p.max_items);
     }
-    const int rank = KS > 1 ? int(cluster_rank()) : 0;
-    const int first = int(blockIdx.x) / KS, step = int(gridDim.x) / KS;
+    const int rank = C::CL > 1 ? int(cluster_rank()) : 0;
+    const int first = int(blockIdx.x) / C::CL, step = int(gridDim.x) / C::CL;
     // this rank's K chunks
     const int k0 = KS > 1 ? rank * p.KC / KS : 0, k1 = KS > 1 ? (rank + 1) * p.KC / KS : p.KC;
     Walk<NT> walk{s_tiles, s_off, p.E, p.MT};
 
     // Copies still in flight after a timeout land before the CTA ends (bounded).
+    // (A pair's copies all count in on the leader's barriers.)
     auto settle = [&](int fills) {
+        if (PAIR && rank > 0) return;
         for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
     };
 
@@ -195,8 +202,19 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         bool ok = true;
         for (int it = first; it < total && ok; it += step) {
             const GItem w = walk.at(it);
-            const int copies = GATHER ? (w.nv + 3) / 4 : (w.nv + C::BOX - 1) / C::BOX;  // of B a chunk, all warps
+            // this CTA's rows of the tile: all, or a pair's half of them (rounded to whole MMA columns)
+            const int half = PAIR ? (w.nv + 31) / 32 * 16 : 0;
+            const int b0 = PAIR ? rank * half : 0, bn = PAIR ? max(0, min(half, w.nv - b0)) : w.nv;
+            const int copies = GATHER ? (bn + 3) / 4 : (bn + C::BOX - 1) / C::BOX;  // of B a chunk, all warps
+            const int mtile = PAIR ? 2 * w.m + rank : w.m;  // this CTA's 128 weight rows
             const int mine = copies > bw ? (copies - bw + C::BW - 1) / C::BW : 0;
+            // bytes this warp's barrier arrival announces: a pair's leader those of both CTAs (an
+            // arrival from the other CTA, with the release it needs, would take over 1000 cycles a stage)
+            const int peer_n = PAIR ? max(0, w.nv - half) : 0;
+            const int peer = GATHER ? (peer_n + 3) / 4 : (peer_n + C::BOX - 1) / C::BOX;
+            const uint32_t announce =
+                isA ? (SWIGLU ? A_TILE / 2 : A_TILE) * (PAIR ? 2 : 1)
+                    : uint32_t(mine + (peer > bw ? (peer - bw + C::BW - 1) / C::BW : 0)) * (GATHER ? 512u : C::BOX * 128u);
             if (GATHER && !isA) {
                 __syncwarp();
                 for (int i = lane; i < mine; i += 32) {
@@ -205,8 +223,8 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     for (int j = 0; j < 4; ++j) {
                         const int l = 4 * (bw + C::BW * i) + j;
                         r[j] = 0;
-                        if (l < w.nv) {
-                            const int pr = __ldg(p.perm + w.row0 + l);
+                        if (l < bn) {
+                            const int pr = __ldg(p.perm + w.row0 + b0 + l);
                             r[j] = pr / p.k;
                             if (pr < 0 || r[j] >= p.x_rows) {
                                 set_status(p.status, LMOE_ERR_DEVICE_CHECK);
@@ -226,33 +244,38 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     break;
                 }
                 uint8_t *sb = stages + stage * C::STAGE;
+                // the barrier of this stage: a pair's is the leader's
+                const uint32_t bar = PAIR ? cluster_map(smem_u32(&full[stage]), 0) : 0;
+                auto expect = [&] {
+                    if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], announce);
+                };
+                auto load = [&](void *dst, const CUtensorMap *tm, int y) {
+                    PAIR ? tma_load_2d_pair(dst, tm, kc * 64, y, bar) : tma_load_2d(dst, tm, kc * 64, y, &full[stage]);
+                };
                 if (isA) {
                     if (elect_one() && !(p.stall && it == first && kc == k0)) {
                         if (SWIGLU) {
-                            mbar_arrive_expect_tx(&full[stage], A_TILE / 2);
+                            expect();
                             const CUtensorMap *tm = warp == 0 ? &tmA : &tmA2;
                             uint8_t *dst = sb + (warp == 0 ? 0 : 2048);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                tma_load_2d(dst + j * 4096, tm, kc * 64, w.e * p.N + w.m * 64 + 16 * j, &full[stage]);
+                            for (int j = 0; j < 4; ++j) load(dst + j * 4096, tm, w.e * p.N + mtile * 64 + 16 * j);
                         } else {
-                            mbar_arrive_expect_tx(&full[stage], A_TILE);
-                            tma_load_2d(sb, &tmA, kc * 64, w.e * p.N + w.m * 128, &full[stage]);
+                            expect();
+                            load(sb, &tmA, w.e * p.N + mtile * 128);
                         }
                     }
                 } else {
                     if (elect_one()) {
-                        if (mine > 0)
-                            mbar_arrive_expect_tx(&full[stage], uint32_t(mine) * (GATHER ? 512u : C::BOX * 128u));
-                        else
-                            mbar_arrive(&full[stage]);
+                        expect();
                         for (int i = 0; i < mine; ++i) {
                             const int c = bw + C::BW * i;
-                            if (GATHER)
-                                tma_gather4(sb + A_TILE + c * 512, &tmB, kc * 64, ids[i], &full[stage]);
+                            if (!GATHER)
+                                load(sb + A_TILE + c * C::BOX * 128, &tmB, w.row0 + b0 + c * C::BOX);
+                            else if (PAIR)
+                                tma_gather4_pair(sb + A_TILE + c * 512, &tmB, kc * 64, ids[i], bar);
                             else
-                                tma_load_2d(sb + A_TILE + c * C::BOX * 128, &tmB, kc * 64, w.row0 + c * C::BOX,
-                                            &full[stage]);
+                                tma_gather4(sb + A_TILE + c * 512, &tmB, kc * 64, ids[i], &full[stage]);
                         }
                     }
                 }
@@ -265,14 +288,15 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
         }
         if (!ok) settle(fills);
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
+    } else if (warp == 1 && (!PAIR || rank == 0)) {
+        // ---------------- MMA issuer (a pair's: the leader's) ----------------
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
         for (int it = first; it < total && ok; it += step) {
             const GItem w = walk.at(it);
-            const uint32_t id = idesc_bf16(uint32_t((w.nv + 15) & ~15));
+            const uint32_t id =
+                PAIR ? idesc_bf16_pair(uint32_t((w.nv + 31) & ~31)) : idesc_bf16(uint32_t((w.nv + 15) & ~15));
             ok = mbar_wait(&acc_empty[acc], acc_phase ^ 1, p.limit);
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * NT);
@@ -285,8 +309,11 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     const uint64_t ad = sdesc_k128(smem_u32(sb)), bd = sdesc_k128(smem_u32(sb + A_TILE));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)  // 4 x K = 16 per 128-byte row
-                        mma_bf16(d, ad + 2 * kk, bd + 2 * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
-                    tc_commit(&empty[stage]);
+                        if (PAIR)
+                            mma_bf16_pair(d, ad + 2 * kk, bd + 2 * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
+                        else
+                            mma_bf16(d, ad + 2 * kk, bd + 2 * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
+                    PAIR ? tc_commit_pair(&empty[stage]) : tc_commit(&empty[stage]);
                 }
                 __syncwarp();
                 if (++stage == S) {
@@ -296,7 +323,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            if (elect_one()) tc_commit(&acc_full[acc]);
+            if (elect_one()) PAIR ? tc_commit_pair(&acc_full[acc]) : tc_commit(&acc_full[acc]);
             __syncwarp();
             if (++acc == C::ACC) {
                 acc = 0;
@@ -306,7 +333,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         if (!ok) {
             if (elect_one()) {
                 set_status(p.status, LMOE_ERR_TIMEOUT);
-                tc_commit(drain);  // this CTA's MMAs in flight end before the tensor memory is freed
+                PAIR ? tc_commit_pair(drain) : tc_commit(drain);  // this CTA's MMAs in flight end before the tensor memory is freed
                 mbar_wait(drain, 0, p.limit);
             }
             __syncwarp();
@@ -326,7 +353,8 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             tc_fence_after();
             const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
             // plain: lane = output column; gated: lanes 0-15 gate, 16-31 up of 16 features
-            const int n = SWIGLU ? w.m * 64 + 16 * q + (lane & 15) : w.m * 128 + 32 * q + lane;
+            const int mtile = PAIR ? 2 * w.m + rank : w.m;
+            const int n = SWIGLU ? mtile * 64 + 16 * q + (lane & 15) : mtile * 128 + 32 * q + lane;
             const bool mine = n < p.N && (!SWIGLU || lane < 16);
             // 16 rows from c0 on (rows [c0, c1) of them wanted) of the tile: weight or gate, round, store
             auto finish = [&](int c0, int c1, float (&y)[16]) {
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 }
             }
             tc_fence_before();
-            mbar_arrive(&acc_empty[acc]);
+            PAIR ? cluster_arrive(cluster_map(smem_u32(&acc_empty[acc]), 0)) : mbar_arrive(&acc_empty[acc]);
             if (++acc == C::ACC) {
                 acc = 0;
                 acc_phase ^= 1;
@@ -401,9 +429,10 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (KS > 1) cluster_sync();  // nobody's shared memory goes while another rank may store into it
+    // nobody's shared or tensor memory goes while another CTA may still write or read it
+    if (C::CL > 1) cluster_sync();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+    if (warp == 1) PAIR ? tmem_dealloc_pair(tmem, C::TMEM_COLS) : tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -453,8 +482,8 @@ cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms,
     auto *kern = k_grouped<NT, SWIGLU, GATHER, KS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    const int64_t slots = sms / KS;
-    const unsigned grid = unsigned((items < slots ? items : slots) * KS);
+    const int64_t slots = sms / C::CL;
+    const unsigned grid = unsigned((items < slots ? items : slots) * C::CL);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(C::THREADS);
@@ -464,10 +493,10 @@ cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms,
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = KS;
+    attr[1].val.clusterDim.x = C::CL;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = KS > 1 ? 2 : 1;
+    cfg.numAttrs = C::CL > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, ma, ma2, mb, g);
 }
 
@@ -507,6 +536,7 @@ cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st)
     const int64_t rows = ceil_div(a.P * 5, active * 4);
     const int NT = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
     // most tiles there can be, whatever the groups are
+    if (NT == 256) g.MT = int(ceil_div(a.N, a.W2 ? 128 : 256));  // pairs of weight tiles
     const int64_t by_rows = (a.P + active * (NT - 1)) / NT;
     const int64_t items = (by_rows < a.P ? by_rows : a.P) * g.MT;
     if (items > INT32_MAX) return cudaErrorInvalidValue;
