@@ -42,15 +42,19 @@ struct ClusterSum {
         }
         return tc::mbar_wait(bar, 0, limit);
     }
-    // The sum of column c (one of this rank's) and row `row` of the tile.
-    __device__ float at(int c, int row) const
+    // The sums of columns [c0, min(c0 + CW, end)) (this rank's) and row `row` of the tile.
+    template <int CW>
+    __device__ void sum(int c0, int row, float (&y)[CW]) const
     {
-        const int own = begin(rank + 1) - begin(rank);
-        const float *part = red + (c - begin(rank)) * 128 + row;
-        float a = 0.f;
-        for (int r = 0; r < KS; ++r)
-            a += r == rank ? stage[c * 128 + row] : part[(r < rank ? r : r - 1) * own * 128];
-        return a;
+        const int b = begin(rank), own = begin(rank + 1) - b;
+#pragma unroll
+        for (int j = 0; j < CW; ++j) y[j] = 0.f;
+        for (int r = 0; r < KS; ++r) {
+            const float *part = (r == rank ? stage + c0 * 128 : red + ((r < rank ? r : r - 1) * own + c0 - b) * 128) + row;
+#pragma unroll
+            for (int j = 0; j < CW; ++j)
+                if (c0 + j < b + own) y[j] += part[j * 128];
+        }
     }
 };
 

@@ -405,8 +405,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 }
                 const int c0 = cs.begin(rank), c1 = cs.begin(rank + 1);  // this rank's rows
                 float y[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = c0 + j < c1 ? cs.at(c0 + j, 32 * q + lane) : 0.f;
+                cs.sum(c0, 32 * q + lane, y);
                 finish(c0, c1, y);
             } else {
                 for (int c0 = 0; c0 < w.nv; c0 += 16) {

@@ -24,7 +24,7 @@
 //
 // k_linear_mx is a persistent kernel over items (weight tile of 128, row tile),
 // its warps: 0 weight tiles and their scale atoms (TMA), 1 MMA issuer, 2-5
-// epilogue, 6.. the rows.  Up to 32 rows, warps 6-9 split the rows themselves
+// epilogue, 6.. the rows.  Up to 16 rows, warps 6.. split the rows themselves
 // as they go (each weight tile's CTAs repeat it, which costs less than a
 // kernel before this one); beyond, k_split_rows has written the parts and warp
 // 6 copies them.  With few items a cluster of KS CTAs shares an item along K
@@ -32,6 +32,8 @@
 // Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
 #include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "cluster_sum.cuh"
 #include "lmoe_internal.cuh"
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(256) k_split_rows(const uint16_t *__restrict__
         *reinterpret_cast<uint2 *>(row) = hi;
         *reinterpret_cast<uint2 *>(row + int64_t(NB) * (KC * 128)) = lo;
         if ((c & 31) == 0) {
-            uint8_t *at = atoms + (tile * KC + (c >> 7)) * (2 * NB / 128 * 512);
+            uint8_t *at = atoms + (tile * KC + (c >> 7)) * int(ceil_div(2 * NB, 128) * 512);
             at[sf_off(rr, (c >> 5) & 3)] = uint8_t(b);
             at[sf_off(NB + rr, (c >> 5) & 3)] = uint8_t(b - 5);
         }
@@ -145,13 +147,13 @@ struct LCfg {
     // Fused: teams of TW warps take the chunks in turn, a warp 8 rows of one
     // (four 8-column pieces a lane).
     static constexpr int TW = FUSED ? NB / 8 : 1;
-    static constexpr int TEAMS = FUSED ? (NB <= 16 ? 4 : 2) : 1;
+    static constexpr int TEAMS = FUSED ? 4 : 1;
     static constexpr int BW = TW * TEAMS;  // warps that bring B
     static constexpr int THREADS = 32 * (6 + BW);
     static constexpr int UNITS = 4;
     // Small row tiles leave room for two CTAs an SM: the next call's start up
     // beside the last ones of this call, and the items spread more evenly.
-    static constexpr int CTAS = NB <= 32 ? 2 : 1;
+    static constexpr int CTAS = FUSED ? 2 : 1;
     static constexpr int ACC = NC <= 128 ? 2 : 1;
     static constexpr int SF_COLS = 4 + 4 * NAT;  // TMEM columns of a stage's scales
     static constexpr int SF_BASE = ACC * NC;
@@ -417,9 +419,14 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                     break;
                 }
-                if (n < p.N)
-                    for (int c = cs.begin(rank); c < cs.begin(rank + 1); ++c)
-                        o[int64_t(c) * p.N] = __float2bfloat16_rn(cs.at(c, 32 * q + lane));
+                for (int c0 = cs.begin(rank); c0 < cs.begin(rank + 1); c0 += 8) {
+                    float y[8];
+                    cs.sum(c0, 32 * q + lane, y);
+                    if (n < p.N)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (c0 + j < cs.begin(rank + 1)) o[int64_t(c0 + j) * p.N] = __float2bfloat16_rn(y[j]);
+                }
             } else {
                 for (int c0 = 0; c0 < nv; c0 += CW) {
                     float y[CW];
@@ -481,8 +488,59 @@ int sm_count()
     return n > 0 ? n : 148;
 }
 
-// Rows of a tile; up to 32 the kernel splits the rows itself.
-int row_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Rows of a tile.  Up to 16 the kernel splits the rows itself, also of small
+// products whose 16-row tiles run at once (512 x 512, 100 rows: 3.9 us, against
+// 5.0 with 64-row tiles and the kernel before them).  Beyond, 64 rows, whose
+// chunks take no longer than 16 rows' (0.2 us, the weights' copies), until the
+// tensor cores are the bound (7168 -> 3584, 64- and 128-row tiles: 200 rows
+// 19.3 and 21.7 us, 512 rows 33.7 and 31.5 us).
+int row_tile(int64_t rows, int64_t K, int64_t N)
+{
+    if (rows <= 8) return 8;
+    if (rows <= 16 || (K <= 12 * 128 && ceil_div(rows, 16) * ceil_div(N, 128) <= 152)) return 16;
+    return rows < 384 ? 64 : 128;
+}
+bool splits_itself(int NB) { return NB <= 16; }
+
+template <int NB, bool FUSED>
+cudaLaunchConfig_t config(unsigned grid, cudaStream_t st, cudaLaunchAttribute (&attr)[2], int ks)
+{
+    using C = LCfg<NB, FUSED>;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(ks);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ks > 1 ? 2 : 1;
+    return cfg;
+}
+
+// How many clusters of ks CTAs run at once, one CTA an SM (a cluster lies within
+// one group of SMs, so sizes that do not divide a group's leave some idle);
+// asked once.  The runtime answers for one CTA an SM whenever a kernel uses
+// tensor memory; two that fit do run side by side.
+template <int NB, bool FUSED>
+int max_clusters(int ks)
+{
+    static std::atomic<int> known[MAX_KS + 1];
+    int n = known[ks].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config<NB, FUSED>(unsigned(ks) * 512, nullptr, attr, ks);
+    attr[0].val.programmaticStreamSerializationAllowed = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear_mx<NB, FUSED>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    known[ks].store(n > 0 ? n : 1, std::memory_order_relaxed);
+    return n > 0 ? n : 1;
+}
 
 template <int NB, bool FUSED>
 cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t st)
@@ -494,35 +552,25 @@ cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t
         mb = ma;  // not used
     else if (!byte_map(&mb, codes, false, int64_t(a.KC) * 128, int64_t(a.NTL) * C::NC, C::NC))
         return cudaErrorInvalidValue;
+    auto *kern = k_linear_mx<NB, FUSED>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
+    if (e != cudaSuccess) return e;
     const int sms = sm_count();
     const int64_t items = int64_t(a.MT) * a.NTL;
-    // With items for fewer CTAs than run at once, as many ranks an item as
-    // make the longest SM's share of the chunks shortest (fewest ranks among
-    // equals).
+    // As many ranks an item as make the longest SM's share of the chunks
+    // shortest, a split's exchange counted as 4 to 28 chunks (measured: 0.2 us
+    // a chunk; 0.9 us for 8 rows, 3.3 us for 64), while every cluster runs at
+    // once, with some to spare: the previous kernel's blocks may still hold SMs.
     a.KS = 1;
-    int64_t best = items <= int64_t(sms) * C::CTAS ? ceil_div(items, sms) * a.KC : 0;
+    int64_t best = ceil_div(items, sms) * a.KC;
     for (int ks = 2; ks <= MAX_KS && items * ks <= int64_t(sms) * C::CTAS && ks * 2 <= a.KC; ++ks) {
-        const int64_t cost = ceil_div(items * ks, sms) * ceil_div(a.KC, ks);
-        if (cost < best) best = cost, a.KS = ks;
+        const int64_t cost = ceil_div(items * ks, sms) * ceil_div(a.KC, ks) + 4 + NB * 3 / 16;
+        if (cost < best && items * 10 <= max_clusters<NB, FUSED>(ks) * C::CTAS * 9) best = cost, a.KS = ks;
     }
-    const size_t smem = C::SMEM;
-    auto *kern = k_linear_mx<NB, FUSED>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
     const int64_t slots = int64_t(sms) * C::CTAS / a.KS;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((items < slots ? items : slots) * a.KS));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = unsigned(a.KS);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.KS > 1 ? 2 : 1;
+    const cudaLaunchConfig_t cfg =
+        config<NB, FUSED>(unsigned((items < slots ? items : slots) * a.KS), st, attr, a.KS);
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
 }
 
@@ -530,16 +578,15 @@ cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t
 
 size_t linear_mxfp4_scratch_bytes(int64_t rows, int K, int N)
 {
-    (void)N;
-    const int64_t KC = ceil_div(K, 128), NB = row_tile(rows);
-    if (NB <= 32) return 0;
-    return size_t(ceil_div(rows, NB) * KC * (2 * NB * 128 + 2 * NB / 128 * 512));
+    const int64_t KC = ceil_div(K, 128), NB = row_tile(rows, K, N);
+    if (splits_itself(int(NB))) return 0;
+    return size_t(ceil_div(rows, NB) * KC * (2 * NB * 128 + ceil_div(2 * NB, 128) * 512));
 }
 
 cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int K, int N,
                                 uint16_t *out, void *scratch, int32_t *status, const WaitArgs &wait, cudaStream_t st)
 {
-    const int NB = row_tile(rows);
+    const int NB = row_tile(rows, K, N);
     LArgs a{};
     a.x = x;
     a.rows = int(rows);
@@ -556,7 +603,6 @@ cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8
     a.stall = wait.stall_first_fill;
     if (NB == 8) return launch<8, true>(a, q, nullptr, st);
     if (NB == 16) return launch<16, true>(a, q, nullptr, st);
-    if (NB == 32) return launch<32, true>(a, q, nullptr, st);
     uint8_t *codes = static_cast<uint8_t *>(scratch);
     uint8_t *atoms = codes + int64_t(a.NTL) * a.KC * (2 * NB * 128);
     a.sfb = atoms;
