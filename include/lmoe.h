@@ -371,6 +371,45 @@ lmoe_status lmoe_grouped_swiglu_bf16(const uint16_t *x, int64_t x_rows, const ui
                                      const lmoe_groups *groups, int32_t gather, int32_t K, int32_t I, uint16_t *h,
                                      void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- block on a residual stream ------------------------------------------------ */
+
+/* A hidden <-> latent projection: bf16 weights w [N][K], or, with w NULL, MXFP4
+ * codes q and scales s in LMOE_LAYOUT_TC (as for lmoe_linear_mxfp4). */
+typedef struct {
+    const uint16_t *w;
+    const uint8_t *q, *s;
+} lmoe_projection;
+
+/* What lmoe_forward_residual_block adds to the layer: the two projections
+ * (in: d x hidden, out: hidden x d), the norm before them (pre_w fp32
+ * [hidden]; may be NULL where the call is given the normalised rows), and
+ * post_w, gate, gate_kind, scale, eps and next_w as for lmoe_residual_norm
+ * (eps is the pre-norm's too). */
+typedef struct {
+    lmoe_projection in, out;
+    const float *pre_w, *post_w;
+    const void *gate;
+    int32_t gate_kind;
+    float scale, eps;
+    const float *next_w;
+} lmoe_residual_block;
+
+size_t lmoe_residual_block_workspace_size(const lmoe_dims *dims, int32_t hidden);
+
+/* The whole block on a residual stream res [T][hidden] (bf16 or fp32):
+ *   n = x_n ? x_n : lmoe_rms_norm(res, pre_w)          bf16 [T][hidden]
+ *   o = lmoe_forward(n W_in^T) W_out^T                 (bf16 at each step)
+ *   res_out, next_out = lmoe_residual_norm(o, res, ...)
+ * x_n: the rows the previous block's next_out already normalised, or NULL.
+ * res_out may be res, next_out may be x_n.  hidden % 64 == 0, hidden <= 32768.
+ * The status word at the workspace's start is cleared by the call and covers
+ * all of it. */
+lmoe_status lmoe_forward_residual_block(const void *res, int32_t res_fmt, const uint16_t *x_n,
+                                        const lmoe_residual_block *block, const uint16_t *Wr3, const float *bias,
+                                        const lmoe_expert_weights *W, const lmoe_dims *dims, int32_t hidden,
+                                        void *res_out, uint16_t *next_out, void *workspace, size_t ws_bytes,
+                                        void *stream);
+
 /* ---- helpers --------------------------------------------------------------- */
 
 /* Reads (synchronously, after all prior work on the device) the status word

@@ -162,6 +162,138 @@ lmoe_status grouped_args(const uint16_t *x, int64_t x_rows, const lmoe_groups *g
     return LMOE_OK;
 }
 
+// lmoe_forward; with keep_status the workspace's status word is left as it is
+// (a caller cleared it before kernels of its own).
+lmoe_status forward_impl(const uint16_t *x_bf16, const uint16_t *Wr3, const float *bias, const lmoe_expert_weights *W,
+                         const lmoe_dims *dims, uint16_t *y_bf16, int32_t *topk_idx, float *topk_w, float *logits,
+                         void *workspace, size_t ws_bytes, void *stream, bool keep_status)
+{
+    if (!dims_ok(dims)) return LMOE_ERR_INVALID_ARG;
+    // MXFP4 activations exist on the small-batch path only
+    lmoe_status a = (dims->act == LMOE_ACT_MXFP4 && small_path(dims)) ? LMOE_OK : act_ok(dims);
+    if (a != LMOE_OK) return a;
+    if (dims->T == 0) return LMOE_OK;
+    if (!x_bf16 || !Wr3 || !y_bf16 || !aligned(x_bf16, 16) || !aligned(Wr3, 16) || !aligned(y_bf16, 16))
+        return LMOE_ERR_INVALID_ARG;
+    if (!weights_ok(W)) return LMOE_ERR_INVALID_ARG;
+    const FwdLayout L = fwd_layout(dims);
+    if (!workspace || ws_bytes < L.total || !aligned(workspace, 256)) return LMOE_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    cudaStream_t st = cudaStream_t(stream);
+    const int T = dims->T, E = dims->E, k = dims->k, d = dims->d;
+    const int64_t P = int64_t(T) * k;
+    float *lg = logits ? logits : reinterpret_cast<float *>(ws + L.logits);
+    int32_t *idx = topk_idx ? topk_idx : reinterpret_cast<int32_t *>(ws + L.idx);
+    float *w = topk_w ? topk_w : reinterpret_cast<float *>(ws + L.w);
+    int32_t *counts = reinterpret_cast<int32_t *>(ws + L.counts);
+    int32_t *offsets = reinterpret_cast<int32_t *>(ws + L.offsets);
+    int32_t *perm = reinterpret_cast<int32_t *>(ws + L.perm);
+    int32_t *inv = reinterpret_cast<int32_t *>(ws + L.inv);
+    int32_t *status = reinterpret_cast<int32_t *>(ws + L.status);
+    // zeroes the first `bytes` of the workspace, but for a status word that is to stay
+    auto clear_from = [&](int32_t *p, size_t bytes) {
+        if (keep_status) ++p, bytes -= sizeof(int32_t);
+        return bytes > 0 ? cudaMemsetAsync(p, 0, bytes, st) : cudaSuccess;
+    };
+    if (L.small) {
+        // three kernels; the status word and the routing kernel's counter
+        // (the next int32) start at zero
+        if (g_hcap && g_hcap_bytes < size_t(P) * dims->I * sizeof(float)) return LMOE_ERR_INVALID_ARG;
+        cudaError_t e = mark(0, st);
+        if (e == cudaSuccess) e = clear_from(status, 2 * sizeof(int32_t));
+        if (e == cudaSuccess)
+            e = launch_small_forward(x_bf16, Wr3, bias, W, T, d, E, k, dims->I, dims->act, lg, idx, w, y_bf16,
+                                     small_layout(T, d, E, k, dims->I), ws + L.sscratch, status, status + 1, g_hcap, st,
+                                     g_stage_events_on ? g_stage_events : nullptr);
+        if (e == cudaSuccess) e = mark(5, st);
+        if (e == cudaSuccess) e = mark(6, st);
+        return cuda_status(e);
+    }
+    char *fs = ws + L.fscratch;
+    const FfnLayout FL = ffn_layout(P, d, E, dims->I);
+    if (g_hcap && g_hcap_bytes < size_t(FL.rows) * dims->I * sizeof(float)) return LMOE_ERR_INVALID_ARG;
+    float *yp = reinterpret_cast<float *>(ws + L.yp);
+    // Large batches fuse the combine into the down GEMM: its epilogue adds
+    // each pair's weighted output into the token's fp32 row (zeroed here),
+    // which one pass then rounds to bf16.
+    float *yacc = FL.fused ? yp : nullptr;
+
+    const bool pr = permute_in_route(T, d, E, k, FL);
+    PermByMask pm;
+    if (pr) {
+        pm.mask = reinterpret_cast<unsigned long long *>(ws + L.tmask);
+        pm.counter = status + 2;
+        pm.counts = counts;
+        pm.offsets = offsets;
+        pm.perm = perm;
+        pm.inv = inv;
+        pm.sc = ffn_sched(FL, d, dims->I, fs);
+    }
+    cudaError_t e = mark(0, st);
+    // the status word (and, with the permute in the routing kernel, its counter and the token masks) start at zero
+    if (e == cudaSuccess) e = clear_from(status, pr ? L.tmask - L.status + size_t(E) * 8 : sizeof(int32_t));
+    if (e == cudaSuccess) e = launch_route(x_bf16, Wr3, bias, T, d, E, k, lg, idx, w, ws + L.rscratch, status, st, pm);
+    if (e == cudaSuccess) e = mark(1, st);
+    if (e == cudaSuccess && !pr)
+        e = launch_permute(idx, P, E, counts, offsets, perm, inv, ws + L.pscratch, status, st,
+                           ffn_sched(FL, d, dims->I, fs));
+    if (e == cudaSuccess) e = mark(2, st);
+    if (e == cudaSuccess) e = launch_quant_scatter_pad(x_bf16, T, d, k, E, dims->I, inv, w, FL, fs, st);
+    if (e == cudaSuccess) e = mark(3, st);
+    if (e == cudaSuccess) {
+        FfnArgs f{W, offsets, perm, w, int(P), d, E, k, dims->I, yp, yacc, status};
+        f.hcap = g_hcap;
+        f.wait_limit = g_wait_limit;
+        f.stall_first_fill = g_stall;
+        e = launch_expert_gemms(f, FL, fs, st, g_stage_events_on ? g_stage_events[4] : nullptr);
+    }
+    if (e == cudaSuccess) e = mark(5, st);
+    if (e == cudaSuccess)
+        e = yacc ? launch_acc_to_bf16(yacc, int64_t(T) * d, y_bf16, st) : launch_combine(yp, inv, T, d, k, y_bf16, st, true);
+    if (e == cudaSuccess) e = mark(6, st);
+    return cuda_status(e);
+}
+
+// ---- the block on a residual stream: layout of its workspace ----
+// forward's workspace first (its status word is the block's), then the
+// normalised rows / projected output (one buffer: the rows are consumed before
+// the output is written), latent rows, layer output, split rows of MXFP4
+// projections.
+struct ResBlockLayout {
+    size_t rows, lat, y, split, total;
+};
+ResBlockLayout res_block_layout(const lmoe_dims *d, int32_t hidden)
+{
+    const int64_t T = d->T;
+    ResBlockLayout L{};
+    size_t off = size_t(round_up(int64_t(fwd_layout(d).total), 256));
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off += size_t(round_up(int64_t(bytes), 256));
+        return o;
+    };
+    L.rows = take(size_t(T) * hidden * 2);
+    L.lat = take(size_t(T) * d->d * 2);
+    L.y = take(size_t(T) * d->d * 2);
+    const size_t a = linear_mxfp4_scratch_bytes(T, hidden, d->d), b = linear_mxfp4_scratch_bytes(T, d->d, hidden);
+    L.split = take(a > b ? a : b);
+    L.total = off;
+    return L;
+}
+
+bool projection_ok(const lmoe_projection &p)
+{
+    if (p.w) return aligned(p.w, 16);
+    return p.q && p.s && aligned(p.q, 32) && aligned(p.s, 16);
+}
+
+cudaError_t project(const lmoe_projection &p, const uint16_t *x, int T, int K, int N, uint16_t *out, void *split,
+                    int32_t *status, cudaStream_t st)
+{
+    if (p.w) return launch_linear_bf16(x, p.w, T, K, N, out, nullptr, status, st);
+    return launch_linear_mxfp4(x, p.q, p.s, T, K, N, out, split, status, wait_args(), st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -359,85 +491,8 @@ lmoe_status lmoe_forward(const uint16_t *x_bf16, const uint16_t *Wr3, const floa
                          const lmoe_dims *dims, uint16_t *y_bf16, int32_t *topk_idx, float *topk_w, float *logits,
                          void *workspace, size_t ws_bytes, void *stream)
 {
-    if (!dims_ok(dims)) return LMOE_ERR_INVALID_ARG;
-    // MXFP4 activations exist on the small-batch path only
-    lmoe_status a = (dims->act == LMOE_ACT_MXFP4 && small_path(dims)) ? LMOE_OK : act_ok(dims);
-    if (a != LMOE_OK) return a;
-    if (dims->T == 0) return LMOE_OK;
-    if (!x_bf16 || !Wr3 || !y_bf16 || !aligned(x_bf16, 16) || !aligned(Wr3, 16) || !aligned(y_bf16, 16))
-        return LMOE_ERR_INVALID_ARG;
-    if (!weights_ok(W)) return LMOE_ERR_INVALID_ARG;
-    const FwdLayout L = fwd_layout(dims);
-    if (!workspace || ws_bytes < L.total || !aligned(workspace, 256)) return LMOE_ERR_WORKSPACE;
-    char *ws = static_cast<char *>(workspace);
-    cudaStream_t st = cudaStream_t(stream);
-    const int T = dims->T, E = dims->E, k = dims->k, d = dims->d;
-    const int64_t P = int64_t(T) * k;
-    float *lg = logits ? logits : reinterpret_cast<float *>(ws + L.logits);
-    int32_t *idx = topk_idx ? topk_idx : reinterpret_cast<int32_t *>(ws + L.idx);
-    float *w = topk_w ? topk_w : reinterpret_cast<float *>(ws + L.w);
-    int32_t *counts = reinterpret_cast<int32_t *>(ws + L.counts);
-    int32_t *offsets = reinterpret_cast<int32_t *>(ws + L.offsets);
-    int32_t *perm = reinterpret_cast<int32_t *>(ws + L.perm);
-    int32_t *inv = reinterpret_cast<int32_t *>(ws + L.inv);
-    int32_t *status = reinterpret_cast<int32_t *>(ws + L.status);
-    if (L.small) {
-        // three kernels; the status word and the routing kernel's counter
-        // (the next int32) start at zero
-        if (g_hcap && g_hcap_bytes < size_t(P) * dims->I * sizeof(float)) return LMOE_ERR_INVALID_ARG;
-        cudaError_t e = mark(0, st);
-        if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, 2 * sizeof(int32_t), st);
-        if (e == cudaSuccess)
-            e = launch_small_forward(x_bf16, Wr3, bias, W, T, d, E, k, dims->I, dims->act, lg, idx, w, y_bf16,
-                                     small_layout(T, d, E, k, dims->I), ws + L.sscratch, status, status + 1, g_hcap, st,
-                                     g_stage_events_on ? g_stage_events : nullptr);
-        if (e == cudaSuccess) e = mark(5, st);
-        if (e == cudaSuccess) e = mark(6, st);
-        return cuda_status(e);
-    }
-    char *fs = ws + L.fscratch;
-    const FfnLayout FL = ffn_layout(P, d, E, dims->I);
-    if (g_hcap && g_hcap_bytes < size_t(FL.rows) * dims->I * sizeof(float)) return LMOE_ERR_INVALID_ARG;
-    float *yp = reinterpret_cast<float *>(ws + L.yp);
-    // Large batches fuse the combine into the down GEMM: its epilogue adds
-    // each pair's weighted output into the token's fp32 row (zeroed here),
-    // which one pass then rounds to bf16.
-    float *yacc = FL.fused ? yp : nullptr;
-
-    const bool pr = permute_in_route(T, d, E, k, FL);
-    PermByMask pm;
-    if (pr) {
-        pm.mask = reinterpret_cast<unsigned long long *>(ws + L.tmask);
-        pm.counter = status + 2;
-        pm.counts = counts;
-        pm.offsets = offsets;
-        pm.perm = perm;
-        pm.inv = inv;
-        pm.sc = ffn_sched(FL, d, dims->I, fs);
-    }
-    cudaError_t e = mark(0, st);
-    // the status word (and, with the permute in the routing kernel, its counter and the token masks) start at zero
-    if (e == cudaSuccess) e = cudaMemsetAsync(status, 0, pr ? L.tmask - L.status + size_t(E) * 8 : sizeof(int32_t), st);
-    if (e == cudaSuccess) e = launch_route(x_bf16, Wr3, bias, T, d, E, k, lg, idx, w, ws + L.rscratch, status, st, pm);
-    if (e == cudaSuccess) e = mark(1, st);
-    if (e == cudaSuccess && !pr)
-        e = launch_permute(idx, P, E, counts, offsets, perm, inv, ws + L.pscratch, status, st,
-                           ffn_sched(FL, d, dims->I, fs));
-    if (e == cudaSuccess) e = mark(2, st);
-    if (e == cudaSuccess) e = launch_quant_scatter_pad(x_bf16, T, d, k, E, dims->I, inv, w, FL, fs, st);
-    if (e == cudaSuccess) e = mark(3, st);
-    if (e == cudaSuccess) {
-        FfnArgs f{W, offsets, perm, w, int(P), d, E, k, dims->I, yp, yacc, status};
-        f.hcap = g_hcap;
-        f.wait_limit = g_wait_limit;
-        f.stall_first_fill = g_stall;
-        e = launch_expert_gemms(f, FL, fs, st, g_stage_events_on ? g_stage_events[4] : nullptr);
-    }
-    if (e == cudaSuccess) e = mark(5, st);
-    if (e == cudaSuccess)
-        e = yacc ? launch_acc_to_bf16(yacc, int64_t(T) * d, y_bf16, st) : launch_combine(yp, inv, T, d, k, y_bf16, st, true);
-    if (e == cudaSuccess) e = mark(6, st);
-    return cuda_status(e);
+    return forward_impl(x_bf16, Wr3, bias, W, dims, y_bf16, topk_idx, topk_w, logits, workspace, ws_bytes, stream,
+                        false);
 }
 
 lmoe_status lmoe_linear_bf16(const uint16_t *x, const uint16_t *W, int64_t rows, int32_t K, int32_t N, uint16_t *out,
@@ -560,6 +615,58 @@ lmoe_status lmoe_grouped_swiglu_bf16(const uint16_t *x, int64_t x_rows, const ui
     a.W2 = Wu;
     a.out_fmt = LMOE_BF16;
     return cuda_status(launch_grouped(a, cudaStream_t(stream)));
+}
+
+size_t lmoe_residual_block_workspace_size(const lmoe_dims *dims, int32_t hidden)
+{
+    if (!dims_ok(dims) || hidden <= 0 || hidden % 64 != 0 || hidden > 32768) return 0;
+    return res_block_layout(dims, hidden).total;
+}
+
+lmoe_status lmoe_forward_residual_block(const void *res, int32_t res_fmt, const uint16_t *x_n,
+                                        const lmoe_residual_block *block, const uint16_t *Wr3, const float *bias,
+                                        const lmoe_expert_weights *W, const lmoe_dims *dims, int32_t hidden,
+                                        void *res_out, uint16_t *next_out, void *workspace, size_t ws_bytes,
+                                        void *stream)
+{
+    if (!dims_ok(dims) || !block || hidden <= 0 || hidden % 64 != 0) return LMOE_ERR_INVALID_ARG;
+    if (!norm_ok(dims->T, hidden, block->eps, res_fmt) || !isfinite(block->scale)) return LMOE_ERR_INVALID_ARG;
+    if (block->gate_kind < LMOE_GATE_NONE || block->gate_kind > LMOE_GATE_FULL) return LMOE_ERR_INVALID_ARG;
+    const lmoe_status a = act_ok(dims);
+    if (a != LMOE_OK) return a;
+    if (dims->T == 0) return LMOE_OK;
+    if (!res || !res_out || (!x_n && !block->pre_w) || (block->gate_kind != LMOE_GATE_NONE) != (block->gate != nullptr) ||
+        (block->next_w && !next_out))
+        return LMOE_ERR_INVALID_ARG;
+    for (const void *p : {res, (const void *)res_out, (const void *)x_n, (const void *)next_out, (const void *)block->pre_w,
+                          (const void *)block->post_w, (const void *)block->next_w, block->gate})
+        if (!aligned(p, 16)) return LMOE_ERR_INVALID_ARG;
+    if (!projection_ok(block->in) || !projection_ok(block->out) || !Wr3 || !aligned(Wr3, 16) || !weights_ok(W))
+        return LMOE_ERR_INVALID_ARG;
+    const ResBlockLayout L = res_block_layout(dims, hidden);
+    if (!workspace || ws_bytes < L.total || !aligned(workspace, 256)) return LMOE_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    int32_t *status = reinterpret_cast<int32_t *>(ws);
+    uint16_t *rows = reinterpret_cast<uint16_t *>(ws + L.rows), *lat = reinterpret_cast<uint16_t *>(ws + L.lat);
+    uint16_t *y = reinterpret_cast<uint16_t *>(ws + L.y);
+    cudaStream_t st = cudaStream_t(stream);
+    const int T = dims->T;
+    cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int32_t), st);
+    if (e == cudaSuccess && !x_n) {
+        NormArgs n{nullptr, res, res_fmt, nullptr, nullptr, LMOE_GATE_NONE, 1.f, block->eps, block->pre_w, T, hidden, nullptr, rows};
+        e = launch_residual_norm(n, st);
+    }
+    if (e == cudaSuccess) e = project(block->in, x_n ? x_n : rows, T, hidden, dims->d, lat, ws + L.split, status, st);
+    if (e != cudaSuccess) return cuda_status(e);
+    const lmoe_status f = forward_impl(lat, Wr3, bias, W, dims, y, nullptr, nullptr, nullptr, ws, L.rows, stream, true);
+    if (f != LMOE_OK) return f;
+    e = project(block->out, y, T, dims->d, hidden, rows, ws + L.split, status, st);
+    if (e == cudaSuccess) {
+        NormArgs n{rows, res, res_fmt, block->post_w, block->gate, block->gate_kind, block->scale, block->eps,
+                   block->next_w, T, hidden, res_out, block->next_w ? next_out : nullptr};
+        e = launch_residual_norm(n, st);
+    }
+    return cuda_status(e);
 }
 
 int32_t lmoe_forward_kernel_count(const lmoe_dims *dims)

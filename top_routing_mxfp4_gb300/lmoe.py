@@ -107,6 +107,19 @@ _grouped_linear = _sig("lmoe_grouped_linear_bf16", ctypes.c_int, _vp, _i64, _vp,
                        _vp, _sz, _vp)
 _grouped_swiglu = _sig("lmoe_grouped_swiglu_bf16", ctypes.c_int, _vp, _i64, _vp, _vp, _GP, _i32, _i32, _i32, _vp, _vp,
                        _sz, _vp)
+class Projection(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("q", ctypes.c_void_p), ("s", ctypes.c_void_p)]
+
+
+class ResidualBlockStruct(ctypes.Structure):
+    _fields_ = [("inp", Projection), ("out", Projection), ("pre_w", ctypes.c_void_p), ("post_w", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_kind", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("next_w", ctypes.c_void_p)]
+
+
+_res_block_ws = _sig("lmoe_residual_block_workspace_size", _sz, _DP, _i32)
+_res_block = _sig("lmoe_forward_residual_block", ctypes.c_int, _vp, _i32, _vp, ctypes.POINTER(ResidualBlockStruct), _vp,
+                  _vp, _WP, _DP, _i32, _vp, _vp, _vp, _sz, _vp)
 BF16, F32 = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
@@ -572,6 +585,15 @@ def _ws_arg(ws, di):
     return ws.data_ptr()
 
 
+def _gate(gate, T, H, di):
+    gs = gate.shape
+    if gate.dtype is torch.bfloat16:
+        return GATE_FULL, _arg(gate, torch.bfloat16, (T, H), "gate", di)
+    if gs == (T, 1):
+        return GATE_TOKEN, _arg(gate, torch.float32, gs, "gate", di)
+    return GATE_CHANNEL, _arg(gate, torch.float32, (1, H) if len(gs) == 2 else (H,), "gate", di)
+
+
 def rms_norm(x, w, eps: float = 1e-5, out=None, stream=None):
     """The norm before a block: x [T, H] bf16 or fp32, w fp32 [H] -> bf16 [T, H] (lmoe_rms_norm)."""
     shape = x.shape
@@ -603,15 +625,7 @@ def residual_norm(y, res, post_w=None, gate=None, scale: float = 1.0, next_w=Non
     yp = _arg(y, torch.bfloat16, shape, "y", di)
     rp = _arg(res, res.dtype, shape, "res", di)
     pp = None if post_w is None else _arg(post_w, torch.float32, (H,), "post_w", di)
-    kind, gp = GATE_NONE, None
-    if gate is not None:
-        gs = gate.shape
-        if gate.dtype is torch.bfloat16:
-            kind, gp = GATE_FULL, _arg(gate, torch.bfloat16, shape, "gate", di)
-        elif gs == (T, 1):
-            kind, gp = GATE_TOKEN, _arg(gate, torch.float32, gs, "gate", di)
-        else:
-            kind, gp = GATE_CHANNEL, _arg(gate, torch.float32, (1, H) if len(gs) == 2 else (H,), "gate", di)
+    kind, gp = (GATE_NONE, None) if gate is None else _gate(gate, T, H, di)
     sp = _handle(stream, di)
     if res_out is None:
         res_out = _make(_empty_on, shape, res.dtype, y, stream)
@@ -721,6 +735,107 @@ def grouped_swiglu_bf16(x, Wg, Wu, offsets, perm=None, k: int = 1, gather=None, 
     grouped_linear_bf16."""
     return _grouped_call("lmoe_grouped_swiglu_bf16", x, Wg, Wu, offsets, perm, k, gather, None, out, torch.bfloat16,
                          ws, stream)
+
+
+class LinearMxfp4:
+    """A linear layer with MXFP4 weights [N, K] in the tensor-core layout: from
+    fp32 or bf16 weights (quantised) or from codes and scales."""
+
+    def __init__(self, W=None, q=None, s=None, N: int = 0, K: int = 0):
+        if W is not None:
+            N, K = W.shape
+            q, s = quant_mxfp4(W.float().contiguous())
+        self.N, self.K, self.q, self.s = N, K, q, s
+        qb, sb = mxfp4_bytes(1, N, K, LAYOUT_TC)
+        _need(q, torch.uint8, (qb,), "q")
+        _need(s, torch.uint8, (sb,), "s")
+
+    def forward(self, x, out=None, ws=None, stream=None):
+        return linear_mxfp4(x, self.q, self.s, self.N, out=out, ws=ws, stream=stream)
+
+
+class ExpertBankBf16:
+    """An unquantised expert bank: gate and up [E, I, d], down [E, d, I], bf16."""
+
+    def __init__(self, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor):
+        E, I, d = gate.shape
+        _need(gate, torch.bfloat16, (E, I, d), "gate")
+        _need(up, torch.bfloat16, (E, I, d), "up")
+        _need(down, torch.bfloat16, (E, d, I), "down")
+        self.gate, self.up, self.down, self.E, self.d, self.I = gate, up, down, E, d, I
+
+
+def expert_ffn_bf16(x, bank: ExpertBankBf16, offsets, perm, topk_w, k: int, ws=None, stream=None):
+    """expert_ffn on a bf16 bank: x bf16 [T, d] in token order -> yp fp32
+    [T*k, d] in permuted order, as combine takes it (grouped_swiglu_bf16, then
+    grouped_linear_bf16 with the gate weights)."""
+    h = grouped_swiglu_bf16(x, bank.gate, bank.up, offsets, perm, k, ws=ws, stream=stream)
+    return grouped_linear_bf16(h, bank.down, offsets, perm, k, gather=False, row_w=topk_w, ws=ws, stream=stream)
+
+
+class ResidualBlock:
+    """The layer in a residual stream (lmoe_forward_residual_block): norm before
+    (pre_w), projection, LatentMoE layer, projection, norm after (post_w), gate
+    (fp32 [hidden]), residual scale.  W_in [d, hidden] and W_out [hidden, d]:
+    bf16 tensors or LinearMxfp4.  One forward at a time: the object owns its
+    workspace."""
+
+    def __init__(self, layer: Layer, W_in, W_out, pre_w=None, post_w=None, gate=None, scale: float = 1.0,
+                 eps: float = 1e-5):
+        d = layer.bank.d
+        hidden = W_in.K if isinstance(W_in, LinearMxfp4) else W_in.shape[1]
+        for W, shape, name in ((W_in, (d, hidden), "W_in"), (W_out, (hidden, d), "W_out")):
+            if isinstance(W, LinearMxfp4):
+                if (W.N, W.K) != shape:
+                    raise ValueError(f"{name}: expected {shape}, got {(W.N, W.K)}")
+            else:
+                _need(W, torch.bfloat16, shape, name)
+        self.layer, self.W_in, self.W_out, self.hidden = layer, W_in, W_out, hidden
+        self.pre_w, self.post_w, self.gate, self.scale, self.eps = pre_w, post_w, gate, scale, eps
+        self._ws = None
+
+    @staticmethod
+    def _proj(W):
+        return Projection(None, W.q.data_ptr(), W.s.data_ptr()) if isinstance(W, LinearMxfp4) else \
+            Projection(W.data_ptr(), None, None)
+
+    def forward(self, res, x_n=None, gate=None, next_w=None, res_out=None, next_out=None, stream=None):
+        """res [T, hidden] bf16 or fp32 -> (res_out, next_out or None).  x_n: the
+        already normalised rows (a previous block's next_out); gate: per call, as
+        residual_norm's, instead of the block's; next_w: the next block's pre_w."""
+        T, H = res.shape
+        di = res.get_device()
+        fmt = _fmt(res, "res")
+        rp = _arg(res, res.dtype, (T, self.hidden), "res", di)
+        vec = lambda t, name: None if t is None else _arg(t, torch.float32, (H,), name, di)
+        xp = None if x_n is None else _arg(x_n, torch.bfloat16, (T, H), "x_n", di)
+        gate = self.gate if gate is None else gate
+        kind, gp = (GATE_NONE, None) if gate is None else _gate(gate, T, H, di)
+        if next_w is None and next_out is not None:
+            raise ValueError("next_out without next_w")
+        B = ResidualBlockStruct(self._proj(self.W_in), self._proj(self.W_out), vec(self.pre_w, "pre_w"),
+                                vec(self.post_w, "post_w"), gp, kind, self.scale, self.eps, vec(next_w, "next_w"))
+        if x_n is None and self.pre_w is None:
+            raise ValueError("neither x_n nor pre_w")
+        sp = _handle(stream, di)
+        res_out = _make(_empty_on, (T, H), res.dtype, res, stream) if res_out is None else res_out
+        rop = _arg(res_out, res.dtype, (T, H), "res_out", di)
+        if next_w is not None and next_out is None:
+            next_out = _make(_empty_on, (T, H), torch.bfloat16, res, stream)
+        nop = None if next_out is None else _arg(next_out, torch.bfloat16, (T, H), "next_out", di)
+        layer, bank = self.layer, self.layer.bank
+        D = dims(T, bank.d, bank.E, layer.k, bank.I, layer.act)
+        need = int(_res_block_ws(ctypes.byref(D), H))
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = _make(_empty_on, (max(need, 256),), torch.uint8, res, stream)
+        W = bank.struct()
+        _run(di, "lmoe_forward_residual_block", _res_block, rp, fmt, xp, ctypes.byref(B), layer.Wr3.data_ptr(),
+             None if layer.bias is None else layer.bias.data_ptr(), ctypes.byref(W), ctypes.byref(D), H, rop, nop,
+             self._ws.data_ptr(), self._ws.numel(), sp)
+        return res_out, next_out
+
+    def device_status(self) -> int:
+        return last_device_status(self._ws)
 
 
 class Block:
