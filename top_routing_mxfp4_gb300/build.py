@@ -2,22 +2,27 @@
 
 Each .cu under csrc/ is compiled to an object in parallel, then the objects
 are linked into top_routing_mxfp4_gb300/liblmoe.so (CUDA runtime linked
-statically).  Rebuilds only when a source or header is newer than the
-library.
+statically).  Beside it, csrc/bind_torch.cpp becomes _lmoe_torch.so, the
+binding of the short calls on torch tensors (g++, torch's headers).  Rebuilds
+only what is older than its sources and headers.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblmoe.so")
+BIND_SRC = os.path.join(CSRC, "bind_torch.cpp")
+BIND = os.path.join(PKG, "_lmoe_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                      "-Xptxas", "-warn-spills", f"-I{os.path.join(ROOT, 'include')}"]
@@ -41,10 +46,43 @@ def _stale() -> bool:
     return max(os.path.getmtime(p) for p in deps) > os.path.getmtime(LIB)
 
 
+def _bind_stale() -> bool:
+    deps = [BIND_SRC, os.path.join(ROOT, "include", "lmoe.h")]
+    return not os.path.exists(BIND) or max(os.path.getmtime(p) for p in deps) > os.path.getmtime(BIND)
+
+
+def build_bind() -> str:
+    """Build _lmoe_torch.so against the installed torch (located, not imported)."""
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    lib = os.path.join(torch_dir, "lib")
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *(f"-isystem{i}" for i in inc[:4]), f"-I{inc[4]}",
+           BIND_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str | None = None) -> str:
     """Build liblmoe.so (or, with `extra_flags` such as -DLMOE_TRACE, a
     variant written to `out`, compiled in its own build folder)."""
     lib = out or LIB
+    if out is None and (force or _bind_stale()):
+        with cf.ThreadPoolExecutor(max_workers=1) as ex:
+            binding = ex.submit(build_bind)  # beside the kernels
+            built = _build_lib(lib, force, verbose, extra_flags)
+            binding.result()
+        return built
+    return _build_lib(lib, force, verbose, extra_flags)
+
+
+def _build_lib(lib: str, force: bool, verbose: bool, extra_flags) -> str:
     if not force and not extra_flags and not _stale():
         return LIB
     nvcc = _nvcc()

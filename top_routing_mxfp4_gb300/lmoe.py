@@ -8,6 +8,7 @@ been built (there is no fallback path).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -17,8 +18,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # LMOE_LIBRARY selects another build of the same library (e.g. a trace build)
 LIB_PATH = os.environ.get("LMOE_LIBRARY") or os.path.join(_PKG, "liblmoe.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError(f"{LIB_PATH} is missing: build it with `python -c \"import __graft_entry__ as g; g.build()\"` "
+if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(_PKG, "_lmoe_torch.so")):
+    raise ImportError(f"{LIB_PATH} or _lmoe_torch.so is missing: build it with `python -c \"import __graft_entry__ as g; g.build()\"` "
                       "or `python top_routing_mxfp4_gb300/build.py`")
 
 _lib = ctypes.CDLL(LIB_PATH)
@@ -523,66 +524,31 @@ def linear_bf16(x, W, out=None, stream=None):
 # ---- norms, MXFP4 linear and grouped products around the layer ----------------------------
 
 # These calls run on the device of their first tensor and, by default, on that
-# device's current stream.  The checks are written for short calls: a call of a
-# few microseconds on the GPU is launched by a few on the host.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_cur_device = torch._C._cuda_getDevice
-_empty_on = torch.empty
+# device's current stream.  The short ones are bound in C++ (csrc/bind_torch.cpp).
+from . import _lmoe_torch as _fast  # noqa: E402
 
-
-def _bad(t, dtype, shape, name):
-    raise ValueError(f"{name}: expected contiguous CUDA {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)} on "
-                     f"{t.device}, strides {t.stride()}")
+_fast.bind(LmoeError, *(ctypes.cast(f, _vp).value for f in (
+    _rms_norm, _residual_norm, _linear_mx, _linear_mx_ws, _grouped_linear, _grouped_swiglu, _grouped_ws)))
 
 
 def _arg(t, dtype, shape, name, di):
     """Checks one tensor (contiguous, on CUDA device `di`); returns its address."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != di or di < 0 or not t.is_contiguous():
-        if di >= 0 and t.is_cuda and t.get_device() != di:
-            raise ValueError(f"{name}: on {t.device}, the call's first tensor on cuda:{di}")
-        _bad(t, dtype, shape, name)
+    if t.dtype is not dtype or t.shape != shape or di < 0 or t.get_device() != di or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{di}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
 
 
-def _make(make, shape, dtype, x, stream):
-    """A tensor for the call's result or scratch, allocated in the order of the call's stream."""
-    if stream is None:
-        return make(shape, dtype=dtype, device=x.device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=x.device)
-
-
-def _handle(stream, di):
-    if stream is None:
-        return _raw_stream(di)
-    if stream.device.index != di:
-        raise ValueError(f"stream on {stream.device}, tensors on cuda:{di}")
-    return stream.cuda_stream
-
-
-def _run(di, what, fn, *args):
-    """A library call with device `di` current."""
-    if _cur_device() == di:
-        code = fn(*args)
-    else:
-        with torch.cuda.device(di):
-            code = fn(*args)
-    if code != OK:
-        raise LmoeError(code, what)
+def _make(shape, dtype, x, stream):
+    """An uninitialised tensor on x's device, allocated in the order of the call's stream."""
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return torch.empty(shape, dtype=dtype, device=x.device)
 
 
 def _fmt(t, name):
-    if t.dtype is torch.bfloat16:
-        return BF16
-    if t.dtype is torch.float32:
-        return F32
-    raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
-
-
-def _ws_arg(ws, di):
-    if ws.dtype is not torch.uint8 or ws.get_device() != di or not ws.is_contiguous():
-        _bad(ws, torch.uint8, ws.shape, "ws")
-    return ws.data_ptr()
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return BF16 if t.dtype is torch.bfloat16 else F32
 
 
 def _gate(gate, T, H, di):
@@ -596,20 +562,7 @@ def _gate(gate, T, H, di):
 
 def rms_norm(x, w, eps: float = 1e-5, out=None, stream=None):
     """The norm before a block: x [T, H] bf16 or fp32, w fp32 [H] -> bf16 [T, H] (lmoe_rms_norm)."""
-    shape = x.shape
-    T, H = shape
-    di = x.get_device()
-    fmt = _fmt(x, "x")
-    xp = _arg(x, x.dtype, shape, "x", di)
-    wp = _arg(w, torch.float32, (H,), "w", di)
-    sp = _handle(stream, di)
-    if out is None:
-        out = _make(_empty_on, shape, torch.bfloat16, x, stream)
-        op = out.data_ptr()
-    else:
-        op = _arg(out, torch.bfloat16, shape, "out", di)
-    _run(di, "lmoe_rms_norm", _rms_norm, xp, fmt, wp, eps, T, H, op, sp)
-    return out
+    return _fast.rms_norm(x, w, eps, out, stream)
 
 
 def residual_norm(y, res, post_w=None, gate=None, scale: float = 1.0, next_w=None, eps: float = 1e-5, res_out=None,
@@ -618,32 +571,7 @@ def residual_norm(y, res, post_w=None, gate=None, scale: float = 1.0, next_w=Non
     and, with next_w, its norm.  y bf16 [T, H]; res [T, H] bf16 or fp32; gate
     fp32 [H] or [1, H] (per channel), fp32 [T, 1] (per token) or bf16 [T, H].
     Returns (res_out, next_out or None)."""
-    shape = y.shape
-    T, H = shape
-    di = y.get_device()
-    fmt = _fmt(res, "res")
-    yp = _arg(y, torch.bfloat16, shape, "y", di)
-    rp = _arg(res, res.dtype, shape, "res", di)
-    pp = None if post_w is None else _arg(post_w, torch.float32, (H,), "post_w", di)
-    kind, gp = (GATE_NONE, None) if gate is None else _gate(gate, T, H, di)
-    sp = _handle(stream, di)
-    if res_out is None:
-        res_out = _make(_empty_on, shape, res.dtype, y, stream)
-        rop = res_out.data_ptr()
-    else:
-        rop = _arg(res_out, res.dtype, shape, "res_out", di)
-    np_ = nop = None
-    if next_w is not None:
-        np_ = _arg(next_w, torch.float32, (H,), "next_w", di)
-        if next_out is None:
-            next_out = _make(_empty_on, shape, torch.bfloat16, y, stream)
-            nop = next_out.data_ptr()
-        else:
-            nop = _arg(next_out, torch.bfloat16, shape, "next_out", di)
-    elif next_out is not None:
-        raise ValueError("next_out without next_w")
-    _run(di, "lmoe_residual_norm", _residual_norm, yp, rp, fmt, pp, gp, kind, scale, eps, np_, T, H, rop, nop, sp)
-    return res_out, next_out
+    return _fast.residual_norm(y, res, post_w, gate, scale, next_w, eps, res_out, next_out, stream)
 
 
 def linear_mxfp4_workspace_size(rows: int, K: int, N: int) -> int:
@@ -655,67 +583,11 @@ def linear_mxfp4(x, q, s, N: int, out=None, ws=None, stream=None):
     tensor-core layout (q, s of quant_mxfp4 or repack_mxfp4).  `ws`: a zeroed
     workspace of linear_mxfp4_workspace_size bytes, kept by the caller; one is
     made for the call without it."""
-    rows, K = x.shape
-    di = x.get_device()
-    if K <= 0 or K % 32 or N <= 0:
-        raise ValueError(f"weights [{N}, {K}]: K must be a multiple of 32")
-    KC = (K + 127) >> 7
-    xp = _arg(x, torch.bfloat16, (rows, K), "x", di)
-    qp = _arg(q, torch.uint8, (N * KC * 64,), "q", di)
-    spp = _arg(s, torch.uint8, (((N + 127) >> 7) * KC * 512,), "s", di)
-    sp = _handle(stream, di)
-    if out is None:
-        out = _make(_empty_on, (rows, N), torch.bfloat16, x, stream)
-        op = out.data_ptr()
-    else:
-        op = _arg(out, torch.bfloat16, (rows, N), "out", di)
-    if ws is None:
-        ws = _make(torch.zeros, (linear_mxfp4_workspace_size(rows, K, N) or 256,), torch.uint8, x, stream)
-    _run(di, "lmoe_linear_mxfp4", _linear_mx, xp, qp, spp, rows, K, N, op, _ws_arg(ws, di), ws.numel(), sp)
-    return out
+    return _fast.linear_mxfp4(x, q, s, N, out, ws, stream)
 
 
 def grouped_workspace_size() -> int:
     return int(_grouped_ws())
-
-
-def _grouped_call(name, x, W, Wu, offsets, perm, k, gather, row_w, out, out_dtype, ws, stream):
-    E, N, K = W.shape
-    di = x.get_device()
-    rows = x.shape[0]
-    xp = _arg(x, torch.bfloat16, (rows, K), "x", di)
-    wp = _arg(W, torch.bfloat16, (E, N, K), "W", di)
-    offp = _arg(offsets, torch.int32, (E + 1,), "offsets", di)
-    if perm is None:
-        P, pp, ga = rows, None, 1 if gather else 0
-    else:
-        P = perm.shape[0]
-        pp, ga = _arg(perm, torch.int32, (P,), "perm", di), 0 if gather is False else 1
-    sp = _handle(stream, di)
-    if out is None:
-        out = _make(_empty_on, (P, N), out_dtype, x, stream)
-        fmt, op = _fmt(out, "out"), out.data_ptr()
-    else:
-        fmt = _fmt(out, "out")
-        op = _arg(out, out.dtype, (P, N), "out", di)
-    if ws is None:
-        ws = _make(torch.zeros, (256,), torch.uint8, x, stream)
-    G = Groups(offp, pp, P, E, k)
-    if Wu is None:
-        rp = None
-        if row_w is not None:
-            if row_w.numel() != P:
-                raise ValueError(f"row_w: {P} values expected, got {row_w.numel()}")
-            rp = _arg(row_w, torch.float32, row_w.shape, "row_w", di)
-        _run(di, name, _grouped_linear, xp, rows, wp, ctypes.byref(G), ga, rp, K, N, fmt, op, _ws_arg(ws, di),
-             ws.numel(), sp)
-    else:
-        if fmt != BF16:
-            raise ValueError("out: expected bfloat16")
-        up = _arg(Wu, torch.bfloat16, (E, N, K), "Wu", di)
-        _run(di, name, _grouped_swiglu, xp, rows, wp, up, ctypes.byref(G), ga, K, N, op, _ws_arg(ws, di), ws.numel(),
-             sp)
-    return out
 
 
 def grouped_linear_bf16(x, W, offsets, perm=None, k: int = 1, gather=None, row_w=None, out=None, ws=None, stream=None):
@@ -725,16 +597,16 @@ def grouped_linear_bf16(x, W, offsets, perm=None, k: int = 1, gather=None, row_w
     [P, N].  With row_w (fp32, P values in pair order): fp32 [P, N], row q
     times row_w[perm[q]].  `out` may be given in either type; rows in no group
     are not written.  `ws`: a zeroed workspace kept by the caller."""
-    return _grouped_call("lmoe_grouped_linear_bf16", x, W, None, offsets, perm, k, gather, row_w, out,
-                         torch.bfloat16 if row_w is None else torch.float32, ws, stream)
+    return _fast.grouped(x, W, None, offsets, perm, k, gather, row_w, out, ws, stream)
 
 
 def grouped_swiglu_bf16(x, Wg, Wu, offsets, perm=None, k: int = 1, gather=None, out=None, ws=None, stream=None):
     """bf16 [P, I] rows silu(x Wg[e]^T) * (x Wu[e]^T), both products and the
     gating in one kernel (lmoe_grouped_swiglu_bf16); arguments as for
     grouped_linear_bf16."""
-    return _grouped_call("lmoe_grouped_swiglu_bf16", x, Wg, Wu, offsets, perm, k, gather, None, out, torch.bfloat16,
-                         ws, stream)
+    if Wu is None:
+        raise ValueError("Wu: expected a tensor")
+    return _fast.grouped(x, Wg, Wu, offsets, perm, k, gather, None, out, ws, stream)
 
 
 class LinearMxfp4:
@@ -817,21 +689,24 @@ class ResidualBlock:
                                 vec(self.post_w, "post_w"), gp, kind, self.scale, self.eps, vec(next_w, "next_w"))
         if x_n is None and self.pre_w is None:
             raise ValueError("neither x_n nor pre_w")
-        sp = _handle(stream, di)
-        res_out = _make(_empty_on, (T, H), res.dtype, res, stream) if res_out is None else res_out
+        if stream is not None and stream.device.index != di:
+            raise ValueError(f"stream on {stream.device}, tensors on cuda:{di}")
+        sp = (torch.cuda.current_stream(di) if stream is None else stream).cuda_stream
+        res_out = _make((T, H), res.dtype, res, stream) if res_out is None else res_out
         rop = _arg(res_out, res.dtype, (T, H), "res_out", di)
         if next_w is not None and next_out is None:
-            next_out = _make(_empty_on, (T, H), torch.bfloat16, res, stream)
+            next_out = _make((T, H), torch.bfloat16, res, stream)
         nop = None if next_out is None else _arg(next_out, torch.bfloat16, (T, H), "next_out", di)
         layer, bank = self.layer, self.layer.bank
         D = dims(T, bank.d, bank.E, layer.k, bank.I, layer.act)
         need = int(_res_block_ws(ctypes.byref(D), H))
         if self._ws is None or self._ws.numel() < need:
-            self._ws = _make(_empty_on, (max(need, 256),), torch.uint8, res, stream)
+            self._ws = _make((max(need, 256),), torch.uint8, res, stream)
         W = bank.struct()
-        _run(di, "lmoe_forward_residual_block", _res_block, rp, fmt, xp, ctypes.byref(B), layer.Wr3.data_ptr(),
-             None if layer.bias is None else layer.bias.data_ptr(), ctypes.byref(W), ctypes.byref(D), H, rop, nop,
-             self._ws.data_ptr(), self._ws.numel(), sp)
+        with torch.cuda.device(di):
+            _check(_res_block(rp, fmt, xp, ctypes.byref(B), layer.Wr3.data_ptr(),
+                              None if layer.bias is None else layer.bias.data_ptr(), ctypes.byref(W), ctypes.byref(D),
+                              H, rop, nop, self._ws.data_ptr(), self._ws.numel(), sp), "lmoe_forward_residual_block")
         return res_out, next_out
 
     def device_status(self) -> int:
