@@ -331,6 +331,38 @@ def test_grouped_swiglu(cuda_lib, name, K, I):
     assert cuda_lib.last_device_status(ws) == cuda_lib.OK
 
 
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("swiglu", [True, False])
+def test_grouped_pairs_with_short_tails(cuda_lib, gather, swiglu):
+    """Large groups whose last row tile holds 1 to 33 rows, so that the second CTA
+    of a pair has none of them, over many items and several runs: every run the
+    same, and right."""
+    counts = [257, 513, 260, 769, 272, 273, 288, 289, 512, 1025, 258, 261, 0, 256, 521, 264]
+    g = gen(31)
+    off, perm, P = make_groups(counts, 1, g)
+    K, N = 192, 1000
+    x = randn(g, P, K)
+    W, V = randn(g, len(counts), N, K, scale=K ** -0.5), randn(g, len(counts), N, K, scale=K ** -0.5)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    pm = perm if gather else None
+    call = (lambda: cuda_lib.grouped_swiglu_bf16(x, W, V, off, pm, 1, ws=ws)) if swiglu else \
+        (lambda: cuda_lib.grouped_linear_bf16(x, W, off, pm, 1, ws=ws))
+    out = call()
+    for _ in range(20):
+        assert torch.equal(call(), out)
+    assert cuda_lib.last_device_status(ws) == cuda_lib.OK
+    src = perm.long() if gather else torch.arange(P, device=DEV)
+    a, ma = grouped_ref(x, W, off, src)
+    da = (K + 2) * U * ma
+    if not swiglu:
+        return within(out, a, a.abs() * HALF + da * (1 + HALF))
+    b, mb = grouped_ref(x, V, off, src)
+    db = (K + 2) * U * mb
+    s = a * torch.sigmoid(a)
+    tol = 1.1 * da * (b.abs() + db) + (s.abs() + 1.1 * da) * db + 16 * U * (s * b).abs()
+    within(out, s * b, (s * b).abs() * HALF + tol * (1 + HALF) + 1e-300)
+
+
 def test_grouped_many_experts(cuda_lib):
     g = gen(3)
     E, T, k, K, N = 896, 64, 16, 192, 144

@@ -30,7 +30,6 @@
 
 #include "cluster_sum.cuh"
 #include "lmoe_internal.cuh"
-#include "schedule.cuh"
 #include "tc_ptx.cuh"
 
 namespace lmoe {
@@ -42,14 +41,14 @@ constexpr uint32_t A_TILE = 128 * 128;  // 128 rows x 64 bf16
 
 template <int NT, bool SWIGLU, bool GATHER, int KS>
 struct GCfg {
-    // Warps that bring B.  A warp issues an asynchronous copy only every 75
-    // cycles or so, however many lanes ask: eight warps for the 64 gather4
-    // copies of a 256-row chunk (a gate/up pass of 8192 tokens over 896
-    // experts took 3.78 ms with one, 2.12 ms with two).
-    static constexpr int BW = !GATHER ? 1 : NT <= 32 ? 1 : NT == 64 ? 4 : 8;
-    static constexpr int THREADS = BW > 1 ? 512 : 256;
+    // Warps that bring B: one warp's gather4 copies, issued one after another,
+    // held the chunks up (a gate/up pass of 8192 tokens over 896 experts took
+    // 3.78 ms with one, 2.12 ms with two).
+    static constexpr int BW = !GATHER || NT <= 32 ? 1 : NT == 64 ? 4 : 8;
     static constexpr int A2 = 6 + BW;  // the second A warp (SWIGLU: the up rows)
-    static_assert(A2 < THREADS / 32, "warps");
+    static constexpr int FEED = A2 + (SWIGLU ? 1 : 0);  // the warp that hands out items
+    static constexpr int THREADS = 32 * (FEED + 1);
+    static_assert(THREADS * 8 >= 2048, "the scan of the offsets takes 8 experts a thread");
     // The largest row tile is shared by a pair of CTAs (cta_group::2): 256
     // weight rows, each CTA bringing 128 of them and half of B.
     static constexpr bool PAIR = NT == 256;
@@ -61,6 +60,8 @@ struct GCfg {
     static constexpr uint32_t RED = KS > 1 ? ClusterSum::red_bytes(NT) : 0;
     static constexpr int S_RAW = int((200 * 1024 - RED) / STAGE);
     static constexpr int S = S_RAW > 10 ? 10 : S_RAW;
+    static constexpr int Q = 4;    // items handed out ahead
+    static constexpr int CONSUMERS = (FEED + (PAIR ? FEED - 1 : 0));  // warps that take them (a pair's second MMA warp idles)
     static constexpr int ACC = 2;  // accumulators: an item's epilogue overlaps the next one's MMAs
     static constexpr uint32_t TMEM_COLS = ACC * NT < 32 ? 32 : ACC * NT;
 };
@@ -68,9 +69,11 @@ struct GCfg {
 struct GArgs {
     const int32_t *offsets, *perm;
     const float *row_w;
-    int64_t P, x_rows;
+    const uint8_t *x;  // gathered rows' bytes
+    int64_t P, x_rows, x_bytes;
     int E, k, N, MT, KC;
     int max_items;  // no valid groups have more
+    int32_t *counter;  // items handed out so far (zero at the start); null: every CTA takes each grid-th
     int out_f32;
     void *out;
     int32_t *status;
@@ -126,11 +129,13 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     uint64_t *acc_empty = acc_full + C::ACC;
     uint64_t *drain = acc_empty + C::ACC;
     uint64_t *red_full = drain + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(red_full + 1);
+    uint64_t *item_full = red_full + 1;
+    uint64_t *item_empty = item_full + C::Q;
+    int32_t *s_item = reinterpret_cast<int32_t *>(item_empty + C::Q);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_item + C::Q);
     int32_t *warp_tot = reinterpret_cast<int32_t *>(tmem_slot + 2);
-    int32_t *s_off = warp_tot + 16;
+    int32_t *s_off = warp_tot + 32;
     int32_t *s_tiles = s_off + p.E + 1;
-    int32_t *s_cnt = s_tiles + p.E + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -144,6 +149,10 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         }
         mbar_init(drain, 1);
         mbar_init(red_full, 1);
+        for (int i = 0; i < C::Q; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], C::CONSUMERS);
+        }
         mbar_init_fence();
     }
     if (warp == 0 && lane == 0) {
@@ -153,20 +162,53 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     if (warp == 6 && lane == 0) prefetch_tensormap(&tmB);
     if (warp == 1) PAIR ? tmem_alloc_pair(tmem_slot, C::TMEM_COLS) : tmem_alloc(tmem_slot, C::TMEM_COLS);
     pdl_enter();
-    // row tiles per expert, scanned; a group that breaks 0 <= o0 <= o1 <= P is empty and reported
-    bool bad = false;
-    for (int e = threadIdx.x; e < p.E; e += THREADS) {
-        const int o0 = __ldg(p.offsets + e), o1 = __ldg(p.offsets + e + 1);
-        const bool ok = o0 >= 0 && o0 <= o1 && o1 <= p.P;
-        bad |= !ok;
-        s_off[e] = o0;
-        if (e == p.E - 1) s_off[p.E] = o1;
-        s_cnt[e] = ok ? (o1 - o0 + NT - 1) / NT : 0;
+    if (GATHER) {
+        // few rows: what the chain offsets -> perm -> x waits for next, on its way to L2
+        const int64_t line = int64_t(blockIdx.x) * THREADS + threadIdx.x;
+        if (p.P <= 32 * THREADS && threadIdx.x * 32 < p.P) prefetch_l2(p.perm + threadIdx.x * 32);
+        if (p.x_bytes <= 1 << 20 && line * 128 < p.x_bytes) prefetch_l2(p.x + line * 128);
     }
-    tc_fence_before();
-    bad = __syncthreads_or(bad);
-    tc_fence_after();
-    block_scan<THREADS>(s_cnt, p.E, s_tiles, warp_tot);
+    // Row tiles per expert, scanned, 8 experts a thread; a group that breaks
+    // 0 <= o0 <= o1 <= P is empty and reported.
+    bool bad = false;
+    {
+        const int e0 = threadIdx.x * 8;
+        int o[9], cnt[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 9; ++j) o[j] = e0 + j <= p.E ? __ldg(p.offsets + e0 + j) : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = e0 + j < p.E, ok = o[j] >= 0 && o[j] <= o[j + 1] && o[j + 1] <= p.P;
+            bad |= in && !ok;
+            cnt[j] = in && ok ? (o[j + 1] - o[j] + NT - 1) / NT : 0;
+            sum += cnt[j];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        if (lane == 31) warp_tot[warp] = incl;
+        tc_fence_before();
+        bad = __syncthreads_or(bad);
+        tc_fence_after();
+        int base = lane < warp ? warp_tot[lane] : 0;  // at most 16 warps
+        base = __reduce_add_sync(0xFFFFFFFFu, base) + incl - sum;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (e0 + j <= p.E) {
+                s_off[e0 + j] = o[j];
+                s_tiles[e0 + j] = base;
+            }
+            base += cnt[j];
+        }
+        if (e0 + 8 == p.E && p.E == 8 * THREADS) {  // the one entry beyond the last thread's eight
+            s_off[p.E] = o[8];
+            s_tiles[p.E] = base;
+        }
+        __syncthreads();
+    }
     if (C::CL > 1) cluster_sync();  // the cluster's barriers are initialised
     const uint32_t tmem = *tmem_slot;
     // Around a bad group others may overlap, so that there are more tiles than
@@ -183,6 +225,35 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     // this rank's K chunks
     const int k0 = KS > 1 ? rank * p.KC / KS : 0, k1 = KS > 1 ? (rank + 1) * p.KC / KS : p.KC;
     Walk<NT> walk{s_tiles, s_off, p.E, p.MT};
+    // This CTA's items, in order, -1 after the last; every lane of a warp calls
+    // it.  Many items are handed out as CTAs come free: SMs do not all stream
+    // equally fast, and groups differ (a weighted down projection of 64 tokens
+    // over 896 experts: its CTAs ended between 351 and 421 us with each
+    // grid-th item).
+    int feed_q = 0, feed_next = first;
+    uint32_t feed_phase = 0;
+    auto next_item = [&]() -> int {
+        if (!p.counter) {
+            const int it = feed_next;
+            feed_next += step;
+            return it < total ? it : -1;
+        }
+        const bool ok = PAIR ? mbar_wait_cluster(&item_full[feed_q], feed_phase, p.limit)
+                             : mbar_wait(&item_full[feed_q], feed_phase, p.limit);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+            if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+            return -1;
+        }
+        const int it = reinterpret_cast<volatile int32_t *>(s_item)[feed_q];
+        __syncwarp();
+        if (lane == 0)
+            PAIR ? cluster_arrive(cluster_map(smem_u32(&item_empty[feed_q]), 0)) : mbar_arrive(&item_empty[feed_q]);
+        if (++feed_q == C::Q) {
+            feed_q = 0;
+            feed_phase ^= 1;
+        }
+        return it;
+    };
 
     // Copies still in flight after a timeout land before the CTA ends (bounded).
     // (A pair's copies all count in on the leader's barriers.)
@@ -200,21 +271,25 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         int stage = 0, fills = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int it = first; it < total && ok; it += step) {
+        bool at_start = true;  // (the failure-path test withholds a CTA's first weight copy)
+        for (int it; ok && (it = next_item()) >= 0; at_start = false) {
             const GItem w = walk.at(it);
-            // this CTA's rows of the tile: all, or a pair's half of them (rounded to whole MMA columns)
+            // This CTA's rows of the tile: all, or a pair's half of them (rounded to whole
+            // MMA columns).  A pair's second CTA does not arrive on the stage's barrier, so
+            // each of its warps has to have a copy in every chunk, if only of padding:
+            // one without could fall a whole turn of the ring behind the MMAs.
             const int half = PAIR ? (w.nv + 31) / 32 * 16 : 0;
-            const int b0 = PAIR ? rank * half : 0, bn = PAIR ? max(0, min(half, w.nv - b0)) : w.nv;
-            const int copies = GATHER ? (bn + 3) / 4 : (bn + C::BOX - 1) / C::BOX;  // of B a chunk, all warps
+            const int b0 = PAIR ? rank * half : 0;
+            const int bn = PAIR ? max(0, min(half, w.nv - b0)) : w.nv;  // rows of the group among them
+            const int copies = GATHER ? (PAIR ? max(half / 4, C::BW) : (bn + 3) / 4)
+                                      : ((PAIR ? half : bn) + C::BOX - 1) / C::BOX;
+            static_assert(!PAIR || C::B_TILE >= C::BW * 512, "room for a copy of each warp");
             const int mtile = PAIR ? 2 * w.m + rank : w.m;  // this CTA's 128 weight rows
             const int mine = copies > bw ? (copies - bw + C::BW - 1) / C::BW : 0;
             // bytes this warp's barrier arrival announces: a pair's leader those of both CTAs (an
             // arrival from the other CTA, with the release it needs, would take over 1000 cycles a stage)
-            const int peer_n = PAIR ? max(0, w.nv - half) : 0;
-            const int peer = GATHER ? (peer_n + 3) / 4 : (peer_n + C::BOX - 1) / C::BOX;
-            const uint32_t announce =
-                isA ? (SWIGLU ? A_TILE / 2 : A_TILE) * (PAIR ? 2 : 1)
-                    : uint32_t(mine + (peer > bw ? (peer - bw + C::BW - 1) / C::BW : 0)) * (GATHER ? 512u : C::BOX * 128u);
+            const uint32_t announce = (isA ? (SWIGLU ? A_TILE / 2 : A_TILE) : uint32_t(mine) * (GATHER ? 512u : C::BOX * 128u)) *
+                                      (PAIR ? 2 : 1);
             if (GATHER && !isA) {
                 __syncwarp();
                 for (int i = lane; i < mine; i += 32) {
@@ -253,7 +328,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     PAIR ? tma_load_2d_pair(dst, tm, kc * 64, y, bar) : tma_load_2d(dst, tm, kc * 64, y, &full[stage]);
                 };
                 if (isA) {
-                    if (elect_one() && !(p.stall && it == first && kc == k0)) {
+                    if (elect_one() && !(p.stall && at_start && kc == k0)) {
                         if (SWIGLU) {
                             expect();
                             const CUtensorMap *tm = warp == 0 ? &tmA : &tmA2;
@@ -293,7 +368,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
-        for (int it = first; it < total && ok; it += step) {
+        for (int it; ok && (it = next_item()) >= 0;) {
             const GItem w = walk.at(it);
             const uint32_t id =
                 PAIR ? idesc_bf16_pair(uint32_t((w.nv + 31) & ~31)) : idesc_bf16(uint32_t((w.nv + 15) & ~15));
@@ -343,7 +418,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         const int q = warp & 3;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int it = first; it < total; it += step) {
+        for (int it; (it = next_item()) >= 0;) {
             const GItem w = walk.at(it);
             const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.limit);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -425,6 +500,31 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 acc_phase ^= 1;
             }
         }
+    } else if (warp == C::FEED && p.counter && rank == 0) {
+        // ---------------- item feed (a pair's: the leader's, for both CTAs) ----------------
+        int q = 0;
+        uint32_t phase = 0;
+        for (bool more = true; more;) {
+            const bool ok = mbar_wait(&item_empty[q], phase ^ 1, p.limit);
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                break;
+            }
+            int it = 0;
+            if (lane == 0) {
+                it = atomicAdd(p.counter, 1);
+                it = it < total ? it : -1;
+                s_item[q] = it;
+                if (PAIR) cluster_store_i32(cluster_map(smem_u32(&s_item[q]), 1), it);
+                if (PAIR) cluster_arrive(cluster_map(smem_u32(&item_full[q]), 1));
+                mbar_arrive(&item_full[q]);
+            }
+            more = __shfl_sync(0xFFFFFFFFu, it, 0) >= 0;
+            if (++q == C::Q) {
+                q = 0;
+                phase ^= 1;
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -468,7 +568,7 @@ int sm_count()
 }
 
 template <int NT, bool SWIGLU, bool GATHER, int KS>
-cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms, cudaStream_t st)
+cudaError_t launch(const GroupedArgs &a, GArgs g, int64_t items, int sms, cudaStream_t st)
 {
     using C = GCfg<NT, SWIGLU, GATHER, KS>;
     CUtensorMap ma, ma2, mb;
@@ -476,13 +576,21 @@ cudaError_t launch(const GroupedArgs &a, const GArgs &g, int64_t items, int sms,
         !bf16_map(&ma2, SWIGLU ? a.W2 : a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
         !bf16_map(&mb, a.x, a.K, a.x_rows, GATHER ? 1 : C::BOX))
         return cudaErrorInvalidValue;
-    const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::RED + (2 * C::S + 2 * C::ACC + 2) * 8 +
-                        16 + 64 + size_t(3 * a.E + 2) * 4;
+    const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::RED + (2 * C::S + 2 * C::ACC + 2 + 2 * C::Q) * 8 +
+                        C::Q * 4 + 8 + 128 + size_t(2 * a.E + 2) * 4;
     auto *kern = k_grouped<NT, SWIGLU, GATHER, KS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     const int64_t slots = sms / C::CL;
     const unsigned grid = unsigned((items < slots ? items : slots) * C::CL);
+    // At four items a CTA and more they are handed out by a counter (cleared
+    // here; it costs a call a microsecond or two).
+    if (KS == 1 && items >= 4 * slots) {
+        e = cudaMemsetAsync(g.counter, 0, sizeof(int32_t), st);
+        if (e != cudaSuccess) return e;
+    } else {
+        g.counter = nullptr;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(C::THREADS);
@@ -519,6 +627,8 @@ cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st)
     g.row_w = a.row_w;
     g.P = a.P;
     g.x_rows = a.x_rows;
+    g.x = reinterpret_cast<const uint8_t *>(a.x);
+    g.x_bytes = a.x_rows * a.K * 2;
     g.E = a.E;
     g.k = a.k;
     g.N = a.N;
@@ -527,6 +637,7 @@ cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st)
     g.out_f32 = a.out_fmt == LMOE_F32;
     g.out = a.out;
     g.status = a.status;
+    g.counter = a.status + 1;  // the status word's neighbour in the workspace
     g.limit = a.wait.limit > 0 ? a.wait.limit : 4000000000LL;  // about 2 s of SM clocks
     g.stall = a.wait.stall_first_fill;
     // Row tile: the smallest that holds a group of average size and a quarter

@@ -261,6 +261,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t *r)
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ---- pairs of CTAs (cta_group::2): one MMA over both CTAs' shared and tensor memory -------
 // The leader (rank 0 of the pair) issues; operands lie at the same
 // shared-memory addresses in both CTAs, each with its own 128 rows of A and
@@ -312,11 +314,33 @@ __device__ __forceinline__ void tma_gather4_pair(void *dst, const CUtensorMap *m
         "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar_addr)
         : "memory");
 }
+__device__ __forceinline__ void cluster_store_i32(uint32_t addr, int32_t v)
+{
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 // Arrival (release at cluster scope) on a barrier of either CTA.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar_addr)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
 }
+// mbar_wait with acquire at cluster scope: sees what other CTAs' threads stored
+// before they arrived (cluster_arrive).
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, long long limit)
+{
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 "
+            "%0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (clock64() - t0 > limit) return false;
+    }
+}
+
 // ---- thread-block clusters ----------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank()
 {
