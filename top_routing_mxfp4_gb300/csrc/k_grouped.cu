@@ -420,6 +420,22 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         uint32_t acc_phase = 0;
         for (int it; (it = next_item()) >= 0;) {
             const GItem w = walk.at(it);
+            // lane l: the weights of rows l, l + 32, .. of the tile, requested before its products are done
+            [[maybe_unused]] float rw[NT > 32 ? NT / 32 : 1];
+            if (!SWIGLU && p.row_w) {
+#pragma unroll
+                for (int i = 0; i < (NT > 32 ? NT / 32 : 1); ++i) {
+                    const int r = 32 * i + lane;
+                    rw[i] = 0.f;
+                    if (r < w.nv) {
+                        const int64_t pr = p.perm ? __ldg(p.perm + w.row0 + r) : w.row0 + r;
+                        if (pr >= 0 && pr < p.P)
+                            rw[i] = __ldg(p.row_w + pr);
+                        else
+                            set_status(p.status, LMOE_ERR_DEVICE_CHECK);
+                    }
+                }
+            }
             const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.limit);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
@@ -440,16 +456,11 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                         y[j] = __fdividef(y[j], 1.f + expf(-y[j])) * u;
                     }
                 } else if (p.row_w) {
-                    float rw = 1.f;  // lane j: the weight of row c0 + j
-                    if (lane < 16 && c0 + lane < c1) {
-                        const int64_t pr = p.perm ? __ldg(p.perm + w.row0 + c0 + lane) : w.row0 + c0 + lane;
-                        if (pr >= 0 && pr < p.P)
-                            rw = __ldg(p.row_w + pr);
-                        else
-                            set_status(p.status, LMOE_ERR_DEVICE_CHECK);
-                    }
+                    float v = rw[0];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] *= __shfl_sync(0xFFFFFFFFu, rw, j);
+                    for (int i = 1; i < (NT > 32 ? NT / 32 : 1); ++i) v = c0 / 32 == i ? rw[i] : v;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] *= __shfl_sync(0xFFFFFFFFu, v, (c0 & 31) + j);
                 }
                 if (!mine) return;
                 const int64_t o = int64_t(w.row0 + c0) * p.N + n;
