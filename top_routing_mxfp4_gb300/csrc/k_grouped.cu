@@ -247,7 +247,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         const int it = reinterpret_cast<volatile int32_t *>(s_item)[feed_q];
         __syncwarp();
         if (lane == 0)
-            PAIR ? cluster_arrive(cluster_map(smem_u32(&item_empty[feed_q]), 0)) : mbar_arrive(&item_empty[feed_q]);
+            PAIR ? cluster_arrive_read(cluster_map(smem_u32(&item_empty[feed_q]), 0)) : mbar_arrive(&item_empty[feed_q]);
         if (++feed_q == C::Q) {
             feed_q = 0;
             feed_phase ^= 1;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 }
             }
             tc_fence_before();
-            PAIR ? cluster_arrive(cluster_map(smem_u32(&acc_empty[acc]), 0)) : mbar_arrive(&acc_empty[acc]);
+            PAIR ? cluster_arrive_read(cluster_map(smem_u32(&acc_empty[acc]), 0)) : mbar_arrive(&acc_empty[acc]);
             if (++acc == C::ACC) {
                 acc = 0;
                 acc_phase ^= 1;

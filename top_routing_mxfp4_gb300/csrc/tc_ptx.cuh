@@ -318,6 +318,14 @@ __device__ __forceinline__ void cluster_store_i32(uint32_t addr, int32_t v)
 {
     asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Arrival on a barrier of either CTA that publishes no memory: it says that this
+// thread has read what it waited for (tensor memory after its wait, a shared
+// word).  Without the cluster-scope release it does not wait for the thread's
+// global stores, which took several microseconds an item.
+__device__ __forceinline__ void cluster_arrive_read(uint32_t bar_addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
+}
 // Arrival (release at cluster scope) on a barrier of either CTA.
 __device__ __forceinline__ void cluster_arrive(uint32_t bar_addr)
 {
