@@ -18,8 +18,8 @@
 // search.
 //
 // Persistent CTA: warp 0 streams A (TMA; gated: another warp the up rows), warp
-// 1 issues the MMAs, warps 2-5 are the epilogue (TMEM lane quarter = warp % 4),
-// warps 6.. bring B: boxes of 16 or 32 rows where a group's rows are
+// 1 issues the MMAs, the next 4 or 8 are the epilogue (TMEM lane quarter =
+// warp % 4), then those that bring B: boxes of 16 or 32 rows where a group's rows are
 // consecutive, or gather4 copies of four rows each where they come through the
 // permutation.
 // Where the host can tell that the items cannot fill the GPU, a cluster of KS
@@ -45,7 +45,11 @@ struct GCfg {
     // held the chunks up (a gate/up pass of 8192 tokens over 896 experts took
     // 3.78 ms with one, 2.12 ms with two).
     static constexpr int BW = !GATHER || NT <= 32 ? 1 : NT == 64 ? 4 : 8;
-    static constexpr int A2 = 6 + BW;  // the second A warp (SWIGLU: the up rows)
+    // Epilogue warps, one or two per TMEM lane quarter (two take 16-column chunks
+    // in turn): with four, short reductions (K = 512) waited for the epilogue.
+    static constexpr int EW = NT >= 128 ? 8 : 4;
+    static constexpr int B0 = 2 + EW;  // the first warp that brings B
+    static constexpr int A2 = B0 + BW;  // the second A warp (SWIGLU: the up rows)
     static constexpr int FEED = A2 + (SWIGLU ? 1 : 0);  // the warp that hands out items
     static constexpr int THREADS = 32 * (FEED + 1);
     static_assert(THREADS * 8 >= 2048, "the scan of the offsets takes 8 experts a thread");
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         }
         for (int a = 0; a < C::ACC; ++a) {
             mbar_init(&acc_full[a], 1);
-            mbar_init(&acc_empty[a], PAIR ? 256 : 128);
+            mbar_init(&acc_empty[a], 32 * C::EW * (PAIR ? 2 : 1));
         }
         mbar_init(drain, 1);
         mbar_init(red_full, 1);
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         prefetch_tensormap(&tmA);
         if (SWIGLU) prefetch_tensormap(&tmA2);
     }
-    if (warp == 6 && lane == 0) prefetch_tensormap(&tmB);
+    if (warp == C::B0 && lane == 0) prefetch_tensormap(&tmB);
     if (warp == 1) PAIR ? tmem_alloc_pair(tmem_slot, C::TMEM_COLS) : tmem_alloc(tmem_slot, C::TMEM_COLS);
     pdl_enter();
     if (GATHER) {
@@ -262,11 +266,11 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
     };
 
-    if (warp == 0 || (warp >= 6 && warp < C::A2 + (SWIGLU ? 1 : 0))) {
-        // ---------------- producers: A (warp 0 and, gated, warp A2), B (warps 6 ..) ----------------
+    if (warp == 0 || (warp >= C::B0 && warp < C::FEED)) {
+        // ---------------- producers: A (warp 0 and, gated, warp A2), B (warps B0 ..) ----------------
         __shared__ int4 s_ids[GATHER ? C::BW : 1][C::COPIES];  // the rows of the warps' gather4 copies
         const bool isA = warp == 0 || warp == C::A2;
-        const int bw = warp - 6;  // B: this warp's copies are bw, bw + BW, ...
+        const int bw = warp - C::B0;  // B: this warp's copies are bw, bw + BW, ...
         [[maybe_unused]] int4 *ids = s_ids[GATHER && !isA ? bw : 0];
         int stage = 0, fills = 0;
         uint32_t phase = 0;
@@ -413,18 +417,22 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
             __syncwarp();
         }
-    } else if (warp >= 2 && warp < 6) {
+    } else if (warp >= 2 && warp < C::B0) {
         // ---------------- epilogue ----------------
         const int q = warp & 3;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int it; (it = next_item()) >= 0;) {
-            const GItem w = walk.at(it);
-            // lane l: the weights of rows l, l + 32, .. of the tile, requested before its products are done
-            [[maybe_unused]] float rw[NT > 32 ? NT / 32 : 1];
+        const int half = (warp - 2) >> 2;  // which of the quarter's warps
+        // lane l: the weights of rows l, l + 32, .. of an item's tile.  They are requested
+        // an item ahead: under the output's traffic a load takes several microseconds.
+        constexpr int NW = NT > 32 ? NT / 32 : 1;
+        auto take = [&](GItem &w, float (&rw)[NW]) -> bool {
+            const int it = next_item();
+            if (it < 0) return false;
+            w = walk.at(it);
             if (!SWIGLU && p.row_w) {
 #pragma unroll
-                for (int i = 0; i < (NT > 32 ? NT / 32 : 1); ++i) {
+                for (int i = 0; i < NW; ++i) {
                     const int r = 32 * i + lane;
                     rw[i] = 0.f;
                     if (r < w.nv) {
@@ -436,10 +444,13 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     }
                 }
             }
+            return true;
+        };
+        auto process = [&](const GItem &w, const float (&rw)[NW]) -> bool {
             const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.limit);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-                break;
+                return false;
             }
             tc_fence_after();
             const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
@@ -458,7 +469,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 } else if (p.row_w) {
                     float v = rw[0];
 #pragma unroll
-                    for (int i = 1; i < (NT > 32 ? NT / 32 : 1); ++i) v = c0 / 32 == i ? rw[i] : v;
+                    for (int i = 1; i < NW; ++i) v = c0 / 32 == i ? rw[i] : v;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) y[j] *= __shfl_sync(0xFFFFFFFFu, v, (c0 & 31) + j);
                 }
@@ -487,14 +498,14 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 const bool in = cs.exchange(p.limit);
                 if (!__all_sync(0xFFFFFFFFu, in)) {
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-                    break;
+                    return false;
                 }
                 const int c0 = cs.begin(rank), c1 = cs.begin(rank + 1);  // this rank's rows
                 float y[16];
                 cs.sum(c0, 32 * q + lane, y);
                 finish(c0, c1, y);
             } else {
-                for (int c0 = 0; c0 < w.nv; c0 += 16) {
+                for (int c0 = 16 * half; c0 < w.nv; c0 += 4 * C::EW) {
                     uint32_t v[16];
                     tmem_ld16(tb + c0, v);
                     tmem_ld_wait();
@@ -510,6 +521,15 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 acc = 0;
                 acc_phase ^= 1;
             }
+            return true;
+        };
+        GItem wa, wb;
+        float ra[NW], rb[NW];
+        for (bool more = take(wa, ra); more;) {
+            more = take(wb, rb);
+            if (!process(wa, ra) || !more) break;
+            more = take(wa, ra);
+            if (!process(wb, rb)) break;
         }
     } else if (warp == C::FEED && p.counter && rank == 0) {
         // ---------------- item feed (a pair's: the leader's, for both CTAs) ----------------
