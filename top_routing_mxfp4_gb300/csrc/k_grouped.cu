@@ -423,28 +423,29 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         const int half = (warp - 2) >> 2;  // which of the quarter's warps
-        // lane l: the weights of rows l, l + 32, .. of an item's tile.  They are requested
-        // an item ahead: under the output's traffic a load takes several microseconds.
+        // lane l: pairs and weights of rows l, l + 32, .. of an item's tile.  Under the
+        // output's traffic a load takes several microseconds, so an item's pairs are
+        // requested two items ahead and its weights one.
         constexpr int NW = NT > 32 ? NT / 32 : 1;
-        auto take = [&](GItem &w, float (&rw)[NW]) -> bool {
+        const bool weighted = !SWIGLU && p.row_w;
+        auto take = [&](GItem &w, int (&pr)[NW]) -> bool {
             const int it = next_item();
             if (it < 0) return false;
             w = walk.at(it);
-            if (!SWIGLU && p.row_w) {
+            if (weighted && p.perm)
 #pragma unroll
-                for (int i = 0; i < NW; ++i) {
-                    const int r = 32 * i + lane;
-                    rw[i] = 0.f;
-                    if (r < w.nv) {
-                        const int64_t pr = p.perm ? __ldg(p.perm + w.row0 + r) : w.row0 + r;
-                        if (pr >= 0 && pr < p.P)
-                            rw[i] = __ldg(p.row_w + pr);
-                        else
-                            set_status(p.status, LMOE_ERR_DEVICE_CHECK);
-                    }
-                }
-            }
+                for (int i = 0; i < NW; ++i) pr[i] = __ldg(p.perm + w.row0 + min(32 * i + lane, w.nv - 1));
             return true;
+        };
+        auto weigh = [&](const GItem &w, const int (&pr)[NW], float (&rw)[NW]) {
+            if (!weighted) return;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                const int q = p.perm ? pr[i] : w.row0 + min(32 * i + lane, w.nv - 1);
+                const bool in = q >= 0 && q < p.P;
+                if (!in) set_status(p.status, LMOE_ERR_DEVICE_CHECK);
+                rw[i] = __ldg(p.row_w + (in ? q : 0));
+            }
         };
         auto process = [&](const GItem &w, const float (&rw)[NW]) -> bool {
             const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.limit);
@@ -523,13 +524,26 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
             return true;
         };
-        GItem wa, wb;
+        // w0 in hand with its weights, w1 with its pairs; weights in two sets by
+        // turns, so that no copy waits for a load
+        GItem w0, w1, w2;
+        int pr[NW];
         float ra[NW], rb[NW];
-        for (bool more = take(wa, ra); more;) {
-            more = take(wb, rb);
-            if (!process(wa, ra) || !more) break;
-            more = take(wa, ra);
-            if (!process(wb, rb)) break;
+        bool have0 = take(w0, pr), have1 = false, have2 = false;
+        if (have0) {
+            weigh(w0, pr, ra);
+            have1 = take(w1, pr);
+        }
+        while (have0) {
+            if (have1) weigh(w1, pr, rb);
+            have2 = have1 && take(w2, pr);
+            if (!process(w0, ra) || !have1) break;
+            if (have2) weigh(w2, pr, ra);
+            w0 = w2;
+            const GItem cur = w1;
+            have1 = have2 && take(w1, pr);
+            if (!process(cur, rb)) break;
+            have0 = have2;
         }
     } else if (warp == C::FEED && p.counter && rank == 0) {
         // ---------------- item feed (a pair's: the leader's, for both CTAs) ----------------
