@@ -60,7 +60,7 @@ def build_bind() -> str:
     lib = os.path.join(torch_dir, "lib")
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *(f"-isystem{i}" for i in inc[:4]), f"-I{inc[4]}",
-           BIND_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           BIND_SRC, "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
            "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -8,6 +8,7 @@
 // The module is not linked to the library: lmoe.py hands it the addresses of the
 // entry points of the library it loaded (bind).
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -119,7 +120,7 @@ struct Out {
             Py_INCREF(given);
             obj = given;
         } else {
-            at::Tensor t = at::empty(shape, like.options().dtype(type));
+            at::Tensor t = at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
             ptr = t.data_ptr();
             obj = THPVariable_Wrap(std::move(t));
         }
