@@ -83,6 +83,7 @@ struct GArgs {
     int32_t *status;
     long long limit;
     int stall;
+    int weights_once;  // most weight tiles have one row tile: their lines leave L2 first
 };
 
 struct GItem {
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         // ---------------- producers: A (warp 0 and, gated, warp A2), B (warps B0 ..) ----------------
         __shared__ int4 s_ids[GATHER ? C::BW : 1][C::COPIES];  // the rows of the warps' gather4 copies
         const bool isA = warp == 0 || warp == C::A2;
+        const uint64_t policy = isA && p.weights_once ? l2_policy_evict_first() : l2_policy_evict_normal();
         const int bw = warp - C::B0;  // B: this warp's copies are bw, bw + BW, ...
         [[maybe_unused]] int4 *ids = s_ids[GATHER && !isA ? bw : 0];
         int stage = 0, fills = 0;
@@ -329,7 +331,8 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], announce);
                 };
                 auto load = [&](void *dst, const CUtensorMap *tm, int y) {
-                    PAIR ? tma_load_2d_pair(dst, tm, kc * 64, y, bar) : tma_load_2d(dst, tm, kc * 64, y, &full[stage]);
+                    PAIR ? tma_load_2d_pair(dst, tm, kc * 64, y, bar, policy)
+                         : tma_load_2d_hint(dst, tm, kc * 64, y, &full[stage], policy);
                 };
                 if (isA) {
                     if (elect_one() && !(p.stall && at_start && kc == k0)) {
@@ -696,6 +699,12 @@ cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st)
     const int64_t items = (by_rows < a.P ? by_rows : a.P) * g.MT;
     if (items > INT32_MAX) return cudaErrorInvalidValue;
     g.max_items = int(items);
+    // Weights read by one row tile each need no place in L2, gathered rows (read
+    // by every weight tile) do.  896 experts, gate and up of 8192 tokens 1163 ->
+    // 1094 us, down of 64 325 -> 317 us; with several row tiles an expert it
+    // costs 1 to 2% (8 experts of 1024 rows 207 -> 210 us), and beside a large
+    // row tile's fp32 output as much (down of 8192 tokens 921 -> 955 us).
+    g.weights_once = a.P <= active * NT && (a.gather || NT < 256);
     const int sms = sm_count();
     if (NT == 16) {
         // Items that cannot fill the GPU: several CTAs along K an item, each at least 4 chunks.
