@@ -324,7 +324,8 @@ lmoe_status lmoe_residual_norm(const uint16_t *y, const void *res, int32_t res_f
  * x as it is (see below).  K % 32 == 0, any N >= 1.  Made for the
  * hidden <-> latent projections of decode batches, whose time is the weight
  * stream (0.53 bytes per weight, against 2 of lmoe_linear_bf16); it holds for
- * any number of rows.  This call and the grouped products below leave the
+ * any number of rows up to 2^29.  A row of x with an infinity or a NaN gives
+ * NaN outputs in that row; out overlaps no input.  This call and the grouped products below leave the
  * workspace's status word alone unless they find an error, and one found
  * stays until it is cleared: clear it once before the workspace's first use
  * (lmoe_clear_device_status).  Calls that may overlap on the GPU, captured
@@ -356,7 +357,7 @@ size_t lmoe_grouped_workspace_size(void);
  * belong to no group are left as they were.  With fp32 out and the gate
  * weights as row_w, out is the yp that lmoe_combine takes.
  * K % 8 == 0, any N >= 1, 1 <= E <= 2048, E * N <= INT32_MAX, 1 <= k,
- * P <= INT32_MAX; without gather x_rows >= P.
+ * P <= 2^29; without gather x_rows >= P.  out overlaps no input.
  * Offsets that break the rule above and source rows outside [0, x_rows) are
  * recorded as LMOE_ERR_DEVICE_CHECK; the call then reads and writes nothing
  * out of bounds, and what the groups concerned hold is undefined. */
@@ -488,14 +489,14 @@ lmoe_status lmoe_forward_workspace_views(const lmoe_dims *dims, lmoe_ffn_views *
  * setting is process-wide and not thread-safe. */
 lmoe_status lmoe_set_h_capture(float *h_f32, size_t bytes);
 
-/* Failure-path test of the expert GEMMs' bounded waits.  Every wait on an
- * mbarrier in the expert GEMMs gives up after a limit of SM clocks (about
+/* Failure-path test of the bounded waits of the expert GEMMs, the MXFP4
+ * linear and the grouped products.  Every wait on an mbarrier there gives up after a limit of SM clocks (about
  * 2 s by default), records LMOE_ERR_TIMEOUT in the status word, and the
  * kernel winds down (an MMA issuer first waits, again bounded, for its MMAs
  * in flight) and returns; so does the wait of a down item, in the kernel
  * that runs both GEMMs, for its token tile's h.  With stall_first_fill set, the first pipeline
- * stage of every CTA of the following lmoe_forward / lmoe_expert_ffn calls
- * is never filled, so those waits run out after wait_limit_cycles; the host
+ * stage of every CTA of the following lmoe_forward / lmoe_expert_ffn /
+ * lmoe_linear_mxfp4 / lmoe_grouped_* calls is never filled, so those waits run out after wait_limit_cycles; the host
  * then reads LMOE_ERR_TIMEOUT with lmoe_last_device_status.  (0, 0) restores
  * the normal behaviour; wait_limit_cycles alone (stall 0) only changes the
  * limit.  After LMOE_ERR_TIMEOUT the outputs of that call are undefined and

@@ -428,6 +428,32 @@ def test_grouped_bad_indices_are_reported(cuda_lib, what, swiglu):
         within(out[8:24], ref, ref.abs() * HALF + 66 * U * (x[8:24].to(D).abs() @ W[1].to(D).abs().t()) * (1 + HALF))
 
 
+def test_outputs_past_32_bit_offsets(cuda_lib):
+    """More than 2^31 output elements: the last rows are right."""
+    g = gen(40)
+    # 66000 rows x 33000 outputs
+    P, N = 66000, 33000
+    x, W = randn(g, P, 32), randn(g, 2, N, 32)
+    off = torch.tensor([0, 30000, P], dtype=torch.int32, device=DEV)
+    out = cuda_lib.grouped_linear_bf16(x, W, off)
+    for rows, e in ((slice(29990, 30000), 0), (slice(P - 300, P), 1)):
+        ref = x[rows].to(D) @ W[e].to(D).t()
+        within(out[rows], ref, ref.abs() * HALF + 34 * U * (x[rows].to(D).abs() @ W[e].to(D).abs().t()) * (1 + HALF))
+    del out
+    q, s, Wm = mx_weights(cuda_lib, g, N, 32)
+    out = cuda_lib.linear_mxfp4(x, q, s, N)
+    rows = slice(P - 130, P)
+    ref = x[rows].to(D) @ Wm.t()
+    within(out[rows], ref, linear_tol(x[rows], Wm, ref))
+    del out
+    T, H = 270000, 8192
+    y = torch.randn(T, H, device=DEV, dtype=torch.bfloat16, generator=g)
+    w = randn(g, H, dtype=torch.float32)
+    n = cuda_lib.rms_norm(y, w)
+    ref = norm_ref(y[-3:].to(D), w, 1e-5)
+    within(n[-3:], ref, ref.abs() * (HALF + 64 * U) * (1 + HALF))
+
+
 # ---- streams, graphs, repeats -------------------------------------------------------
 
 def _calls(lmoe, g):

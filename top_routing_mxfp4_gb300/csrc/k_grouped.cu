@@ -31,6 +31,7 @@
 #include "cluster_sum.cuh"
 #include "lmoe_internal.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace lmoe {
 namespace {
@@ -582,47 +583,14 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     if (warp == 1) PAIR ? tmem_dealloc_pair(tmem, C::TMEM_COLS) : tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-bool bf16_map(CUtensorMap *m, const void *base, int64_t K, int64_t rows, int box_rows)
-{
-    static const EncodeTiledFn fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void *f = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(f);
-    }();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(K) * 2};
-    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
-    const cuuint32_t es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count()
-{
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 0 ? n : 148;
-}
-
 template <int NT, bool SWIGLU, bool GATHER, int KS>
 cudaError_t launch(const GroupedArgs &a, GArgs g, int64_t items, int sms, cudaStream_t st)
 {
     using C = GCfg<NT, SWIGLU, GATHER, KS>;
     CUtensorMap ma, ma2, mb;
-    if (!bf16_map(&ma, a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
-        !bf16_map(&ma2, SWIGLU ? a.W2 : a.W, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
-        !bf16_map(&mb, a.x, a.K, a.x_rows, GATHER ? 1 : C::BOX))
+    if (!make_tensor_map(&ma, a.W, MapType::BF16, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
+        !make_tensor_map(&ma2, SWIGLU ? a.W2 : a.W, MapType::BF16, a.K, int64_t(a.E) * a.N, SWIGLU ? 16 : 128) ||
+        !make_tensor_map(&mb, a.x, MapType::BF16, a.K, a.x_rows, GATHER ? 1 : C::BOX))
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::RED + (2 * C::S + 2 * C::ACC + 2 + 2 * C::Q) * 8 +
                         C::Q * 4 + 8 + 128 + size_t(2 * a.E + 2) * 4;
@@ -705,7 +673,7 @@ cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st)
     // costs 1 to 2% (8 experts of 1024 rows 207 -> 210 us), and beside a large
     // row tile's fp32 output as much (down of 8192 tokens 921 -> 955 us).
     g.weights_once = a.P <= active * NT && (a.gather || NT < 256);
-    const int sms = sm_count();
+    const int sms = device_sms();
     if (NT == 16) {
         // Items that cannot fill the GPU: several CTAs along K an item, each at least 4 chunks.
         if (items * 8 <= sms && g.KC >= 32) return pick<16, 8>(a, g, items, sms, st);

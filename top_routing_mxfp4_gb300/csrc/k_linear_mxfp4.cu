@@ -38,6 +38,7 @@
 #include "cluster_sum.cuh"
 #include "lmoe_internal.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace lmoe {
 namespace {
@@ -452,42 +453,6 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// A map of [rows][K] elements, boxes of 128 columns x box_rows: packed FP4
-// (64 bytes per 128 columns in memory, 128 in shared memory) or bytes.
-bool byte_map(CUtensorMap *m, const void *base, bool fp4, int64_t K, int64_t rows, int box_rows)
-{
-    static const EncodeTiledFn fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void *f = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(f);
-    }();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(fp4 ? K / 2 : K)};
-    const cuuint32_t box[2] = {128, cuuint32_t(box_rows)};
-    const cuuint32_t es[2] = {1, 1};
-    return fn(m, fp4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count()
-{
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 0 ? n : 148;
-}
-
 // Rows of a tile.  Up to 16 the kernel splits the rows itself, also of small
 // products whose 16-row tiles run at once (512 x 512, 100 rows: 3.9 us, against
 // 5.0 with 64-row tiles and the kernel before them).  Beyond, 64 rows, whose
@@ -547,15 +512,15 @@ cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t
 {
     using C = LCfg<NB, FUSED>;
     CUtensorMap ma, mb;
-    if (!byte_map(&ma, q, true, int64_t(a.KC) * 128, a.N, 128)) return cudaErrorInvalidValue;
+    if (!make_tensor_map(&ma, q, MapType::FP4, int64_t(a.KC) * 128, a.N, 128)) return cudaErrorInvalidValue;
     if (FUSED)
         mb = ma;  // not used
-    else if (!byte_map(&mb, codes, false, int64_t(a.KC) * 128, int64_t(a.NTL) * C::NC, C::NC))
+    else if (!make_tensor_map(&mb, codes, MapType::BYTES, int64_t(a.KC) * 128, int64_t(a.NTL) * C::NC, C::NC))
         return cudaErrorInvalidValue;
     auto *kern = k_linear_mx<NB, FUSED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
     if (e != cudaSuccess) return e;
-    const int sms = sm_count();
+    const int sms = device_sms();
     const int64_t items = int64_t(a.MT) * a.NTL;
     // As many ranks an item as make the longest SM's share of the chunks
     // shortest, a split's exchange counted as 4 to 28 chunks (measured: 0.2 us
@@ -606,7 +571,7 @@ cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8
     uint8_t *codes = static_cast<uint8_t *>(scratch);
     uint8_t *atoms = codes + int64_t(a.NTL) * a.KC * (2 * NB * 128);
     a.sfb = atoms;
-    const int64_t blocks = ceil_div(rows * a.KC * 16, 256), most = int64_t(sm_count()) * 8;
+    const int64_t blocks = ceil_div(rows * a.KC * 16, 256), most = int64_t(device_sms()) * 8;
     const cudaError_t e = launch_pdl(NB == 64 ? k_split_rows<64> : k_split_rows<128>,
                                      dim3(unsigned(blocks < most ? blocks : most)), dim3(256), 0, st, x, rows, K, a.KC,
                                      codes, atoms);

@@ -11,6 +11,7 @@ using namespace lmoe;
 namespace {
 
 constexpr int32_t kStatusBytes = 256;
+constexpr int64_t kMaxRows = int64_t(1) << 29;  // rows of the MXFP4 linear and the grouped products: tile arithmetic stays in 32 bits
 
 cudaEvent_t g_stage_events[LMOE_NUM_STAGE_EVENTS] = {};
 bool g_stage_events_on = false;
@@ -136,7 +137,7 @@ bool norm_ok(int64_t T, int32_t H, float eps, int32_t fmt)
 lmoe_status grouped_args(const uint16_t *x, int64_t x_rows, const lmoe_groups *g, int32_t gather, int32_t K, int32_t N,
                          void *out, void *workspace, size_t ws_bytes, GroupedArgs &a)
 {
-    if (!g || g->P < 0 || g->P > INT32_MAX || g->E <= 0 || g->E > 2048 || g->k <= 0 || K <= 0 || K % 8 != 0 || N <= 0 ||
+    if (!g || g->P < 0 || g->P > kMaxRows || g->E <= 0 || g->E > 2048 || g->k <= 0 || K <= 0 || K % 8 != 0 || N <= 0 ||
         x_rows < 0 || x_rows > INT32_MAX || int64_t(g->E) * N > INT32_MAX)
         return LMOE_ERR_INVALID_ARG;
     if (gather && (!g->perm || x_rows == 0) && g->P > 0) return LMOE_ERR_INVALID_ARG;
@@ -568,14 +569,14 @@ lmoe_status lmoe_residual_norm(const uint16_t *y, const void *res, int32_t res_f
 
 size_t lmoe_linear_mxfp4_workspace_size(int64_t rows, int32_t K, int32_t N)
 {
-    if (rows < 0 || rows > INT32_MAX || K <= 0 || K % 32 != 0 || N <= 0) return 0;
+    if (rows < 0 || rows > kMaxRows || K <= 0 || K % 32 != 0 || N <= 0) return 0;
     return kStatusBytes + linear_mxfp4_scratch_bytes(rows, K, N);
 }
 
 lmoe_status lmoe_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int32_t K, int32_t N,
                               uint16_t *out, void *workspace, size_t ws_bytes, void *stream)
 {
-    if (rows < 0 || rows > INT32_MAX || K <= 0 || K % 32 != 0 || N <= 0) return LMOE_ERR_INVALID_ARG;
+    if (rows < 0 || rows > kMaxRows || K <= 0 || K % 32 != 0 || N <= 0) return LMOE_ERR_INVALID_ARG;
     if (rows == 0) return LMOE_OK;
     if (!x || !q || !s || !out || !aligned(x, 16) || !aligned(q, 32) || !aligned(s, 16) || !aligned(out, 16))
         return LMOE_ERR_INVALID_ARG;
