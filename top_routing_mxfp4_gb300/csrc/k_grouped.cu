@@ -578,7 +578,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     tc_fence_before();
     __syncthreads();
     // nobody's shared or tensor memory goes while another CTA may still write or read it
-    if (C::CL > 1) cluster_sync();
+    if (C::CL > 1) cluster_sync_end();
     tc_fence_after();
     if (warp == 1) PAIR ? tmem_dealloc_pair(tmem, C::TMEM_COLS) : tmem_dealloc(tmem, C::TMEM_COLS);
 }

@@ -448,7 +448,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
     }
     tc_fence_before();
     __syncthreads();
-    if (KS > 1) cluster_sync();  // nobody's shared memory goes while another rank may store into it
+    if (KS > 1) cluster_sync_end();  // nobody's shared memory goes while another rank may store into it
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }

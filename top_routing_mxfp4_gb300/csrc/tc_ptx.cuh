@@ -367,6 +367,13 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same at a kernel's end, where it publishes nothing (it only keeps the
+// CTAs' memories alive for one another): without the release it does not wait
+// for the threads' global stores.
+__device__ __forceinline__ void cluster_sync_end()
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // Address of this CTA's shared-memory address `saddr` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank)
 {
