@@ -268,6 +268,8 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
         // ---------------- the rows, split here: team t takes chunks t, t + TEAMS, .. ----------------
         const int per = k1 - k0, mine = total > first ? (total - first + step - 1) / step : 0;
         const int fills = per * mine, r0 = (warp - 6) % C::TW * 8, c16 = (lane & 15) >> 1;
+        // rows of the tile this warp has to split (the others' columns are dropped)
+        const int live = p.NTL == 1 ? p.rows - r0 : 8;
         // the pieces of the chunk of fill f: lanes 0-15 one row, lanes 16-31 the next
         auto fetch = [&](int f, uint4 (&u)[C::UNITS]) {
             const int i = f / per, nt = (first + i * step) / p.MT;
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
             uint8_t *bt = stages + stage * C::STAGE + A_TILE, *sf = stages + stage * C::STAGE + C::SF_OFF + 512;
 #pragma unroll
             for (int j = 0; j < C::UNITS; ++j) {
+                if (2 * j >= live) break;
                 const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
                 uint32_t m = amax8(w);
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
