@@ -493,7 +493,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             };
             if (KS > 1) {
                 static_assert(KS == 1 || NT == 16, "one chunk of columns");
-                const ClusterSum cs{KS, rank, w.nv, reinterpret_cast<float *>(stages), red, red_full};
+                const ClusterSum cs(KS, rank, w.nv, reinterpret_cast<float *>(stages), red, red_full);
                 uint32_t v[16];
                 tmem_ld16(tb, v);
                 tmem_ld_wait();
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                     return false;
                 }
-                const int c0 = cs.begin(rank), c1 = cs.begin(rank + 1);  // this rank's rows
+                const int c0 = cs.own0, c1 = cs.own1;  // this rank's rows
                 float y[16];
                 cs.sum(c0, 32 * q + lane, y);
                 finish(c0, c1, y);

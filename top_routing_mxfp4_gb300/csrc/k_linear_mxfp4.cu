@@ -145,13 +145,13 @@ struct LCfg {
     static constexpr uint32_t B_TILE = NC * 128;
     static constexpr uint32_t SF_OFF = A_TILE + B_TILE;  // scale atoms: weights, rows
     static constexpr uint32_t STAGE = (SF_OFF + (1 + NAT) * 512 + 1023) / 1024 * 1024;
-    // Fused: teams of TW warps take the chunks in turn, a warp 8 rows of one
-    // (four 8-column pieces a lane).
-    static constexpr int TW = FUSED ? NB / 8 : 1;
+    // Fused: four teams of two warps take the chunks in turn, a warp half the
+    // tile's rows (two rows a step, an 8-column piece a lane).
+    static constexpr int TW = FUSED ? 2 : 1;
     static constexpr int TEAMS = FUSED ? 4 : 1;
     static constexpr int BW = TW * TEAMS;  // warps that bring B
     static constexpr int THREADS = 32 * (6 + BW);
-    static constexpr int UNITS = 4;
+    static constexpr int UNITS = FUSED ? NB / 4 : 1;
     // Small row tiles leave room for two CTAs an SM: the next call's start up
     // beside the last ones of this call, and the items spread more evenly.
     static constexpr int CTAS = FUSED ? 2 : 1;
@@ -267,9 +267,9 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
     } else if (FUSED && warp >= 6) {
         // ---------------- the rows, split here: team t takes chunks t, t + TEAMS, .. ----------------
         const int per = k1 - k0, mine = total > first ? (total - first + step - 1) / step : 0;
-        const int fills = per * mine, r0 = (warp - 6) % C::TW * 8, c16 = (lane & 15) >> 1;
+        const int fills = per * mine, r0 = (warp - 6) % C::TW * (NB / 2), c16 = (lane & 15) >> 1;
         // rows of the tile this warp has to split (the others' columns are dropped)
-        const int live = p.NTL == 1 ? p.rows - r0 : 8;
+        const int live = p.NTL == 1 ? p.rows - r0 : NB / 2;
         // the pieces of the chunk of fill f: lanes 0-15 one row, lanes 16-31 the next
         auto fetch = [&](int f, uint4 (&u)[C::UNITS]) {
             const int i = f / per, nt = (first + i * step) / p.MT;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
             const int n = mt * 128 + 32 * q + lane;
             __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.out) + int64_t(row0) * p.N + n;
             if (KS > 1) {
-                const ClusterSum cs{KS, rank, nv, reinterpret_cast<float *>(stages), red, red_full};
+                const ClusterSum cs(KS, rank, nv, reinterpret_cast<float *>(stages), red, red_full);
                 for (int c0 = 0; c0 < nv; c0 += CW) {
                     float y[CW];
                     sums(c0, y);
@@ -423,13 +423,13 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                     break;
                 }
-                for (int c0 = cs.begin(rank); c0 < cs.begin(rank + 1); c0 += 8) {
+                for (int c0 = cs.own0; c0 < cs.own1; c0 += 8) {
                     float y[8];
                     cs.sum(c0, 32 * q + lane, y);
                     if (n < p.N)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            if (c0 + j < cs.begin(rank + 1)) o[int64_t(c0 + j) * p.N] = __float2bfloat16_rn(y[j]);
+                            if (c0 + j < cs.own1) o[int64_t(c0 + j) * p.N] = __float2bfloat16_rn(y[j]);
                 }
             } else {
                 for (int c0 = 0; c0 < nv; c0 += CW) {
