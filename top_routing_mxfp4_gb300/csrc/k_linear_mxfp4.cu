@@ -222,7 +222,9 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
     __syncthreads();
     tc_fence_after();
     if (KS > 1) cluster_sync();  // the cluster's barriers are initialised
-    pdl_enter();
+    // After k_split_rows the weights' warp does not wait: that kernel writes no
+    // weights, and what came before it was complete when it let this one start.
+    if (FUSED || warp != 0) pdl_enter();
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0 || (!FUSED && warp == 6)) {
