@@ -177,6 +177,7 @@ struct LArgs {
     int32_t *status;
     long long limit;
     int stall;
+    int weights_ready;  // the previous kernel of the stream writes no weights
 };
 
 template <int NB, bool FUSED>
@@ -222,9 +223,10 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
     __syncthreads();
     tc_fence_after();
     if (KS > 1) cluster_sync();  // the cluster's barriers are initialised
-    // After k_split_rows the weights' warp does not wait: that kernel writes no
-    // weights, and what came before it was complete when it let this one start.
-    if (FUSED || warp != 0) pdl_enter();
+    // Behind a kernel that is known not to write them (k_split_rows, the block's
+    // own kernels) the weights' warp does not wait: what came before that kernel
+    // was complete when it let this one start.
+    if (!p.weights_ready || warp != 0) pdl_enter();
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 0 || (!FUSED && warp == 6)) {
@@ -554,7 +556,8 @@ size_t linear_mxfp4_scratch_bytes(int64_t rows, int K, int N)
 }
 
 cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int K, int N,
-                                uint16_t *out, void *scratch, int32_t *status, const WaitArgs &wait, cudaStream_t st)
+                                uint16_t *out, void *scratch, int32_t *status, const WaitArgs &wait, cudaStream_t st,
+                                bool weights_ready)
 {
     const int NB = row_tile(rows, K, N);
     LArgs a{};
@@ -571,6 +574,7 @@ cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8
     a.status = status;
     a.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
     a.stall = wait.stall_first_fill;
+    a.weights_ready = weights_ready || !splits_itself(NB);
     if (NB == 8) return launch<8, true>(a, q, nullptr, st);
     if (NB == 16) return launch<16, true>(a, q, nullptr, st);
     uint8_t *codes = static_cast<uint8_t *>(scratch);

@@ -288,11 +288,12 @@ bool projection_ok(const lmoe_projection &p)
     return p.q && p.s && aligned(p.q, 32) && aligned(p.s, 16);
 }
 
+// (the call before it in the block is the norm, the combine or the clearing of the status word)
 cudaError_t project(const lmoe_projection &p, const uint16_t *x, int T, int K, int N, uint16_t *out, void *split,
                     int32_t *status, cudaStream_t st)
 {
     if (p.w) return launch_linear_bf16(x, p.w, T, K, N, out, nullptr, status, st);
-    return launch_linear_mxfp4(x, p.q, p.s, T, K, N, out, split, status, wait_args(), st);
+    return launch_linear_mxfp4(x, p.q, p.s, T, K, N, out, split, status, wait_args(), st, true);
 }
 
 }  // namespace

@@ -361,9 +361,12 @@ struct NormArgs {
 cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t st);
 
 // ---- MXFP4 linear on bf16 rows (k_linear_mxfp4.cu) -------------------------------------
+// weights_ready: the stream's previous kernel is one of this library that writes
+// no weights, so their copies need not wait for it.
 size_t linear_mxfp4_scratch_bytes(int64_t rows, int K, int N);
 cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int K, int N,
-                                uint16_t *out, void *scratch, int32_t *status, const WaitArgs &wait, cudaStream_t st);
+                                uint16_t *out, void *scratch, int32_t *status, const WaitArgs &wait, cudaStream_t st,
+                                bool weights_ready = false);
 
 // ---- bf16 products grouped by expert (k_grouped.cu) ------------------------------------
 struct GroupedArgs {
