@@ -28,6 +28,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "cluster_sum.cuh"
 #include "lmoe_internal.cuh"
 #include "tc_ptx.cuh"
@@ -79,7 +81,6 @@ struct GArgs {
     int E, k, N, MT, KC;
     int max_items;  // no valid groups have more
     int32_t *counter;  // items handed out so far (zero at the start); null: every CTA takes each grid-th
-    int out_f32;
     void *out;
     int32_t *status;
     long long limit;
@@ -118,7 +119,8 @@ struct Walk {
     }
 };
 
-template <int NT, bool SWIGLU, bool GATHER, int KS>
+// F32: the output's type (else bf16).
+template <int NT, bool SWIGLU, bool GATHER, int KS, bool F32>
 __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     k_grouped(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
               const __grid_constant__ CUtensorMap tmB, const GArgs p)
@@ -459,36 +461,74 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
             tc_fence_after();
             const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
-            // plain: lane = output column; gated: lanes 0-15 gate, 16-31 up of 16 features
+            // the lane's output column (gated: lanes 0-15 hold the gates of 16 features, 16-31 the ups)
             const int mtile = PAIR ? 2 * w.m + rank : w.m;
             const int n = SWIGLU ? mtile * 64 + 16 * q + (lane & 15) : mtile * 128 + 32 * q + lane;
-            const bool mine = n < p.N && (!SWIGLU || lane < 16);
+            const bool mine = n < p.N;
+            using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
+            using Out2 = typename std::conditional<F32, float2, __nv_bfloat162>::type;
+            const bool pairs = p.N % 2 == 0;  // neighbouring outputs in one store
+            auto round1 = [](float v) -> Out {
+                if constexpr (F32) return v;
+                else return __float2bfloat16_rn(v);
+            };
+            auto round2 = [](float lo, float hi) -> Out2 {
+                if constexpr (F32) return make_float2(lo, hi);
+                else return __floats2bfloat162_rn(lo, hi);
+            };
             // 16 rows from c0 on (rows [c0, c1) of them wanted) of the tile: weight or gate, round, store
             auto finish = [&](int c0, int c1, float (&y)[16]) {
-                if (SWIGLU) {
+                const int odd = lane & 1, up = lane >> 4;
+                Out *const base = static_cast<Out *>(p.out) + int64_t(w.row0 + c0) * p.N;
+                const int64_t N = p.N;
+                if constexpr (SWIGLU) {
+                    // both halves of the warp gate: lanes 0-15 the even rows, 16-31 the odd ones
+                    float h[8];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float u = __shfl_down_sync(0xFFFFFFFFu, y[j], 16);
-                        y[j] = __fdividef(y[j], 1.f + expf(-y[j])) * u;
+                    for (int i = 0; i < 8; ++i) {
+                        const float r = __shfl_xor_sync(0xFFFFFFFFu, up ? y[2 * i] : y[2 * i + 1], 16);
+                        const float g = up ? r : y[2 * i], u = up ? y[2 * i + 1] : r;
+                        h[i] = __fdividef(g, 1.f + expf(-g)) * u;
                     }
-                } else if (p.row_w) {
+                    if (pairs) {
+                        int row = c0 + 2 * odd + up;
+                        Out *o = base + (2 * odd + up) * N + (n & ~1);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2, row += 4, o += 4 * N) {
+                            const float r = __shfl_xor_sync(0xFFFFFFFFu, odd ? h[i] : h[i + 1], 1);
+                            if (mine && row < c1)
+                                *reinterpret_cast<Out2 *>(o) = odd ? round2(r, h[i + 1]) : round2(h[i], r);
+                        }
+                    } else {
+                        int row = c0 + up;
+                        Out *o = base + up * N + n;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i, row += 2, o += 2 * N)
+                            if (mine && row < c1) *o = round1(h[i]);
+                    }
+                    return;
+                }
+                if (p.row_w) {
                     float v = rw[0];
 #pragma unroll
                     for (int i = 1; i < NW; ++i) v = c0 / 32 == i ? rw[i] : v;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) y[j] *= __shfl_sync(0xFFFFFFFFu, v, (c0 & 31) + j);
                 }
-                if (!mine) return;
-                const int64_t o = int64_t(w.row0 + c0) * p.N + n;
-                if (!SWIGLU && p.out_f32) {
+                if (pairs) {  // even lanes store the even rows' pairs of columns, odd lanes the odd rows'
+                    int row = c0 + odd;
+                    Out *o = base + odd * N + (n & ~1);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + j < c1) static_cast<float *>(p.out)[o + int64_t(j) * p.N] = y[j];
+                    for (int j = 0; j < 16; j += 2, row += 2, o += 2 * N) {
+                        const float r = __shfl_xor_sync(0xFFFFFFFFu, odd ? y[j] : y[j + 1], 1);
+                        if (mine && row < c1)
+                            *reinterpret_cast<Out2 *>(o) = odd ? round2(r, y[j + 1]) : round2(y[j], r);
+                    }
                 } else {
+                    Out *o = base + n;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c0 + j < c1)
-                            static_cast<__nv_bfloat16 *>(p.out)[o + int64_t(j) * p.N] = __float2bfloat16_rn(y[j]);
+                    for (int j = 0; j < 16; ++j, o += N)
+                        if (mine && c0 + j < c1) *o = round1(y[j]);
                 }
             };
             if (KS > 1) {
@@ -583,7 +623,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     if (warp == 1) PAIR ? tmem_dealloc_pair(tmem, C::TMEM_COLS) : tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-template <int NT, bool SWIGLU, bool GATHER, int KS>
+template <int NT, bool SWIGLU, bool GATHER, int KS, bool F32 = false>
 cudaError_t launch(const GroupedArgs &a, GArgs g, int64_t items, int sms, cudaStream_t st)
 {
     using C = GCfg<NT, SWIGLU, GATHER, KS>;
@@ -594,7 +634,7 @@ cudaError_t launch(const GroupedArgs &a, GArgs g, int64_t items, int sms, cudaSt
         return cudaErrorInvalidValue;
     const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::RED + (2 * C::S + 2 * C::ACC + 2 + 2 * C::Q) * 8 +
                         C::Q * 4 + 8 + 128 + size_t(2 * a.E + 2) * 4;
-    auto *kern = k_grouped<NT, SWIGLU, GATHER, KS>;
+    auto *kern = k_grouped<NT, SWIGLU, GATHER, KS, F32>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     const int64_t slots = sms / C::CL;
@@ -629,6 +669,9 @@ cudaError_t pick(const GroupedArgs &a, const GArgs &g, int64_t items, int sms, c
     if (a.W2)
         return a.gather ? launch<NT, true, true, KS>(a, g, items, sms, st)
                         : launch<NT, true, false, KS>(a, g, items, sms, st);
+    if (a.out_fmt == LMOE_F32)
+        return a.gather ? launch<NT, false, true, KS, true>(a, g, items, sms, st)
+                        : launch<NT, false, false, KS, true>(a, g, items, sms, st);
     return a.gather ? launch<NT, false, true, KS>(a, g, items, sms, st)
                     : launch<NT, false, false, KS>(a, g, items, sms, st);
 }
@@ -650,7 +693,6 @@ cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st)
     g.N = a.N;
     g.MT = int(ceil_div(a.N, a.W2 ? 64 : 128));
     g.KC = int(ceil_div(a.K, 64));
-    g.out_f32 = a.out_fmt == LMOE_F32;
     g.out = a.out;
     g.status = a.status;
     g.counter = a.status + 1;  // the status word's neighbour in the workspace
