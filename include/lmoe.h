@@ -347,7 +347,7 @@ typedef struct {
     int32_t E, k;
 } lmoe_groups;
 
-/* Workspace of the two calls below: the status word alone. */
+/* Workspace of the two calls below: the status word and a counter. */
 size_t lmoe_grouped_workspace_size(void);
 
 /* out[q][n] = w(q) * sum_c x[src(q)][c] * W[e(q)][n][c], for every row q of a

@@ -463,6 +463,10 @@ def _calls(lmoe, g):
     x, xm, xb = randn(g, T, 256), randn(g, 3, 1024), randn(g, 100, 1024)
     W, V = randn(g, 5, 136, 256), randn(g, 5, 136, 256)
     y, r, w = randn(g, 33, 1024), randn(g, 33, 1024, dtype=torch.float32), randn(g, 1024, dtype=torch.float32)
+    # many items: handed out by the counter in the workspace, for single CTAs and for pairs
+    off1, perm1, T1 = make_groups([2, 1] * 32, 1, g)
+    off2, perm2, T2 = make_groups([700, 300, 513, 5], 1, g)
+    x1, W1, x2, W2 = randn(g, T1, 64), randn(g, 64, 1300, 64), randn(g, T2, 64), randn(g, 4, 10000, 64)
     return [
         (lambda **a: lmoe.rms_norm(r, w, **a), None),
         (lambda **a: lmoe.residual_norm(y, r, post_w=w, next_w=w, scale=0.5, **a)[1], None),
@@ -470,6 +474,9 @@ def _calls(lmoe, g):
         (lambda **a: lmoe.linear_mxfp4(xb, q, s, 512, **a), lmoe.linear_mxfp4_workspace_size(100, 1024, 512)),
         (lambda **a: lmoe.grouped_linear_bf16(x, W, off, perm, 4, **a), 256),
         (lambda **a: lmoe.grouped_swiglu_bf16(x, W, V, off, perm, 4, **a), 256),
+        (lambda **a: lmoe.grouped_linear_bf16(x1, W1, off1, perm1, 1, **a), 256),
+        (lambda **a: lmoe.grouped_linear_bf16(x2, W2, off2, perm2, 1, **a), 256),
+        (lambda **a: lmoe.grouped_swiglu_bf16(x2, W2, W2, off2, perm2, 1, **a), 256),
     ]
 
 

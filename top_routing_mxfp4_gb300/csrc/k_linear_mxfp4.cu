@@ -12,8 +12,7 @@
 // times it is at most 256 and neither part saturates), and a multiple of x's
 // own last bit, 2^-7 of its binade: at most 4 significant bits, hence exact,
 // down to elements of 2^-14 of the block's largest; below, lo rounds at 2^-14
-// of 2^a, an error of at most 2^-15 2^a <= 2^-22 amax.  Both parts' products
-// go into one fp32 accumulator.
+// of 2^a, an error of at most 2^-15 2^a <= 2^-22 amax.
 //
 // Bounded by the weight stream (17/32 byte a weight) up to about a hundred
 // rows, then by the tensor cores at half their 8-bit rate (two parts).
@@ -30,6 +29,10 @@
 // 6 copies them.  With few items a cluster of KS CTAs shares an item along K
 // (cluster_sum.cuh).
 // Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
+//
+// Measured, 7168 -> 3584: 1, 16, 64 and 512 rows 6.6, 8.5, 10.5 and 31.6 us
+// (3.2 us of any dependent kernel's start among them); 1 row 7168 -> 28672 19.8
+// us (5.5 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
