@@ -384,7 +384,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
         }
     } else {
         // ---------------- epilogue ----------------
-        constexpr int CW = NB < 16 ? NB : 16;  // rows of x a step
+        constexpr int CW = NB < 32 ? NB : 32;  // rows of x a step: their loads go out together
         const int q = warp & 3;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -406,12 +406,12 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] = __uint_as_float(v[j]) + __uint_as_float(v[8 + j]);
                 } else {
-                    uint32_t v[16], l[16];
-                    tmem_ld16(tb + c0, v);
-                    tmem_ld16(tb + NB + c0, l);
+                    uint32_t v[CW], l[CW];
+                    tmem_ld_cols<CW>(tb + c0, v);
+                    tmem_ld_cols<CW>(tb + NB + c0, l);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]) + __uint_as_float(l[j]);
+                    for (int j = 0; j < CW; ++j) y[j] = __uint_as_float(v[j]) + __uint_as_float(l[j]);
                 }
             };
             const int n = mt * 128 + 32 * q + lane;
