@@ -98,12 +98,15 @@ __device__ __forceinline__ uint32_t amax8(const uint32_t (&w)[4])
     return m;
 }
 
-// x[rows][K] -> codes [tiles][2 NB][Kp] (hi rows, then lo rows, of a tile of NB
-// rows) and scale atoms [tiles][KC][2 NB / 128][512]; eight columns a thread,
-// four threads a block of 32.
+// x[rows][K] -> per tile of NB rows and chunk of 128 columns one block of bytes
+// as a pipeline stage holds it: 2 NB rows of 128 codes (hi rows, then lo rows),
+// 16-byte units swizzled by the row, and behind them the scale atoms; eight
+// columns a thread, four threads a block of 32.
+__host__ __device__ constexpr int rows_block(int NB) { return 2 * NB * 128 + (2 * NB + 127) / 128 * 512; }
+
 template <int NB>
 __global__ void __launch_bounds__(256) k_split_rows(const uint16_t *__restrict__ x, int64_t rows, int K, int KC,
-                                                    uint8_t *__restrict__ codes, uint8_t *__restrict__ atoms)
+                                                    uint8_t *__restrict__ blocks)
 {
     pdl_enter();
     const int per = KC * 16;  // threads a row
@@ -124,13 +127,14 @@ __global__ void __launch_bounds__(256) k_split_rows(const uint16_t *__restrict__
         split8(w, b, hi, lo);
         const int64_t tile = r / NB;
         const int rr = int(r - tile * NB);
-        uint8_t *row = codes + (tile * 2 * NB + rr) * (KC * 128) + c;
-        *reinterpret_cast<uint2 *>(row) = hi;
-        *reinterpret_cast<uint2 *>(row + int64_t(NB) * (KC * 128)) = lo;
+        uint8_t *block = blocks + (tile * KC + (c >> 7)) * rows_block(NB);
+        const int at = rr * 128 + ((((c >> 4) & 7) ^ (rr & 7)) << 4) + (c & 8);
+        *reinterpret_cast<uint2 *>(block + at) = hi;
+        *reinterpret_cast<uint2 *>(block + NB * 128 + at) = lo;  // NB % 8 == 0: the same swizzle
         if ((c & 31) == 0) {
-            uint8_t *at = atoms + (tile * KC + (c >> 7)) * int(ceil_div(2 * NB, 128) * 512);
-            at[sf_off(rr, (c >> 5) & 3)] = uint8_t(b);
-            at[sf_off(NB + rr, (c >> 5) & 3)] = uint8_t(b - 5);
+            uint8_t *sf = block + 2 * NB * 128;
+            sf[sf_off(rr, (c >> 5) & 3)] = uint8_t(b);
+            sf[sf_off(NB + rr, (c >> 5) & 3)] = uint8_t(b - 5);
         }
     }
 }
@@ -173,7 +177,8 @@ struct LCfg {
 
 struct LArgs {
     const uint16_t *x;         // fused: the rows
-    const uint8_t *sfa, *sfb;  // weight scale atoms [MT][KC][512], row scale atoms [NTL][KC][NAT][512]
+    const uint8_t *sfa;        // weight scale atoms [MT][KC][512]
+    const uint8_t *split;      // else: the split rows [NTL][KC][rows_block]
     int rows, K, N, MT, NTL, KC;
     int KS;
     uint16_t *out;
@@ -185,7 +190,7 @@ struct LArgs {
 
 template <int NB, bool FUSED>
 __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::CTAS))
-    k_linear_mx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LArgs p)
+    k_linear_mx(const __grid_constant__ CUtensorMap tmA, const LArgs p)
 {
     using C = LCfg<NB, FUSED>;
     constexpr int S = C::S;
@@ -207,7 +212,6 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
     const int total = p.MT * p.NTL;
     const int k0 = rank * p.KC / KS, k1 = (rank + 1) * p.KC / KS;  // this rank's chunks of 128 columns
     if (warp == 0 && lane == 0) prefetch_tensormap(&tmA);
-    if (!FUSED && warp == 6 && lane == 0) prefetch_tensormap(&tmB);
     if (threadIdx.x == 64) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1 + C::TW);  // the weights' producer and the rows'
@@ -255,10 +259,11 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
                             bulk_load(sb + C::SF_OFF, p.sfa + (int64_t(mt) * p.KC + kc) * 512, 512, &full[stage]);
                         }
                     } else {
+                        // codes to the operand, the atoms behind them to the scales behind the weights'
+                        const uint8_t *src = p.split + (int64_t(nt) * p.KC + kc) * rows_block(NB);
                         mbar_arrive_expect_tx(&full[stage], C::B_TILE + C::NAT * 512);
-                        tma_load_2d(sb + A_TILE, &tmB, kc * 128, nt * C::NC, &full[stage]);
-                        bulk_load(sb + C::SF_OFF + 512, p.sfb + (int64_t(nt) * p.KC + kc) * (C::NAT * 512),
-                                  C::NAT * 512, &full[stage]);
+                        bulk_load(sb + A_TILE, src, C::B_TILE, &full[stage]);
+                        bulk_load(sb + C::SF_OFF + 512, src + C::B_TILE, C::NAT * 512, &full[stage]);
                     }
                 }
                 __syncwarp();
@@ -518,15 +523,11 @@ int max_clusters(int ks)
 }
 
 template <int NB, bool FUSED>
-cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t st)
+cudaError_t launch(LArgs a, const uint8_t *q, cudaStream_t st)
 {
     using C = LCfg<NB, FUSED>;
-    CUtensorMap ma, mb;
+    CUtensorMap ma;
     if (!make_tensor_map(&ma, q, MapType::FP4, int64_t(a.KC) * 128, a.N, 128)) return cudaErrorInvalidValue;
-    if (FUSED)
-        mb = ma;  // not used
-    else if (!make_tensor_map(&mb, codes, MapType::BYTES, int64_t(a.KC) * 128, int64_t(a.NTL) * C::NC, C::NC))
-        return cudaErrorInvalidValue;
     auto *kern = k_linear_mx<NB, FUSED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
     if (e != cudaSuccess) return e;
@@ -546,7 +547,7 @@ cudaError_t launch(LArgs a, const uint8_t *q, const uint8_t *codes, cudaStream_t
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg =
         config<NB, FUSED>(unsigned((items < slots ? items : slots) * a.KS), st, attr, a.KS);
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
+    return cudaLaunchKernelEx(&cfg, kern, ma, a);
 }
 
 }  // namespace
@@ -555,7 +556,7 @@ size_t linear_mxfp4_scratch_bytes(int64_t rows, int K, int N)
 {
     const int64_t KC = ceil_div(K, 128), NB = row_tile(rows, K, N);
     if (splits_itself(int(NB))) return 0;
-    return size_t(ceil_div(rows, NB) * KC * (2 * NB * 128 + ceil_div(2 * NB, 128) * 512));
+    return size_t(ceil_div(rows, NB) * KC * rows_block(int(NB)));
 }
 
 cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int K, int N,
@@ -578,17 +579,15 @@ cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8
     a.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
     a.stall = wait.stall_first_fill;
     a.weights_ready = weights_ready || !splits_itself(NB);
-    if (NB == 8) return launch<8, true>(a, q, nullptr, st);
-    if (NB == 16) return launch<16, true>(a, q, nullptr, st);
-    uint8_t *codes = static_cast<uint8_t *>(scratch);
-    uint8_t *atoms = codes + int64_t(a.NTL) * a.KC * (2 * NB * 128);
-    a.sfb = atoms;
+    if (NB == 8) return launch<8, true>(a, q, st);
+    if (NB == 16) return launch<16, true>(a, q, st);
+    a.split = static_cast<uint8_t *>(scratch);
     const int64_t blocks = ceil_div(rows * a.KC * 16, 256), most = int64_t(device_sms()) * 8;
     const cudaError_t e = launch_pdl(NB == 64 ? k_split_rows<64> : k_split_rows<128>,
                                      dim3(unsigned(blocks < most ? blocks : most)), dim3(256), 0, st, x, rows, K, a.KC,
-                                     codes, atoms);
+                                     static_cast<uint8_t *>(scratch));
     if (e != cudaSuccess) return e;
-    return NB == 64 ? launch<64, false>(a, q, codes, st) : launch<128, false>(a, q, codes, st);
+    return NB == 64 ? launch<64, false>(a, q, st) : launch<128, false>(a, q, st);
 }
 
 }  // namespace lmoe
