@@ -85,6 +85,38 @@ def test_two_blocks_in_place_and_captured(cuda_lib):
     assert torch.equal(res, want)
 
 
+def test_one_block_in_two_graphs_at_once(cuda_lib):
+    """The same block captured into two graphs, replayed on two streams at the same time, and run eagerly beside them
+    on a workspace of the caller's."""
+    lmoe = cuda_lib
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    layer, wl = _layer(lmoe)
+    b = _block(lmoe, layer, wl, 1024, True, g)
+    xs = [torch.randn(16, 1024, device=DEV, generator=g) for _ in range(3)]
+    want = [b.forward(x)[0] for x in xs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in xs[:2]:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(b.forward(x)[0])
+        graphs.append(gr)
+    streams = [torch.cuda.Stream(DEV) for _ in range(3)]
+    ws = torch.empty(b.workspace_size(16), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = b.forward(xs[2], ws=ws)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(eager, want[2])
+    with pytest.raises(lmoe.LmoeError):
+        b.forward(xs[0], ws=ws[:256])
+
+
 def test_block_refusals(cuda_lib):
     lmoe = cuda_lib
     g = torch.Generator(device=DEV)

@@ -649,8 +649,9 @@ class ResidualBlock:
     """The layer in a residual stream (lmoe_forward_residual_block): norm before
     (pre_w), projection, LatentMoE layer, projection, norm after (post_w), gate
     (fp32 [hidden]), residual scale.  W_in [d, hidden] and W_out [hidden, d]:
-    bf16 tensors or LinearMxfp4.  One forward at a time: the object owns its
-    workspace."""
+    bf16 tensors or LinearMxfp4.  One forward at a time on the object's own
+    workspace; forwards that may overlap on the GPU are given one each (`ws`), and
+    a forward captured into a graph without one gets its own."""
 
     def __init__(self, layer: Layer, W_in, W_out, pre_w=None, post_w=None, gate=None, scale: float = 1.0,
                  eps: float = 1e-5):
@@ -671,7 +672,11 @@ class ResidualBlock:
         return Projection(None, W.q.data_ptr(), W.s.data_ptr()) if isinstance(W, LinearMxfp4) else \
             Projection(W.data_ptr(), None, None)
 
-    def forward(self, res, x_n=None, gate=None, next_w=None, res_out=None, next_out=None, stream=None):
+    def workspace_size(self, T: int) -> int:
+        bank = self.layer.bank
+        return int(_res_block_ws(ctypes.byref(dims(T, bank.d, bank.E, self.layer.k, bank.I, self.layer.act)), self.hidden))
+
+    def forward(self, res, x_n=None, gate=None, next_w=None, res_out=None, next_out=None, ws=None, stream=None):
         """res [T, hidden] bf16 or fp32 -> (res_out, next_out or None).  x_n: the
         already normalised rows (a previous block's next_out); gate: per call, as
         residual_norm's, instead of the block's; next_w: the next block's pre_w."""
@@ -699,17 +704,24 @@ class ResidualBlock:
         nop = None if next_out is None else _arg(next_out, torch.bfloat16, (T, H), "next_out", di)
         layer, bank = self.layer, self.layer.bank
         D = dims(T, bank.d, bank.E, layer.k, bank.I, layer.act)
-        need = int(_res_block_ws(ctypes.byref(D), H))
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = _make((max(need, 256),), torch.uint8, res, stream)
+        if ws is None:
+            need = max(self.workspace_size(T), 256)
+            if torch.cuda.is_current_stream_capturing():
+                ws = _make((need,), torch.uint8, res, stream)
+            else:
+                if self._ws is None or self._ws.numel() < need:
+                    self._ws = _make((need,), torch.uint8, res, stream)
+                ws = self._ws
+        wsp = _arg(ws, torch.uint8, ws.shape, "ws", di)
         W = bank.struct()
         with torch.cuda.device(di):
             _check(_res_block(rp, fmt, xp, ctypes.byref(B), layer.Wr3.data_ptr(),
                               None if layer.bias is None else layer.bias.data_ptr(), ctypes.byref(W), ctypes.byref(D),
-                              H, rop, nop, self._ws.data_ptr(), self._ws.numel(), sp), "lmoe_forward_residual_block")
+                              H, rop, nop, wsp, ws.numel(), sp), "lmoe_forward_residual_block")
         return res_out, next_out
 
     def device_status(self) -> int:
+        """Of the last forward on the object's own workspace."""
         return last_device_status(self._ws)
 
 
