@@ -85,6 +85,39 @@ def test_grouped_refusals(lmoe):
     assert lmoe._grouped_linear(P, 32, P, None, 1, NULL, 64, 40, 0, P, P, need, NULL) == lmoe.ERR_INVALID_ARG
 
 
+def test_residual_block_refusals(lmoe):
+    size = lambda D, hidden: lmoe._res_block_ws(ctypes.byref(D), hidden)
+    D = lmoe.dims(8, 512, 896, 16, 64)
+    need = size(D, 1024)
+    assert need > lmoe.workspace_size(8, 512, 896, 16, 64)
+    assert size(lmoe.dims(8, 500, 896, 16, 64), 1024) == 0
+    for hidden in (0, 1000, -64, 32768 + 64):
+        assert size(D, hidden) == 0
+    W = lmoe.ExpertWeights(256, 256, 256, 256, 256, 256, lmoe.LAYOUT_TC)
+    bf, mx = lmoe.Projection(4096, None, None), lmoe.Projection(None, 4096, 4096)
+
+    def block(inp=bf, out=mx, pre=4096, post=4096, gate=None, kind=0, scale=1.0, eps=1e-5, nw=4096):
+        return lmoe.ResidualBlockStruct(inp, out, pre, post, gate, kind, scale, eps, nw)
+
+    def call(res=P, fmt=0, x_n=NULL, b=None, dims=D, hidden=1024, ro=P, no=P, ws=P, n=need, Wr3=P, weights=W):
+        b = block() if b is None else b
+        return lmoe._res_block(res, fmt, x_n, ctypes.byref(b), Wr3, NULL, ctypes.byref(weights), ctypes.byref(dims), hidden,
+                               ro, no, ws, n, NULL)
+
+    for bad in (dict(res=NULL), dict(res=ODD), dict(ro=NULL), dict(ro=ODD), dict(no=NULL), dict(fmt=2), dict(x_n=ODD),
+                dict(Wr3=NULL), dict(hidden=1000), dict(hidden=65536), dict(dims=lmoe.dims(8, 500, 896, 16, 64)),
+                dict(b=block(pre=None)), dict(b=block(kind=1)), dict(b=block(gate=4096)), dict(b=block(kind=5, gate=4096)),
+                dict(b=block(scale=float("nan"))), dict(b=block(eps=-1.0)), dict(b=block(inp=lmoe.Projection(None, 4096, None))),
+                dict(b=block(out=lmoe.Projection(None, 4096 + 16, 4096))), dict(b=block(inp=lmoe.Projection(4100, None, None))),
+                dict(b=block(post=4100)),
+                dict(weights=lmoe.ExpertWeights(256, 256, 256, 256, 256, 256, lmoe.LAYOUT_CANONICAL))):
+        assert call(**bad) == lmoe.ERR_INVALID_ARG, bad
+    for bad in (dict(ws=NULL), dict(n=need - 1), dict(ws=vp(4096 + 16))):
+        assert call(**bad) == lmoe.ERR_WORKSPACE, bad
+    assert call(dims=lmoe.dims(8, 512, 896, 16, 64, 2)) == lmoe.ERR_UNSUPPORTED
+    assert call(dims=lmoe.dims(0, 512, 896, 16, 64), res=NULL, ro=NULL, ws=NULL) == lmoe.OK
+
+
 def test_binding_refuses_tensors_off_the_gpu(lmoe):
     import torch
     x = torch.zeros(2, 64, dtype=torch.bfloat16)
