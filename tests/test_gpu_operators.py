@@ -183,6 +183,14 @@ def test_linear_mxfp4_wide(cuda_lib, rows, K, N):
     check_linear(cuda_lib, randn(g, rows, K), W, q, s)
 
 
+# enough tiles that 128-row ones are taken: several a CTA, a long K, ragged rows and columns
+@pytest.mark.parametrize("rows,K,N", [(161, 384, 14330), (383, 1632, 14337), (513, 7168, 2600), (1000, 1600, 2050)])
+def test_linear_mxfp4_large_tiles(cuda_lib, rows, K, N):
+    g = gen(rows + K + N)
+    q, s, W = mx_weights(cuda_lib, g, N, K)
+    check_linear(cuda_lib, randn(g, rows, K), W, q, s)
+
+
 @pytest.mark.parametrize("rows", [3, 24])
 def test_linear_mxfp4_keeps_every_bit_of_x(cuda_lib, rows):
     """One nonzero weight per output: out is x times it, exactly, for every

@@ -130,3 +130,10 @@ def test_binding_refuses_tensors_off_the_gpu(lmoe):
         lmoe.linear_mxfp4(x, torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8), 4)
     with pytest.raises(ValueError):
         lmoe.grouped_linear_bf16(x, torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32))
+
+
+def test_linear_workspace_never_shrinks(lmoe):
+    # a workspace for the most rows serves every smaller call, whichever tiles it takes
+    for K, N in ((96, 512), (1536, 8192), (2048, 8192), (7168, 14336)):
+        need = [lmoe.linear_mxfp4_workspace_size(rows, K, N) for rows in range(1, 1200)]
+        assert need == sorted(need), (K, N)

@@ -166,7 +166,10 @@ struct LCfg {
     static constexpr int SF_COLS = 4 + 4 * NAT;  // TMEM columns of a stage's scales
     static constexpr int SF_BASE = ACC * NC;
     static constexpr uint32_t TAIL = 1024 + (2 * 12 + 2 * ACC + 2) * 8 + 16;
-    static constexpr uint32_t RED = ClusterSum::red_bytes(NB);
+    // 128-row tiles run unsplit, and the room of the exchange is one more stage of
+    // the ring (7168 -> 3584, 512 rows: 26.1 us, against 30.0 with a shorter ring).
+    static constexpr bool SPLITS = NB < 128;
+    static constexpr uint32_t RED = SPLITS ? ClusterSum::red_bytes(NB) : 0;
     static constexpr int S_RAW = int(((227 * 1024) / CTAS - 1024 - TAIL - RED) / STAGE);
     static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
     static constexpr int COLS = SF_BASE + S * SF_COLS;
@@ -194,6 +197,8 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
 {
     using C = LCfg<NB, FUSED>;
     constexpr int S = C::S;
+    // 1 for 128-row tiles, and yet not a constant there: the code built for one was
+    // slower (7168 -> 3584, 512 rows: 28.3 us, against 26.1).
     const int KS = p.KS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -470,15 +475,20 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
 
 // Rows of a tile.  Up to 16 the kernel splits the rows itself, also of small
 // products whose 16-row tiles run at once (512 x 512, 100 rows: 3.9 us, against
-// 5.0 with 64-row tiles and the kernel before them).  Beyond, 64 rows, whose
-// chunks take no longer than 16 rows' (0.2 us, the weights' copies), until the
-// tensor cores are the bound (7168 -> 3584, 64- and 128-row tiles: 200 rows
-// 19.3 and 21.7 us, 512 rows 33.7 and 31.5 us).
+// 5.0 with 64-row tiles and the kernel before them).  Beyond, 64 or 128 rows,
+// whichever takes less time when all SMs take a tile at once, wave by wave: a
+// wave of 128 rows takes about 5/4 of one of 64 (7168 -> 14336, one wave each:
+// 24.8 and 19.5 us).  64 and 128 rows: 7168 -> 2304, 512 rows (one wave, one)
+// 21.5 and 25.1 us; 7168 -> 3584, 512 rows (two, one) 33.0 and 26.1 us;
+// 7168 -> 14336, 100 rows (two, one) 31.6 and 25.8 us, 383 rows (five, three)
+// 71.7 and 62.0 us.  Of 45 products measured it was wrong by at most 4%.
 int row_tile(int64_t rows, int64_t K, int64_t N)
 {
     if (rows <= 8) return 8;
     if (rows <= 16 || (K <= 12 * 128 && ceil_div(rows, 16) * ceil_div(N, 128) <= 152)) return 16;
-    return rows < 384 ? 64 : 128;
+    const int64_t cols = ceil_div(N, 128), waves64 = ceil_div(ceil_div(rows, 64) * cols, 152),
+                  waves128 = ceil_div(ceil_div(rows, 128) * cols, 152);
+    return waves64 * 4 <= waves128 * 5 ? 64 : 128;
 }
 bool splits_itself(int NB) { return NB <= 16; }
 
@@ -539,7 +549,7 @@ cudaError_t launch(LArgs a, const uint8_t *q, cudaStream_t st)
     // once, with some to spare: the previous kernel's blocks may still hold SMs.
     a.KS = 1;
     int64_t best = ceil_div(items, sms) * a.KC;
-    for (int ks = 2; ks <= MAX_KS && items * ks <= int64_t(sms) * C::CTAS && ks * 2 <= a.KC; ++ks) {
+    for (int ks = 2; C::SPLITS && ks <= MAX_KS && items * ks <= int64_t(sms) * C::CTAS && ks * 2 <= a.KC; ++ks) {
         const int64_t cost = ceil_div(items * ks, sms) * ceil_div(a.KC, ks) + 4 + NB * 3 / 16;
         if (cost < best && items * 10 <= max_clusters<NB, FUSED>(ks) * C::CTAS * 9) best = cost, a.KS = ks;
     }
@@ -554,9 +564,11 @@ cudaError_t launch(LArgs a, const uint8_t *q, cudaStream_t st)
 
 size_t linear_mxfp4_scratch_bytes(int64_t rows, int K, int N)
 {
-    const int64_t KC = ceil_div(K, 128), NB = row_tile(rows, K, N);
-    if (splits_itself(int(NB))) return 0;
-    return size_t(ceil_div(rows, NB) * KC * rows_block(int(NB)));
+    // The room of 128-row tiles for either size, so that more rows never need
+    // less and a workspace made for the most rows serves every smaller call.
+    static_assert(rows_block(128) == 2 * rows_block(64), "two small blocks in a large one");
+    if (splits_itself(row_tile(rows, K, N))) return 0;
+    return size_t(ceil_div(rows, 128) * ceil_div(K, 128) * rows_block(128));
 }
 
 cudaError_t launch_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int K, int N,
