@@ -544,7 +544,7 @@ cudaError_t launch(LArgs a, const uint8_t *q, cudaStream_t st)
     const int sms = device_sms();
     const int64_t items = int64_t(a.MT) * a.NTL;
     // As many ranks an item as make the longest SM's share of the chunks
-    // shortest, a split's exchange counted as 4 to 28 chunks (measured: 0.2 us
+    // shortest, a split's exchange counted as 5 to 16 chunks (measured: 0.2 us
     // a chunk; 0.9 us for 8 rows, 3.3 us for 64), while every cluster runs at
     // once, with some to spare: the previous kernel's blocks may still hold SMs.
     a.KS = 1;
