@@ -1,0 +1,34 @@
+"""Bounded waits in front of warp-wide instructions.  A wait on an mbarrier may
+run out for one lane of a warp and not for another (the barrier completes as the
+limit is reached); where the whole warp goes on to elect.sync, __syncwarp, votes
+or tcgen05 loads, all lanes have to take the same branch, so the wait's answer is
+one vote of the warp (mbar_wait_warp).  Read from the sources: no GPU is made to
+run into the fault."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "top_routing_mxfp4_gb300", "csrc")
+
+
+def waits(name):
+    """(line number, line) of every wait by single lanes in a source file, comments taken out."""
+    src = open(os.path.join(CSRC, name)).read()
+    src = re.sub(r"/\*.*?\*/", lambda m: re.sub(r"[^\n]", " ", m.group()), src, flags=re.S)
+    lines = [re.sub(r"//.*", "", l) for l in src.split("\n")]
+    return [(i + 1, l.strip()) for i, l in enumerate(lines) if re.search(r"\bmbar_wait(_cluster)?\(", l)]
+
+
+def test_the_warp_wait_is_a_vote():
+    src = open(os.path.join(CSRC, "tc_ptx.cuh")).read()
+    for f, inner in (("mbar_wait_warp", "mbar_wait"), ("mbar_wait_cluster_warp", "mbar_wait_cluster")):
+        body = re.search(r"bool %s\([^)]*\)\s*\{(.*?)\n\}" % f, src, flags=re.S)
+        assert body and "__all_sync(0xFFFFFFFFu, %s(" % inner in body.group(1)
+
+
+@pytest.mark.parametrize("name", ["k_grouped.cu", "k_linear_mxfp4.cu", "cluster_sum.cuh"])
+def test_operator_kernels_wait_by_warps(name):
+    """All roles of these kernels are whole warps; only the drain is waited for by one elected thread."""
+    alone = [w for w in waits(name) if "mbar_wait(drain," not in w[1]]
+    assert not alone, alone

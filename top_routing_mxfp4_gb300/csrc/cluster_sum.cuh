@@ -32,7 +32,7 @@ struct ClusterSum {
     static constexpr uint32_t red_bytes(int max_cols) { return uint32_t(max_cols + 8) * 512; }
 
     // By the 128 epilogue threads (named barrier 1), all columns staged: send,
-    // and wait for the others'.  False on timeout.
+    // and wait for the others'.  False on timeout (one answer a warp).
     __device__ bool exchange(long long limit) const
     {
         tc::fence_async_shared();
@@ -46,7 +46,8 @@ struct ClusterSum {
                                      n * 512, tc::cluster_map(tc::smem_u32(bar), t));
             }
         }
-        return tc::mbar_wait(bar, 0, limit);
+        __syncwarp();
+        return tc::mbar_wait_warp(bar, 0, limit);
     }
     // The sums of columns [c0, min(c0 + CW, end)) (this rank's) and row `row` of the tile.
     template <int CW>

@@ -257,9 +257,9 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             feed_next += step;
             return it < total ? it : -1;
         }
-        const bool ok = PAIR ? mbar_wait_cluster(&item_full[feed_q], feed_phase, p.limit)
-                             : mbar_wait(&item_full[feed_q], feed_phase, p.limit);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
+        const bool ok = PAIR ? mbar_wait_cluster_warp(&item_full[feed_q], feed_phase, p.limit)
+                             : mbar_wait_warp(&item_full[feed_q], feed_phase, p.limit);
+        if (!ok) {
             if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
             return -1;
         }
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     // (A pair's copies all count in on the leader's barriers.)
     auto settle = [&](int fills) {
         if (PAIR && rank > 0) return;
-        for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
+        for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait_warp(&full[f % S], (f / S) & 1, p.limit);
     };
 
     if (warp == 0 || (warp >= C::B0 && warp < C::FEED)) {
@@ -332,10 +332,9 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                 __syncwarp();
             }
             for (int kc = k0; kc < k1; ++kc) {
-                ok = mbar_wait(&empty[stage], phase ^ 1, p.limit);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = mbar_wait_warp(&empty[stage], phase ^ 1, p.limit);
+                if (!ok) {
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-                    ok = false;
                     break;
                 }
                 uint8_t *sb = stages + stage * C::STAGE;
@@ -393,11 +392,11 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             const GItem w = walk.at(it);
             const uint32_t id =
                 PAIR ? idesc_bf16_pair(uint32_t((w.nv + 31) & ~31)) : idesc_bf16(uint32_t((w.nv + 15) & ~15));
-            ok = mbar_wait(&acc_empty[acc], acc_phase ^ 1, p.limit);
+            ok = mbar_wait_warp(&acc_empty[acc], acc_phase ^ 1, p.limit);
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * NT);
             for (int kc = k0; kc < k1 && ok; ++kc) {
-                ok = mbar_wait(&full[stage], phase, p.limit);
+                ok = mbar_wait_warp(&full[stage], phase, p.limit);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -417,7 +416,6 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     phase ^= 1;
                 }
             }
-            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (elect_one()) PAIR ? tc_commit_pair(&acc_full[acc]) : tc_commit(&acc_full[acc]);
             __syncwarp();
@@ -465,8 +463,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             }
         };
         auto process = [&](const GItem &w, const float (&rw)[NW]) -> bool {
-            const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.limit);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
+            if (!mbar_wait_warp(&acc_full[acc], acc_phase, p.limit)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                 return false;
             }
@@ -551,8 +548,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (j < w.nv) cs.stage[j * 128 + 32 * q + lane] = __uint_as_float(v[j]);
-                const bool in = cs.exchange(p.limit);
-                if (!__all_sync(0xFFFFFFFFu, in)) {
+                if (!cs.exchange(p.limit)) {
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                     return false;
                 }
@@ -605,8 +601,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         int q = 0;
         uint32_t phase = 0;
         for (bool more = true; more;) {
-            const bool ok = mbar_wait(&item_empty[q], phase ^ 1, p.limit);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
+            if (!mbar_wait_warp(&item_empty[q], phase ^ 1, p.limit)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                 break;
             }

@@ -249,10 +249,9 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
         for (int it = first; it < total && ok; it += step) {
             const int mt = it % p.MT, nt = it / p.MT;
             for (int kc = k0; kc < k1; ++kc) {
-                ok = mbar_wait(&empty[stage], phase ^ 1, p.limit);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = mbar_wait_warp(&empty[stage], phase ^ 1, p.limit);
+                if (!ok) {
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-                    ok = false;
                     break;
                 }
                 uint8_t *sb = stages + stage * C::STAGE;
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
             }
         }
         if (!ok)  // copies still in flight land before the CTA ends (bounded)
-            for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait(&full[f % S], (f / S) & 1, p.limit);
+            for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait_warp(&full[f % S], (f / S) & 1, p.limit);
     } else if (FUSED && warp >= 6) {
         // ---------------- the rows, split here: team t takes chunks t, t + TEAMS, .. ----------------
         const int per = k1 - k0, mine = total > first ? (total - first + step - 1) / step : 0;
@@ -300,8 +299,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
         };
         auto split = [&](int f, const uint4 (&u)[C::UNITS]) -> bool {
             const int stage = f % S;
-            const bool ok = mbar_wait(&empty[stage], uint32_t(f / S + 1) & 1, p.limit);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
+            if (!mbar_wait_warp(&empty[stage], uint32_t(f / S + 1) & 1, p.limit)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                 return false;
             }
@@ -349,11 +347,11 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
         for (int it = first; it < total && ok; it += step) {
             const int nv = min(NB, p.rows - it / p.MT * NB);
             const uint32_t N = uint32_t((NB + nv + 15) & ~15);  // hi rows, padding, lo rows
-            ok = mbar_wait(&acc_empty[acc], acc_phase ^ 1, p.limit);
+            ok = mbar_wait_warp(&acc_empty[acc], acc_phase ^ 1, p.limit);
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * C::NC);
             for (int kc = k0; kc < k1 && ok; ++kc) {
-                ok = mbar_wait(&full[stage], phase, p.limit);
+                ok = mbar_wait_warp(&full[stage], phase, p.limit);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -375,7 +373,6 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
                     phase ^= 1;
                 }
             }
-            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (elect_one()) tc_commit(&acc_full[acc]);
             __syncwarp();
@@ -401,8 +398,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
         for (int it = first; it < total; it += step) {
             const int mt = it % p.MT, row0 = it / p.MT * NB;
             const int nv = min(NB, p.rows - row0);
-            const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.limit);
-            if (!__all_sync(0xFFFFFFFFu, ok)) {
+            if (!mbar_wait_warp(&acc_full[acc], acc_phase, p.limit)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                 break;
             }
@@ -435,8 +431,7 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
                     for (int j = 0; j < CW; ++j)
                         if (c0 + j < nv) cs.stage[(c0 + j) * 128 + 32 * q + lane] = y[j];
                 }
-                const bool in = cs.exchange(p.limit);
-                if (!__all_sync(0xFFFFFFFFu, in)) {
+                if (!cs.exchange(p.limit)) {
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                     break;
                 }

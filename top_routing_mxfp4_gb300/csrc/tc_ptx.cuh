@@ -56,6 +56,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, long l
         if (clock64() - t0 > limit) return false;
     return true;
 }
+// The same by all lanes of a warp, which get one answer: a barrier that completes
+// as the limit is reached is too late for some lanes and not for others, and what
+// follows (elect.sync, __syncwarp, tcgen05 loads) needs all of them.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, long long limit = 4000000000LL)
+{
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, limit));
+}
 
 // ---- TMA and bulk copies --------------------------------------------------------------
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
@@ -354,6 +361,10 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
         if (done) return true;
         if (clock64() - t0 > limit) return false;
     }
+}
+__device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t *bar, uint32_t parity, long long limit)
+{
+    return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity, limit));
 }
 
 // ---- thread-block clusters ----------------------------------------------------------------
