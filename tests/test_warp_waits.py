@@ -32,3 +32,15 @@ def test_operator_kernels_wait_by_warps(name):
     """All roles of these kernels are whole warps; only the drain is waited for by one elected thread."""
     alone = [w for w in waits(name) if "mbar_wait(drain," not in w[1]]
     assert not alone, alone
+
+
+def test_a_lost_item_is_not_the_end_of_the_items():
+    """A wait for the next item that runs out sends producers and the MMA warp down their failure path (copies and
+    MMAs in flight are waited for before shared and tensor memory go), unlike the end of the items."""
+    src = open(os.path.join(CSRC, "k_grouped.cu")).read()
+    src = re.sub(r"//.*", "", src)
+    fetch = re.search(r"auto next_item = .*?\n    \};", src, flags=re.S).group()
+    assert re.search(r"LMOE_ERR_TIMEOUT\);\s*return LOST;", fetch)
+    assert re.search(r"constexpr int NO_MORE = -1, LOST = -2;", src)
+    takers = re.findall(r"const int it = next_item\(\);\s*if \(it < 0\) \{\s*ok = it != LOST;\s*break;", src)
+    assert len(takers) == 2  # the producers, the MMA warp

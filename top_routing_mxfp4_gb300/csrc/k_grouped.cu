@@ -244,24 +244,25 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     // this rank's K chunks
     const int k0 = KS > 1 ? rank * p.KC / KS : 0, k1 = KS > 1 ? (rank + 1) * p.KC / KS : p.KC;
     Walk<NT> walk{s_tiles, s_off, p.E, p.MT};
-    // This CTA's items, in order, -1 after the last; every lane of a warp calls
-    // it.  Many items are handed out as CTAs come free: SMs do not all stream
+    // This CTA's items, in order, NO_MORE after the last and LOST where the wait for
+    // one ran out; every lane of a warp calls it.  Many items are handed out as CTAs come free: SMs do not all stream
     // equally fast, and groups differ (a weighted down projection of 64 tokens
     // over 896 experts: its CTAs ended between 351 and 421 us with each
     // grid-th item).
+    constexpr int NO_MORE = -1, LOST = -2;
     int feed_q = 0, feed_next = first;
     uint32_t feed_phase = 0;
     auto next_item = [&]() -> int {
         if (!p.counter) {
             const int it = feed_next;
             feed_next += step;
-            return it < total ? it : -1;
+            return it < total ? it : NO_MORE;
         }
         const bool ok = PAIR ? mbar_wait_cluster_warp(&item_full[feed_q], feed_phase, p.limit)
                              : mbar_wait_warp(&item_full[feed_q], feed_phase, p.limit);
         if (!ok) {
             if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
-            return -1;
+            return LOST;
         }
         const int it = reinterpret_cast<volatile int32_t *>(s_item)[feed_q];
         __syncwarp();
@@ -292,7 +293,12 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         uint32_t phase = 0;
         bool ok = true;
         bool at_start = true;  // (the failure-path test withholds a CTA's first weight copy)
-        for (int it; ok && (it = next_item()) >= 0; at_start = false) {
+        for (; ok; at_start = false) {
+            const int it = next_item();
+            if (it < 0) {
+                ok = it != LOST;
+                break;
+            }
             const GItem w = walk.at(it);
             // This CTA's rows of the tile: all, or a pair's half of them (rounded to whole
             // MMA columns).  A pair's second CTA does not arrive on the stage's barrier, so
@@ -388,7 +394,12 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
-        for (int it; ok && (it = next_item()) >= 0;) {
+        while (ok) {
+            const int it = next_item();
+            if (it < 0) {
+                ok = it != LOST;
+                break;
+            }
             const GItem w = walk.at(it);
             const uint32_t id =
                 PAIR ? idesc_bf16_pair(uint32_t((w.nv + 31) & ~31)) : idesc_bf16(uint32_t((w.nv + 15) & ~15));
@@ -608,7 +619,7 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
             int it = 0;
             if (lane == 0) {
                 it = atomicAdd(p.counter, 1);
-                it = it < total ? it : -1;
+                it = it < total ? it : NO_MORE;
                 s_item[q] = it;
                 if (PAIR) cluster_store_i32(cluster_map(smem_u32(&s_item[q]), 1), it);
                 if (PAIR) cluster_arrive(cluster_map(smem_u32(&item_full[q]), 1));
