@@ -44,3 +44,12 @@ def test_a_lost_item_is_not_the_end_of_the_items():
     assert re.search(r"constexpr int NO_MORE = -1, LOST = -2;", src)
     takers = re.findall(r"const int it = next_item\(\);\s*if \(it < 0\) \{\s*ok = it != LOST;\s*break;", src)
     assert len(takers) == 2  # the producers, the MMA warp
+
+
+@pytest.mark.parametrize("name,whole", [("k_ffn_tc.cu", r"&acc_full\["), ("k_gemm_bf16.cu", r"&acc_full\["),
+                                        ("k_small.cu", r"&bar\["), ("k_route.cu", r"&bar\[buf\]")])
+def test_layer_kernels_wait_by_warps_where_warps_go_on(name, whole):
+    """The layer's kernels: producers and MMA issuers are single threads, but the epilogues' tcgen05 loads and the
+    small-batch and selection kernels' warp-wide products, sums and votes follow waits of whole warps."""
+    alone = [w for w in waits(name) if re.search(r"mbar_wait\(" + whole, w[1])]
+    assert not alone, alone

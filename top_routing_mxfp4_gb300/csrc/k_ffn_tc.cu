@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::THREADS, 1)
             const int mode = mode_of(it);
             [[maybe_unused]] const int qbase = s_off[w.e] + w.n_tile * NT;  // first permuted row of the tile (down)
             if (threadIdx.x == 64) LMOE_TRACE_EV(2, 0x40 | MODE, it, 0);  // epilogue: waiting
-            if (!mbar_wait(&acc_full[acc], acc_phase, p.wait_limit)) {
+            if (!mbar_wait_warp(&acc_full[acc], acc_phase, p.wait_limit)) {
                 set_status(p.status, LMOE_ERR_TIMEOUT);
                 return false;
             }

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(192, 1)
         for (int it = blockIdx.x; it < total; it += gridDim.x) {
             const int mt = it % p.MT, rest = it / p.MT, nt = rest % p.NTL, ks = rest / p.NTL;
             const int nv = min(NB, p.T - nt * NB);
-            if (!mbar_wait(&acc_full[acc], acc_phase)) {
+            if (!mbar_wait_warp(&acc_full[acc], acc_phase)) {
                 set_status(p.status, LMOE_ERR_TIMEOUT);
                 break;
             }

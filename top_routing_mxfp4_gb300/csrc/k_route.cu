@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) k_topk_softmax_staged(const float *__rest
         const int buf = it & 1;
         const int gn = gidx + int(gridDim.x);
         if (threadIdx.x == 0 && gn < ngroups) issue(gn, buf ^ 1);  // the other buffer is free (barrier below)
-        if (!tc::mbar_wait(&bar[buf], uint32_t((it >> 1) & 1))) {
+        if (!tc::mbar_wait_warp(&bar[buf], uint32_t((it >> 1) & 1))) {
             if (threadIdx.x == 0) set_status(status, LMOE_ERR_TIMEOUT);
             break;
         }

@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(32 * G_WARPS) k_small_gateup(const uint8_t *__
         group_sync();  // the quarter's scales are in place (and, the first time, x^)
         // a wait that runs out records the timeout; every thread then leaves
         // at the CTA barrier below (the products of this unit are discarded)
-        const bool landed = tc::mbar_wait(&bar[q], parity);
+        const bool landed = tc::mbar_wait_warp(&bar[q], parity);
         if (!landed && gt == 0) set_status(sp.status, LMOE_ERR_TIMEOUT);
         // block products on the tensor cores: lane (g, t4) reads pair slot g's
         // token (the B column) and accumulates pair slots 2 t4, 2 t4 + 1 (C)
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(32 * G_WARPS) k_small_gateup(const uint8_t *__
         if (next) issue(unit_n, e_n);
         if (__syncthreads_or(!landed)) {  // every quarter's sums are in place, or some wait ran out
             // copies already issued for the next unit land before the CTA ends (bounded)
-            if (next) tc::mbar_wait(&bar[q], parity);
+            if (next) tc::mbar_wait_warp(&bar[q], parity);
             return;
         }
         if (warp < np) {
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(32 * D_WARPS) k_small_down(const uint8_t *__re
         }
     };
     for (int g = 0; g < ngroups; ++g) {
-        if (!tc::mbar_wait(&bar[g & 1], uint32_t((g >> 1) & 1))) {
+        if (!tc::mbar_wait_warp(&bar[g & 1], uint32_t((g >> 1) & 1))) {
             set_status(sp.status, LMOE_ERR_TIMEOUT);
             return;
         }
