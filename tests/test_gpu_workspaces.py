@@ -1,0 +1,59 @@
+"""Who may write a workspace, and when: the ones that layers and blocks keep
+between calls, across streams and captures."""
+import pytest
+import torch
+
+import lmoe_inputs as gen
+from test_gpu_residual_block import _block, _layer
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _made(lmoe, kind):
+    """(object with a kept workspace, a call of it on T rows)."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    layer, wl = _layer(lmoe)
+    if kind == "layer":
+        return layer, lambda T, **a: layer.forward(torch.ones(T, wl.d, device=DEV, dtype=torch.bfloat16), **a)
+    b = _block(lmoe, layer, wl, 1024, False, g)
+    x = lambda T: torch.ones(T, 1024, device=DEV, dtype=torch.bfloat16)
+    if kind == "residual_block":
+        return b, lambda T, **a: b.forward(x(T), **a)
+    c = lmoe.Block(b.W_in, layer, b.W_out)
+    return c, lambda T, **a: c.forward(x(T), **a)
+
+
+@pytest.mark.parametrize("kind", ["layer", "block", "residual_block"])
+@pytest.mark.parametrize("how", ["current", "argument"])
+def test_a_replaced_workspace_waits_for_its_last_stream(cuda_lib, kind, how):
+    """A workspace made on one stream, used on another behind long work and then replaced by a larger one is not given
+    to the first stream's next allocations while that work runs."""
+    _made(cuda_lib, kind)[1](400)  # (kernels are loaded before the long work)
+    obj, call = _made(cuda_lib, kind)
+    a, b = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
+    with torch.cuda.stream(a):
+        call(40)
+    a.synchronize()
+    old, n = obj._ws.data_ptr(), obj._ws.numel()
+    run = (lambda T: call(T)) if how == "current" else (lambda T: call(T, stream=b))
+    torch.cuda.synchronize()
+    b.wait_stream(a)
+    with torch.cuda.stream(b):
+        torch.cuda._sleep(1_000_000_000)  # about half a second
+        if how == "current":
+            run(40)
+    if how == "argument":
+        with torch.cuda.stream(a):
+            run(40)
+            run(400)
+    else:
+        with torch.cuda.stream(b):
+            run(400)
+    assert obj._ws.numel() > n
+    with torch.cuda.stream(a):
+        got = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(20)]
+    assert not b.query()  # still in the long work
+    assert all(t.data_ptr() + n <= old or old + n <= t.data_ptr() for t in got)
+    torch.cuda.synchronize()

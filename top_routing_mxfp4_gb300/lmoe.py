@@ -241,6 +241,23 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _on(stream):
+    """Allocations in the order of a call's stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _kept_workspace(ws, nbytes: int, device, stream):
+    """The workspace an object keeps between calls: `ws`, or a larger one made in
+    the order of the call's stream.  It is recorded on that stream, so that its
+    memory, once it is replaced or dropped, goes to no other tensor while the
+    stream still works on it."""
+    if ws is None or ws.numel() < nbytes:
+        with _on(stream):
+            ws = workspace(nbytes, device)
+    ws.record_stream(torch.cuda.current_stream(ws.device) if stream is None else stream)
+    return ws
+
+
 # ---- load-time conversion ----------------------------------------------------------
 
 def mxfp4_bytes(nmat: int, rows: int, K: int, layout: int):
@@ -488,10 +505,10 @@ class Layer:
         self.Wr3 = prepare_router(Wr)
         self._ws = None
 
-    def workspace(self, T: int) -> torch.Tensor:
-        need = workspace_size(T, self.bank.d, self.bank.E, self.k, self.bank.I)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = workspace(need, self.Wr.device)
+    def workspace(self, T: int, stream=None) -> torch.Tensor:
+        """The layer's own workspace, made larger if T tokens need it, for a call on `stream`."""
+        self._ws = _kept_workspace(self._ws, workspace_size(T, self.bank.d, self.bank.E, self.k, self.bank.I),
+                                   self.Wr.device, stream)
         return self._ws
 
     def forward(self, x, y=None, topk_idx=None, topk_w=None, logits=None, stream=None):
@@ -499,7 +516,7 @@ class Layer:
         _need(x, torch.bfloat16, (T, d), "x")
         D = dims(T, d, self.bank.E, self.k, self.bank.I, self.act)
         y = _empty((T, d), torch.bfloat16, x.device) if y is None else y
-        ws = self.workspace(T)
+        ws = self.workspace(T, stream)
         W = self.bank.struct()
         _check(_forward(_ptr(x), _ptr(self.Wr3), _ptr(self.bias), ctypes.byref(W), ctypes.byref(D), _ptr(y),
                         _ptr(topk_idx), _ptr(topk_w), _ptr(logits), _ptr(ws), ws.numel(), _stream(stream)),
@@ -541,7 +558,7 @@ def _arg(t, dtype, shape, name, di):
 
 def _make(shape, dtype, x, stream):
     """An uninitialised tensor on x's device, allocated in the order of the call's stream."""
-    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+    with _on(stream):
         return torch.empty(shape, dtype=dtype, device=x.device)
 
 
@@ -709,9 +726,7 @@ class ResidualBlock:
             if torch.cuda.is_current_stream_capturing():
                 ws = _make((need,), torch.uint8, res, stream)
             else:
-                if self._ws is None or self._ws.numel() < need:
-                    self._ws = _make((need,), torch.uint8, res, stream)
-                ws = self._ws
+                ws = self._ws = _kept_workspace(self._ws, need, res.device, stream)
         wsp = _arg(ws, torch.uint8, ws.shape, "ws", di)
         W = bank.struct()
         with torch.cuda.device(di):
@@ -740,8 +755,7 @@ class Block:
         _need(self.W_out, torch.bfloat16, (hidden, bank.d), "W_out")
         D = dims(T, bank.d, bank.E, k, bank.I)
         need = int(_block_ws(ctypes.byref(D), hidden))
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = workspace(need, x_h.device)
+        self._ws = _kept_workspace(self._ws, need, x_h.device, stream)
         out = _empty((T, hidden), torch.bfloat16, x_h.device) if out is None else out
         W = bank.struct()
         _check(_forward_block(_ptr(x_h), _ptr(self.W_in), _ptr(self.layer.Wr3), _ptr(self.layer.bias), ctypes.byref(W),
