@@ -57,3 +57,38 @@ def test_a_replaced_workspace_waits_for_its_last_stream(cuda_lib, kind, how):
     assert not b.query()  # still in the long work
     assert all(t.data_ptr() + n <= old or old + n <= t.data_ptr() for t in got)
     torch.cuda.synchronize()
+
+
+def test_a_forward_captured_through_its_stream_argument_has_its_own_workspace(cuda_lib):
+    """Whether a forward is captured is a question about the call's stream, not the current one: captured on `stream`
+    with another stream current, the graph does not use the workspace that the block keeps for eager calls."""
+    lmoe = cuda_lib
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    layer, wl = _layer(lmoe)
+    b = _block(lmoe, layer, wl, 1024, True, g)
+    x = torch.randn(16, 1024, device=DEV, generator=g)
+    want = b.forward(x)[0].clone()
+    s, gr = torch.cuda.Stream(DEV), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        gr.capture_begin()
+    out = b.forward(x, stream=s)[0]
+    with torch.cuda.stream(s):
+        gr.capture_end()
+    b._ws.fill_(255)
+    torch.cuda.synchronize()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert bool((b._ws == 255).all())
+    # the other way round: an eager call beside a capture on the current stream keeps the block's workspace
+    y = torch.zeros(64, device=DEV)
+    gr, s2 = torch.cuda.CUDAGraph(), torch.cuda.Stream(DEV)
+    with torch.cuda.graph(gr, stream=s, capture_error_mode="relaxed"):
+        y.add_(1)
+        out = b.forward(x, stream=s2)[0]
+    s2.synchronize()
+    assert torch.equal(out, want)
+    assert not bool((b._ws == 255).all())
+    assert b.device_status() == lmoe.OK

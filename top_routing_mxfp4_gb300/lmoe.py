@@ -723,7 +723,9 @@ class ResidualBlock:
         D = dims(T, bank.d, bank.E, layer.k, bank.I, layer.act)
         if ws is None:
             need = max(self.workspace_size(T), 256)
-            if torch.cuda.is_current_stream_capturing():
+            with _on(stream):
+                captured = torch.cuda.is_current_stream_capturing()
+            if captured:
                 ws = _make((need,), torch.uint8, res, stream)
             else:
                 ws = self._ws = _kept_workspace(self._ws, need, res.device, stream)
