@@ -1,9 +1,8 @@
-"""Who may write a workspace, and when: the ones that layers and blocks keep
-between calls, across streams and captures."""
+"""Memory that layers and blocks hold: the workspaces kept between calls, across
+streams and captures, and weights that have to lie on the call's device."""
 import pytest
 import torch
 
-import lmoe_inputs as gen
 from test_gpu_residual_block import _block, _layer
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +91,41 @@ def test_a_forward_captured_through_its_stream_argument_has_its_own_workspace(cu
     assert torch.equal(out, want)
     assert not bool((b._ws == 255).all())
     assert b.device_status() == lmoe.OK
+
+
+WEIGHTS = ["layer.Wr3", "layer.bias", "W_in.q", "W_in.s", "W_out.q", "W_out.s"] + \
+    [f"layer.bank.{w}_{p}" for w in ("gate", "up", "down") for p in "qs"]
+
+
+def _swap(b, path, change):
+    obj = b
+    *way, last = path.split(".")
+    for p in way:
+        obj = getattr(obj, p)
+    old = getattr(obj, last)
+    setattr(obj, last, change(old))
+    return lambda: setattr(obj, last, old)
+
+
+@pytest.mark.parametrize("mx", [True, False])
+def test_weights_off_the_calls_device_are_refused(cuda_lib, mx):
+    """Host addresses among the weights (a module moved by hand) are refused before anything is launched."""
+    lmoe = cuda_lib
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    layer, wl = _layer(lmoe)
+    layer.bias = torch.zeros(wl.E, device=DEV)
+    b = _block(lmoe, layer, wl, 1024, mx, g)
+    x = torch.randn(4, 1024, device=DEV, generator=g)
+    want = b.forward(x)[0]
+    for path in WEIGHTS if mx else ["W_in", "W_out"]:
+        back = _swap(b, path, lambda t: t.cpu())
+        with pytest.raises(ValueError, match=path.split(".")[-1]):
+            b.forward(x)
+        back()
+    for path, change in (("layer.bias", lambda t: t.double()), ("layer.bias", lambda t: t[:-1])):
+        back = _swap(b, path, change)
+        with pytest.raises(ValueError, match="bias"):
+            b.forward(x)
+        back()
+    assert torch.equal(b.forward(x)[0], want)

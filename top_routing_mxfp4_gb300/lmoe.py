@@ -556,6 +556,13 @@ def _arg(t, dtype, shape, name, di):
     return t.data_ptr()
 
 
+def _on_device(t, name, di):
+    """The address of weights whose type and shape were checked when they were taken in."""
+    if t.get_device() != di:
+        raise ValueError(f"{name}: on {t.device}, the call's tensors on cuda:{di}")
+    return t.data_ptr()
+
+
 def _make(shape, dtype, x, stream):
     """An uninitialised tensor on x's device, allocated in the order of the call's stream."""
     with _on(stream):
@@ -685,9 +692,10 @@ class ResidualBlock:
         self._ws = None
 
     @staticmethod
-    def _proj(W):
-        return Projection(None, W.q.data_ptr(), W.s.data_ptr()) if isinstance(W, LinearMxfp4) else \
-            Projection(W.data_ptr(), None, None)
+    def _proj(W, name, di):
+        if isinstance(W, LinearMxfp4):
+            return Projection(None, _on_device(W.q, name + ".q", di), _on_device(W.s, name + ".s", di))
+        return Projection(_on_device(W, name, di), None, None)
 
     def workspace_size(self, T: int) -> int:
         bank = self.layer.bank
@@ -707,8 +715,9 @@ class ResidualBlock:
         kind, gp = (GATE_NONE, None) if gate is None else _gate(gate, T, H, di)
         if next_w is None and next_out is not None:
             raise ValueError("next_out without next_w")
-        B = ResidualBlockStruct(self._proj(self.W_in), self._proj(self.W_out), vec(self.pre_w, "pre_w"),
-                                vec(self.post_w, "post_w"), gp, kind, self.scale, self.eps, vec(next_w, "next_w"))
+        B = ResidualBlockStruct(self._proj(self.W_in, "W_in", di), self._proj(self.W_out, "W_out", di),
+                                vec(self.pre_w, "pre_w"), vec(self.post_w, "post_w"), gp, kind, self.scale, self.eps,
+                                vec(next_w, "next_w"))
         if x_n is None and self.pre_w is None:
             raise ValueError("neither x_n nor pre_w")
         if stream is not None and stream.device.index != di:
@@ -721,6 +730,10 @@ class ResidualBlock:
         nop = None if next_out is None else _arg(next_out, torch.bfloat16, (T, H), "next_out", di)
         layer, bank = self.layer, self.layer.bank
         D = dims(T, bank.d, bank.E, layer.k, bank.I, layer.act)
+        router = _arg(layer.Wr3, torch.bfloat16, (3, bank.E, bank.d), "Wr3", di)
+        bias = None if layer.bias is None else _arg(layer.bias, torch.float32, (bank.E,), "bias", di)
+        W = ExpertWeights(*(_on_device(getattr(bank, name), name, di) for name in
+                            ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s")), LAYOUT_TC)
         if ws is None:
             need = max(self.workspace_size(T), 256)
             with _on(stream):
@@ -730,11 +743,9 @@ class ResidualBlock:
             else:
                 ws = self._ws = _kept_workspace(self._ws, need, res.device, stream)
         wsp = _arg(ws, torch.uint8, ws.shape, "ws", di)
-        W = bank.struct()
         with torch.cuda.device(di):
-            _check(_res_block(rp, fmt, xp, ctypes.byref(B), layer.Wr3.data_ptr(),
-                              None if layer.bias is None else layer.bias.data_ptr(), ctypes.byref(W), ctypes.byref(D),
-                              H, rop, nop, wsp, ws.numel(), sp), "lmoe_forward_residual_block")
+            _check(_res_block(rp, fmt, xp, ctypes.byref(B), router, bias, ctypes.byref(W), ctypes.byref(D), H, rop,
+                              nop, wsp, ws.numel(), sp), "lmoe_forward_residual_block")
         return res_out, next_out
 
     def device_status(self) -> int:
