@@ -18,9 +18,10 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # LMOE_LIBRARY selects another build of the same library (e.g. a trace build)
 LIB_PATH = os.environ.get("LMOE_LIBRARY") or os.path.join(_PKG, "liblmoe.so")
 
-if not os.path.exists(LIB_PATH) or not os.path.exists(os.path.join(_PKG, "_lmoe_torch.so")):
-    raise ImportError(f"{LIB_PATH} or _lmoe_torch.so is missing: build it with `python -c \"import __graft_entry__ as g; g.build()\"` "
-                      "or `python top_routing_mxfp4_gb300/build.py`")
+_HOW = ("build it with `python -c \"import __graft_entry__ as g; g.build()\"` or "
+        "`python top_routing_mxfp4_gb300/build.py`")
+if not os.path.exists(LIB_PATH):
+    raise ImportError(f"{LIB_PATH} is missing: {_HOW}")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -90,11 +91,21 @@ _set_events = _sig("lmoe_set_stage_events", ctypes.c_int, ctypes.POINTER(_vp), _
 _kernel_count = _sig("lmoe_forward_kernel_count", _i32, _DP)
 
 
-_rms_norm = _sig("lmoe_rms_norm", ctypes.c_int, _vp, _i32, _vp, ctypes.c_float, _i64, _i32, _vp, _vp)
-_residual_norm = _sig("lmoe_residual_norm", ctypes.c_int, _vp, _vp, _i32, _vp, _vp, _i32, ctypes.c_float,
-                      ctypes.c_float, _vp, _i64, _i32, _vp, _vp, _vp)
-_linear_mx_ws = _sig("lmoe_linear_mxfp4_workspace_size", _sz, _i64, _i32, _i32)
-_linear_mx = _sig("lmoe_linear_mxfp4", ctypes.c_int, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _sz, _vp)
+def _sig_later(name, restype, *argtypes):
+    """As _sig; an earlier library chosen by LMOE_LIBRARY may lack the entry point, which a call then says."""
+    if hasattr(_lib, name):
+        return _sig(name, restype, *argtypes)
+
+    def missing(*_):
+        raise RuntimeError(f"{name} is not in {LIB_PATH}")
+    return missing
+
+
+_rms_norm = _sig_later("lmoe_rms_norm", ctypes.c_int, _vp, _i32, _vp, ctypes.c_float, _i64, _i32, _vp, _vp)
+_residual_norm = _sig_later("lmoe_residual_norm", ctypes.c_int, _vp, _vp, _i32, _vp, _vp, _i32, ctypes.c_float,
+                            ctypes.c_float, _vp, _i64, _i32, _vp, _vp, _vp)
+_linear_mx_ws = _sig_later("lmoe_linear_mxfp4_workspace_size", _sz, _i64, _i32, _i32)
+_linear_mx = _sig_later("lmoe_linear_mxfp4", ctypes.c_int, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _sz, _vp)
 
 
 class Groups(ctypes.Structure):
@@ -103,11 +114,11 @@ class Groups(ctypes.Structure):
 
 
 _GP = ctypes.POINTER(Groups)
-_grouped_ws = _sig("lmoe_grouped_workspace_size", _sz)
-_grouped_linear = _sig("lmoe_grouped_linear_bf16", ctypes.c_int, _vp, _i64, _vp, _GP, _i32, _vp, _i32, _i32, _i32, _vp,
-                       _vp, _sz, _vp)
-_grouped_swiglu = _sig("lmoe_grouped_swiglu_bf16", ctypes.c_int, _vp, _i64, _vp, _vp, _GP, _i32, _i32, _i32, _vp, _vp,
-                       _sz, _vp)
+_grouped_ws = _sig_later("lmoe_grouped_workspace_size", _sz)
+_grouped_linear = _sig_later("lmoe_grouped_linear_bf16", ctypes.c_int, _vp, _i64, _vp, _GP, _i32, _vp, _i32, _i32, _i32,
+                             _vp, _vp, _sz, _vp)
+_grouped_swiglu = _sig_later("lmoe_grouped_swiglu_bf16", ctypes.c_int, _vp, _i64, _vp, _vp, _GP, _i32, _i32, _i32, _vp,
+                             _vp, _sz, _vp)
 class Projection(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("q", ctypes.c_void_p), ("s", ctypes.c_void_p)]
 
@@ -118,9 +129,9 @@ class ResidualBlockStruct(ctypes.Structure):
                 ("eps", ctypes.c_float), ("next_w", ctypes.c_void_p)]
 
 
-_res_block_ws = _sig("lmoe_residual_block_workspace_size", _sz, _DP, _i32)
-_res_block = _sig("lmoe_forward_residual_block", ctypes.c_int, _vp, _i32, _vp, ctypes.POINTER(ResidualBlockStruct), _vp,
-                  _vp, _WP, _DP, _i32, _vp, _vp, _vp, _sz, _vp)
+_res_block_ws = _sig_later("lmoe_residual_block_workspace_size", _sz, _DP, _i32)
+_res_block = _sig_later("lmoe_forward_residual_block", ctypes.c_int, _vp, _i32, _vp,
+                        ctypes.POINTER(ResidualBlockStruct), _vp, _vp, _WP, _DP, _i32, _vp, _vp, _vp, _sz, _vp)
 BF16, F32 = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
@@ -542,10 +553,27 @@ def linear_bf16(x, W, out=None, stream=None):
 
 # These calls run on the device of their first tensor and, by default, on that
 # device's current stream.  The short ones are bound in C++ (csrc/bind_torch.cpp).
-from . import _lmoe_torch as _fast  # noqa: E402
+# It is loaded at the first of them, so that the rest needs only the library.
+class _Binding:
+    def __getattr__(self, name):
+        global _fast
+        if name.startswith("_"):
+            raise AttributeError(name)
+        entries = (_rms_norm, _residual_norm, _linear_mx, _linear_mx_ws, _grouped_linear, _grouped_swiglu, _grouped_ws)
+        for f in entries:
+            if not hasattr(f, "argtypes"):
+                f()  # raises: not in this library
+        try:
+            from . import _lmoe_torch
+        except ImportError as e:
+            path = os.path.join(_PKG, "_lmoe_torch.so")
+            raise ImportError(f"{path} is missing or does not load ({e}): {_HOW}") from e
+        _lmoe_torch.bind(LmoeError, *(ctypes.cast(f, _vp).value for f in entries))
+        _fast = _lmoe_torch
+        return getattr(_fast, name)
 
-_fast.bind(LmoeError, *(ctypes.cast(f, _vp).value for f in (
-    _rms_norm, _residual_norm, _linear_mx, _linear_mx_ws, _grouped_linear, _grouped_swiglu, _grouped_ws)))
+
+_fast = _Binding()
 
 
 def _arg(t, dtype, shape, name, di):
