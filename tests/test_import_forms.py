@@ -78,3 +78,25 @@ for call in (lambda: lmoe.rms_norm(x, w), lambda: lmoe.residual_norm(x, x), lamb
 print(lmoe.version(), lmoe.small_batch_pairs())
 """, ROOT, LMOE_LIBRARY=str(lib))
     assert out.split() == ["earlier", "0"]
+
+
+def test_the_compiled_binding_is_of_this_torch_and_python(library, monkeypatch):
+    """It is rebuilt when torch or Python changed under it, whatever the files' times say, and one built for others is
+    refused."""
+    from top_routing_mxfp4_gb300 import build
+    import torch
+    assert not build._bind_stale()
+    assert torch.__version__ in build._bind_tag() and sys.implementation.cache_tag in build._bind_tag()
+    with monkeypatch.context() as m:
+        m.setattr(build, "_bind_tag", lambda: "another torch")
+        assert build._bind_stale()
+    out = _python("""
+import torch
+torch.__version__ = '0.0.0'
+from top_routing_mxfp4_gb300 import lmoe
+try:
+    lmoe.rms_norm(torch.zeros(2, 64, dtype=torch.bfloat16), torch.ones(64))
+except ImportError as e:
+    print(e)
+""", ROOT)
+    assert "0.0.0" in out and torch.__version__ in out

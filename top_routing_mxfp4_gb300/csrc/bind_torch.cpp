@@ -392,4 +392,14 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lmoe_torch", nullptr, -1, methods
 
 }  // namespace
 
-extern "C" PyObject *PyInit__lmoe_torch(void) { return PyModule_Create(&module); }
+// BUILT_FOR: the torch and Python of the build (build.py), whose layouts are
+// compiled in; lmoe.py compares it with what runs.
+extern "C" PyObject *PyInit__lmoe_torch(void)
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "BUILT_FOR", LMOE_BUILT_FOR) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import sys
 
 import torch
 
@@ -568,6 +569,9 @@ class _Binding:
         except ImportError as e:
             path = os.path.join(_PKG, "_lmoe_torch.so")
             raise ImportError(f"{path} is missing or does not load ({e}): {_HOW}") from e
+        here = f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+        if _lmoe_torch.BUILT_FOR != here:
+            raise ImportError(f"_lmoe_torch.so was built for {_lmoe_torch.BUILT_FOR}, this is {here}: {_HOW}")
         _lmoe_torch.bind(LmoeError, *(ctypes.cast(f, _vp).value for f in entries))
         _fast = _lmoe_torch
         return getattr(_fast, name)
