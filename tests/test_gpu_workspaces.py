@@ -129,3 +129,53 @@ def test_weights_off_the_calls_device_are_refused(cuda_lib, mx):
             b.forward(x)
         back()
     assert torch.equal(b.forward(x)[0], want)
+
+
+def test_errors_of_calls_without_a_workspace_can_be_asked_for(cuda_lib):
+    lmoe = cuda_lib
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    randn = lambda *s: torch.randn(*s, device=DEV, generator=g).bfloat16()
+    x, W, D = randn(40, 64), randn(3, 64, 64), randn(3, 64, 64)
+    off = torch.tensor([0, 8, 24, 40], dtype=torch.int32, device=DEV)
+    perm = torch.arange(40, dtype=torch.int32, device=DEV)
+    bad = torch.tensor([0, 8, 24, 4000], dtype=torch.int32, device=DEV)
+    w = torch.ones(40, device=DEV)
+    lin = lmoe.LinearMxfp4(torch.randn(96, 64, device=DEV, generator=g))
+    bank = lmoe.ExpertBankBf16(W, W, D)
+    calls = [(lambda o: lmoe.grouped_linear_bf16(x, W, o), lmoe.ERR_DEVICE_CHECK),
+             (lambda o: lmoe.grouped_swiglu_bf16(x, W, W, o), lmoe.ERR_DEVICE_CHECK),
+             (lambda o: lmoe.expert_ffn_bf16(x, bank, o, perm, w, 1), lmoe.ERR_DEVICE_CHECK)]
+    for call, code in calls:
+        call(off)
+        assert lmoe.last_call_status() == lmoe.OK
+        call(bad)
+        assert lmoe.last_call_status() == code
+    # only the first of the two products reads x's rows
+    lmoe.expert_ffn_bf16(x[:39], bank, off, perm, w, 1)
+    assert lmoe.last_call_status() == lmoe.ERR_DEVICE_CHECK
+    # a workspace of the caller's is asked by itself
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    lmoe.grouped_linear_bf16(x, W, bad, ws=ws)
+    lmoe.grouped_linear_bf16(x, W, off)
+    assert lmoe.last_call_status() == lmoe.OK and lmoe.last_device_status(ws) == lmoe.ERR_DEVICE_CHECK
+    for rows in (4, 40):
+        lmoe.set_wait_test(True, 20_000_000)  # about 10 ms of SM clocks
+        try:
+            lin.forward(randn(rows, 64))
+            torch.cuda.synchronize()
+        finally:
+            lmoe.set_wait_test(False, 0)
+        assert lmoe.last_call_status() == lmoe.ERR_TIMEOUT
+        lin.forward(randn(rows, 64))
+        assert lmoe.last_call_status() == lmoe.OK
+    # captured: of the latest replay
+    gr, o = torch.cuda.CUDAGraph(), off.clone()
+    lmoe.grouped_linear_bf16(x, W, o)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(gr):
+        lmoe.grouped_linear_bf16(x, W, o)
+    for now, code in ((bad, lmoe.ERR_DEVICE_CHECK), (off, lmoe.OK)):
+        o.copy_(now)
+        gr.replay()
+        assert lmoe.last_call_status() == code

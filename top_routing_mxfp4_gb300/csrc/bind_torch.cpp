@@ -31,6 +31,9 @@ struct Entries {
     decltype(&lmoe_grouped_workspace_size) grouped_workspace_size;
 } E = {};
 PyObject *g_error = nullptr;  // lmoe.LmoeError
+// The workspace of the latest call that made its own, kept so that the errors
+// the call found on the GPU can be asked for (lmoe.last_call_status).
+PyObject *g_own_ws = nullptr;
 
 struct Bad : std::runtime_error {
     using std::runtime_error::runtime_error;
@@ -148,6 +151,9 @@ struct Ws {
             need(*t, at::kByte, t->sizes(), "ws", dev);
         } else {
             own = at::zeros({int64_t(want < 256 ? 256 : want)}, like.options().dtype(at::kByte));
+            PyObject *o = THPVariable_Wrap(own);
+            if (!o) throw PyError();
+            Py_XSETREF(g_own_ws, o);
         }
         ptr = t->data_ptr();
         bytes = size_t(t->numel());
@@ -369,6 +375,22 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
+// own_ws() -> the workspace of the latest call that made its own, or None
+PyObject *own_ws(PyObject *, PyObject *)
+{
+    PyObject *o = g_own_ws ? g_own_ws : Py_None;
+    Py_INCREF(o);
+    return o;
+}
+
+// keep_ws(workspace): as if the latest call had made it
+PyObject *keep_ws(PyObject *, PyObject *ws)
+{
+    Py_INCREF(ws);
+    Py_XSETREF(g_own_ws, ws);
+    Py_RETURN_NONE;
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n)
 {
@@ -386,6 +408,8 @@ PyMethodDef methods[] = {
     {"residual_norm", FAST((counted<residual_norm, 10>)), METH_FASTCALL, nullptr},
     {"linear_mxfp4", FAST((counted<linear_mxfp4, 7>)), METH_FASTCALL, nullptr},
     {"grouped", FAST((counted<grouped, 11>)), METH_FASTCALL, nullptr},
+    {"own_ws", own_ws, METH_NOARGS, nullptr},
+    {"keep_ws", keep_ws, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lmoe_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

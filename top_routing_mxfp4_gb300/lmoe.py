@@ -637,8 +637,9 @@ def linear_mxfp4_workspace_size(rows: int, K: int, N: int) -> int:
 def linear_mxfp4(x, q, s, N: int, out=None, ws=None, stream=None):
     """out = bf16(x W^T): x bf16 [rows, K], W one MXFP4 matrix [N, K] in the
     tensor-core layout (q, s of quant_mxfp4 or repack_mxfp4).  `ws`: a zeroed
-    workspace of linear_mxfp4_workspace_size bytes, kept by the caller; one is
-    made for the call without it."""
+    workspace of linear_mxfp4_workspace_size bytes, kept by the caller
+    (last_device_status(ws) says what calls with it found); one is made for the
+    call without it (last_call_status)."""
     return _fast.linear_mxfp4(x, q, s, N, out, ws, stream)
 
 
@@ -652,7 +653,9 @@ def grouped_linear_bf16(x, W, offsets, perm=None, k: int = 1, gather=None, row_w
     with perm) or x[q], times W[e]^T, W bf16 [E, N, K].  Without row_w: bf16
     [P, N].  With row_w (fp32, P values in pair order): fp32 [P, N], row q
     times row_w[perm[q]].  `out` may be given in either type; rows in no group
-    are not written.  `ws`: a zeroed workspace kept by the caller."""
+    are not written.  `ws`: a zeroed workspace kept by the caller
+    (last_device_status(ws) says whether offsets or rows were bad); one is made
+    for the call without it (last_call_status)."""
     return _fast.grouped(x, W, None, offsets, perm, k, gather, row_w, out, ws, stream)
 
 
@@ -663,6 +666,19 @@ def grouped_swiglu_bf16(x, Wg, Wu, offsets, perm=None, k: int = 1, gather=None, 
     if Wu is None:
         raise ValueError("Wu: expected a tensor")
     return _fast.grouped(x, Wg, Wu, offsets, perm, k, gather, None, out, ws, stream)
+
+
+def last_call_status() -> int:
+    """The device status (as last_device_status) of the latest linear_mxfp4,
+    grouped_linear_bf16, grouped_swiglu_bf16 or expert_ffn_bf16 call, of any
+    thread, that was given no workspace; of its latest replay, if it was
+    captured.  The call's workspace is kept for this until the next such call.
+    Calls with a workspace of the caller's are asked with last_device_status."""
+    ws = _fast.own_ws()
+    if ws is None:
+        return OK
+    with torch.cuda.device(ws.device):
+        return last_device_status(ws)
 
 
 class LinearMxfp4:
@@ -697,6 +713,10 @@ def expert_ffn_bf16(x, bank: ExpertBankBf16, offsets, perm, topk_w, k: int, ws=N
     """expert_ffn on a bf16 bank: x bf16 [T, d] in token order -> yp fp32
     [T*k, d] in permuted order, as combine takes it (grouped_swiglu_bf16, then
     grouped_linear_bf16 with the gate weights)."""
+    if ws is None:  # one for both, so that neither's errors are lost
+        with _on(stream):
+            ws = torch.zeros(max(grouped_workspace_size(), 256), dtype=torch.uint8, device=x.device)
+        _fast.keep_ws(ws)
     h = grouped_swiglu_bf16(x, bank.gate, bank.up, offsets, perm, k, ws=ws, stream=stream)
     return grouped_linear_bf16(h, bank.down, offsets, perm, k, gather=False, row_w=topk_w, ws=ws, stream=stream)
 
@@ -707,7 +727,8 @@ class ResidualBlock:
     (fp32 [hidden]), residual scale.  W_in [d, hidden] and W_out [hidden, d]:
     bf16 tensors or LinearMxfp4.  One forward at a time on the object's own
     workspace; forwards that may overlap on the GPU are given one each (`ws`), and
-    a forward captured into a graph without one gets its own."""
+    a forward captured into a graph without one gets its own, which goes back to
+    the graph's memory behind it: give `ws` to ask for a captured forward's status."""
 
     def __init__(self, layer: Layer, W_in, W_out, pre_w=None, post_w=None, gate=None, scale: float = 1.0,
                  eps: float = 1e-5):
@@ -781,7 +802,7 @@ class ResidualBlock:
         return res_out, next_out
 
     def device_status(self) -> int:
-        """Of the last forward on the object's own workspace."""
+        """Of the last forward on the object's own workspace (one that was given no `ws` and not captured)."""
         return last_device_status(self._ws)
 
 
