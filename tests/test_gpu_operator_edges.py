@@ -1,0 +1,44 @@
+"""Values at the edges of the formats, and arguments that are no plain value, in
+the norms, the MXFP4 linear and the grouped products.
+
+Tolerances as in test_gpu_operators.py: U = 2^-24, a bf16 result off by at most
+half a step (2^-8 of its value, or 2^-134 among the subnormals)."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+U, HALF = 2.0 ** -24, 2.0 ** -8
+D = torch.float64
+
+
+@pytest.mark.parametrize("rows", [3, 40, 300])
+def test_gated_pair_far_below_zero(cuda_lib, rows):
+    """silu(g) u where exp(-g) comes near fp32's largest value and passes it.  One product a gate, so g and u are exact:
+    what is left is the exponential (2 ulp, absolute 2^-148 where it is subnormal), the add, the division and the
+    products (below 16 U), and the output's rounding."""
+    n = 128
+    gate = -torch.linspace(80, 104, n, device=DEV).bfloat16()
+    up = torch.tensor([1.0, -3.0, 8.0, 0.5], device=DEV).bfloat16().repeat(n // 4)
+    Wg, Wu = torch.zeros(1, n, 8, device=DEV).bfloat16(), torch.zeros(1, n, 8, device=DEV).bfloat16()
+    Wg[0, :, 0], Wu[0, :, 1] = gate, up
+    x = torch.zeros(rows, 8, device=DEV).bfloat16()
+    x[:, :2] = 1
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    h = cuda_lib.grouped_swiglu_bf16(x, Wg, Wu, off)
+    g, u = gate.to(D), up.to(D)
+    ref = g * torch.exp(g) / (1 + torch.exp(g)) * u
+    tol = ref.abs() * (HALF + 16 * U) + 2.0 ** -134 + 2.0 ** -148 * (g * u).abs()
+    assert bool(((h.to(D) - ref).abs() <= tol).all())
+
+
+def test_gated_pair_far_above_zero(cuda_lib):
+    """silu(g) = g up to fp32's exponential's end and beyond."""
+    n = 64
+    gate = torch.linspace(20, 200, n, device=DEV).bfloat16()
+    Wg, Wu = torch.zeros(1, n, 8, device=DEV).bfloat16(), torch.zeros(1, n, 8, device=DEV).bfloat16()
+    Wg[0, :, 0], Wu[0, :, 1] = gate, 1
+    x = torch.zeros(2, 8, device=DEV).bfloat16()
+    x[:, :2] = 1
+    h = cuda_lib.grouped_swiglu_bf16(x, Wg, Wu, torch.tensor([0, 2], dtype=torch.int32, device=DEV))
+    assert torch.equal(h, gate.expand(2, n))

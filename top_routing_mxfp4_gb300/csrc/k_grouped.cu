@@ -507,7 +507,10 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
                     for (int i = 0; i < 8; ++i) {
                         const float r = __shfl_xor_sync(0xFFFFFFFFu, up ? y[2 * i] : y[2 * i + 1], 16);
                         const float g = up ? r : y[2 * i], u = up ? y[2 * i + 1] : r;
-                        h[i] = __fdividef(g, 1.f + expf(-g)) * u;
+                        // g sigmoid(g) by exp(-|g|), so that the divisor stays in [1, 2]: one beyond
+                        // 2^126 (g < -87.3) would make the quick division's result 0
+                        const float e = expf(-fabsf(g));
+                        h[i] = __fdividef(g < 0.f ? g * e : g, 1.f + e) * u;
                     }
                     if (pairs) {
                         int row = c0 + 2 * odd + up;
