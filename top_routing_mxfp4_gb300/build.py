@@ -46,7 +46,8 @@ def sources():
 def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    deps = sources() + [h for p in (os.path.join(CSRC, "*.cuh"), os.path.join(CSRC, "*.h"), os.path.join(ROOT, "include", "*.h"))
+                        for h in glob.glob(p)]
     return max(os.path.getmtime(p) for p in deps) > os.path.getmtime(LIB)
 
 

@@ -36,9 +36,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include <atomic>
-
 #include "cluster_sum.cuh"
+#include "device_cache.h"
 #include "lmoe_internal.cuh"
 #include "tc_ptx.cuh"
 #include "tensor_map.cuh"
@@ -507,24 +506,24 @@ cudaLaunchConfig_t config(unsigned grid, cudaStream_t st, cudaLaunchAttribute (&
 }
 
 // How many clusters of ks CTAs run at once, one CTA an SM (a cluster lies within
-// one group of SMs, so sizes that do not divide a group's leave some idle);
-// asked once.  The runtime answers for one CTA an SM whenever a kernel uses
-// tensor memory; two that fit do run side by side.
+// one group of SMs, so sizes that do not divide a group's leave some idle), asked
+// once a device; 0 where the runtime does not say.  It answers for one CTA an SM
+// whenever a kernel uses tensor memory; two that fit do run side by side.
 template <int NB, bool FUSED>
 int max_clusters(int ks)
 {
-    static std::atomic<int> known[MAX_KS + 1];
-    int n = known[ks].load(std::memory_order_relaxed);
-    if (n > 0) return n;
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config<NB, FUSED>(unsigned(ks) * 512, nullptr, attr, ks);
-    attr[0].val.programmaticStreamSerializationAllowed = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_linear_mx<NB, FUSED>, &cfg) != cudaSuccess) {
+    static DeviceCache<MAX_KS + 1> known;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    return known.get(dev, ks, [ks] {
+        int n = 0;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = config<NB, FUSED>(unsigned(ks) * 512, nullptr, attr, ks);
+        attr[0].val.programmaticStreamSerializationAllowed = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k_linear_mx<NB, FUSED>, &cfg) == cudaSuccess) return n;
         cudaGetLastError();
-        n = 0;
-    }
-    known[ks].store(n > 0 ? n : 1, std::memory_order_relaxed);
-    return n > 0 ? n : 1;
+        return 0;
+    });
 }
 
 template <int NB, bool FUSED>
