@@ -287,7 +287,7 @@ typedef enum { LMOE_BF16 = 0, LMOE_F32 = 1 } lmoe_fmt;
 
 /* out[t][c] = bf16( x[t][c] * rsqrt(mean_c x[t][c]^2 + eps) * w[c] ): the norm
  * before a block.  x [T][H] of type x_fmt (the residual stream), w fp32 [H],
- * fp32 arithmetic.  H % 8 == 0, H <= 32768, eps >= 0. */
+ * fp32 arithmetic (a row's sum of squares stays below 2^128).  H % 8 == 0, H <= 32768, eps >= 0. */
 lmoe_status lmoe_rms_norm(const void *x, int32_t x_fmt, const float *w, float eps, int64_t T, int32_t H, uint16_t *out,
                           void *stream);
 
@@ -319,16 +319,21 @@ lmoe_status lmoe_residual_norm(const uint16_t *y, const void *res, int32_t res_f
 
 /* out[r][n] = bf16( sum_c x[r][c] * W[n][c] ): x bf16 [rows][K], W one MXFP4
  * matrix of N x K in LMOE_LAYOUT_TC (lmoe_quant_mxfp4 or lmoe_repack_mxfp4
- * with nmat = 1; q 32-byte, s 16-byte aligned), fp32 accumulation.  Unlike
- * the expert GEMMs the activations are not rounded to MXFP8: the products use
- * x as it is (see below).  K % 32 == 0, any N >= 1.  Made for the
+ * with nmat = 1; q 32-byte, s 16-byte aligned), accumulated in fp32 by the
+ * tensor core.  Unlike in the expert GEMMs the activations are not rounded to
+ * MXFP8: each 32 columns of a row enter as two e4m3 parts, which hold an
+ * element exactly down to 2^-14 of the 32's largest magnitude and to within
+ * 2^-22 of that magnitude below (a row whose outliers are larger than that
+ * loses bits of its smallest elements).  The larger part may exceed its element
+ * by 1/16, so sums are sure to stay finite where sum_c |x[r][c] W[n][c]| is
+ * below 2^128 / 1.0625.  K % 32 == 0, any N >= 1.  Made for the
  * hidden <-> latent projections of decode batches, whose time is the weight
  * stream (0.53 bytes per weight, against 2 of lmoe_linear_bf16); it holds for
  * any number of rows up to 2^29.  A row of x with an infinity or a NaN gives
- * NaN outputs in that row; out overlaps no input.  This call and the grouped products below leave the
- * workspace's status word alone unless they find an error, and one found
- * stays until it is cleared: clear it once before the workspace's first use
- * (lmoe_clear_device_status).  Calls that may overlap on the GPU, captured
+ * NaN outputs in that row; out overlaps no input.  This call and the grouped
+ * products below leave the workspace's status word alone unless they find an
+ * error, and one found stays until it is cleared: clear it once before the
+ * workspace's first use (lmoe_clear_device_status).  Calls that may overlap on the GPU, captured
  * graphs among them, need a workspace each. */
 size_t lmoe_linear_mxfp4_workspace_size(int64_t rows, int32_t K, int32_t N);
 lmoe_status lmoe_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int32_t K, int32_t N,
@@ -351,8 +356,10 @@ typedef struct {
 size_t lmoe_grouped_workspace_size(void);
 
 /* out[q][n] = w(q) * sum_c x[src(q)][c] * W[e(q)][n][c], for every row q of a
- * group: x bf16 [x_rows][K], W bf16 [E][N][K], fp32 accumulation; src(q) =
- * perm[q] / k with gather != 0, else q; w(q) = row_w[perm[q]] (row_w [P]), or 1 without
+ * group: x bf16 [x_rows][K], W bf16 [E][N][K], accumulated in fp32 by the tensor
+ * core (whose sums err about three times as much as fp32 sums one after another
+ * in a good order: fp32 rows of K = 512, relative norm 4.7e-7 against 1.6e-7);
+ * src(q) = perm[q] / k with gather != 0, else q; w(q) = row_w[perm[q]] (row_w [P]), or 1 without
  * row_w; out [P][N] bf16 or fp32 (out_fmt), rounded once.  Rows of out that
  * belong to no group are left as they were.  With fp32 out and the gate
  * weights as row_w, out is the yp that lmoe_combine takes.

@@ -42,3 +42,33 @@ def test_gated_pair_far_above_zero(cuda_lib):
     x[:, :2] = 1
     h = cuda_lib.grouped_swiglu_bf16(x, Wg, Wu, torch.tensor([0, 2], dtype=torch.int32, device=DEV))
     assert torch.equal(h, gate.expand(2, n))
+
+
+@pytest.mark.parametrize("rows", [2, 20, 200])
+def test_linear_mxfp4_near_the_largest_values(cuda_lib, rows):
+    """bf16's largest magnitudes and the smallest ones through weights of 1/2 and 1/4: sums as large as are sure to stay
+    finite, exact (one or two terms an output)."""
+    lmoe, K, N = cuda_lib, 64, 32
+    big = torch.finfo(torch.bfloat16).max
+    # output n: x[n] / 2 + x[n + 32] / 4
+    q = torch.zeros(N, K // 2, dtype=torch.uint8, device=DEV)
+    n = torch.arange(N, device=DEV)
+    for c in (n, n + 32):
+        q[n, c // 2] = torch.where(c % 2 == 0, 0x02, 0x20).to(torch.uint8)  # 1.0
+    s = torch.tensor([126, 125], dtype=torch.uint8, device=DEV).expand(N, 2).contiguous()
+    qt, st = lmoe.repack_mxfp4(q, s, 1, N, K)
+    x = torch.zeros(rows, K, device=DEV).bfloat16()
+    x[:, :32] = torch.tensor([big, -big, 2.0 ** 127, -(2.0 ** 126)], device=DEV).bfloat16().repeat(8)
+    x[1, 32:] = x[1, :32]
+    out = lmoe.linear_mxfp4(x, qt, st, N).to(D)
+    xd = x.to(D)
+    ref = xd[:, :32] / 2 + xd[:, 32:] / 4
+    assert torch.equal(out, ref.bfloat16().to(D)) and bool(torch.isfinite(out).all())
+    # the smallest: subnormal elements beside nothing larger are held exactly; half of one is rounded once
+    tiny = torch.finfo(torch.bfloat16).smallest_normal
+    x[:, :32] = torch.tensor([tiny, -tiny * 1.5, tiny * 2.0 ** -4, 4 * tiny], device=DEV).bfloat16().repeat(8)
+    x[:, 32:] = 0
+    out, ref = lmoe.linear_mxfp4(x, qt, st, N).to(D), x[:, :32].to(D) / 2
+    # a product below fp32's normal range may be flushed by the tensor core: 2^-126
+    assert bool(((out - ref).abs() <= 2.0 ** -126 + 2.0 ** -134).all())
+    assert torch.equal(out[:, 3::4], ref[:, 3::4])
