@@ -72,3 +72,14 @@ def test_linear_mxfp4_near_the_largest_values(cuda_lib, rows):
     # a product below fp32's normal range may be flushed by the tensor core: 2^-126
     assert bool(((out - ref).abs() <= 2.0 ** -126 + 2.0 ** -134).all())
     assert torch.equal(out[:, 3::4], ref[:, 3::4])
+
+
+def test_gather_without_a_truth_value_is_refused(cuda_lib):
+    """An argument whose truth value raises: that error, and no result beside it."""
+    x, W = torch.ones(4, 64, device=DEV).bfloat16(), torch.ones(1, 16, 64, device=DEV).bfloat16()
+    off = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    perm = torch.arange(4, dtype=torch.int32, device=DEV)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        cuda_lib.grouped_linear_bf16(x, W, off, perm, gather=torch.ones(2))
+    for gather in (True, torch.ones(1), 1):
+        assert bool((cuda_lib.grouped_linear_bf16(x, W, off, perm, gather=gather) == 64).all())

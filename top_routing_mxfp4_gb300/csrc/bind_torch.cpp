@@ -320,7 +320,8 @@ PyObject *grouped(PyObject *const *a)
     g.P = P;
     g.E = int32_t(n_exp);
     g.k = int32_t(k);
-    const bool gather = a[6] == Py_None ? perm : PyObject_IsTrue(a[6]) == 1;
+    const int gather = a[6] == Py_None ? int(perm) : PyObject_IsTrue(a[6]);
+    if (gather < 0) throw PyError();
     const void *rw = nullptr;
     if (a[7] != Py_None) {
         const at::Tensor &r = tensor(a[7], "row_w");
