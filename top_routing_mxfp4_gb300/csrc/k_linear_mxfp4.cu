@@ -476,6 +476,9 @@ __global__ void __launch_bounds__((LCfg<NB, FUSED>::THREADS), (LCfg<NB, FUSED>::
 // 21.5 and 25.1 us; 7168 -> 3584, 512 rows (two, one) 33.0 and 26.1 us;
 // 7168 -> 14336, 100 rows (two, one) 31.6 and 25.8 us, 383 rows (five, three)
 // 71.7 and 62.0 us.  Of 45 products measured it was wrong by at most 4%.
+// The tile decides the workspace's size, which must not depend on the device that
+// happens to be current, so the rule counts on the GB300's 152 SMs; the grid goes
+// by the device's own number.
 int row_tile(int64_t rows, int64_t K, int64_t N)
 {
     if (rows <= 8) return 8;

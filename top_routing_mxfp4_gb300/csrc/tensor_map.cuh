@@ -10,8 +10,7 @@ namespace lmoe {
 
 enum class MapType {
     BF16,  // boxes of 64 columns
-    BYTES,  // 128 columns
-    FP4     // packed, two a byte in memory; 128 columns, a byte each in shared memory
+    FP4    // packed, two a byte in memory; 128 columns, a byte each in shared memory
 };
 
 // A map of [rows][K] elements (rows K elements apart) in boxes of box_rows rows.
@@ -31,12 +30,11 @@ inline bool make_tensor_map(CUtensorMap *m, const void *base, MapType type, int6
     }();
     if (!encode) return false;
     const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(type == MapType::BF16 ? 2 * K : type == MapType::FP4 ? K / 2 : K)};
+    const cuuint64_t strides[1] = {cuuint64_t(type == MapType::BF16 ? 2 * K : K / 2)};
     const cuuint32_t box[2] = {type == MapType::BF16 ? 64u : 128u, cuuint32_t(box_rows)};
     const cuuint32_t step[2] = {1, 1};
-    const CUtensorMapDataType t = type == MapType::BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                  : type == MapType::FP4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
-                                                         : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapDataType t =
+        type == MapType::BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B;
     return encode(m, t, 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
