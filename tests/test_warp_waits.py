@@ -2,7 +2,7 @@
 run out for one lane of a warp and not for another (the barrier completes as the
 limit is reached); where the whole warp goes on to elect.sync, __syncwarp, votes
 or tcgen05 loads, all lanes have to take the same branch, so the wait's answer is
-one vote of the warp (mbar_wait_warp).  Read from the sources: no GPU is made to
+the warp's (mbar_wait_warp).  Read from the sources: no GPU is made to
 run into the fault."""
 import os
 import re
@@ -17,14 +17,18 @@ def waits(name):
     src = open(os.path.join(CSRC, name)).read()
     src = re.sub(r"/\*.*?\*/", lambda m: re.sub(r"[^\n]", " ", m.group()), src, flags=re.S)
     lines = [re.sub(r"//.*", "", l) for l in src.split("\n")]
-    return [(i + 1, l.strip()) for i, l in enumerate(lines) if re.search(r"\bmbar_wait(_cluster)?\(", l)]
+    return [(i + 1, l.strip()) for i, l in enumerate(lines) if re.search(r"\bmbar_(try_)?wait(_cluster)?\(", l)]
 
 
-def test_the_warp_wait_is_a_vote():
+def test_the_warp_wait_branches_by_votes():
     src = open(os.path.join(CSRC, "tc_ptx.cuh")).read()
-    for f, inner in (("mbar_wait_warp", "mbar_wait"), ("mbar_wait_cluster_warp", "mbar_wait_cluster")):
+    for f, look in (("mbar_wait_warp", "mbar_try_wait"), ("mbar_wait_cluster_warp", "mbar_try_wait_cluster")):
         body = re.search(r"bool %s\([^)]*\)\s*\{(.*?)\n\}" % f, src, flags=re.S)
-        assert body and "__all_sync(0xFFFFFFFFu, %s(" % inner in body.group(1)
+        assert body
+        branches = re.findall(r"\b(?:if|while) \((.*)\)", body.group(1))
+        assert len(branches) == 3
+        for b in branches:
+            assert re.match(r"!?__all_sync\(0xFFFFFFFFu, %s\(bar, parity\)\)|__any_sync\(0xFFFFFFFFu, clock64\(\)" % look, b), b
 
 
 @pytest.mark.parametrize("name", ["k_grouped.cu", "k_linear_mxfp4.cu", "cluster_sum.cuh"])
