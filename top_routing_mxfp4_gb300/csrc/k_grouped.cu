@@ -27,11 +27,11 @@
 // CTAs shares an item along K (cluster_sum.cuh).
 // Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
 //
-// Measured (896 experts, 3584 <-> 512): gate and up of 64 tokens 610 us (7.4
-// TB/s), of 8192 tokens 1060 us (94% of the floor by bytes), weighted down of 64
-// and 8192 tokens 312 and 824 us.  With several hundred gathered rows an expert
-// the copies of B bound it (8 experts x 1024 rows, 4096 x 4096: 202 us, 1.36
-// PFLOP/s; in expert order 1.5).
+// Measured (896 experts, 3584 <-> 512): gate and up of 64 tokens 609 to 623 us
+// (7.3 TB/s), of 8192 tokens 1072 to 1111 us by card (90 to 93% of the floor by
+// bytes), weighted down of 64 and 8192 tokens 317 and 820 us.  With several
+// hundred gathered rows an expert the copies of B bound it (8 experts x 1024 rows,
+// 4096 x 4096: 200 us, 1.37 PFLOP/s; in expert order 1.55).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

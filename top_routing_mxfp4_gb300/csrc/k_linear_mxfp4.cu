@@ -30,9 +30,10 @@
 // (cluster_sum.cuh).
 // Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
 //
-// Measured, 7168 -> 3584: 1, 16, 64 and 512 rows 6.6, 8.5, 10.5 and 31.6 us
-// (3.2 us of any dependent kernel's start among them); 1 row 7168 -> 28672 19.8
-// us (5.5 TB/s).
+// Measured, 7168 -> 3584: 1, 16, 64, 512 and 8192 rows 6.7, 8.4, 10.5, 26.3 and
+// 294 us (3.2 us of any dependent kernel's start among them; the last 1.43
+// PFLOP/s); 7168 -> 28672: 1 row 20 us (5.4 TB/s), 16 and 64 rows 33 us: there 224
+// weight tiles on 152 SMs take two whole tiles' time.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -174,6 +175,10 @@ struct LCfg {
     static constexpr int COLS = SF_BASE + S * SF_COLS;
     static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(COLS <= 512 && int(TMEM_COLS) * CTAS <= 512 && S >= 3, "pipeline");
+    // A team that comes to a slot has seen the slot freed TEAMS chunks before it: with
+    // fewer slots than teams its wait could be two turns of the ring ahead, where the
+    // barrier's parity says nothing.
+    static_assert(S >= TEAMS, "no team more than one turn of the ring ahead");
     static constexpr size_t SMEM = size_t(S) * STAGE + RED + TAIL;
 };
 
