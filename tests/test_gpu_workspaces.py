@@ -179,3 +179,62 @@ def test_errors_of_calls_without_a_workspace_can_be_asked_for(cuda_lib):
         o.copy_(now)
         gr.replay()
         assert lmoe.last_call_status() == code
+
+
+def test_what_a_call_on_another_stream_allocates_stays_its_own(cuda_lib, monkeypatch):
+    """Outputs and workspaces that a call with a stream argument allocates, let go while the call is still to run: their
+    memory goes to no allocation of the current stream before it has."""
+    lmoe = cuda_lib
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    layer, wl = _layer(lmoe)
+    T, d, E, k = 40, wl.d, wl.E, wl.k
+    x = torch.randn(T, d, device=DEV, generator=g).bfloat16()
+    Wr = torch.randn(E, d, device=DEV, generator=g)
+    w32 = torch.randn(1, 256, d, device=DEV, generator=g)
+    Wl = torch.randn(256, d, device=DEV, generator=g).bfloat16()
+    logits, idx, w = lmoe.route(x, Wr, k)
+    _, off, perm, inv, _ = lmoe.permute(idx, E)
+    xq, xs = lmoe.quant_mxfp8(x)
+    qc, sc = lmoe.quant_mxfp4(w32, layout=lmoe.LAYOUT_CANONICAL)
+    yp = lmoe.expert_ffn(xq, xs, layer.bank, off, perm, w, k)[0]
+    block = lmoe.Block(torch.randn(d, 1024, device=DEV, generator=g).bfloat16(), layer,
+                       torch.randn(1024, d, device=DEV, generator=g).bfloat16())
+    xh = torch.randn(T, 1024, device=DEV, generator=g).bfloat16()
+    calls = {
+        "prepare_router": lambda **a: lmoe.prepare_router(Wr, **a), "route": lambda **a: lmoe.route(x, Wr, k, **a),
+        "topk_from_logits": lambda **a: lmoe.topk_from_logits(logits, k, **a),
+        "permute": lambda **a: lmoe.permute(idx, E, **a), "permute_noalloc": lambda **a: lmoe.permute_noalloc(idx, E, **a),
+        "quant_mxfp4": lambda **a: lmoe.quant_mxfp4(w32, **a), "quant_mxfp8": lambda **a: lmoe.quant_mxfp8(x, **a),
+        "repack_mxfp4": lambda **a: lmoe.repack_mxfp4(qc, sc, 1, 256, d, **a),
+        "scale_histogram": lambda **a: lmoe.scale_histogram(sc, 1, 256, d, lmoe.LAYOUT_CANONICAL, **a),
+        "expert_ffn": lambda **a: lmoe.expert_ffn(xq, xs, layer.bank, off, perm, w, k, **a),
+        "combine": lambda **a: lmoe.combine(yp, inv, T, k, **a), "linear_bf16": lambda **a: lmoe.linear_bf16(x, Wl, **a),
+        "layer": lambda **a: layer.forward(x, **a), "block": lambda **a: block.forward(xh, **a),
+    }
+    for f in calls.values():
+        f()  # (kernels are loaded, kept workspaces made)
+    side, empty = torch.cuda.Stream(DEV), torch.empty
+    torch.cuda.synchronize()
+    wrong = []
+    for name, f in calls.items():
+        made = []
+
+        def watched(*a, **kw):
+            t = empty(*a, **kw)
+            made.append((t.data_ptr(), t.numel() * t.element_size()))
+            return t
+
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # about 0.1 s
+        with monkeypatch.context() as m:
+            m.setattr(torch, "empty", watched)
+            f(stream=side)
+        got = [empty(n, dtype=torch.uint8, device=DEV) for _, n in made for _ in range(4)]
+        assert not side.query() and made, name
+        if any(p < t.data_ptr() + t.numel() and t.data_ptr() < p + n for p, n in made for t in got):
+            wrong.append(name)
+        side.synchronize()
+        del got
+    assert not wrong, wrong

@@ -244,13 +244,18 @@ def dims(T: int, d: int, E: int, k: int, I: int, act: int = ACT_MXFP8) -> Dims:
     return Dims(T, d, E, k, I, act)
 
 
-def _empty(shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device)
+def _empty(shape, dtype, device, stream=None):
+    """An uninitialised tensor for a call on `stream` (None: the current one): where that is not the stream it is
+    allocated on, it is recorded there, so that its memory goes to no other tensor while the call runs."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
-def workspace(nbytes: int, device) -> torch.Tensor:
+def workspace(nbytes: int, device, stream=None) -> torch.Tensor:
     # torch's caching allocator returns 512-byte aligned blocks
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    return _empty(max(int(nbytes), 256), torch.uint8, device, stream)
 
 
 def _on(stream):
@@ -286,8 +291,8 @@ def quant_mxfp4(w: torch.Tensor, layout: int = LAYOUT_TC, q=None, s=None, stream
     nmat, rows, K = w3.shape
     _need(w3, torch.float32, (nmat, rows, K), "w")
     qb, sb = mxfp4_bytes(nmat, rows, K, layout)
-    q = _empty(qb, torch.uint8, w.device) if q is None else q
-    s = _empty(sb, torch.uint8, w.device) if s is None else s
+    q = _empty(qb, torch.uint8, w.device, stream) if q is None else q
+    s = _empty(sb, torch.uint8, w.device, stream) if s is None else s
     assert q.numel() >= qb and s.numel() >= sb
     _check(_quant_mxfp4(_ptr(w3), nmat, rows, K, _ptr(q), _ptr(s), layout, _stream(stream)), "lmoe_quant_mxfp4")
     return q, s
@@ -302,8 +307,8 @@ def repack_mxfp4(q: torch.Tensor, s: torch.Tensor, nmat: int, rows: int, K: int,
     _need(s, torch.uint8, s.shape, "s")
     if q.numel() != nmat * rows * K // 2 or s.numel() != nmat * rows * K // 32:
         raise ValueError("canonical MXFP4 arrays of the wrong size")
-    q_tc = _empty(qb, torch.uint8, q.device) if q_tc is None else q_tc
-    s_tc = _empty(sb, torch.uint8, q.device) if s_tc is None else s_tc
+    q_tc = _empty(qb, torch.uint8, q.device, stream) if q_tc is None else q_tc
+    s_tc = _empty(sb, torch.uint8, q.device, stream) if s_tc is None else s_tc
     if q_tc.numel() < qb or s_tc.numel() < sb:
         raise ValueError("tensor-core layout destination too small")
     _check(_repack_mxfp4(_ptr(q), _ptr(s), nmat, rows, K, _ptr(q_tc), _ptr(s_tc), _stream(stream)),
@@ -314,7 +319,7 @@ def repack_mxfp4(q: torch.Tensor, s: torch.Tensor, nmat: int, rows: int, K: int,
 def scale_histogram(s: torch.Tensor, nmat: int, rows: int, K: int, layout: int = LAYOUT_TC, stream=None):
     """Per-matrix counts of each E8M0 scale byte: int32-viewed uint32 [nmat, 256]."""
     _need(s, torch.uint8, s.shape, "s")
-    hist = _empty((nmat, 256), torch.int32, s.device)
+    hist = _empty((nmat, 256), torch.int32, s.device, stream)
     _check(_scale_hist(_ptr(s), nmat, rows, K, layout, _ptr(hist), _stream(stream)), "lmoe_mxfp4_scale_histogram")
     return hist
 
@@ -323,8 +328,8 @@ def quant_mxfp8(x: torch.Tensor, stream=None):
     """bf16 [rows, K] -> (e4m3 codes uint8 [rows, K], scales uint8 [rows, K/32])."""
     rows, K = x.shape
     _need(x, torch.bfloat16, (rows, K), "x")
-    q = _empty((rows, K), torch.uint8, x.device)
-    s = _empty((rows, K // 32), torch.uint8, x.device)
+    q = _empty((rows, K), torch.uint8, x.device, stream)
+    s = _empty((rows, K // 32), torch.uint8, x.device, stream)
     _check(_quant_mxfp8(_ptr(x), rows, K, _ptr(q), _ptr(s), _stream(stream)), "lmoe_quant_mxfp8")
     return q, s
 
@@ -396,7 +401,7 @@ def prepare_router(Wr, stream=None):
     _need(Wr, torch.float32, (E, d), "Wr")
     if int(_router_bytes(E, d)) == 0:
         raise ValueError(f"router weights [{E}, {d}]: d must be a multiple of 64")
-    Wr3 = _empty((3, E, d), torch.bfloat16, Wr.device)
+    Wr3 = _empty((3, E, d), torch.bfloat16, Wr.device, stream)
     _check(_prepare_router(_ptr(Wr), E, d, _ptr(Wr3), _stream(stream)), "lmoe_prepare_router")
     return Wr3
 
@@ -413,10 +418,10 @@ def route(x, Wr, k: int, bias=None, stream=None, Wr3=None):
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
     D = dims(T, d, E, k, 32)
-    logits = _empty((T, E), torch.float32, x.device)
-    idx = _empty((T, k), torch.int32, x.device)
-    w = _empty((T, k), torch.float32, x.device)
-    ws = workspace(_route_ws(ctypes.byref(D)), x.device)
+    logits = _empty((T, E), torch.float32, x.device, stream)
+    idx = _empty((T, k), torch.int32, x.device, stream)
+    w = _empty((T, k), torch.float32, x.device, stream)
+    ws = workspace(_route_ws(ctypes.byref(D)), x.device, stream)
     _check(_route(_ptr(x), _ptr(Wr3), _ptr(bias), ctypes.byref(D), _ptr(logits), _ptr(idx), _ptr(w), _ptr(ws),
                   ws.numel(), _stream(stream)), "lmoe_route")
     return logits, idx, w
@@ -426,8 +431,8 @@ def topk_from_logits(logits, k: int, stream=None):
     T, E = logits.shape
     _need(logits, torch.float32, (T, E), "logits")
     D = dims(T, 128, E, k, 32)
-    idx = _empty((T, k), torch.int32, logits.device)
-    w = _empty((T, k), torch.float32, logits.device)
+    idx = _empty((T, k), torch.int32, logits.device, stream)
+    w = _empty((T, k), torch.float32, logits.device, stream)
     _check(_topk(_ptr(logits), ctypes.byref(D), _ptr(idx), _ptr(w), _stream(stream)), "lmoe_topk_from_logits")
     return idx, w
 
@@ -442,11 +447,11 @@ def permute(idx, E: int, ws=None, stream=None):
     _need(idx, torch.int32, (T, k), "topk_idx")
     D = dims(T, 128, E, k, 32)
     dev = idx.device
-    counts = _empty(E, torch.int32, dev)
-    offsets = _empty(E + 1, torch.int32, dev)
-    perm = _empty(T * k, torch.int32, dev)
-    inv = _empty(T * k, torch.int32, dev)
-    ws = workspace(_perm_ws(ctypes.byref(D)), dev) if ws is None else ws
+    counts = _empty(E, torch.int32, dev, stream)
+    offsets = _empty(E + 1, torch.int32, dev, stream)
+    perm = _empty(T * k, torch.int32, dev, stream)
+    inv = _empty(T * k, torch.int32, dev, stream)
+    ws = workspace(_perm_ws(ctypes.byref(D)), dev, stream) if ws is None else ws
     _check(_permute(_ptr(idx), ctypes.byref(D), _ptr(counts), _ptr(offsets), _ptr(perm), _ptr(inv), _ptr(ws),
                     ws.numel(), _stream(stream)), "lmoe_permute")
     return counts, offsets, perm, inv, ws
@@ -462,8 +467,7 @@ def permute_noalloc(idx, E: int, out=None, stream=None):
     D = dims(T, 128, E, k, 32)
     dev = idx.device
     if out is None:
-        out = (_empty(E, torch.int32, dev), _empty(E + 1, torch.int32, dev), _empty(T * k, torch.int32, dev),
-               _empty(T * k, torch.int32, dev), _empty(1, torch.int32, dev))
+        out = tuple(_empty(n, torch.int32, dev, stream) for n in (E, E + 1, T * k, T * k, 1))
     counts, offsets, perm, inv, status = out
     for t, shape, name in ((counts, (E,), "counts"), (offsets, (E + 1,), "offsets"), (perm, (T * k,), "perm"),
                            (inv, (T * k,), "inv"), (status, (1,), "device_status")):
@@ -483,8 +487,8 @@ def expert_ffn(xq, xs, bank: ExpertBank, offsets, perm, topk_w, k: int, ws=None,
     _need(offsets, torch.int32, (bank.E + 1,), "offsets")
     _need(perm, torch.int32, (T * k,), "perm")
     _need(topk_w, torch.float32, (T, k), "topk_w")
-    yp = _empty((T * k, d), torch.float32, xq.device)
-    ws = workspace(_ffn_ws(ctypes.byref(D)), xq.device) if ws is None else ws
+    yp = _empty((T * k, d), torch.float32, xq.device, stream)
+    ws = workspace(_ffn_ws(ctypes.byref(D)), xq.device, stream) if ws is None else ws
     W = bank.struct()
     _check(_ffn(_ptr(xq), _ptr(xs), ctypes.byref(W), _ptr(offsets), _ptr(perm), _ptr(topk_w), ctypes.byref(D),
                 _ptr(yp), _ptr(ws), ws.numel(), _stream(stream)), "lmoe_expert_ffn")
@@ -496,7 +500,7 @@ def combine(yp, inv, T: int, k: int, stream=None):
     _need(yp, torch.float32, (T * k, d), "yp")
     _need(inv, torch.int32, (T * k,), "inv")
     D = dims(T, d, 32, k, 32)
-    y = _empty((T, d), torch.bfloat16, yp.device)
+    y = _empty((T, d), torch.bfloat16, yp.device, stream)
     _check(_combine(_ptr(yp), _ptr(inv), ctypes.byref(D), _ptr(y), _stream(stream)), "lmoe_combine")
     return y
 
@@ -527,7 +531,7 @@ class Layer:
         T, d = x.shape
         _need(x, torch.bfloat16, (T, d), "x")
         D = dims(T, d, self.bank.E, self.k, self.bank.I, self.act)
-        y = _empty((T, d), torch.bfloat16, x.device) if y is None else y
+        y = _empty((T, d), torch.bfloat16, x.device, stream) if y is None else y
         ws = self.workspace(T, stream)
         W = self.bank.struct()
         _check(_forward(_ptr(x), _ptr(self.Wr3), _ptr(self.bias), ctypes.byref(W), ctypes.byref(D), _ptr(y),
@@ -545,7 +549,7 @@ def linear_bf16(x, W, out=None, stream=None):
     N = W.shape[0]
     _need(x, torch.bfloat16, (rows, K), "x")
     _need(W, torch.bfloat16, (N, K), "W")
-    out = _empty((rows, N), torch.bfloat16, x.device) if out is None else out
+    out = _empty((rows, N), torch.bfloat16, x.device, stream) if out is None else out
     _check(_linear(_ptr(x), _ptr(W), rows, K, N, _ptr(out), _stream(stream)), "lmoe_linear_bf16")
     return out
 
@@ -553,7 +557,8 @@ def linear_bf16(x, W, out=None, stream=None):
 # ---- norms, MXFP4 linear and grouped products around the layer ----------------------------
 
 # These calls run on the device of their first tensor and, by default, on that
-# device's current stream.  The short ones are bound in C++ (csrc/bind_torch.cpp).
+# device's current stream; what they allocate is allocated on the call's stream,
+# as within torch.cuda.stream(stream).  The short ones are bound in C++ (csrc/bind_torch.cpp).
 # It is loaded at the first of them, so that the rest needs only the library.
 class _Binding:
     def __getattr__(self, name):
@@ -752,7 +757,8 @@ class ResidualBlock:
 
     def workspace_size(self, T: int) -> int:
         bank = self.layer.bank
-        return int(_res_block_ws(ctypes.byref(dims(T, bank.d, bank.E, self.layer.k, bank.I, self.layer.act)), self.hidden))
+        D = dims(T, bank.d, bank.E, self.layer.k, bank.I, self.layer.act)
+        return int(_res_block_ws(ctypes.byref(D), self.hidden))
 
     def forward(self, res, x_n=None, gate=None, next_w=None, res_out=None, next_out=None, ws=None, stream=None):
         """res [T, hidden] bf16 or fp32 -> (res_out, next_out or None).  x_n: the
@@ -822,7 +828,7 @@ class Block:
         D = dims(T, bank.d, bank.E, k, bank.I)
         need = int(_block_ws(ctypes.byref(D), hidden))
         self._ws = _kept_workspace(self._ws, need, x_h.device, stream)
-        out = _empty((T, hidden), torch.bfloat16, x_h.device) if out is None else out
+        out = _empty((T, hidden), torch.bfloat16, x_h.device, stream) if out is None else out
         W = bank.struct()
         _check(_forward_block(_ptr(x_h), _ptr(self.W_in), _ptr(self.layer.Wr3), _ptr(self.layer.bias), ctypes.byref(W),
                               _ptr(self.W_out), ctypes.byref(D), hidden, _ptr(out), _ptr(lat), _ptr(y), _ptr(topk_idx),
