@@ -287,7 +287,8 @@ typedef enum { LMOE_BF16 = 0, LMOE_F32 = 1 } lmoe_fmt;
 
 /* out[t][c] = bf16( x[t][c] * rsqrt(mean_c x[t][c]^2 + eps) * w[c] ): the norm
  * before a block.  x [T][H] of type x_fmt (the residual stream), w fp32 [H],
- * fp32 arithmetic (a row's sum of squares stays below 2^128).  H % 8 == 0, H <= 32768, eps >= 0. */
+ * fp32 arithmetic (a row's sum of squares stays below 2^128).  H % 8 == 0,
+ * H <= 32768, eps >= 0. */
 lmoe_status lmoe_rms_norm(const void *x, int32_t x_fmt, const float *w, float eps, int64_t T, int32_t H, uint16_t *out,
                           void *stream);
 
@@ -333,8 +334,8 @@ lmoe_status lmoe_residual_norm(const uint16_t *y, const void *res, int32_t res_f
  * NaN outputs in that row; out overlaps no input.  This call and the grouped
  * products below leave the workspace's status word alone unless they find an
  * error, and one found stays until it is cleared: clear it once before the
- * workspace's first use (lmoe_clear_device_status).  Calls that may overlap on the GPU, captured
- * graphs among them, need a workspace each. */
+ * workspace's first use (lmoe_clear_device_status).  Calls that may overlap on
+ * the GPU, captured graphs among them, need a workspace each. */
 size_t lmoe_linear_mxfp4_workspace_size(int64_t rows, int32_t K, int32_t N);
 lmoe_status lmoe_linear_mxfp4(const uint16_t *x, const uint8_t *q, const uint8_t *s, int64_t rows, int32_t K, int32_t N,
                               uint16_t *out, void *workspace, size_t ws_bytes, void *stream);
@@ -359,8 +360,8 @@ size_t lmoe_grouped_workspace_size(void);
  * group: x bf16 [x_rows][K], W bf16 [E][N][K], accumulated in fp32 by the tensor
  * core (whose sums err about three times as much as fp32 sums one after another
  * in a good order: fp32 rows of K = 512, relative norm 4.7e-7 against 1.6e-7);
- * src(q) = perm[q] / k with gather != 0, else q; w(q) = row_w[perm[q]] (row_w [P]), or 1 without
- * row_w; out [P][N] bf16 or fp32 (out_fmt), rounded once.  Rows of out that
+ * src(q) = perm[q] / k with gather != 0, else q; w(q) = row_w[perm[q]] (row_w
+ * [P]), or 1 without row_w; out [P][N] bf16 or fp32 (out_fmt), rounded once.  Rows of out that
  * belong to no group are left as they were.  With fp32 out and the gate
  * weights as row_w, out is the yp that lmoe_combine takes.
  * K % 8 == 0, any N >= 1, 1 <= E <= 2048, E * N <= INT32_MAX, 1 <= k,

@@ -245,10 +245,10 @@ __global__ void __launch_bounds__((GCfg<NT, SWIGLU, GATHER, KS>::THREADS), 1)
     const int k0 = KS > 1 ? rank * p.KC / KS : 0, k1 = KS > 1 ? (rank + 1) * p.KC / KS : p.KC;
     Walk<NT> walk{s_tiles, s_off, p.E, p.MT};
     // This CTA's items, in order, NO_MORE after the last and LOST where the wait for
-    // one ran out; every lane of a warp calls it.  Many items are handed out as CTAs come free: SMs do not all stream
-    // equally fast, and groups differ (a weighted down projection of 64 tokens
-    // over 896 experts: its CTAs ended between 351 and 421 us with each
-    // grid-th item).
+    // one ran out; every lane of a warp calls it.  Many items are handed out as
+    // CTAs come free: SMs do not all stream equally fast, and groups differ (a
+    // weighted down projection of 64 tokens over 896 experts: its CTAs ended
+    // between 351 and 421 us with each grid-th item).
     constexpr int NO_MORE = -1, LOST = -2;
     int feed_q = 0, feed_next = first;
     uint32_t feed_phase = 0;

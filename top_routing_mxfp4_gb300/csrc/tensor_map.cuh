@@ -10,7 +10,7 @@ namespace lmoe {
 
 enum class MapType {
     BF16,  // boxes of 64 columns
-    FP4    // packed, two a byte in memory; 128 columns, a byte each in shared memory
+    FP4  // packed, two a byte in memory; 128 columns, a byte each in shared memory
 };
 
 // A map of [rows][K] elements (rows K elements apart) in boxes of box_rows rows.
