@@ -380,6 +380,122 @@ lmoe_status lmoe_grouped_swiglu_bf16(const uint16_t *x, int64_t x_rows, const ui
                                      const lmoe_groups *groups, int32_t gather, int32_t K, int32_t I, uint16_t *h,
                                      void *workspace, size_t ws_bytes, void *stream);
 
+/* ---- linear layer with bias, activation and residual ---------------------------- */
+
+/* The function a linear layer's sums go through: z; max(z, 0); z / (1 + e^-z);
+ * z Phi(z), Phi the normal distribution function; and
+ * z / (1 + e^-2u), u = sqrt(2/pi) (z + 0.044715 z^3). */
+typedef enum {
+    LMOE_FN_NONE = 0,
+    LMOE_FN_RELU = 1,
+    LMOE_FN_SILU = 2,
+    LMOE_FN_GELU = 3,
+    LMOE_FN_GELU_TANH = 4
+} lmoe_fn;
+
+/* What lmoe_linear_act_bf16 does to the product: bias [N] of type bias_fmt (NULL:
+ * none), fn, res [rows][N] of type res_fmt (NULL: none). */
+typedef struct {
+    const void *bias;
+    int32_t bias_fmt;
+    int32_t fn;
+    const void *res;
+    int32_t res_fmt;
+} lmoe_linear_act;
+
+/* z[r][n]   = sum_c x[r][c] * W[n][c] + bias[n]
+ * out[r][n] = fn(z) + res[r][n], rounded once to out_fmt;  pre[r][n] = bf16(z)
+ * x bf16 [rows][K], W bf16 [N][K], products accumulated in fp32 by the tensor
+ * core, the rest in fp32.  pre may be NULL; out may be res where they have one
+ * type; otherwise outputs overlap no input.  act NULL: no bias, no function, no
+ * residual.  K % 8 == 0, any N >= 1, rows <= 2^29, no matrix
+ * of more than 2^40 elements.  The status word is used as
+ * by lmoe_linear_mxfp4: cleared by the caller once, before the workspace's first
+ * use; calls that may overlap on the GPU need a workspace each. */
+size_t lmoe_linear_act_workspace_size(int64_t rows, int32_t K, int32_t N);
+lmoe_status lmoe_linear_act_bf16(const uint16_t *x, const uint16_t *W, const lmoe_linear_act *act, int64_t rows, int32_t K,
+                                 int32_t N, int32_t out_fmt, void *out, uint16_t *pre, void *workspace, size_t ws_bytes,
+                                 void *stream);
+
+/* The gradients of lmoe_linear_act_bf16, dout = dL/dout [rows][N] of type
+ * dout_fmt, pre as the forward call stored it (NULL where fn is LMOE_FN_NONE):
+ *   dz = dout * fn'(pre)           (fp32, then bf16 for the two products)
+ *   dx[r][c]  = bf16( sum_n dz[r][n] W[n][c] )
+ *   dW[n][c]  = sum_r dz[r][n] x[r][c], rounded once to dW_fmt
+ *   dbias[n]  = sum_r dz[r][n], fp32, of the unrounded dz
+ * (the residual's gradient is dout).  fn' of relu at 0 is 0.  Each of dx, dW and
+ * dbias may be NULL; x is needed for dW alone and W for dx alone.  Without rows,
+ * dW and dbias are zero.  The sums have one order, so a call repeats bit for bit.
+ * Limits, overlaps and the workspace as above. */
+size_t lmoe_linear_act_backward_workspace_size(int64_t rows, int32_t K, int32_t N);
+lmoe_status lmoe_linear_act_bf16_backward(const void *dout, int32_t dout_fmt, const uint16_t *x, const uint16_t *W,
+                                          const uint16_t *pre, int32_t fn, int64_t rows, int32_t K, int32_t N,
+                                          uint16_t *dx, void *dW, int32_t dW_fmt, float *dbias, void *workspace,
+                                          size_t ws_bytes, void *stream);
+
+/* ---- layer norm -------------------------------------------------------------------- */
+
+/* m = mean_c x[t][c], s = 1 / sqrt(mean_c (x[t][c] - m)^2 + eps)
+ * out[t][c] = bf16( (x[t][c] - m) * s * w[c] + b[c] );  mean[t] = m, rstd[t] = s
+ * x [T][H] of type x_fmt; w, b fp32 [H], either may be NULL (1 and 0); mean and
+ * rstd fp32 [T], both or neither.  fp32 arithmetic, the squares of the centred
+ * values; limits as for lmoe_rms_norm.  out overlaps no input. */
+lmoe_status lmoe_layer_norm(const void *x, int32_t x_fmt, const float *w, const float *b, float eps, int64_t T, int32_t H,
+                            uint16_t *out, float *mean, float *rstd, void *stream);
+
+/* The gradients of lmoe_layer_norm, dy = dL/dout bf16 [T][H]; x, mean, rstd as the
+ * forward call took and gave them, h = (x - mean) rstd, g = dy w:
+ *   dx[t][c] = rstd[t] (g - mean_c g - h mean_c(g h)) + add[t][c]   (type of x)
+ *   dw[c] = sum_t dy h,  db[c] = sum_t dy                           (fp32)
+ * add [T][H] of x's type, or NULL: the gradient that reaches x by another way (a
+ * residual stream's own).  dx may be add.  w may be NULL (1); dw and db may be
+ * NULL, each by itself.  Without rows dw and db are zero.  One order of sums.
+ * Limits as for lmoe_rms_norm.  The workspace holds partial sums of dw and db; it
+ * need not be cleared.  Calls that may overlap need a workspace each. */
+size_t lmoe_layer_norm_backward_workspace_size(int64_t T, int32_t H);
+lmoe_status lmoe_layer_norm_backward(const uint16_t *dy, const void *x, int32_t x_fmt, const float *mean,
+                                     const float *rstd, const float *w, const void *add, int64_t T, int32_t H, void *dx,
+                                     float *dw, float *db, void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- balance loss ------------------------------------------------------------------- */
+
+/* The gradient part of lmoe_balance_loss: dlogits [T][E] fp32 (written whole);
+ * coef_balance and coef_z, the weights of the two losses in L; scale, an fp32 on
+ * the device that multiplies both (NULL: 1); topk_w [T][k] and dtopk_w = dL/dtopk_w
+ * [T][k], both or neither, for the way through the gate weights. */
+typedef struct {
+    float *dlogits;
+    float coef_balance, coef_z;
+    const float *scale;
+    const float *topk_w, *dtopk_w;
+} lmoe_balance_grad;
+
+/* Losses that keep a router's experts evenly used and its logits small, the
+ * per-expert counts, and with `grad` the gradient by the logits, in one pass over
+ * the logits.  logits [T][E] and topk_idx [T][k] as lmoe_route gives them; mask
+ * [T] bytes, 0 for a token that does not count (padding), or NULL; N the number
+ * of tokens that count, p the softmax of a token's E logits:
+ *   counts[e] = slots of counted tokens with topk_idx == e
+ *   probs[e]  = 1/N sum_t p[t][e]
+ *   loss[0]   = sum_e f[e] probs[e],  f[e] = counts[e] E / (k N)     (balance: 1 where all are even)
+ *   loss[1]   = 1/N sum_t lse[t]^2,   lse the logarithm of sum_e exp(logits)  (z)
+ *   dlogits[t][e] = scale (coef_balance / N p (f[e] - sum_j f[j] p[t][j]) + coef_z 2 / N lse p)
+ *                   + sum over slots i with topk_idx[t][i] == e of
+ *                     topk_w[t][i] (dtopk_w[t][i] - sum_j topk_w[t][j] dtopk_w[t][j])
+ * (counts have no gradient).  Rows that do not count are not looked at, whatever
+ * they hold, and have a zero gradient.  A row without a finite maximum has no
+ * probabilities where that is -infinity (it adds nothing to the sums and its
+ * losses' gradient is zero) and NaN otherwise.  With N = 0 all outputs are zero.
+ * An id outside [0, E) is skipped and recorded as LMOE_ERR_DEVICE_CHECK.
+ * loss fp32 [2], counts int32 [E], probs fp32 [E].  1 <= E <= 2048,
+ * 1 <= k <= min(E, 32), T * k <= INT32_MAX / 2, coefficients finite.  Outputs
+ * overlap no input and one another, but dlogits may be logits.  The status word
+ * as for lmoe_linear_mxfp4. */
+size_t lmoe_balance_loss_workspace_size(int64_t T, int32_t E, int32_t k);
+lmoe_status lmoe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t *mask, int64_t T, int32_t E,
+                              int32_t k, float *loss, int32_t *counts, float *probs, const lmoe_balance_grad *grad,
+                              void *workspace, size_t ws_bytes, void *stream);
+
 /* ---- block on a residual stream ------------------------------------------------ */
 
 /* A hidden <-> latent projection: bf16 weights w [N][K], or, with w NULL, MXFP4

@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -30,6 +31,17 @@ struct Entries {
     decltype(&lmoe_grouped_swiglu_bf16) grouped_swiglu;
     decltype(&lmoe_grouped_workspace_size) grouped_workspace_size;
 } E = {};
+struct TrainEntries {
+    decltype(&lmoe_linear_act_bf16) linear_act;
+    decltype(&lmoe_linear_act_workspace_size) linear_act_ws;
+    decltype(&lmoe_linear_act_bf16_backward) linear_act_back;
+    decltype(&lmoe_linear_act_backward_workspace_size) linear_act_back_ws;
+    decltype(&lmoe_layer_norm) layer_norm;
+    decltype(&lmoe_layer_norm_backward) layer_norm_back;
+    decltype(&lmoe_layer_norm_backward_workspace_size) layer_norm_back_ws;
+    decltype(&lmoe_balance_loss) balance;
+    decltype(&lmoe_balance_loss_workspace_size) balance_ws;
+} TE = {};
 PyObject *g_error = nullptr;  // lmoe.LmoeError
 // The workspace of the latest call that made its own, kept so that the errors
 // the call found on the GPU can be asked for (lmoe.last_call_status).
@@ -143,14 +155,21 @@ struct Ws {
     at::Tensor own;
     void *ptr;
     size_t bytes;
-    Ws(PyObject *given, size_t want, const at::Tensor &like, int dev)
+    // zeroed: bytes from the start that the call wants zero (0: all)
+    Ws(PyObject *given, size_t want, const at::Tensor &like, int dev, size_t zeroed = 0)
     {
         const at::Tensor *t = &own;
         if (given != Py_None) {
             t = &tensor(given, "ws");
             need(*t, at::kByte, t->sizes(), "ws", dev);
         } else {
-            own = at::zeros({int64_t(want < 256 ? 256 : want)}, like.options().dtype(at::kByte));
+            const int64_t n = int64_t(want < 256 ? 256 : want);
+            if (zeroed) {
+                own = at::detail::empty_cuda({n}, at::kByte, like.device(), std::nullopt);
+                own.narrow(0, 0, int64_t(zeroed)).zero_();
+            } else {
+                own = at::zeros({n}, like.options().dtype(at::kByte));
+            }
             PyObject *o = THPVariable_Wrap(own);
             if (!o) throw PyError();
             Py_XSETREF(g_own_ws, o);
@@ -348,6 +367,230 @@ PyObject *grouped(PyObject *const *a)
     return out.release();
 }
 
+bool as_bool(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PyError();
+    return v != 0;
+}
+int32_t size32(int64_t n, const char *name)
+{
+    if (n > INT32_MAX) throw Bad(std::string(name) + ": too large");
+    return int32_t(n);
+}
+void need_train()
+{
+    if (!TE.linear_act) throw Bad("not bound to a library");
+}
+
+// A tuple of outputs; a null one becomes None.
+template <typename... O>
+PyObject *pack(O &...outs)
+{
+    PyObject *t = PyTuple_New(sizeof...(outs));
+    if (!t) throw PyError();
+    Py_ssize_t i = 0;
+    auto put = [&](PyObject *o) {
+        if (!o) {
+            o = Py_None;
+            Py_INCREF(o);
+        }
+        PyTuple_SET_ITEM(t, i++, o);
+    };
+    (put(outs.release()), ...);
+    return t;
+}
+
+// An output that may not be wanted.
+struct MaybeOut {
+    std::optional<Out> out;
+    void *ptr = nullptr;
+    void make(PyObject *given, const at::Tensor &like, at::IntArrayRef shape, at::ScalarType type, const char *name, int dev)
+    {
+        out.emplace(given, like, shape, type, name, dev);
+        ptr = out->ptr;
+    }
+    PyObject *release() { return out ? out->release() : nullptr; }
+};
+
+// (x, W, bias, fn, res, out, pre, ws, stream)
+PyObject *linear_act(PyObject *const *a)
+{
+    need_train();
+    const at::Tensor &x = tensor(a[0], "x"), &W = tensor(a[1], "W");
+    rank_is(x, 2, "x");
+    rank_is(W, 2, "W");
+    const int dev = cuda_index(x, "x");
+    const int64_t rows = x.size(0);
+    const int32_t K = size32(x.size(1), "x"), N = size32(W.size(0), "W");
+    const void *xp = need(x, at::kBFloat16, {rows, K}, "x", dev), *wp = need(W, at::kBFloat16, {N, K}, "W", dev);
+    lmoe_linear_act f = {};
+    if (a[2] != Py_None) {
+        const at::Tensor &b = tensor(a[2], "bias");
+        f.bias_fmt = float_fmt(b, "bias");
+        f.bias = need(b, b.scalar_type(), {N}, "bias", dev);
+    }
+    f.fn = int32_t(as_int(a[3]));
+    int fmt = LMOE_BF16;
+    if (a[4] != Py_None) {
+        const at::Tensor &r = tensor(a[4], "res");
+        fmt = f.res_fmt = float_fmt(r, "res");
+        f.res = need(r, r.scalar_type(), {rows, N}, "res", dev);
+    }
+    if (a[5] != Py_None) fmt = float_fmt(tensor(a[5], "out"), "out");
+    const bool pre_given = THPVariable_Check(a[6]), want_pre = pre_given || (a[6] != Py_None && as_bool(a[6]));
+    On on(dev, a[8]);
+    Out out(a[5], x, {rows, N}, fmt == LMOE_F32 ? at::kFloat : at::kBFloat16, "out", dev);
+    MaybeOut pre;
+    if (want_pre) pre.make(pre_given ? a[6] : Py_None, x, {rows, N}, at::kBFloat16, "pre", dev);
+    Ws ws(a[7], a[7] == Py_None ? TE.linear_act_ws(rows, K, N) : 0, x, dev);
+    check(TE.linear_act(static_cast<const uint16_t *>(xp), static_cast<const uint16_t *>(wp), &f, rows, K, N, fmt, out.ptr,
+                        static_cast<uint16_t *>(pre.ptr), ws.ptr, ws.bytes, on.stream),
+          "lmoe_linear_act_bf16");
+    return want_pre ? pack(out, pre) : out.release();
+}
+
+// (dout, x, W, fn, pre, want_dx, want_dW, want_dbias, dx, dW, dbias, ws, stream) -> (dx, dW, dbias)
+PyObject *linear_act_backward(PyObject *const *a)
+{
+    need_train();
+    const at::Tensor &dout = tensor(a[0], "dout"), &x = tensor(a[1], "x"), &W = tensor(a[2], "W");
+    rank_is(x, 2, "x");
+    rank_is(W, 2, "W");
+    const int dev = cuda_index(x, "x"), dfmt = float_fmt(dout, "dout");
+    const int64_t rows = x.size(0);
+    const int32_t K = size32(x.size(1), "x"), N = size32(W.size(0), "W");
+    const void *dp = need(dout, dout.scalar_type(), {rows, N}, "dout", dev);
+    const void *xp = need(x, at::kBFloat16, {rows, K}, "x", dev), *wp = need(W, at::kBFloat16, {N, K}, "W", dev);
+    const int32_t fn = int32_t(as_int(a[3]));
+    const void *pre = need_or_null(a[4], at::kBFloat16, {rows, N}, "pre", dev);
+    if (rows > 0 && (fn != LMOE_FN_NONE) != (pre != nullptr))
+        throw Bad(pre ? "pre: given without a function" : "pre: expected a tensor");
+    const bool wx = as_bool(a[5]), wW = as_bool(a[6]), wb = as_bool(a[7]);
+    const int wfmt = a[9] != Py_None ? float_fmt(tensor(a[9], "dW"), "dW") : LMOE_BF16;
+    On on(dev, a[12]);
+    MaybeOut dx, dW, db;
+    if (wx) dx.make(a[8], x, {rows, K}, at::kBFloat16, "dx", dev);
+    if (wW) dW.make(a[9], x, {N, K}, wfmt == LMOE_F32 ? at::kFloat : at::kBFloat16, "dW", dev);
+    if (wb) db.make(a[10], x, {N}, at::kFloat, "dbias", dev);
+    Ws ws(a[11], a[11] == Py_None ? TE.linear_act_back_ws(rows, K, N) : 0, x, dev, 256);
+    check(TE.linear_act_back(dp, dfmt, static_cast<const uint16_t *>(xp), static_cast<const uint16_t *>(wp),
+                             static_cast<const uint16_t *>(pre), fn, rows, K, N, static_cast<uint16_t *>(dx.ptr), dW.ptr,
+                             wfmt, static_cast<float *>(db.ptr), ws.ptr, ws.bytes, on.stream),
+          "lmoe_linear_act_bf16_backward");
+    return pack(dx, dW, db);
+}
+
+// (x, w, b, eps, stats, out, mean, rstd, stream)
+PyObject *layer_norm(PyObject *const *a)
+{
+    need_train();
+    const at::Tensor &x = tensor(a[0], "x");
+    rank_is(x, 2, "x");
+    const int dev = cuda_index(x, "x"), fmt = float_fmt(x, "x");
+    const int64_t T = x.size(0);
+    const int32_t H = size32(x.size(1), "x");
+    const void *xp = need(x, x.scalar_type(), {T, H}, "x", dev);
+    const void *wp = need_or_null(a[1], at::kFloat, {H}, "w", dev), *bp = need_or_null(a[2], at::kFloat, {H}, "b", dev);
+    const double eps = as_double(a[3]);
+    const bool stats = as_bool(a[4]) || a[6] != Py_None || a[7] != Py_None;
+    On on(dev, a[8]);
+    Out out(a[5], x, {T, H}, at::kBFloat16, "out", dev);
+    MaybeOut mean, rstd;
+    if (stats) {
+        mean.make(a[6], x, {T}, at::kFloat, "mean", dev);
+        rstd.make(a[7], x, {T}, at::kFloat, "rstd", dev);
+    }
+    check(TE.layer_norm(xp, fmt, static_cast<const float *>(wp), static_cast<const float *>(bp), float(eps), T, H,
+                        static_cast<uint16_t *>(out.ptr), static_cast<float *>(mean.ptr), static_cast<float *>(rstd.ptr),
+                        on.stream),
+          "lmoe_layer_norm");
+    return stats ? pack(out, mean, rstd) : out.release();
+}
+
+// (dy, x, mean, rstd, w, add, want_params, dx, dw, db, ws, stream) -> (dx, dw, db)
+PyObject *layer_norm_backward(PyObject *const *a)
+{
+    need_train();
+    const at::Tensor &x = tensor(a[1], "x");
+    rank_is(x, 2, "x");
+    const int dev = cuda_index(x, "x"), fmt = float_fmt(x, "x");
+    const int64_t T = x.size(0);
+    const int32_t H = size32(x.size(1), "x");
+    const void *xp = need(x, x.scalar_type(), {T, H}, "x", dev);
+    const void *dy = need(tensor(a[0], "dy"), at::kBFloat16, {T, H}, "dy", dev);
+    const void *mean = need(tensor(a[2], "mean"), at::kFloat, {T}, "mean", dev);
+    const void *rstd = need(tensor(a[3], "rstd"), at::kFloat, {T}, "rstd", dev);
+    const void *wp = need_or_null(a[4], at::kFloat, {H}, "w", dev);
+    const void *add = need_or_null(a[5], x.scalar_type(), {T, H}, "add", dev);
+    const bool params = as_bool(a[6]);
+    On on(dev, a[11]);
+    Out dx(a[7], x, {T, H}, x.scalar_type(), "dx", dev);
+    MaybeOut dw, db;
+    if (params) {
+        dw.make(a[8], x, {H}, at::kFloat, "dw", dev);
+        db.make(a[9], x, {H}, at::kFloat, "db", dev);
+    }
+    at::Tensor own;
+    void *wsp = nullptr;
+    size_t bytes = 0;
+    if (params) {
+        if (a[10] != Py_None) {
+            const at::Tensor &t = tensor(a[10], "ws");
+            wsp = need(t, at::kByte, t.sizes(), "ws", dev);
+            bytes = size_t(t.numel());
+        } else {
+            bytes = TE.layer_norm_back_ws(T, H);
+            own = at::detail::empty_cuda({int64_t(bytes < 256 ? 256 : bytes)}, at::kByte, x.device(), std::nullopt);
+            wsp = own.data_ptr();
+        }
+    }
+    check(TE.layer_norm_back(static_cast<const uint16_t *>(dy), xp, fmt, static_cast<const float *>(mean),
+                             static_cast<const float *>(rstd), static_cast<const float *>(wp), add, T, H, dx.ptr,
+                             static_cast<float *>(dw.ptr), static_cast<float *>(db.ptr), wsp, bytes, on.stream),
+          "lmoe_layer_norm_backward");
+    return pack(dx, dw, db);
+}
+
+// (logits, topk_idx, mask, coef_balance, coef_z, grad, topk_w, dtopk_w, scale, dlogits, ws, stream)
+PyObject *balance_loss(PyObject *const *a)
+{
+    need_train();
+    const at::Tensor &l = tensor(a[0], "logits"), &idx = tensor(a[1], "topk_idx");
+    rank_is(l, 2, "logits");
+    rank_is(idx, 2, "topk_idx");
+    const int dev = cuda_index(l, "logits");
+    const int64_t T = l.size(0);
+    const int32_t n_exp = size32(l.size(1), "logits"), k = size32(idx.size(1), "topk_idx");
+    const void *lp = need(l, at::kFloat, {T, n_exp}, "logits", dev), *ip = need(idx, at::kInt, {T, k}, "topk_idx", dev);
+    const void *mask = need_or_null(a[2], at::kBool, {T}, "mask", dev);
+    lmoe_balance_grad g = {};
+    g.coef_balance = float(as_double(a[3]));
+    g.coef_z = float(as_double(a[4]));
+    const bool grad = as_bool(a[5]) || a[9] != Py_None;
+    g.topk_w = static_cast<const float *>(need_or_null(a[6], at::kFloat, {T, k}, "topk_w", dev));
+    g.dtopk_w = static_cast<const float *>(need_or_null(a[7], at::kFloat, {T, k}, "dtopk_w", dev));
+    if ((a[6] == Py_None) != (a[7] == Py_None)) throw Bad("topk_w and dtopk_w: both or neither");
+    if (!grad && (a[6] != Py_None || a[8] != Py_None)) throw Bad("topk_w, dtopk_w, scale: without grad");
+    if (a[8] != Py_None) {
+        const at::Tensor &s = tensor(a[8], "scale");
+        if (s.numel() != 1) throw Bad("scale: expected one value");
+        g.scale = static_cast<const float *>(need(s, at::kFloat, s.sizes(), "scale", dev));
+    }
+    On on(dev, a[11]);
+    Out loss(Py_None, l, {2}, at::kFloat, "loss", dev), counts(Py_None, l, {n_exp}, at::kInt, "counts", dev);
+    Out probs(Py_None, l, {n_exp}, at::kFloat, "probs", dev);
+    MaybeOut d;
+    if (grad) d.make(a[9], l, {T, n_exp}, at::kFloat, "dlogits", dev);
+    g.dlogits = static_cast<float *>(d.ptr);
+    Ws ws(a[10], a[10] == Py_None ? TE.balance_ws(T, n_exp, k) : 0, l, dev, 256);
+    check(TE.balance(static_cast<const float *>(lp), static_cast<const int32_t *>(ip), static_cast<const uint8_t *>(mask), T,
+                     n_exp, k, static_cast<float *>(loss.ptr), static_cast<int32_t *>(counts.ptr),
+                     static_cast<float *>(probs.ptr), grad ? &g : nullptr, ws.ptr, ws.bytes, on.stream),
+          "lmoe_balance_loss");
+    return grad ? pack(loss, counts, probs, d) : pack(loss, counts, probs);
+}
+
 // bind(error class, addresses of the seven entry points in the order of Entries)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -373,6 +616,33 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     E.grouped_linear = reinterpret_cast<decltype(E.grouped_linear)>(p[4]);
     E.grouped_swiglu = reinterpret_cast<decltype(E.grouped_swiglu)>(p[5]);
     E.grouped_workspace_size = reinterpret_cast<decltype(E.grouped_workspace_size)>(p[6]);
+    Py_RETURN_NONE;
+}
+
+// bind_train(addresses of the nine entry points in the order of TrainEntries), after bind
+PyObject *bind_train(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 9) {
+        PyErr_SetString(PyExc_TypeError, "bind_train: nine addresses");
+        return nullptr;
+    }
+    void *p[9];
+    for (int i = 0; i < 9; ++i) {
+        p[i] = PyLong_AsVoidPtr(a[i]);
+        if (!p[i]) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_train: a null address");
+            return nullptr;
+        }
+    }
+    TE.linear_act = reinterpret_cast<decltype(TE.linear_act)>(p[0]);
+    TE.linear_act_ws = reinterpret_cast<decltype(TE.linear_act_ws)>(p[1]);
+    TE.linear_act_back = reinterpret_cast<decltype(TE.linear_act_back)>(p[2]);
+    TE.linear_act_back_ws = reinterpret_cast<decltype(TE.linear_act_back_ws)>(p[3]);
+    TE.layer_norm = reinterpret_cast<decltype(TE.layer_norm)>(p[4]);
+    TE.layer_norm_back = reinterpret_cast<decltype(TE.layer_norm_back)>(p[5]);
+    TE.layer_norm_back_ws = reinterpret_cast<decltype(TE.layer_norm_back_ws)>(p[6]);
+    TE.balance = reinterpret_cast<decltype(TE.balance)>(p[7]);
+    TE.balance_ws = reinterpret_cast<decltype(TE.balance_ws)>(p[8]);
     Py_RETURN_NONE;
 }
 
@@ -409,6 +679,12 @@ PyMethodDef methods[] = {
     {"residual_norm", FAST((counted<residual_norm, 10>)), METH_FASTCALL, nullptr},
     {"linear_mxfp4", FAST((counted<linear_mxfp4, 7>)), METH_FASTCALL, nullptr},
     {"grouped", FAST((counted<grouped, 11>)), METH_FASTCALL, nullptr},
+    {"bind_train", FAST(bind_train), METH_FASTCALL, nullptr},
+    {"linear_act", FAST((counted<linear_act, 9>)), METH_FASTCALL, nullptr},
+    {"linear_act_backward", FAST((counted<linear_act_backward, 13>)), METH_FASTCALL, nullptr},
+    {"layer_norm", FAST((counted<layer_norm, 9>)), METH_FASTCALL, nullptr},
+    {"layer_norm_backward", FAST((counted<layer_norm_backward, 12>)), METH_FASTCALL, nullptr},
+    {"balance_loss", FAST((counted<balance_loss, 12>)), METH_FASTCALL, nullptr},
     {"own_ws", own_ws, METH_NOARGS, nullptr},
     {"keep_ws", keep_ws, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},

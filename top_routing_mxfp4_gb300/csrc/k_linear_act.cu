@@ -1,0 +1,651 @@
+// Linear layer with bias, function and residual, and its gradients, on the tensor
+// cores (tcgen05.mma kind::f16, fp32 accumulation in TMEM):
+//   z = x W^T + bias,  out = fn(z) + res,  pre = bf16(z)
+//   dz = dout fn'(pre),  dx = dz W,  dW = dz^T x,  dbias = sum of dz's rows
+//
+// One kernel makes all three products, D[m][n] = sum_k A(m, k) B(n, k): the operands
+// are read as they lie, K-major (x and W forward, dz in dx: the reduction runs along
+// a row) or MN-major (W in dx; dz and x in dW: it runs over the rows), 64 of the
+// reduction a chunk, and TMA zero-fills what lies beyond an edge.
+//
+// Persistent CTAs: warp 0 copies (TMA), warp 1 issues the MMAs, the others are the
+// epilogue (TMEM lane quarter = warp % 4), which adds bias, applies the function,
+// adds the residual and stores, a row a lane, while the next tile's MMAs run in the
+// other accumulator.  Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "lmoe_internal.cuh"
+#include "row_vec.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.cuh"
+
+namespace lmoe {
+namespace {
+
+using namespace tc;
+
+constexpr uint32_t A_TILE = 128 * 128;  // 128 x 64 bf16
+
+template <int NT, bool PAIR>
+struct LCfg {
+    static constexpr int EW = NT >= 128 ? 8 : 4;  // epilogue warps
+    static constexpr int THREADS = 32 * (2 + EW);
+    static constexpr int CL = PAIR ? 2 : 1;  // CTAs a tile: a pair (cta_group::2) has 256 rows of A, each CTA half of B
+    static constexpr int MT = 128 * CL;
+    static constexpr int BROWS = NT / CL;
+    static constexpr uint32_t B_TILE = BROWS * 128;
+    static constexpr uint32_t STAGE = A_TILE + B_TILE;
+    static constexpr int S_RAW = int(200 * 1024 / STAGE);
+    static constexpr int S = S_RAW > 8 ? 8 : S_RAW;
+    static constexpr int ACC = 2;  // accumulators: a tile's epilogue overlaps the next one's MMAs
+    static constexpr uint32_t TMEM_COLS = ACC * NT;
+};
+
+struct LArgs {
+    int64_t M;
+    int N, KC;       // chunks of the reduction
+    int MTL, NTL;    // tiles
+    // epilogue
+    const void *bias, *res;
+    int bias_f32, res_f32, out_f32, fn;
+    int vec;         // outputs' and residual's rows take vectors of this many bytes (32, 16) or single elements (0)
+    void *out;
+    uint16_t *pre;
+    int32_t *status;
+    long long limit;
+    int stall;
+};
+
+// ---- functions ---------------------------------------------------------------------------
+
+// z / (1 + e^-u) by e^-|u|, so that the divisor stays in [1, 2].
+__device__ __forceinline__ float times_logistic(float z, float u)
+{
+    const float e = expf(-fabsf(u));
+    return __fdividef(u < 0.f ? z * e : z, 1.f + e);
+}
+constexpr float TANH_C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+template <int FN>
+__device__ __forceinline__ float apply(float z)
+{
+    if (FN == LMOE_FN_RELU) return z < 0.f ? 0.f : z;  // (a NaN stays)
+    if (FN == LMOE_FN_SILU) return times_logistic(z, z);
+    if (FN == LMOE_FN_GELU) return 0.5f * z * erfcf(-0.70710678f * z);  // by erfc: 1 + erf would lose the left tail
+    if (FN == LMOE_FN_GELU_TANH) return times_logistic(z, TANH_C * fmaf(0.044715f * z, z * z, z));
+    return z;
+}
+template <int FN>
+__device__ __forceinline__ float slope(float z)
+{
+    if (FN == LMOE_FN_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+    if (FN == LMOE_FN_GELU) return fmaf(z * 0.39894228f, expf(-0.5f * z * z), 0.5f * erfcf(-0.70710678f * z));
+    if (FN == LMOE_FN_SILU || FN == LMOE_FN_GELU_TANH) {
+        const float u = FN == LMOE_FN_SILU ? z : TANH_C * fmaf(0.044715f * z, z * z, z);
+        const float du = FN == LMOE_FN_SILU ? 1.f : TANH_C * fmaf(3 * 0.044715f * z, z, 1.f);
+        const float e = expf(-fabsf(u)), r = 1.f / (1.f + e);
+        const float s = u < 0.f ? e * r : r, rest = u < 0.f ? r : e * r;  // the logistic function and 1 - it
+        return e == 0.f ? s : fmaf(z * du, s * rest, s);  // (e = 0: z du may be infinite)
+    }
+    return 1.f;
+}
+
+// ---- rows of outputs ---------------------------------------------------------------------
+
+// 32 consecutive elements of a row, fp32 or bf16, as 32-bit words.
+template <bool F32>
+constexpr int WORDS = F32 ? 32 : 16;
+
+template <bool F32>
+__device__ __forceinline__ void row_load(uint32_t (&u)[32], const void *base, int64_t at, int n, int vec)
+{
+    const char *p = static_cast<const char *>(base) + at * (F32 ? 4 : 2);
+    if (n == 32 && vec == 32) {
+#pragma unroll
+        for (int i = 0; i < WORDS<F32>; i += 8)
+            asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(u[i]), "=r"(u[i + 1]), "=r"(u[i + 2]), "=r"(u[i + 3]), "=r"(u[i + 4]), "=r"(u[i + 5]),
+                           "=r"(u[i + 6]), "=r"(u[i + 7])
+                         : "l"(p + 4 * i)
+                         : "memory");
+    } else if (n == 32 && vec == 16) {
+#pragma unroll
+        for (int i = 0; i < WORDS<F32>; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            u[i] = v.x, u[i + 1] = v.y, u[i + 2] = v.z, u[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS<F32>; ++i) {
+            if (F32) {
+                u[i] = i < n ? reinterpret_cast<const uint32_t *>(p)[i] : 0u;
+            } else {
+                const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+                u[i] = (2 * i < n ? uint32_t(h[2 * i]) : 0u) | (2 * i + 1 < n ? uint32_t(h[2 * i + 1]) << 16 : 0u);
+            }
+        }
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void row_add(const uint32_t (&u)[32], float (&y)[32])
+{
+#pragma unroll
+    for (int i = 0; i < WORDS<F32>; ++i) {
+        if (F32) {
+            y[i] += __uint_as_float(u[i]);
+        } else {
+            y[2 * i] += __uint_as_float(u[i] << 16);
+            y[2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+    }
+}
+// Rounded to nearest even.
+template <bool F32>
+__device__ __forceinline__ void row_store(const float (&y)[32], void *base, int64_t at, int n, int vec)
+{
+    uint32_t u[WORDS<F32>];
+#pragma unroll
+    for (int i = 0; i < WORDS<F32>; ++i) {
+        if (F32) {
+            u[i] = __float_as_uint(y[i]);
+        } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+    char *p = static_cast<char *>(base) + at * (F32 ? 4 : 2);
+    if (n == 32 && vec == 32) {
+#pragma unroll
+        for (int i = 0; i < WORDS<F32>; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + 4 * i), "r"(u[i]), "r"(u[i + 1]),
+                         "r"(u[i + 2]), "r"(u[i + 3]), "r"(u[i + 4]), "r"(u[i + 5]), "r"(u[i + 6]), "r"(u[i + 7])
+                         : "memory");
+    } else if (n == 32 && vec == 16) {
+#pragma unroll
+        for (int i = 0; i < WORDS<F32>; i += 4)
+            *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS<F32>; ++i) {
+            if (F32) {
+                if (i < n) reinterpret_cast<uint32_t *>(p)[i] = u[i];
+            } else {
+                uint16_t *h = reinterpret_cast<uint16_t *>(p);
+                if (2 * i < n) h[2 * i] = uint16_t(u[i]);
+                if (2 * i + 1 < n) h[2 * i + 1] = uint16_t(u[i] >> 16);
+            }
+        }
+    }
+}
+
+// y[j] = fn(y[j]), the function chosen once.
+__device__ __forceinline__ void apply32(int fn, float (&y)[32])
+{
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = f(y[j]);
+    };
+    switch (fn) {
+    case LMOE_FN_RELU: all([](float z) { return apply<LMOE_FN_RELU>(z); }); break;
+    case LMOE_FN_SILU: all([](float z) { return apply<LMOE_FN_SILU>(z); }); break;
+    case LMOE_FN_GELU: all([](float z) { return apply<LMOE_FN_GELU>(z); }); break;
+    case LMOE_FN_GELU_TANH: all([](float z) { return apply<LMOE_FN_GELU_TANH>(z); }); break;
+    default: break;
+    }
+}
+
+// y[j] += bias[n + j], j < cols <= 32; n % 32 == 0.
+__device__ __forceinline__ void add_bias(const void *bias, int f32, int n, int cols, float (&y)[32])
+{
+    const float *bf = static_cast<const float *>(bias) + n;
+    const uint16_t *bh = static_cast<const uint16_t *>(bias) + n;
+    if (cols < 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < cols) y[j] += f32 ? __ldg(bf + j) : bf16_bits_to_f32(__ldg(bh + j));
+    } else if (f32) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(bf + j));
+            y[j] += f.x, y[j + 1] += f.y, y[j + 2] += f.z, y[j + 3] += f.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            const uint4 f = __ldg(reinterpret_cast<const uint4 *>(bh + j));
+            const uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[j + 2 * i] += __uint_as_float(w[i] << 16);
+                y[j + 2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    }
+}
+
+// ---- the products ------------------------------------------------------------------------
+
+// A_MN, B_MN: the operand's reduction runs over the rows of its matrix.
+template <int NT, bool PAIR, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
+    k_linear_act(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LArgs p)
+{
+    using C = LCfg<NT, PAIR>;
+    constexpr int S = C::S;
+    static_assert(!B_MN || C::BROWS % 64 == 0, "blocks of 64 elements");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(stages + S * C::STAGE);
+    uint64_t *empty = full + S;
+    uint64_t *acc_full = empty + S;
+    uint64_t *acc_empty = acc_full + C::ACC;
+    uint64_t *drain = acc_empty + C::ACC;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < C::ACC; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], 32 * C::EW * C::CL);
+        }
+        mbar_init(drain, 1);
+        mbar_init_fence();
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == 1) PAIR ? tmem_alloc_pair(tmem_slot, C::TMEM_COLS) : tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (PAIR) cluster_sync();  // the pair's barriers are initialised
+    const uint32_t tmem = *tmem_slot;
+    pdl_enter();
+
+    const int rank = PAIR ? int(cluster_rank()) : 0;
+    const int first = int(blockIdx.x) / C::CL, step = int(gridDim.x) / C::CL;
+    const int items = p.MTL * p.NTL;
+    auto tile_m = [&](int it) { return int64_t(it / p.NTL) * C::MT + rank * 128; };  // this CTA's rows
+    auto tile_n = [&](int it) { return (it % p.NTL) * NT; };
+
+    if (warp == 0) {
+        // ---------------- copies ----------------
+        int stage = 0, fills = 0;
+        uint32_t phase = 0;
+        bool ok = true, at_start = true;  // (the failure-path test withholds a CTA's first stage)
+        for (int it = first; it < items && ok; it += step) {
+            const int m0 = int(tile_m(it)), n0 = tile_n(it) + rank * C::BROWS;
+            for (int kc = 0; kc < p.KC; ++kc) {
+                ok = mbar_wait_warp(&empty[stage], phase ^ 1, p.limit);
+                if (!ok) {
+                    if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                    break;
+                }
+                if (elect_one() && !(p.stall && at_start)) {
+                    uint8_t *sa = stages + stage * C::STAGE, *sb = sa + A_TILE;
+                    // the barrier of this stage: a pair's is the leader's, which announces both CTAs' bytes
+                    const uint32_t bar = PAIR ? cluster_map(smem_u32(&full[stage]), 0) : 0;
+                    const uint64_t policy = l2_policy_evict_normal();
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::STAGE * C::CL);
+                    auto load = [&](void *dst, const CUtensorMap *tm, int x, int y) {
+                        PAIR ? tma_load_2d_pair(dst, tm, x, y, bar, policy) : tma_load_2d_hint(dst, tm, x, y, &full[stage], policy);
+                    };
+                    if (A_MN) {
+                        load(sa, &tmA, m0, kc * 64);
+                        load(sa + 8192, &tmA, m0 + 64, kc * 64);
+                    } else {
+                        load(sa, &tmA, kc * 64, m0);
+                    }
+                    if (B_MN) {
+#pragma unroll
+                        for (int b = 0; b < C::BROWS / 64; ++b) load(sb + b * 8192, &tmB, n0 + 64 * b, kc * 64);
+                    } else {
+                        load(sb, &tmB, kc * 64, n0);
+                    }
+                }
+                __syncwarp();
+                at_start = false;
+                ++fills;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // Copies still in flight after a timeout land before the CTA ends (bounded; a
+        // pair's all count in on the leader's barriers).
+        if (!ok && rank == 0)
+            for (int f = fills > S ? fills - S : 0; f < fills; ++f) mbar_wait_warp(&full[f % S], (f / S) & 1, p.limit);
+    } else if (warp == 1 && rank == 0) {
+        // ---------------- MMA issuer (a pair's: the leader's) ----------------
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        const uint32_t id = (PAIR ? idesc_bf16_pair(NT) : idesc_bf16(NT)) | (A_MN ? IDESC_A_MN : 0) | (B_MN ? IDESC_B_MN : 0);
+        constexpr uint32_t a_step = A_MN ? 128 : 2, b_step = B_MN ? 128 : 2;  // 16 of the reduction, in 16-byte units
+        for (int it = first; it < items && ok; it += step) {
+            ok = mbar_wait_warp(&acc_empty[acc], acc_phase ^ 1, p.limit);
+            tc_fence_after();
+            const uint32_t d = tmem + uint32_t(acc * NT);
+            for (int kc = 0; kc < p.KC && ok; ++kc) {
+                ok = mbar_wait_warp(&full[stage], phase, p.limit);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sa = smem_u32(stages + stage * C::STAGE), sb = sa + A_TILE;
+                    const uint64_t ad = A_MN ? sdesc_mn128(sa, 8192) : sdesc_k128(sa);
+                    const uint64_t bd = B_MN ? sdesc_mn128(sb, 8192) : sdesc_k128(sb);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (PAIR)
+                            mma_bf16_pair(d, ad + a_step * kk, bd + b_step * kk, id, (kc > 0 || kk > 0) ? 1u : 0u);
+                        else
+                            mma_bf16(d, ad + a_step * kk, bd + b_step * kk, id, (kc > 0 || kk > 0) ? 1u : 0u);
+                    PAIR ? tc_commit_pair(&empty[stage]) : tc_commit(&empty[stage]);
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (elect_one()) PAIR ? tc_commit_pair(&acc_full[acc]) : tc_commit(&acc_full[acc]);
+            __syncwarp();
+            if (++acc == C::ACC) {
+                acc = 0;
+                acc_phase ^= 1;
+            }
+        }
+        if (!ok) {
+            if (elect_one()) {
+                set_status(p.status, LMOE_ERR_TIMEOUT);
+                PAIR ? tc_commit_pair(drain) : tc_commit(drain);  // MMAs in flight end before the tensor memory is freed
+                mbar_wait(drain, 0, p.limit);
+            }
+            __syncwarp();
+        }
+    } else if (warp >= 2) {
+        // ---------------- epilogue ----------------
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int it = first; it < items; it += step) {
+            const int64_t m = tile_m(it) + 32 * q + lane;
+            const int n0 = tile_n(it);
+            if (!mbar_wait_warp(&acc_full[acc], acc_phase, p.limit)) {
+                if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
+            for (int c = 32 * half; c < NT && n0 + c < p.N; c += 8 * C::EW) {
+                uint32_t v[32];
+                tmem_ld_cols<32>(tb + c, v);
+                const int n = n0 + c, cols = min(32, p.N - n);
+                const bool mine = m < p.M;
+                const int64_t at = m * p.N + n;
+                uint32_t r[32];  // the residual's words
+                if (p.res && mine) {
+                    if (p.res_f32) row_load<true>(r, p.res, at, cols, p.vec);
+                    else row_load<false>(r, p.res, at, cols, p.vec);
+                }
+                float y[32];
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                if (p.bias) add_bias(p.bias, p.bias_f32, n, cols, y);
+                if (p.pre && mine) row_store<false>(y, p.pre, at, cols, p.vec);
+                apply32(p.fn, y);
+                if (p.res) {
+                    if (p.res_f32) row_add<true>(r, y);
+                    else row_add<false>(r, y);
+                }
+                if (mine) {
+                    if (p.out_f32) row_store<true>(y, p.out, at, cols, p.vec);
+                    else row_store<false>(y, p.out, at, cols, p.vec);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            PAIR ? cluster_arrive_read(cluster_map(smem_u32(&acc_empty[acc]), 0)) : mbar_arrive(&acc_empty[acc]);
+            if (++acc == C::ACC) {
+                acc = 0;
+                acc_phase ^= 1;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    // nobody's shared or tensor memory goes while the pair's other CTA may still write or read it
+    if (PAIR) cluster_sync_end();
+    tc_fence_after();
+    if (warp == 1) PAIR ? tmem_dealloc_pair(tmem, C::TMEM_COLS) : tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// An operand: [rows][cols] bf16, rows `stride` elements apart.
+struct Operand {
+    const uint16_t *p;
+    int64_t rows, cols, stride;
+};
+
+template <int NT, bool PAIR, bool A_MN, bool B_MN>
+cudaError_t launch(const Operand &A, const Operand &B, LArgs g, cudaStream_t st)
+{
+    using C = LCfg<NT, PAIR>;
+    CUtensorMap ma, mb;
+    if (!make_tensor_map(&ma, A.p, MapType::BF16, A.cols, A.rows, A_MN ? 64 : 128, A.stride) ||
+        !make_tensor_map(&mb, B.p, MapType::BF16, B.cols, B.rows, B_MN ? 64 : C::BROWS, B.stride))
+        return cudaErrorInvalidValue;
+    g.MTL = int(ceil_div(g.M, C::MT));
+    g.NTL = int(ceil_div(g.N, NT));
+    const int64_t items = int64_t(g.MTL) * g.NTL;
+    if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + size_t(C::S) * C::STAGE + (2 * C::S + 2 * C::ACC + 1) * 8 + 8;
+    auto *kern = k_linear_act<NT, PAIR, A_MN, B_MN>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    const int64_t slots = device_sms() / C::CL;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((items < slots ? items : slots) * C::CL));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::CL;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
+}
+
+// Vectors of 32 or 16 bytes where every row of every tensor starts on one.
+int vector_bytes(const LArgs &g)
+{
+    auto fits = [&](const void *p, int bytes, int v) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % v == 0 && int64_t(g.N) * bytes % v == 0);
+    };
+    for (int v : {32, 16})
+        if (fits(g.out, g.out_f32 ? 4 : 2, v) && fits(g.pre, 2, v) && fits(g.res, g.res_f32 ? 4 : 2, v)) return v;
+    return 0;
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t product(const Operand &A, const Operand &B, LArgs g, int64_t K, const WaitArgs &wait, cudaStream_t st)
+{
+    g.KC = int(ceil_div(K, 64));
+    g.vec = vector_bytes(g);
+    g.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
+    g.stall = wait.stall_first_fill;
+    return launch<128, false, A_MN, B_MN>(A, B, g, st);
+}
+
+// ---- dz and its column sums ----------------------------------------------------------------
+
+struct DzArgs {
+    const void *dout;
+    const uint16_t *pre;
+    int64_t rows;
+    int N, Np;       // dz's rows are Np elements apart, the columns beyond N zero
+    uint16_t *dz;    // null: only the column sums
+    float *part;     // [gridDim.y][N], or null
+};
+
+// A block takes 256 columns and every gridDim.y-th group of eight rows, a warp a row
+// of it, a lane eight columns.  VEC: rows start on 16 bytes.
+template <bool F32, int FN, bool VEC>
+__global__ void __launch_bounds__(256) k_act_back(const DzArgs p)
+{
+    __shared__ float s_cols[8][256 + 8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = (int(blockIdx.x) * 32 + lane) * 8;
+    float sum[8] = {};
+    pdl_enter();
+    if (c < p.Np)
+        for (int64_t t = int64_t(blockIdx.y) * 8 + warp; t < p.rows; t += int64_t(gridDim.y) * 8) {
+            float d[8], z[8] = {};
+            const int64_t at = t * p.N + c;
+            if (VEC) {
+                if (F32) {
+                    Pack<float, 8> q;
+                    q.load(static_cast<const float *>(p.dout) + at);
+                    q.get(d);
+                } else {
+                    Pack<uint16_t, 8> q;
+                    q.load(static_cast<const uint16_t *>(p.dout) + at);
+                    q.get(d);
+                }
+                if (FN != LMOE_FN_NONE) {
+                    Pack<uint16_t, 8> q;
+                    q.load(p.pre + at);
+                    q.get(z);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = c + j < p.N;
+                    d[j] = !in ? 0.f : F32 ? static_cast<const float *>(p.dout)[at + j] : bf16_bits_to_f32(static_cast<const uint16_t *>(p.dout)[at + j]);
+                    if (FN != LMOE_FN_NONE && in) z[j] = bf16_bits_to_f32(p.pre[at + j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (FN != LMOE_FN_NONE) d[j] *= slope<FN>(z[j]);
+                sum[j] += d[j];
+            }
+            if (p.dz) {
+                Pack<uint16_t, 8> q;
+                q.set(d);
+                q.store(p.dz + t * p.Np + c);
+            }
+        }
+    if (!p.part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_cols[warp][lane * 8 + j] = sum[j];
+    __syncthreads();
+    const int col = int(blockIdx.x) * 256 + threadIdx.x;
+    if (col >= p.N) return;
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v += s_cols[q][threadIdx.x];
+    p.part[int64_t(blockIdx.y) * p.N + col] = v;
+}
+
+// Groups of rows of k_act_back: four blocks an SM, eight rows a block at least.
+int64_t dz_splits(int64_t rows, int N)
+{
+    const int64_t want = ceil_div(152 * 4, ceil_div(N, 256)), most = ceil_div(rows, 8);
+    return want < most ? want : most;
+}
+
+template <bool F32, bool VEC>
+cudaError_t dz_fn(const DzArgs &g, int fn, dim3 grid, cudaStream_t st)
+{
+    switch (fn) {
+    case LMOE_FN_NONE: return launch_pdl(k_act_back<F32, LMOE_FN_NONE, VEC>, grid, dim3(256), 0, st, g);
+    case LMOE_FN_RELU: return launch_pdl(k_act_back<F32, LMOE_FN_RELU, VEC>, grid, dim3(256), 0, st, g);
+    case LMOE_FN_SILU: return launch_pdl(k_act_back<F32, LMOE_FN_SILU, VEC>, grid, dim3(256), 0, st, g);
+    case LMOE_FN_GELU: return launch_pdl(k_act_back<F32, LMOE_FN_GELU, VEC>, grid, dim3(256), 0, st, g);
+    default: return launch_pdl(k_act_back<F32, LMOE_FN_GELU_TANH, VEC>, grid, dim3(256), 0, st, g);
+    }
+}
+
+}  // namespace
+
+size_t linear_act_scratch_bytes(int64_t, int, int) { return 0; }
+
+cudaError_t launch_linear_act(const LinearActArgs &a, void *, cudaStream_t st)
+{
+    LArgs g{};
+    g.M = a.rows;
+    g.N = a.N;
+    g.bias = a.bias;
+    g.bias_f32 = a.bias_fmt == LMOE_F32;
+    g.res = a.res;
+    g.res_f32 = a.res_fmt == LMOE_F32;
+    g.out_f32 = a.out_fmt == LMOE_F32;
+    g.fn = a.fn;
+    g.out = a.out;
+    g.pre = a.pre;
+    g.status = a.status;
+    return product<false, false>({a.x, a.rows, a.K, a.K}, {a.W, a.N, a.K, a.K}, g, a.K, a.wait, st);
+}
+
+// dz [rows][Np] bf16 | column sums
+size_t linear_act_back_scratch_bytes(int64_t rows, int, int N)
+{
+    const int64_t Np = round_up(N, 8);
+    return size_t(round_up(rows * Np * 2, 256)) + size_t(round_up(dz_splits(rows, N) * N * 4, 256));
+}
+
+cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cudaStream_t st)
+{
+    cudaError_t e = cudaSuccess;
+    if (a.rows == 0) {
+        if (a.dW) e = cudaMemsetAsync(a.dW, 0, size_t(a.N) * a.K * (a.dW_fmt == LMOE_F32 ? 4 : 2), st);
+        if (a.dbias && e == cudaSuccess) e = cudaMemsetAsync(a.dbias, 0, size_t(a.N) * 4, st);
+        return e;
+    }
+    const int64_t Np = round_up(a.N, 8);
+    uint16_t *dz = static_cast<uint16_t *>(scratch);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(scratch) + round_up(a.rows * Np * 2, 256));
+    // bf16 gradients that go through no function are the operand as they are
+    const bool as_is = a.fn == LMOE_FN_NONE && a.dout_fmt == LMOE_BF16 && Np == a.N;
+    const bool need_dz = (a.dx || a.dW) && !as_is;
+    if (need_dz || a.dbias) {
+        const DzArgs g{a.dout, a.pre, a.rows, a.N, int(Np), need_dz ? dz : nullptr, a.dbias ? part : nullptr};
+        const dim3 grid(unsigned(ceil_div(Np, 256)), unsigned(dz_splits(a.rows, a.N)));
+        const bool f32 = a.dout_fmt == LMOE_F32, vec = Np == a.N;
+        e = f32 ? (vec ? dz_fn<true, true>(g, a.fn, grid, st) : dz_fn<true, false>(g, a.fn, grid, st))
+                : (vec ? dz_fn<false, true>(g, a.fn, grid, st) : dz_fn<false, false>(g, a.fn, grid, st));
+        if (e == cudaSuccess && a.dbias) e = launch_col_sums(part, grid.y, a.N, 1, a.dbias, nullptr, st);
+        if (e != cudaSuccess) return e;
+    }
+    const Operand d{as_is ? static_cast<const uint16_t *>(a.dout) : dz, a.rows, a.N, Np};
+    LArgs g{};
+    g.status = a.status;
+    if (a.dx) {
+        g.M = a.rows;
+        g.N = a.K;
+        g.out = a.dx;
+        e = product<false, true>(d, {a.W, a.N, a.K, a.K}, g, a.N, a.wait, st);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.dW) {
+        g.M = a.N;
+        g.N = a.K;
+        g.out = a.dW;
+        g.out_f32 = a.dW_fmt == LMOE_F32;
+        e = product<true, true>(d, {a.x, a.rows, a.K, a.K}, g, a.rows, a.wait, st);
+    }
+    return e;
+}
+
+}  // namespace lmoe

@@ -9,95 +9,11 @@
 // One pass over the data: a row's elements stay in registers between the two statistics, so y and res are read once and r' and n
 // written once.  All arithmetic and both sums of squares are fp32; r' and n
 // are rounded once, to nearest even.
-#include <cuda_bf16.h>
-
 #include "lmoe_internal.cuh"
+#include "row_vec.cuh"
 
 namespace lmoe {
 namespace {
-
-// W consecutive elements as they lie in memory (aligned: H % 8 == 0, 16-byte
-// aligned rows) and as fp32.
-template <typename T, int W>
-struct Pack;
-template <int W>
-struct Pack<uint16_t, W> {
-    uint32_t u[W / 2];
-    __device__ __forceinline__ void load(const uint16_t *p)
-    {
-        if constexpr (W == 8) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p);
-            u[0] = v.x, u[1] = v.y;
-        }
-    }
-    __device__ __forceinline__ void get(float (&v)[W]) const
-    {
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
-    }
-    __device__ __forceinline__ void set(const float (&v)[W])  // rounded to nearest even
-    {
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-    }
-    __device__ __forceinline__ void store(uint16_t *p) const
-    {
-        if constexpr (W == 8)
-            *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-        else
-            *reinterpret_cast<uint2 *>(p) = make_uint2(u[0], u[1]);
-    }
-};
-template <int W>
-struct Pack<float, W> {
-    float4 q[W / 4];
-    __device__ __forceinline__ void load(const float *p)
-    {
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) q[i] = reinterpret_cast<const float4 *>(p)[i];
-    }
-    __device__ __forceinline__ void get(float (&v)[W]) const
-    {
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) v[4 * i] = q[i].x, v[4 * i + 1] = q[i].y, v[4 * i + 2] = q[i].z, v[4 * i + 3] = q[i].w;
-    }
-    __device__ __forceinline__ void set(const float (&v)[W])
-    {
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) q[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-    __device__ __forceinline__ void store(float *p) const
-    {
-#pragma unroll
-        for (int i = 0; i < W / 4; ++i) reinterpret_cast<float4 *>(p)[i] = q[i];
-    }
-};
-
-// Sum over a row's threads (a warp, or the whole block), the same value in
-// every thread and in a fixed order.  `part` is used once per call.
-template <bool WARP>
-__device__ __forceinline__ float row_sum(float s, float *part)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (WARP) return s;
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
-    __syncthreads();
-    const int nw = int(blockDim.x) >> 5, lane = threadIdx.x & 31;
-    s = lane < nw ? part[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    return s;
-}
 
 // R: the residual stream's type.  E8: eighths of a thread's elements.  WARP: a
 // warp takes a row (several rows a block), else a block takes one.  All of a

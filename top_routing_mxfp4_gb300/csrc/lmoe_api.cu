@@ -132,6 +132,20 @@ bool norm_ok(int64_t T, int32_t H, float eps, int32_t fmt)
            (fmt == LMOE_BF16 || fmt == LMOE_F32);
 }
 
+bool fmt_ok(int32_t fmt) { return fmt == LMOE_BF16 || fmt == LMOE_F32; }
+bool fn_ok(int32_t fn) { return fn >= LMOE_FN_NONE && fn <= LMOE_FN_GELU_TANH; }
+bool linear_act_ok(int64_t rows, int32_t K, int32_t N)
+{
+    if (rows < 0 || rows > kMaxRows || K <= 0 || K % 8 != 0 || N <= 0 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
+        return false;
+    constexpr int64_t most = int64_t(1) << 40;  // tiles of 64 x 64 and more, counted in 32 bits
+    return rows <= most / K && rows <= most / N && N <= most / K;
+}
+bool balance_ok(int64_t T, int32_t E, int32_t k)
+{
+    return T >= 0 && E > 0 && E <= 2048 && k > 0 && k <= 32 && k <= E && T <= INT32_MAX / 2 / k;
+}
+
 // The checks the two grouped products share; fills all of `a` but the weights,
 // row weights and output type.
 lmoe_status grouped_args(const uint16_t *x, int64_t x_rows, const lmoe_groups *g, int32_t gather, int32_t K, int32_t N,
@@ -617,6 +631,119 @@ lmoe_status lmoe_grouped_swiglu_bf16(const uint16_t *x, int64_t x_rows, const ui
     a.W2 = Wu;
     a.out_fmt = LMOE_BF16;
     return cuda_status(launch_grouped(a, cudaStream_t(stream)));
+}
+
+size_t lmoe_linear_act_workspace_size(int64_t rows, int32_t K, int32_t N)
+{
+    if (!linear_act_ok(rows, K, N)) return 0;
+    return kStatusBytes + linear_act_scratch_bytes(rows, K, N);
+}
+
+lmoe_status lmoe_linear_act_bf16(const uint16_t *x, const uint16_t *W, const lmoe_linear_act *act, int64_t rows, int32_t K,
+                                 int32_t N, int32_t out_fmt, void *out, uint16_t *pre, void *workspace, size_t ws_bytes,
+                                 void *stream)
+{
+    const lmoe_linear_act f = act ? *act : lmoe_linear_act{};
+    if (!linear_act_ok(rows, K, N) || !fn_ok(f.fn) || !fmt_ok(out_fmt) || !fmt_ok(f.bias_fmt) || !fmt_ok(f.res_fmt))
+        return LMOE_ERR_INVALID_ARG;
+    if (rows == 0) return LMOE_OK;
+    if (!x || !W || !out) return LMOE_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)x, (const void *)W, (const void *)out, (const void *)pre, f.bias, f.res})
+        if (!aligned(p, 16)) return LMOE_ERR_INVALID_ARG;
+    if (f.res == out && f.res_fmt != out_fmt) return LMOE_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < lmoe_linear_act_workspace_size(rows, K, N) || !aligned(workspace, 256))
+        return LMOE_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    LinearActArgs a{x, W, f.bias, f.res, f.bias_fmt, f.res_fmt, f.fn, rows, K, N, out_fmt, out, pre,
+                    reinterpret_cast<int32_t *>(ws), wait_args()};
+    return cuda_status(launch_linear_act(a, ws + kStatusBytes, cudaStream_t(stream)));
+}
+
+size_t lmoe_linear_act_backward_workspace_size(int64_t rows, int32_t K, int32_t N)
+{
+    if (!linear_act_ok(rows, K, N)) return 0;
+    return kStatusBytes + linear_act_back_scratch_bytes(rows, K, N);
+}
+
+lmoe_status lmoe_linear_act_bf16_backward(const void *dout, int32_t dout_fmt, const uint16_t *x, const uint16_t *W,
+                                          const uint16_t *pre, int32_t fn, int64_t rows, int32_t K, int32_t N,
+                                          uint16_t *dx, void *dW, int32_t dW_fmt, float *dbias, void *workspace,
+                                          size_t ws_bytes, void *stream)
+{
+    if (!linear_act_ok(rows, K, N) || !fn_ok(fn) || !fmt_ok(dout_fmt) || !fmt_ok(dW_fmt)) return LMOE_ERR_INVALID_ARG;
+    for (const void *p : {dout, (const void *)x, (const void *)W, (const void *)pre, (const void *)dx,
+                          (const void *)dW, (const void *)dbias})
+        if (!aligned(p, 16)) return LMOE_ERR_INVALID_ARG;
+    if (rows > 0 && (!dout || (fn != LMOE_FN_NONE) != (pre != nullptr) || (dx && !W) || (dW && !x)))
+        return LMOE_ERR_INVALID_ARG;
+    if (!dx && !dW && !dbias) return LMOE_OK;
+    if (rows > 0 && (!workspace || ws_bytes < lmoe_linear_act_backward_workspace_size(rows, K, N) || !aligned(workspace, 256)))
+        return LMOE_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    LinearActBackArgs a{dout, dout_fmt, x, W, pre, fn, rows, K, N, dx, dW, dW_fmt, dbias,
+                        reinterpret_cast<int32_t *>(ws), wait_args()};
+    return cuda_status(launch_linear_act_back(a, ws ? ws + kStatusBytes : nullptr, cudaStream_t(stream)));
+}
+
+lmoe_status lmoe_layer_norm(const void *x, int32_t x_fmt, const float *w, const float *b, float eps, int64_t T, int32_t H,
+                            uint16_t *out, float *mean, float *rstd, void *stream)
+{
+    if (!norm_ok(T, H, eps, x_fmt) || (mean != nullptr) != (rstd != nullptr)) return LMOE_ERR_INVALID_ARG;
+    if (T == 0) return LMOE_OK;
+    if (!x || !out || !aligned(x, 16) || !aligned(w, 16) || !aligned(b, 16) || !aligned(out, 16) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return LMOE_ERR_INVALID_ARG;
+    return cuda_status(launch_layer_norm({x, x_fmt, w, b, eps, T, H, out, mean, rstd}, cudaStream_t(stream)));
+}
+
+size_t lmoe_layer_norm_backward_workspace_size(int64_t T, int32_t H)
+{
+    if (!norm_ok(T, H, 0.f, LMOE_BF16)) return 0;
+    return kStatusBytes + layer_norm_back_scratch_bytes(T, H);
+}
+
+lmoe_status lmoe_layer_norm_backward(const uint16_t *dy, const void *x, int32_t x_fmt, const float *mean,
+                                     const float *rstd, const float *w, const void *add, int64_t T, int32_t H, void *dx,
+                                     float *dw, float *db, void *workspace, size_t ws_bytes, void *stream)
+{
+    if (!norm_ok(T, H, 0.f, x_fmt)) return LMOE_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)dy, x, (const void *)w, add, (const void *)dx})
+        if (!aligned(p, 16)) return LMOE_ERR_INVALID_ARG;
+    for (const float *p : {mean, rstd, (const float *)dw, (const float *)db})
+        if (!aligned(p, 4)) return LMOE_ERR_INVALID_ARG;
+    if (T > 0 && (!dy || !x || !mean || !rstd || !dx)) return LMOE_ERR_INVALID_ARG;
+    if (T > 0 && (dw || db) && (!workspace || ws_bytes < lmoe_layer_norm_backward_workspace_size(T, H) || !aligned(workspace, 256)))
+        return LMOE_ERR_WORKSPACE;
+    LayerNormBackArgs a{dy, x, x_fmt, mean, rstd, w, add, T, H, dx, dw, db,
+                        workspace ? reinterpret_cast<float *>(static_cast<char *>(workspace) + kStatusBytes) : nullptr};
+    return cuda_status(launch_layer_norm_back(a, cudaStream_t(stream)));
+}
+
+size_t lmoe_balance_loss_workspace_size(int64_t T, int32_t E, int32_t k)
+{
+    if (!balance_ok(T, E, k)) return 0;
+    return kStatusBytes + balance_scratch_bytes(T, E, k);
+}
+
+lmoe_status lmoe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t *mask, int64_t T, int32_t E,
+                              int32_t k, float *loss, int32_t *counts, float *probs, const lmoe_balance_grad *grad,
+                              void *workspace, size_t ws_bytes, void *stream)
+{
+    const lmoe_balance_grad g = grad ? *grad : lmoe_balance_grad{};
+    if (!balance_ok(T, E, k) || !isfinite(g.coef_balance) || !isfinite(g.coef_z)) return LMOE_ERR_INVALID_ARG;
+    if (!loss || !counts || !probs || (T > 0 && (!logits || !topk_idx || (grad && !g.dlogits))) ||
+        (g.topk_w != nullptr) != (g.dtopk_w != nullptr))
+        return LMOE_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)logits, (const void *)topk_idx, (const void *)loss, (const void *)counts,
+                          (const void *)probs, (const void *)g.dlogits, (const void *)g.topk_w, (const void *)g.dtopk_w})
+        if (!aligned(p, 16)) return LMOE_ERR_INVALID_ARG;
+    if (!aligned(g.scale, 4)) return LMOE_ERR_INVALID_ARG;
+    if (!workspace || ws_bytes < lmoe_balance_loss_workspace_size(T, E, k) || !aligned(workspace, 256))
+        return LMOE_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    BalanceArgs a{logits, topk_idx, mask, T, E, k, loss, counts, probs, T > 0 ? g.dlogits : nullptr, g.coef_balance,
+                  g.coef_z, g.scale, g.topk_w, g.dtopk_w, reinterpret_cast<int32_t *>(ws), nullptr, nullptr, nullptr};
+    return cuda_status(launch_balance(a, ws + kStatusBytes, cudaStream_t(stream)));
 }
 
 size_t lmoe_residual_block_workspace_size(const lmoe_dims *dims, int32_t hidden)

@@ -385,4 +385,86 @@ struct GroupedArgs {
 };
 cudaError_t launch_grouped(const GroupedArgs &a, cudaStream_t st);
 
+// out_k[c] = sum_g part[g][k][c], k < sets <= 2, in one order (k_layer_norm.cu); a null out is skipped.
+cudaError_t launch_col_sums(const float *part, int64_t G, int64_t C, int sets, float *out0, float *out1, cudaStream_t st);
+
+// ---- layer norm (k_layer_norm.cu) -------------------------------------------------------
+struct LayerNormArgs {
+    const void *x;
+    int x_fmt;
+    const float *w, *b;
+    float eps;
+    int64_t T;
+    int H;
+    uint16_t *out;
+    float *mean, *rstd;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t st);
+struct LayerNormBackArgs {
+    const uint16_t *dy;
+    const void *x;
+    int x_fmt;
+    const float *mean, *rstd, *w;
+    const void *add;
+    int64_t T;
+    int H;
+    void *dx;  // may be add: each thread reads its elements before it writes them
+    float *dw, *db;
+    float *part;
+};
+size_t layer_norm_back_scratch_bytes(int64_t T, int H);
+cudaError_t launch_layer_norm_back(const LayerNormBackArgs &a, cudaStream_t st);
+
+// ---- balance loss (k_balance.cu) ----------------------------------------------------------
+struct BalanceArgs {
+    const float *logits;
+    const int32_t *idx;
+    const uint8_t *mask;
+    int64_t T;
+    int E, k;
+    float *loss;
+    int32_t *counts;
+    float *probs;
+    float *dlogits;  // null: no gradient
+    float coef_balance, coef_z;
+    const float *scale, *topk_w, *dtopk_w;
+    int32_t *status;
+    int32_t *tokens, *count_part;  // scratch
+    float *part;
+};
+size_t balance_scratch_bytes(int64_t T, int E, int k);
+cudaError_t launch_balance(BalanceArgs a, void *scratch, cudaStream_t st);
+
+// ---- linear layer with bias, function and residual (k_linear_act.cu) ------------------------
+struct LinearActArgs {
+    const uint16_t *x, *W;
+    const void *bias, *res;
+    int bias_fmt, res_fmt, fn;
+    int64_t rows;
+    int K, N;
+    int out_fmt;
+    void *out;
+    uint16_t *pre;
+    int32_t *status;
+    WaitArgs wait;
+};
+size_t linear_act_scratch_bytes(int64_t rows, int K, int N);
+cudaError_t launch_linear_act(const LinearActArgs &a, void *scratch, cudaStream_t st);
+struct LinearActBackArgs {
+    const void *dout;
+    int dout_fmt;
+    const uint16_t *x, *W, *pre;
+    int fn;
+    int64_t rows;
+    int K, N;
+    uint16_t *dx;
+    void *dW;
+    int dW_fmt;
+    float *dbias;
+    int32_t *status;
+    WaitArgs wait;
+};
+size_t linear_act_back_scratch_bytes(int64_t rows, int K, int N);
+cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cudaStream_t st);
+
 }  // namespace lmoe

@@ -241,6 +241,14 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc, ui
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate));
 }
 
+// MN-major operand tile: rows of the reduction, 64 elements (128 bytes, swizzled by
+// TMA) of the operand's own dimension each; `block` bytes between blocks of 64
+// elements, groups of 8 reduction rows 1024 bytes apart.  An MMA's 16 reduction rows
+// are 2048 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t block) { return sdesc(saddr, block, 1024, 2); }
+// The bits of a kind::f16 instruction descriptor that say so of A and of B.
+constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
+
 // kind::f16 instruction descriptor: fp32 accumulator, A and B bf16, both
 // K-major, M = 128, N given.
 __device__ __forceinline__ uint32_t idesc_bf16(uint32_t N)

@@ -13,8 +13,9 @@ enum class MapType {
     FP4  // packed, two a byte in memory; 128 columns, a byte each in shared memory
 };
 
-// A map of [rows][K] elements (rows K elements apart) in boxes of box_rows rows.
-inline bool make_tensor_map(CUtensorMap *m, const void *base, MapType type, int64_t K, int64_t rows, int box_rows)
+// A map of [rows][K] elements (rows K elements apart, or `stride` where given) in boxes of box_rows rows.
+inline bool make_tensor_map(CUtensorMap *m, const void *base, MapType type, int64_t K, int64_t rows, int box_rows,
+                            int64_t stride = 0)
 {
     typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -30,7 +31,8 @@ inline bool make_tensor_map(CUtensorMap *m, const void *base, MapType type, int6
     }();
     if (!encode) return false;
     const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(type == MapType::BF16 ? 2 * K : K / 2)};
+    if (!stride) stride = K;
+    const cuuint64_t strides[1] = {cuuint64_t(type == MapType::BF16 ? 2 * stride : stride / 2)};
     const cuuint32_t box[2] = {type == MapType::BF16 ? 64u : 128u, cuuint32_t(box_rows)};
     const cuuint32_t step[2] = {1, 1};
     const CUtensorMapDataType t =

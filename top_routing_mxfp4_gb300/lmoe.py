@@ -133,6 +133,31 @@ class ResidualBlockStruct(ctypes.Structure):
 _res_block_ws = _sig_later("lmoe_residual_block_workspace_size", _sz, _DP, _i32)
 _res_block = _sig_later("lmoe_forward_residual_block", ctypes.c_int, _vp, _i32, _vp,
                         ctypes.POINTER(ResidualBlockStruct), _vp, _vp, _WP, _DP, _i32, _vp, _vp, _vp, _sz, _vp)
+class LinearAct(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_fmt", ctypes.c_int32), ("fn", ctypes.c_int32),
+                ("res", ctypes.c_void_p), ("res_fmt", ctypes.c_int32)]
+
+
+class BalanceGrad(ctypes.Structure):
+    _fields_ = [("dlogits", ctypes.c_void_p), ("coef_balance", ctypes.c_float), ("coef_z", ctypes.c_float),
+                ("scale", ctypes.c_void_p), ("topk_w", ctypes.c_void_p), ("dtopk_w", ctypes.c_void_p)]
+
+
+_linear_act_ws = _sig_later("lmoe_linear_act_workspace_size", _sz, _i64, _i32, _i32)
+_linear_act = _sig_later("lmoe_linear_act_bf16", ctypes.c_int, _vp, _vp, ctypes.POINTER(LinearAct), _i64, _i32, _i32, _i32,
+                         _vp, _vp, _vp, _sz, _vp)
+_linear_act_back_ws = _sig_later("lmoe_linear_act_backward_workspace_size", _sz, _i64, _i32, _i32)
+_linear_act_back = _sig_later("lmoe_linear_act_bf16_backward", ctypes.c_int, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i32,
+                              _i32, _vp, _vp, _i32, _vp, _vp, _sz, _vp)
+_layer_norm = _sig_later("lmoe_layer_norm", ctypes.c_int, _vp, _i32, _vp, _vp, ctypes.c_float, _i64, _i32, _vp, _vp, _vp,
+                         _vp)
+_layer_norm_back_ws = _sig_later("lmoe_layer_norm_backward_workspace_size", _sz, _i64, _i32)
+_layer_norm_back = _sig_later("lmoe_layer_norm_backward", ctypes.c_int, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i64, _i32,
+                              _vp, _vp, _vp, _vp, _sz, _vp)
+_balance_ws = _sig_later("lmoe_balance_loss_workspace_size", _sz, _i64, _i32, _i32)
+_balance = _sig_later("lmoe_balance_loss", ctypes.c_int, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp,
+                      ctypes.POINTER(BalanceGrad), _vp, _sz, _vp)
+FUNCTIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 BF16, F32 = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
@@ -673,10 +698,109 @@ def grouped_swiglu_bf16(x, Wg, Wu, offsets, perm=None, k: int = 1, gather=None, 
     return _fast.grouped(x, Wg, Wu, offsets, perm, k, gather, None, out, ws, stream)
 
 
+# ---- the layer's dense, trained neighbours: linear with bias, function and residual, layer norm, balance loss ----
+
+class _TrainBinding:
+    """The entry points of these calls, handed to the compiled binding at the first of them."""
+
+    def __getattr__(self, name):
+        global _train
+        if name.startswith("_"):
+            raise AttributeError(name)
+        entries = (_linear_act, _linear_act_ws, _linear_act_back, _linear_act_back_ws, _layer_norm, _layer_norm_back,
+                   _layer_norm_back_ws, _balance, _balance_ws)
+        for f in entries:
+            if not hasattr(f, "argtypes"):
+                f()  # raises: not in this library
+        _fast.own_ws  # loads the binding
+        _fast.bind_train(*(ctypes.cast(f, _vp).value for f in entries))
+        _train = _fast
+        return getattr(_train, name)
+
+
+_train = _TrainBinding()
+
+
+def _function(act: str) -> int:
+    if act not in FUNCTIONS:
+        raise ValueError(f"act: expected one of {', '.join(FUNCTIONS)}, got {act!r}")
+    return FUNCTIONS[act]
+
+
+def linear_act_workspace_size(rows: int, K: int, N: int) -> int:
+    return int(_linear_act_ws(rows, K, N))
+
+
+def linear_act_bf16(x, W, bias=None, act: str = "none", res=None, out=None, pre=None, ws=None, stream=None):
+    """out = act(x W^T + bias) + res (lmoe_linear_act_bf16): x bf16 [rows, K], W
+    bf16 [N, K], bias fp32 or bf16 [N], act one of FUNCTIONS, res bf16 or fp32
+    [rows, N].  Without `out`: of res's type, bf16 without one.  With pre=True, or a
+    bf16 tensor [rows, N] to write, returns (out, pre), pre = x W^T + bias as the
+    backward call takes it.  `ws`: a zeroed workspace of linear_act_workspace_size
+    bytes, kept by the caller (last_device_status(ws) says what calls with it
+    found); one is made for the call without it (last_call_status)."""
+    return _train.linear_act(x, W, bias, _function(act), res, out, pre, ws, stream)
+
+
+def linear_act_backward_workspace_size(rows: int, K: int, N: int) -> int:
+    return int(_linear_act_back_ws(rows, K, N))
+
+
+def linear_act_bf16_backward(dout, x, W, act: str = "none", pre=None, want_dx: bool = True, want_dW: bool = True,
+                             want_dbias: bool = True, dx=None, dW=None, dbias=None, ws=None, stream=None):
+    """The gradients of linear_act_bf16 (lmoe_linear_act_bf16_backward): dout bf16
+    or fp32 [rows, N], pre as the forward call gave it (None where act is "none").
+    Returns (dx bf16 [rows, K], dW [N, K], dbias fp32 [N]), None for what is not
+    wanted; dW is bf16, or of the type of the one given.  The residual's gradient is
+    dout.  `ws` as for linear_act_bf16, of linear_act_backward_workspace_size bytes."""
+    return _train.linear_act_backward(dout, x, W, _function(act), pre, want_dx, want_dW, want_dbias, dx, dW, dbias, ws,
+                                      stream)
+
+
+def layer_norm(x, w=None, b=None, eps: float = 1e-5, stats: bool = False, out=None, mean=None, rstd=None, stream=None):
+    """Layer norm (lmoe_layer_norm): x [T, H] bf16 or fp32, w and b fp32 [H] or None
+    -> bf16 [T, H]; with stats (or mean and rstd to write, fp32 [T]) returns (out,
+    mean, rstd), the rows' statistics for the backward call."""
+    return _train.layer_norm(x, w, b, eps, stats, out, mean, rstd, stream)
+
+
+def layer_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(_layer_norm_back_ws(T, H))
+
+
+def layer_norm_backward(dy, x, mean, rstd, w=None, add=None, want_params: bool = True, dx=None, dw=None, db=None, ws=None,
+                        stream=None):
+    """The gradients of layer_norm (lmoe_layer_norm_backward): dy bf16 [T, H], x,
+    mean, rstd as the forward call took and gave them; add (x's type): a gradient
+    that is added to dx.  Returns (dx of x's type, dw fp32 [H], db fp32 [H]), without
+    want_params (dx, None, None).  `ws`: a workspace of
+    layer_norm_backward_workspace_size bytes (its content does not matter)."""
+    return _train.layer_norm_backward(dy, x, mean, rstd, w, add, want_params, dx, dw, db, ws, stream)
+
+
+def balance_loss_workspace_size(T: int, E: int, k: int) -> int:
+    return int(_balance_ws(T, E, k))
+
+
+def balance_loss(logits, topk_idx, mask=None, coef=(0.01, 0.001), grad: bool = False, topk_w=None, dtopk_w=None, scale=None,
+                 dlogits=None, ws=None, stream=None):
+    """A router's losses and per-expert counts (lmoe_balance_loss): logits fp32
+    [T, E] and topk_idx int32 [T, k] as route gives them, mask bool [T] (False: a
+    token that does not count).  Returns (loss fp32 [2]: balance and z, counts int32
+    [E], probs fp32 [E]), and with grad (or `dlogits` to write) a fourth, dlogits
+    fp32 [T, E]: the gradient of coef[0] loss[0] + coef[1] loss[1], times the fp32
+    scalar on the device `scale` where given, plus with topk_w and dtopk_w (fp32
+    [T, k]) the gradient that comes through the gate weights.  `ws`: a zeroed
+    workspace of balance_loss_workspace_size bytes, kept by the caller
+    (last_device_status(ws) says whether ids were bad); one is made for the call
+    without it (last_call_status)."""
+    return _train.balance_loss(logits, topk_idx, mask, coef[0], coef[1], grad, topk_w, dtopk_w, scale, dlogits, ws, stream)
+
+
 def last_call_status() -> int:
     """The device status (as last_device_status) of the latest linear_mxfp4,
-    grouped_linear_bf16, grouped_swiglu_bf16 or expert_ffn_bf16 call, of any
-    thread, that was given no workspace; of its latest replay, if it was
+    grouped_linear_bf16, grouped_swiglu_bf16, expert_ffn_bf16, linear_act_bf16,
+    linear_act_bf16_backward or balance_loss call, of any thread, that was given no workspace; of its latest replay, if it was
     captured.  The call's workspace is kept for this until the next such call.
     Calls with a workspace of the caller's are asked with last_device_status."""
     ws = _fast.own_ws()
