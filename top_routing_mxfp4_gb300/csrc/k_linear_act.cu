@@ -484,6 +484,8 @@ cudaError_t product(const Operand &A, const Operand &B, LArgs g, int64_t K, cons
     g.vec = vector_bytes(g);
     g.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
     g.stall = wait.stall_first_fill;
+    // A pair's 256 x 256 tile where there are tiles for most of the GPU.
+    if (ceil_div(g.M, 256) * ceil_div(g.N, 256) >= 40) return launch<256, true, A_MN, B_MN>(A, B, g, st);
     return launch<128, false, A_MN, B_MN>(A, B, g, st);
 }
 
