@@ -15,6 +15,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "act_fn.cuh"
 #include "lmoe_internal.cuh"
 #include "row_vec.cuh"
 #include "tc_ptx.cuh"
@@ -26,6 +27,7 @@ namespace {
 using namespace tc;
 
 constexpr uint32_t A_TILE = 128 * 128;  // 128 x 64 bf16
+constexpr int MAX_PARTS = 16;
 
 template <int NT, bool PAIR>
 struct LCfg {
@@ -46,6 +48,7 @@ struct LArgs {
     int64_t M;
     int N, KC;       // chunks of the reduction
     int MTL, NTL;    // tiles
+    int KS;          // parts of the reduction; with more than one, part k's sums go to out + k M N (fp32)
     // epilogue
     const void *bias, *res;
     int bias_f32, res_f32, out_f32, fn;
@@ -56,40 +59,6 @@ struct LArgs {
     long long limit;
     int stall;
 };
-
-// ---- functions ---------------------------------------------------------------------------
-
-// z / (1 + e^-u) by e^-|u|, so that the divisor stays in [1, 2].
-__device__ __forceinline__ float times_logistic(float z, float u)
-{
-    const float e = expf(-fabsf(u));
-    return __fdividef(u < 0.f ? z * e : z, 1.f + e);
-}
-constexpr float TANH_C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-
-template <int FN>
-__device__ __forceinline__ float apply(float z)
-{
-    if (FN == LMOE_FN_RELU) return z < 0.f ? 0.f : z;  // (a NaN stays)
-    if (FN == LMOE_FN_SILU) return times_logistic(z, z);
-    if (FN == LMOE_FN_GELU) return 0.5f * z * erfcf(-0.70710678f * z);  // by erfc: 1 + erf would lose the left tail
-    if (FN == LMOE_FN_GELU_TANH) return times_logistic(z, TANH_C * fmaf(0.044715f * z, z * z, z));
-    return z;
-}
-template <int FN>
-__device__ __forceinline__ float slope(float z)
-{
-    if (FN == LMOE_FN_RELU) return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
-    if (FN == LMOE_FN_GELU) return fmaf(z * 0.39894228f, expf(-0.5f * z * z), 0.5f * erfcf(-0.70710678f * z));
-    if (FN == LMOE_FN_SILU || FN == LMOE_FN_GELU_TANH) {
-        const float u = FN == LMOE_FN_SILU ? z : TANH_C * fmaf(0.044715f * z, z * z, z);
-        const float du = FN == LMOE_FN_SILU ? 1.f : TANH_C * fmaf(3 * 0.044715f * z, z, 1.f);
-        const float e = expf(-fabsf(u)), r = 1.f / (1.f + e);
-        const float s = u < 0.f ? e * r : r, rest = u < 0.f ? r : e * r;  // the logistic function and 1 - it
-        return e == 0.f ? s : fmaf(z * du, s * rest, s);  // (e = 0: z du may be infinite)
-    }
-    return 1.f;
-}
 
 // ---- rows of outputs ---------------------------------------------------------------------
 
@@ -268,9 +237,11 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
 
     const int rank = PAIR ? int(cluster_rank()) : 0;
     const int first = int(blockIdx.x) / C::CL, step = int(gridDim.x) / C::CL;
-    const int items = p.MTL * p.NTL;
-    auto tile_m = [&](int it) { return int64_t(it / p.NTL) * C::MT + rank * 128; };  // this CTA's rows
-    auto tile_n = [&](int it) { return (it % p.NTL) * NT; };
+    const int tiles = p.MTL * p.NTL, items = tiles * p.KS;
+    auto tile_m = [&](int it) { return int64_t(it % tiles / p.NTL) * C::MT + rank * 128; };  // this CTA's rows
+    auto tile_n = [&](int it) { return (it % tiles % p.NTL) * NT; };
+    auto chunk0 = [&](int it) { return it / tiles * p.KC / p.KS; };  // an item's chunks of the reduction
+    auto chunk1 = [&](int it) { return (it / tiles + 1) * p.KC / p.KS; };
 
     if (warp == 0) {
         // ---------------- copies ----------------
@@ -278,8 +249,8 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
         uint32_t phase = 0;
         bool ok = true, at_start = true;  // (the failure-path test withholds a CTA's first stage)
         for (int it = first; it < items && ok; it += step) {
-            const int m0 = int(tile_m(it)), n0 = tile_n(it) + rank * C::BROWS;
-            for (int kc = 0; kc < p.KC; ++kc) {
+            const int m0 = int(tile_m(it)), n0 = tile_n(it) + rank * C::BROWS, k1 = chunk1(it);
+            for (int kc = chunk0(it); kc < k1; ++kc) {
                 ok = mbar_wait_warp(&empty[stage], phase ^ 1, p.limit);
                 if (!ok) {
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
@@ -331,7 +302,8 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
             ok = mbar_wait_warp(&acc_empty[acc], acc_phase ^ 1, p.limit);
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * NT);
-            for (int kc = 0; kc < p.KC && ok; ++kc) {
+            const int k0 = chunk0(it), k1 = chunk1(it);
+            for (int kc = k0; kc < k1 && ok; ++kc) {
                 ok = mbar_wait_warp(&full[stage], phase, p.limit);
                 if (!ok) break;
                 tc_fence_after();
@@ -342,9 +314,9 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         if (PAIR)
-                            mma_bf16_pair(d, ad + a_step * kk, bd + b_step * kk, id, (kc > 0 || kk > 0) ? 1u : 0u);
+                            mma_bf16_pair(d, ad + a_step * kk, bd + b_step * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
                         else
-                            mma_bf16(d, ad + a_step * kk, bd + b_step * kk, id, (kc > 0 || kk > 0) ? 1u : 0u);
+                            mma_bf16(d, ad + a_step * kk, bd + b_step * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
                     PAIR ? tc_commit_pair(&empty[stage]) : tc_commit(&empty[stage]);
                 }
                 __syncwarp();
@@ -388,7 +360,7 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
                 tmem_ld_cols<32>(tb + c, v);
                 const int n = n0 + c, cols = min(32, p.N - n);
                 const bool mine = m < p.M;
-                const int64_t at = m * p.N + n;
+                const int64_t at = (it / tiles * p.M + m) * p.N + n;  // (parts: fp32 rows one after another)
                 uint32_t r[32];  // the residual's words
                 if (p.res && mine) {
                     if (p.res_f32) row_load<true>(r, p.res, at, cols, p.vec);
@@ -443,8 +415,7 @@ cudaError_t launch(const Operand &A, const Operand &B, LArgs g, cudaStream_t st)
         return cudaErrorInvalidValue;
     g.MTL = int(ceil_div(g.M, C::MT));
     g.NTL = int(ceil_div(g.N, NT));
-    const int64_t items = int64_t(g.MTL) * g.NTL;
-    if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
+    const int64_t items = int64_t(g.MTL) * g.NTL * g.KS;
     const size_t smem = 1024 + size_t(C::S) * C::STAGE + (2 * C::S + 2 * C::ACC + 1) * 8 + 8;
     auto *kern = k_linear_act<NT, PAIR, A_MN, B_MN>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -477,16 +448,163 @@ int vector_bytes(const LArgs &g)
     return 0;
 }
 
-template <bool A_MN, bool B_MN>
-cudaError_t product(const Operand &A, const Operand &B, LArgs g, int64_t K, const WaitArgs &wait, cudaStream_t st)
+// ---- parts of the reduction ------------------------------------------------------------------
+
+// The parts' sums added in order, then the epilogue.  W columns a thread (8: rows of all
+// tensors start on 16 bytes).
+template <int W>
+__global__ void __launch_bounds__(256) k_split_sum(const float *part, const LArgs p)
 {
+    const int64_t per_row = (p.N + W - 1) / W, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    pdl_enter();
+    if (i >= p.M * per_row) return;
+    const int64_t m = i / per_row, at = m * p.N + (i - m * per_row) * W;
+    const int n = int(i - m * per_row) * W;
+    float y[W] = {};
+    for (int k = 0; k < p.KS; ++k) {
+        const float *s = part + int64_t(k) * p.M * p.N + at;
+        if constexpr (W == 8) {
+            Pack<float, 8> q;
+            q.load(s);
+            float v[8];
+            q.get(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] += v[j];
+        } else {
+            y[0] += *s;
+        }
+    }
+    if (p.bias)
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            y[j] += p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + n + j)
+                               : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p.bias) + n + j));
+    auto put = [&](void *base, bool f32) {
+        if constexpr (W == 8) {
+            if (f32) {
+                Pack<float, 8> q;
+                q.set(y);
+                q.store(static_cast<float *>(base) + at);
+            } else {
+                Pack<uint16_t, 8> q;
+                q.set(y);
+                q.store(static_cast<uint16_t *>(base) + at);
+            }
+        } else {
+            if (f32) static_cast<float *>(base)[at] = y[0];
+            else static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(y[0]);
+        }
+    };
+    if (p.pre) put(p.pre, false);
+#pragma unroll
+    for (int j = 0; j < W; ++j) y[j] = apply_fn(p.fn, y[j]);
+    if (p.res) {
+        float v[W];
+        if constexpr (W == 8) {
+            if (p.res_f32) {
+                Pack<float, 8> q;
+                q.load(static_cast<const float *>(p.res) + at);
+                q.get(v);
+            } else {
+                Pack<uint16_t, 8> q;
+                q.load(static_cast<const uint16_t *>(p.res) + at);
+                q.get(v);
+            }
+        } else {
+            v[0] = p.res_f32 ? static_cast<const float *>(p.res)[at] : bf16_bits_to_f32(static_cast<const uint16_t *>(p.res)[at]);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[j] += v[j];
+    }
+    put(p.out, p.out_f32);
+}
+
+// ---- the choice of tiles and parts -----------------------------------------------------------
+
+// Tiles: rows x columns, CTAs, a chunk's bytes a CTA and its time in ns where it has the
+// copies it asks for.
+struct Tile {
+    int M, N, ctas, bytes, chunk;
+};
+constexpr Tile TILES[4] = {
+    {256, 256, 2, 32768, 295}, {256, 128, 2, 24576, 175}, {128, 128, 1, 32768, 213}, {128, 64, 1, 24576, 190}};
+
+struct Plan {
+    int tile, KS;
+};
+
+// The tile and the number of parts of the reduction with the least time by this model: whole
+// waves of items, a chunk's time or that of its bytes at the 14 TB/s that all SMs' copies
+// together get out of L2, and for parts the second kernel and its traffic.  Measured, us:
+//                          256x256  256x128  128x128  128x64   256x128, 2 parts   128x128, 2 / 3 / 4 parts
+//   512 rows 7168 -> 3584    39.1     28.1     34.2     54.2        -                 -
+//   200 rows 7168 -> 3584    38.5     24.7     28.8     29.8       20.5              23.2
+//   128 rows 7168 -> 3584    38.5     24.6     28.9     26.5       23.1              20.1 / 18.1 / 18.0
+//   600 rows 7168 -> 1024    38.4     24.4     28.4     26.8       19.5              20.4 / 18.8 / -
+//   331 rows 1056 -> 1000    14.1      9.6      9.9      9.2        8.2               8.4 / 8.2 / 8.7
+//   300 rows  512 -> 512     10.5      6.9      7.1      5.9        7.2               7.2
+//   1000 rows 1024 -> 2048   13.0      9.2      9.9     12.0        -                 -
+Plan plan(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t KC = ceil_div(K, 64);
+    const int sms = device_sms();
+    Plan best{0, 1};
+    double least = 1e30;
+    for (int t = 0; t < 4; ++t) {
+        const Tile &T = TILES[t];
+        const int64_t tiles = ceil_div(M, T.M) * ceil_div(N, T.N), slots = sms / T.ctas;
+        for (int ks = 1; ks <= MAX_PARTS; ++ks) {
+            if (ks > 1 && (tiles * ks > slots || KC < 4 * ks)) break;
+            const int64_t items = tiles * ks, busy = items < slots ? items : slots;
+            const double from_l2 = double(busy * T.ctas) * T.bytes / 14000;
+            double ns = double(ceil_div(items, slots) * ceil_div(KC, ks)) * (from_l2 > T.chunk ? from_l2 : T.chunk);
+            if (ks > 1) ns += 1000 + double(ks) * double(M) * double(N) * 8 / 5000;
+            if (ns < least) {
+                least = ns;
+                best = {t, ks};
+            }
+        }
+    }
+    return best;
+}
+
+// Bytes of the parts.
+size_t part_bytes(int64_t M, int64_t N, int64_t K)
+{
+    const Plan pl = plan(M, N, K);
+    return pl.KS > 1 ? size_t(round_up(pl.KS * M * N * 4, 256)) : 0;
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t product(const Operand &A, const Operand &B, LArgs g, int64_t K, const WaitArgs &wait, void *parts, cudaStream_t st)
+{
+    const Plan pl = plan(g.M, g.N, K);
     g.KC = int(ceil_div(K, 64));
+    g.KS = pl.KS;
     g.vec = vector_bytes(g);
     g.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
     g.stall = wait.stall_first_fill;
-    // A pair's 256 x 256 tile where there are tiles for most of the GPU.
-    if (ceil_div(g.M, 256) * ceil_div(g.N, 256) >= 40) return launch<256, true, A_MN, B_MN>(A, B, g, st);
-    return launch<128, false, A_MN, B_MN>(A, B, g, st);
+    LArgs h = g;
+    if (pl.KS > 1) {
+        h.bias = h.res = nullptr;
+        h.pre = nullptr;
+        h.fn = LMOE_FN_NONE;
+        h.out = parts;
+        h.out_f32 = 1;
+        h.vec = vector_bytes(h);
+    }
+    cudaError_t e;
+    switch (pl.tile) {
+    case 0: e = launch<256, true, A_MN, B_MN>(A, B, h, st); break;
+    case 1: e = launch<128, true, A_MN, B_MN>(A, B, h, st); break;
+    case 2: e = launch<128, false, A_MN, B_MN>(A, B, h, st); break;
+    default: e = launch<64, false, A_MN, B_MN>(A, B, h, st); break;
+    }
+    if (e != cudaSuccess || pl.KS == 1) return e;
+    const bool wide = g.vec && g.N % 8 == 0;
+    const dim3 grid(unsigned(ceil_div(g.M * ceil_div(g.N, wide ? 8 : 1), 256)));
+    const float *part = static_cast<const float *>(parts);
+    return wide ? launch_pdl(k_split_sum<8>, grid, dim3(256), 0, st, part, g) : launch_pdl(k_split_sum<1>, grid, dim3(256), 0, st, part, g);
 }
 
 // ---- dz and its column sums ----------------------------------------------------------------
@@ -581,10 +699,15 @@ cudaError_t dz_fn(const DzArgs &g, int fn, dim3 grid, cudaStream_t st)
 
 }  // namespace
 
-size_t linear_act_scratch_bytes(int64_t, int, int) { return 0; }
+// Up to this many rows the weights' stream is the bound (k_linear_few.cu); at 96 and 128
+// it took 23.4 and 21.1 us (3584 -> 7168, 7168 -> 3584) against 18.0 and 18.0 here.
+constexpr int64_t FEW = 64;
 
-cudaError_t launch_linear_act(const LinearActArgs &a, void *, cudaStream_t st)
+size_t linear_act_scratch_bytes(int64_t rows, int K, int N) { return rows <= FEW ? 0 : part_bytes(rows, N, K); }
+
+cudaError_t launch_linear_act(const LinearActArgs &a, void *scratch, cudaStream_t st)
 {
+    if (a.rows <= FEW) return launch_linear_few(a, st);
     LArgs g{};
     g.M = a.rows;
     g.N = a.N;
@@ -597,14 +720,16 @@ cudaError_t launch_linear_act(const LinearActArgs &a, void *, cudaStream_t st)
     g.out = a.out;
     g.pre = a.pre;
     g.status = a.status;
-    return product<false, false>({a.x, a.rows, a.K, a.K}, {a.W, a.N, a.K, a.K}, g, a.K, a.wait, st);
+    return product<false, false>({a.x, a.rows, a.K, a.K}, {a.W, a.N, a.K, a.K}, g, a.K, a.wait, scratch, st);
 }
 
-// dz [rows][Np] bf16 | column sums
-size_t linear_act_back_scratch_bytes(int64_t rows, int, int N)
+// dz [rows][Np] bf16 | column sums | parts of a product's reduction
+size_t linear_act_back_scratch_bytes(int64_t rows, int K, int N)
 {
+    if (rows == 0) return 0;
     const int64_t Np = round_up(N, 8);
-    return size_t(round_up(rows * Np * 2, 256)) + size_t(round_up(dz_splits(rows, N) * N * 4, 256));
+    const size_t dx = part_bytes(rows, K, N), dW = part_bytes(N, K, rows);
+    return size_t(round_up(rows * Np * 2, 256)) + size_t(round_up(dz_splits(rows, N) * N * 4, 256)) + (dx > dW ? dx : dW);
 }
 
 cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cudaStream_t st)
@@ -618,6 +743,7 @@ cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cu
     const int64_t Np = round_up(a.N, 8);
     uint16_t *dz = static_cast<uint16_t *>(scratch);
     float *part = reinterpret_cast<float *>(static_cast<char *>(scratch) + round_up(a.rows * Np * 2, 256));
+    void *parts = reinterpret_cast<char *>(part) + round_up(dz_splits(a.rows, a.N) * a.N * 4, 256);
     // bf16 gradients that go through no function are the operand as they are
     const bool as_is = a.fn == LMOE_FN_NONE && a.dout_fmt == LMOE_BF16 && Np == a.N;
     const bool need_dz = (a.dx || a.dW) && !as_is;
@@ -637,7 +763,7 @@ cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cu
         g.M = a.rows;
         g.N = a.K;
         g.out = a.dx;
-        e = product<false, true>(d, {a.W, a.N, a.K, a.K}, g, a.N, a.wait, st);
+        e = product<false, true>(d, {a.W, a.N, a.K, a.K}, g, a.N, a.wait, parts, st);
         if (e != cudaSuccess) return e;
     }
     if (a.dW) {
@@ -645,7 +771,7 @@ cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cu
         g.N = a.K;
         g.out = a.dW;
         g.out_f32 = a.dW_fmt == LMOE_F32;
-        e = product<true, true>(d, {a.x, a.rows, a.K, a.K}, g, a.rows, a.wait, st);
+        e = product<true, true>(d, {a.x, a.rows, a.K, a.K}, g, a.rows, a.wait, parts, st);
     }
     return e;
 }

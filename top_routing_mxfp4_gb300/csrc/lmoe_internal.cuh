@@ -450,6 +450,8 @@ struct LinearActArgs {
 };
 size_t linear_act_scratch_bytes(int64_t rows, int K, int N);
 cudaError_t launch_linear_act(const LinearActArgs &a, void *scratch, cudaStream_t st);
+// the same for few rows (k_linear_few.cu)
+cudaError_t launch_linear_few(const LinearActArgs &a, cudaStream_t st);
 struct LinearActBackArgs {
     const void *dout;
     int dout_fmt;
