@@ -89,4 +89,74 @@ __device__ __forceinline__ float row_sum(float s, float *part)
     return s;
 }
 
+// Two fp32 values as one operand of the packed instructions (each rounded as by itself).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
+__device__ __forceinline__ void f2_get(F2 a, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(F2 a)
+{
+    float lo, hi;
+    f2_get(a, lo, hi);
+    return lo + hi;
+}
+// A Pack's elements as pairs, and back.
+template <int W>
+__device__ __forceinline__ void pairs(const Pack<uint16_t, W> &p, F2 (&v)[W / 2])
+{
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) v[i] = f2(__uint_as_float(p.u[i] << 16), __uint_as_float(p.u[i] & 0xFFFF0000u));
+}
+template <int W>
+__device__ __forceinline__ void pairs(const Pack<float, W> &p, F2 (&v)[W / 2])
+{
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) v[2 * i] = f2(p.q[i].x, p.q[i].y), v[2 * i + 1] = f2(p.q[i].z, p.q[i].w);
+}
+template <int W>
+__device__ __forceinline__ void set_pairs(Pack<uint16_t, W> &p, const F2 (&v)[W / 2])
+{
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+        float lo, hi;
+        f2_get(v[i], lo, hi);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        p.u[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+}
+template <int W>
+__device__ __forceinline__ void set_pairs(Pack<float, W> &p, const F2 (&v)[W / 2])
+{
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+        f2_get(v[2 * i], p.q[i].x, p.q[i].y);
+        f2_get(v[2 * i + 1], p.q[i].z, p.q[i].w);
+    }
+}
+
 }  // namespace lmoe
