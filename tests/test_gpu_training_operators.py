@@ -608,9 +608,26 @@ def test_a_training_step_of_a_routers_neighbourhood(cuda_lib):
     total = coef[0] * bal + coef[1] * zl + (torch.softmax(l6.gather(1, idx.long()), 1) * dgate.to(D) * m).sum() + (s6 * add.to(D)).sum()
     total.backward()
     # the losses: logits carry the roundings of n and lat (bf16), 2^-7 relative each in norm
-    bal, zl = float(bal), float(zl)
+    bal, zl = float(bal.detach()), float(zl.detach())
     assert abs(float(loss[0]) - bal) < 1e-3 * bal and abs(float(loss[1]) - zl) < 1e-2 * zl
     # gradients: five bf16 roundings on the way (n, lat, dl or Wr, dlat, dz), below 2^-8 in norm each, and W's products
     # keep norms apart by at most their condition, measured here by the ratio of 1: 6 half steps with room for two
     for got, ref in ((dWr, Wr6.grad), (dW, W6.grad), (dbias, bias6.grad), (dw, w6.grad), (db, b6.grad), (dstream, s6.grad)):
         assert float((got.to(D) - ref).norm()) < 8 * HALF * float(ref.norm())
+
+
+@pytest.mark.parametrize("E", [896, 50])
+def test_balance_loss_rows_of_extreme_logits(cuda_lib, E):
+    """Rows of one value have even probabilities whatever the value, the type's lowest and largest among them; a
+    difference that overflows is a probability of zero."""
+    T, k = 30, 2
+    big = torch.finfo(torch.float32).max
+    l = torch.zeros(T, E, device=DEV)
+    l[0], l[1], l[2], l[3] = -big, big, -1e38, 300.0
+    l[4], l[4, 3] = -big, big
+    idx = picks(gen(E), T, E, k)
+    _, counts, probs, d = cuda_lib.balance_loss(l, idx, coef=(1.0, 0.0), grad=True)
+    p = torch.softmax(l.to(D), 1)
+    f = counts.to(D) / (k * T) * E
+    within(probs, p.mean(0), 800 * U * p.mean(0))
+    within(d, p * (f - (p * f).sum(1, keepdim=True)) / T, 400 * U / T * p * (f + (p * f).sum(1, keepdim=True)) + TINY)

@@ -15,17 +15,32 @@
 // writes its sums and a cluster adds the blocks' in order.  Integer atomics count
 // (in shared memory; any order gives the same counts); nothing else is atomic, so
 // a call repeats bit for bit.
+#include <stdlib.h>
 #include "lmoe_internal.cuh"
+#include "row_vec.cuh"
 #include "tc_ptx.cuh"
 
 namespace lmoe {
 namespace {
 
-constexpr int kCountBlocks = 32;
+constexpr int kCountCluster = 8, kCountParts = 16;
+constexpr int kFinalCtas = 8;  // of the cluster that adds up the blocks' sums
 // Up to this many picks every block counts them all by itself; more are counted by
 // a kernel of their own.
-constexpr int64_t kOwnCount = 16384;
+static const int64_t kOwnCount = getenv("OC") ? atoi(getenv("OC")) : 4096;
+static const int64_t kOneCluster = getenv("ONE") ? atoi(getenv("ONE")) : 128;
 
+__device__ __forceinline__ float exp2_quick(float x)  // off by 2 u, results below 2^-126 are 0
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_max(float v)
+{
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(v) : "f"(v));
+    return v;
+}
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -34,135 +49,229 @@ __device__ __forceinline__ float warp_sum(float v)
 }
 
 // Adds the picks p of [p0, P) in steps of `step` to the block's counts, and the
-// tokens they belong to (those of slot 0) to *tokens.
+// tokens they belong to (those of slot 0) to *tokens.  Eight picks' loads at a time.
 __device__ __forceinline__ void count_picks(const BalanceArgs &a, int64_t p0, int64_t step, int32_t *s_counts,
                                             int32_t *s_tokens)
 {
     const int64_t P = a.T * a.k;
     int tokens = 0;
-    for (int64_t p = p0; p < P; p += step) {
-        const int64_t t = int64_t(uint32_t(p) / uint32_t(a.k));
-        if (a.mask && !a.mask[t]) continue;
-        if (p == t * a.k) ++tokens;
-        const int e = __ldg(a.idx + p);
-        if (uint32_t(e) < uint32_t(a.E))
-            atomicAdd(s_counts + e, 1);
-        else
-            set_status(a.status, LMOE_ERR_DEVICE_CHECK);
+    for (int64_t p = p0; p < P; p += 8 * step) {
+        int e[8];
+        bool in[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t q = p + i * step;
+            in[i] = q < P;
+            e[i] = in[i] ? __ldg(a.idx + q) : 0;
+            const uint32_t t = uint32_t(q) / uint32_t(a.k);
+            if (in[i] && a.mask) in[i] = __ldg(a.mask + t) != 0;
+            tokens += in[i] && uint32_t(q) == t * uint32_t(a.k);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (!in[i]) continue;
+            if (uint32_t(e[i]) < uint32_t(a.E))
+                atomicAdd(s_counts + e[i], 1);
+            else
+                set_status(a.status, LMOE_ERR_DEVICE_CHECK);
+        }
     }
     tokens = __reduce_add_sync(0xFFFFFFFFu, tokens);
     if ((threadIdx.x & 31) == 0 && tokens) atomicAdd(s_tokens, tokens);
 }
 
-// Many picks: the counts of kCountBlocks blocks, [block][E + 1] (the last: tokens).
-__global__ void __launch_bounds__(1024) k_balance_count(const BalanceArgs a)
+// Rows of counts lie this many apart: the experts', the tokens, whole 16 bytes.
+__host__ __device__ constexpr int count_stride(int E) { return (E + 4) & ~3; }
+
+// Many picks: the counts of kCountParts clusters (the entry behind the experts: tokens).
+// A cluster's CTAs count for themselves, then each adds up a share of the experts.
+__global__ void __cluster_dims__(kCountCluster, 1, 1) __launch_bounds__(512) k_balance_count(const BalanceArgs a)
 {
     extern __shared__ int32_t s_counts[];
-    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) s_counts[e] = 0;
+    const int Cs = count_stride(a.E), rank = int(tc::cluster_rank());
+    for (int e = threadIdx.x; e < Cs; e += blockDim.x) s_counts[e] = 0;
     pdl_enter();
     __syncthreads();
     count_picks(a, int64_t(blockIdx.x) * blockDim.x + threadIdx.x, int64_t(gridDim.x) * blockDim.x, s_counts, s_counts + a.E);
     __syncthreads();
-    int32_t *out = a.count_part + int64_t(blockIdx.x) * (a.E + 1);
-    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) out[e] = s_counts[e];
+    tc::cluster_sync();
+    int32_t *out = a.count_part + int64_t(blockIdx.x / kCountCluster) * Cs;
+    for (int e = rank * int(blockDim.x) + threadIdx.x; e < Cs; e += kCountCluster * int(blockDim.x)) {
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < kCountCluster; ++r) n += tc::cluster_load_i32(tc::cluster_map(tc::smem_u32(s_counts + e), r));
+        out[e] = n;
+    }
+    __syncthreads();
+    tc::cluster_sync_end();  // no CTA's counts go while another reads them
 }
 
 // A row's logits and the column sums in registers: half the warps beyond 1024 columns.
 template <int NV>
 constexpr int ROW_THREADS = NV <= 8 ? 512 : 256;
+template <int NV>
+constexpr int ROW_BLOCKS = NV <= 2 ? 2 : 1;  // an SM
 
 // NV: 128 columns each; VEC: E % 4 == 0, a lane's columns are fours of them.
-// own: the block counts the picks itself.
+// own: the block counts the picks itself.  one: the grid is one cluster, which adds up its
+// blocks' sums itself.
 template <int NV, bool VEC, bool GRAD>
-__global__ void __launch_bounds__(ROW_THREADS<NV>, 1) k_balance_rows(const BalanceArgs a, bool own)
+__global__ void __launch_bounds__(ROW_THREADS<NV>, ROW_BLOCKS<NV>) k_balance_rows(const BalanceArgs a, bool own, bool one)
 {
     constexpr int kBlock = ROW_THREADS<NV>, kWarps = kBlock / 32;
     extern __shared__ __align__(16) float s_mem[];
-    const int Ep = (a.E + 3) & ~3;
-    float *s_f = s_mem;                                             // [Ep]
+    const int Ep = (a.E + 3) & ~3, Cs = count_stride(a.E);
+    float *s_f = s_mem;                                             // [Ep]: scale * coef_balance / N * f
     float *s_row = s_mem + Ep;                                      // [kWarps][Ep]
-    int32_t *s_counts = reinterpret_cast<int32_t *>(s_row + kWarps * Ep);  // [E + 1]
+    int32_t *s_counts = reinterpret_cast<int32_t *>(s_row + kWarps * Ep);  // [Cs]
     __shared__ float s_z[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *mine = s_row + warp * Ep;
-    for (int e = threadIdx.x; e <= a.E; e += kBlock) s_counts[e] = 0;
-    for (int e = threadIdx.x; e < kWarps * Ep; e += kBlock) s_row[e] = 0.f;
+    for (int e = threadIdx.x; e < Cs; e += kBlock) s_counts[e] = 0;
+    if (GRAD && a.topk_w)
+        for (int e = threadIdx.x; e < kWarps * Ep; e += kBlock) s_row[e] = 0.f;
     pdl_enter();
     __syncthreads();
     if (own) {
         count_picks(a, threadIdx.x, kBlock, s_counts, s_counts + a.E);
     } else {
-        for (int e = threadIdx.x; e <= a.E; e += kBlock) {
-            int32_t n = 0;
-#pragma unroll 8
-            for (int b = 0; b < kCountBlocks; ++b) n += a.count_part[int64_t(b) * (a.E + 1) + e];
-            s_counts[e] = n;
+        // four experts a thread, eight parts' counts at a time
+        for (int i = threadIdx.x; i < Cs / 4 * (kCountParts / 8); i += kBlock) {
+            const int e = i % (Cs / 4) * 4, b = i / (Cs / 4) * 8;
+            int4 n = make_int4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int4 q = *reinterpret_cast<const int4 *>(a.count_part + int64_t(b + j) * Cs + e);
+                n.x += q.x, n.y += q.y, n.z += q.z, n.w += q.w;
+            }
+            atomicAdd(s_counts + e, n.x);
+            atomicAdd(s_counts + e + 1, n.y);
+            atomicAdd(s_counts + e + 2, n.z);
+            atomicAdd(s_counts + e + 3, n.w);
         }
     }
+    const float up = GRAD && a.scale ? __ldg(a.scale) : 1.f;
     __syncthreads();
     const int tokens = s_counts[a.E];
     const float inv_n = tokens > 0 ? 1.f / float(tokens) : 0.f;
-    const float scale = float(a.E) / float(a.k) * inv_n;
-    for (int e = threadIdx.x; e < Ep; e += kBlock) s_f[e] = e < a.E ? float(s_counts[e]) * scale : 0.f;
+    const float cb = GRAD ? up * a.coef_balance * inv_n * (float(a.E) / float(a.k) * inv_n) : 0.f;
+    const float cz = GRAD ? up * a.coef_z * 2.f * inv_n : 0.f;
+    if (GRAD)
+        for (int e = threadIdx.x; e < Ep; e += kBlock) s_f[e] = e < a.E ? float(s_counts[e]) * cb : 0.f;
     if (blockIdx.x == 0) {
         for (int e = threadIdx.x; e < a.E; e += kBlock) a.counts[e] = s_counts[e];
         if (threadIdx.x == 0) *a.tokens = tokens;
     }
     __syncthreads();
 
-    const float up = GRAD && a.scale ? __ldg(a.scale) : 1.f;
-    const float cb = GRAD ? up * a.coef_balance * inv_n : 0.f, cz = GRAD ? up * a.coef_z * 2.f * inv_n : 0.f;
+    // a lane's columns: fours of consecutive ones, or (E % 4) single ones, 32 lanes apart
     auto col = [&](int i) { return VEC ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane; };
-    auto each4 = [&](auto f) {  // the lane's columns, by fours of registers
+    auto get4 = [&](const float *p, int i, float none, float (&q)[4]) {  // the lane's i-th four of a row
+        if (VEC) {
+            float4 r = make_float4(none, none, none, none);
+            if (col(4 * i) < a.E) r = *reinterpret_cast<const float4 *>(p + col(4 * i));
+            q[0] = r.x, q[1] = r.y, q[2] = r.z, q[3] = r.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) f(i);
+            for (int j = 0; j < 4; ++j) q[j] = col(4 * i + j) < a.E ? p[col(4 * i + j)] : none;
+        }
     };
-    float acc[NV * 4];
+    auto put4 = [&](float *p, int i, const float (&q)[4]) {
+        if (VEC) {
+            if (col(4 * i) < a.E) *reinterpret_cast<float4 *>(p + col(4 * i)) = make_float4(q[0], q[1], q[2], q[3]);
+        } else {
 #pragma unroll
-    for (int i = 0; i < NV * 4; ++i) acc[i] = 0.f;
-    float z = 0.f;
-    for (int64_t t = int64_t(warp) * gridDim.x + blockIdx.x; t < a.T; t += int64_t(gridDim.x) * kWarps) {
-        float v[NV * 4] = {};
+            for (int j = 0; j < 4; ++j)
+                if (col(4 * i + j) < a.E) p[col(4 * i + j)] = q[j];
+        }
+    };
+    const int64_t step = int64_t(gridDim.x) * kWarps;
+    auto counts_in = [&](int64_t t) { return t < a.T && (!a.mask || __ldg(a.mask + t)); };
+    // what a row needs, on its way while the row before is worked on
+    float next[NV * 4];
+    int ne = -1;
+    float nw = 0.f, ng = 0.f;
+    auto load = [&](int64_t t) {
         const float *l = a.logits + t * a.E;
-        float *d = GRAD ? a.dlogits + t * a.E : nullptr;
-        auto store = [&] {
-            each4([&](int i) {
-                if (VEC) {
-                    if (col(4 * i) < a.E)
-                        *reinterpret_cast<float4 *>(d + col(4 * i)) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (col(4 * i + j) < a.E) d[col(4 * i + j)] = v[4 * i + j];
-                }
-            });
-        };
-        if (a.mask && !a.mask[t]) {
-            if (GRAD) store();
+        for (int i = 0; i < NV; ++i) {
+            float q[4];
+            get4(l, i, -INFINITY, q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) next[4 * i + j] = q[j];
+        }
+        if (GRAD && a.topk_w && lane < a.k) {
+            ne = __ldg(a.idx + t * a.k + lane);
+            nw = __ldg(a.topk_w + t * a.k + lane);
+            ng = __ldg(a.dtopk_w + t * a.k + lane);
+            if (uint32_t(ne) >= uint32_t(a.E)) ne = -1;
+        }
+    };
+    F2 acc[NV * 2];
+#pragma unroll
+    for (int i = 0; i < NV * 2; ++i) acc[i] = f2(0.f);
+    float z = 0.f;
+    int64_t t = int64_t(warp) * gridDim.x + blockIdx.x;
+    bool in = counts_in(t), in_next = counts_in(t + step);
+    if (in) load(t);
+    for (; t < a.T; t += step) {
+        float *d = GRAD ? a.dlogits + t * a.E : nullptr;
+        const bool in_after = counts_in(t + 2 * step);
+        F2 v[NV * 2];
+        float m = -INFINITY;
+        int e = -1;
+        float w = 0.f, g = 0.f;
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < NV * 2; ++i) {
+                v[i] = f2(next[2 * i], next[2 * i + 1]);
+                m = fmaxf(m, fmaxf(next[2 * i], next[2 * i + 1]));
+            }
+            e = ne, w = nw, g = ng;
+        }
+        if (in_next) load(t + step);
+        const bool here = in;
+        in = in_next;
+        in_next = in_after;
+        if (!here) {
+            if (GRAD) {
+                const float none[4] = {};
+#pragma unroll
+                for (int i = 0; i < NV; ++i) put4(d, i, none);
+            }
             continue;
         }
-        each4([&](int i) {
-            if (VEC) {
-                float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (col(4 * i) < a.E) q = *reinterpret_cast<const float4 *>(l + col(4 * i));
-                v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-            } else {
+        m = warp_max(m);
+        // all -infinity: no probabilities (a NaN among them is no maximum, but makes the sum NaN)
+        if (m == -INFINITY) m = 0.f;
+        // (the difference first: its terms times log2 e could overflow)
+        const F2 l2e = f2(1.44269504f), off = f2(-m);
+        F2 s2 = f2(0.f), f2s = f2(0.f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * i + j] = col(4 * i + j) < a.E ? l[col(4 * i + j)] : -INFINITY;
+        for (int i = 0; i < NV; ++i) {
+            float q[4];
+            f2_get((v[2 * i] + off) * l2e, q[0], q[1]);
+            f2_get((v[2 * i + 1] + off) * l2e, q[2], q[3]);
+            v[2 * i] = f2(exp2_quick(q[0]), exp2_quick(q[1]));
+            v[2 * i + 1] = f2(exp2_quick(q[2]), exp2_quick(q[3]));
+            s2 = s2 + (v[2 * i] + v[2 * i + 1]);
+            if (GRAD) {
+                get4(s_f, i, 0.f, q);
+                f2s = fma2(f2(q[0], q[1]), v[2 * i], fma2(f2(q[2], q[3]), v[2 * i + 1], f2s));
             }
-        });
-        // the slot's way through the gate weights
-        if (GRAD && a.topk_w) {
-            float w = 0.f, g = 0.f;
-            int e = -1;
-            if (lane < a.k) {
-                e = __ldg(a.idx + t * a.k + lane);
-                w = __ldg(a.topk_w + t * a.k + lane);
-                g = __ldg(a.dtopk_w + t * a.k + lane);
-                if (uint32_t(e) >= uint32_t(a.E)) e = -1;
-            }
-            const float s = warp_sum(w * g);
-            g = w * (g - s);
+        }
+        // the sums of the exponentials, of f times them, and of the slots' w dw
+        const bool gate = GRAD && a.topk_w;
+        float s, sf = 0.f, sg = 0.f;
+        if (GRAD) {
+            if (gate) sg = warp_sum(w * g);
+            const float2 both = warp_sum2(f2_sum(s2), f2_sum(f2s));
+            s = both.x, sf = both.y;
+        } else {
+            s = warp_sum(f2_sum(s2));
+        }
+        if (gate) {
+            g = w * (g - sg);
             const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
             if (__any_sync(0xFFFFFFFFu, e >= 0 && (same & (same - 1)))) {  // an expert twice: one slot after another
                 for (int j = 0; j < a.k; ++j) {
@@ -174,107 +283,97 @@ __global__ void __launch_bounds__(ROW_THREADS<NV>, 1) k_balance_rows(const Balan
             }
             __syncwarp();
         }
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NV * 4; ++i) m = fmaxf(m, v[i]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        // all -infinity: no probabilities (a NaN among them is no maximum, but makes the sum NaN)
-        if (m == -INFINITY) m = 0.f;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV * 4; ++i) {
-            v[i] = expf(v[i] - m);
-            s += v[i];
-        }
-        s = warp_sum(s);
         const float inv = s == 0.f ? 0.f : 1.f / s;
         const float lse = s == 0.f ? 0.f : m + logf(s);
         z = fmaf(lse, lse, z);
-        float sf = 0.f;
-        each4([&](int i) {
-            float f[4] = {};
-            if (GRAD) {
-                if (VEC) {
-                    if (col(4 * i) < a.E) {
-                        const float4 q = *reinterpret_cast<const float4 *>(s_f + col(4 * i));
-                        f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
-                    }
-                } else {
+        const F2 inv2 = f2(inv), base = f2(fmaf(cz, lse, -sf * inv));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) f[j] = col(4 * i + j) < a.E ? s_f[col(4 * i + j)] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[4 * i + j] *= inv;
-                acc[4 * i + j] += v[4 * i + j];
-                if (GRAD) sf = fmaf(f[j], v[4 * i + j], sf);
-            }
-        });
-        if (!GRAD) continue;
-        const float base = fmaf(-cb, warp_sum(sf), cz * lse);
-        each4([&](int i) {
-            float f[4] = {}, g[4] = {};
-            if (VEC) {
-                if (col(4 * i) < a.E) {
-                    const float4 q = *reinterpret_cast<const float4 *>(s_f + col(4 * i));
-                    f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
-                    if (a.topk_w) {
-                        const float4 r = *reinterpret_cast<const float4 *>(mine + col(4 * i));
-                        g[0] = r.x, g[1] = r.y, g[2] = r.z, g[3] = r.w;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (col(4 * i + j) < a.E) {
-                        f[j] = s_f[col(4 * i + j)];
-                        g[j] = mine[col(4 * i + j)];
-                    }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * i + j] = fmaf(v[4 * i + j], fmaf(cb, f[j], base), g[j]);
-        });
-        store();
-        if (a.topk_w) {
+        for (int i = 0; i < NV; ++i) {
+            const F2 p0 = v[2 * i] * inv2, p1 = v[2 * i + 1] * inv2;
+            acc[2 * i] = acc[2 * i] + p0;
+            acc[2 * i + 1] = acc[2 * i + 1] + p1;
+            if (!GRAD) continue;
+            float f[4], q[4] = {};
+            get4(s_f, i, 0.f, f);
+            if (gate) get4(mine, i, 0.f, q);
+            f2_get(fma2(p0, f2(f[0], f[1]) + base, f2(q[0], q[1])), q[0], q[1]);
+            f2_get(fma2(p1, f2(f[2], f[3]) + base, f2(q[2], q[3])), q[2], q[3]);
+            put4(d, i, q);
+        }
+        if (gate) {
             __syncwarp();
-            if (lane < a.k) {
-                const int e = __ldg(a.idx + t * a.k + lane);
-                if (uint32_t(e) < uint32_t(a.E)) mine[e] = 0.f;
-            }
+            if (e >= 0) mine[e] = 0.f;
             __syncwarp();
         }
     }
     // the block's sums
 #pragma unroll
-    for (int i = 0; i < NV * 4; ++i)
-        if (col(i) < a.E) mine[col(i)] = acc[i];
+    for (int i = 0; i < NV * 2; ++i) {
+        float lo, hi;
+        f2_get(acc[i], lo, hi);
+        if (col(2 * i) < a.E) mine[col(2 * i)] = lo;
+        if (col(2 * i + 1) < a.E) mine[col(2 * i + 1)] = hi;
+    }
     if (lane == 0) s_z[warp] = z;
     __syncthreads();
-    float *out = a.part + int64_t(blockIdx.x) * (a.E + 1);
+    float zs = 0.f;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < kWarps; ++w) zs += s_z[w];
+    float *out = one ? s_f : a.part + int64_t(blockIdx.x) * (a.E + 1);
     for (int e = threadIdx.x; e < a.E; e += kBlock) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += s_row[w * Ep + e];
         out[e] = v;
     }
-    if (threadIdx.x == 0) {
+    if (!one) {
+        if (threadIdx.x == 0) out[a.E] = zs;
+        return;
+    }
+    __shared__ float s_loss[2][kFinalCtas];  // rank 0's: the ranks' shares
+    const int rank = int(tc::cluster_rank());
+    auto at_rank0 = [&](float *p) { return tc::cluster_map(tc::smem_u32(p), 0); };
+    __syncthreads();
+    tc::cluster_sync();
+    float loss = 0.f;
+    const float scale = float(a.E) / float(a.k) * inv_n;
+    for (int e = rank * kBlock + threadIdx.x; e < a.E; e += kFinalCtas * kBlock) {
         float v = 0.f;
-        for (int w = 0; w < kWarps; ++w) v += s_z[w];
-        out[a.E] = v;
+#pragma unroll
+        for (int r = 0; r < kFinalCtas; ++r) v += __int_as_float(tc::cluster_load_i32(tc::cluster_map(tc::smem_u32(s_f + e), r)));
+        v *= inv_n;
+        a.probs[e] = v;
+        loss = fmaf(float(s_counts[e]) * scale, v, loss);
+    }
+    loss = warp_sum(loss);
+    if (lane == 0) s_z[warp] = loss;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        loss = 0.f;
+        for (int w = 0; w < kWarps; ++w) loss += s_z[w];
+        tc::cluster_store_i32(at_rank0(&s_loss[0][rank]), __float_as_int(loss));
+        tc::cluster_store_i32(at_rank0(&s_loss[1][rank]), __float_as_int(zs * inv_n));
+    }
+    __syncthreads();
+    tc::cluster_sync();  // (and no CTA's sums go while another reads them)
+    if (rank == 0 && threadIdx.x < 2) {
+        loss = 0.f;
+#pragma unroll
+        for (int r = 0; r < kFinalCtas; ++r) loss += s_loss[threadIdx.x][r];
+        a.loss[threadIdx.x] = loss;
     }
 }
 
-// The blocks' sums added in order (within 16 strands, added in order), probs, and
-// the losses.  One cluster: each CTA takes a share of the experts, rank 0 adds the
+// The blocks' sums added in order (within eight strands, added in order), probs, and the
+// losses.  One cluster: each CTA takes 128 columns at a time, rank 0 adds the CTAs'
 // shares of the loss.
-constexpr int kFinalCtas = 8, kFinalWarps = 16;
-__global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(32 * kFinalWarps) k_balance_final(const BalanceArgs a, int blocks)
+constexpr int kFinalCols = 128, kStrands = 8;
+__global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalCols *kStrands)
+    k_balance_final(const BalanceArgs a, int blocks)
 {
-    __shared__ float s[kFinalWarps][33];
-    __shared__ float s_loss[kFinalCtas];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float s[kStrands][kFinalCols];
+    __shared__ float s_warp[kFinalCols / 32], s_loss[kFinalCtas];
+    const int at = threadIdx.x % kFinalCols, strand = threadIdx.x / kFinalCols;
     const int rank = int(tc::cluster_rank());
     pdl_enter();
     const int tokens = *a.tokens;
@@ -282,31 +381,42 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(32 * kFinal
     const float scale = float(a.E) / float(a.k) * inv_n;
     float loss = 0.f;
     // column E holds the sums of lse^2
-    for (int c0 = rank * 32; c0 <= a.E; c0 += kFinalCtas * 32) {
-        const int c = c0 + lane;
+    for (int c = rank * kFinalCols + at; c - at <= a.E; c += kFinalCtas * kFinalCols) {
         float v = 0.f;
         if (c <= a.E)
-#pragma unroll 4
-            for (int b = warp; b < blocks; b += kFinalWarps) v += a.part[int64_t(b) * (a.E + 1) + c];
-        __syncthreads();
-        s[warp][lane] = v;
-        __syncthreads();
-        if (warp == 0) {
-            v = 0.f;
+            for (int b = strand; b < blocks; b += 10 * kStrands) {
+                float q[10];
 #pragma unroll
-            for (int w = 0; w < kFinalWarps; ++w) v += s[w][lane];
+                for (int i = 0; i < 10; ++i)
+                    q[i] = b + i * kStrands < blocks ? a.part[int64_t(b + i * kStrands) * (a.E + 1) + c] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 10; ++i) v += q[i];
+            }
+        const int n = strand == 0 && c < a.E ? a.counts[c] : 0;
+        s[strand][at] = v;
+        __syncthreads();
+        if (strand == 0) {
+#pragma unroll
+            for (int q = 1; q < kStrands; ++q) v += s[q][at];
             v *= inv_n;
             if (c < a.E) {
                 a.probs[c] = v;
-                loss = fmaf(float(a.counts[c]) * scale, v, loss);
+                loss = fmaf(float(n) * scale, v, loss);
             } else if (c == a.E) {
                 a.loss[1] = v;
             }
         }
+        __syncthreads();
     }
-    if (warp == 0) {
+    if (strand == 0) {
         loss = warp_sum(loss);
-        if (lane == 0) tc::cluster_store_i32(tc::cluster_map(tc::smem_u32(&s_loss[rank]), 0), __float_as_int(loss));
+        if (at % 32 == 0) s_warp[at / 32] = loss;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        loss = 0.f;
+        for (int q = 0; q < kFinalCols / 32; ++q) loss += s_warp[q];
+        tc::cluster_store_i32(tc::cluster_map(tc::smem_u32(&s_loss[rank]), 0), __float_as_int(loss));
     }
     __syncthreads();
     tc::cluster_sync();
@@ -319,40 +429,58 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(32 * kFinal
 }
 
 template <int NV, bool VEC, bool GRAD>
-cudaError_t rows(const BalanceArgs &a, unsigned grid, bool own, cudaStream_t st)
+cudaError_t rows(const BalanceArgs &a, unsigned grid, bool own, bool one, cudaStream_t st)
 {
     const int Ep = (a.E + 3) & ~3;
     constexpr int kBlock = ROW_THREADS<NV>;
-    const size_t smem = size_t(1 + kBlock / 32) * Ep * 4 + size_t(a.E + 1) * 4;
+    const size_t smem = size_t(1 + kBlock / 32) * Ep * 4 + size_t(count_stride(a.E)) * 4;
     auto *kern = k_balance_rows<NV, VEC, GRAD>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(kBlock), smem, st, a, own);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kBlock);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kFinalCtas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = one ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, own, one);
 }
 
 template <int NV>
-cudaError_t pick(const BalanceArgs &a, unsigned grid, bool own, cudaStream_t st)
+cudaError_t pick(const BalanceArgs &a, unsigned grid, bool own, bool one, cudaStream_t st)
 {
-    if (a.E % 4 == 0) return a.dlogits ? rows<NV, true, true>(a, grid, own, st) : rows<NV, true, false>(a, grid, own, st);
-    return a.dlogits ? rows<NV, false, true>(a, grid, own, st) : rows<NV, false, false>(a, grid, own, st);
+    if (a.E % 4 == 0)
+        return a.dlogits ? rows<NV, true, true>(a, grid, own, one, st) : rows<NV, true, false>(a, grid, own, one, st);
+    return a.dlogits ? rows<NV, false, true>(a, grid, own, one, st) : rows<NV, false, false>(a, grid, own, one, st);
 }
 
-unsigned row_blocks(int64_t T)
+// Few rows are the work of one cluster, which needs no second kernel.
+bool one_cluster(int64_t T) { return T <= kOneCluster; }
+
+unsigned row_blocks(int64_t T, int E)
 {
-    return unsigned(T < 152 ? (T > 0 ? T : 1) : 152);
+    const int64_t most = 152 * (E <= 256 ? ROW_BLOCKS<2> : 1);
+    return one_cluster(T) ? unsigned(kFinalCtas) : unsigned(T < most ? T : most);
 }
 
 size_t count_bytes(int64_t T, int E, int k)
 {
-    return T * k > kOwnCount ? size_t(round_up(int64_t(kCountBlocks) * (E + 1) * 4, 256)) : 0;
+    return T * k > kOwnCount ? size_t(round_up(int64_t(kCountParts) * count_stride(E) * 4, 256)) : 0;
 }
 
 }  // namespace
 
-// tokens (256 bytes) | counts of k_balance_count's blocks | sums of the row blocks
+// tokens (256 bytes) | counts of k_balance_count's parts | sums of the row blocks
 size_t balance_scratch_bytes(int64_t T, int E, int k)
 {
-    return 256 + count_bytes(T, E, k) + size_t(row_blocks(T)) * size_t(E + 1) * 4;
+    return 256 + count_bytes(T, E, k) + size_t(row_blocks(T, E)) * size_t(E + 1) * 4;
 }
 
 cudaError_t launch_balance(BalanceArgs a, void *scratch, cudaStream_t st)
@@ -361,18 +489,19 @@ cudaError_t launch_balance(BalanceArgs a, void *scratch, cudaStream_t st)
     a.tokens = reinterpret_cast<int32_t *>(s);
     a.count_part = reinterpret_cast<int32_t *>(s + 256);
     a.part = reinterpret_cast<float *>(s + 256 + count_bytes(a.T, a.E, a.k));
-    const bool own = a.T * a.k <= kOwnCount;
-    const unsigned grid = row_blocks(a.T);
+    const bool own = a.T * a.k <= kOwnCount, one = one_cluster(a.T);
+    const unsigned grid = row_blocks(a.T, a.E);
     cudaError_t e = cudaSuccess;
-    if (!own) e = launch_pdl(k_balance_count, dim3(kCountBlocks), dim3(1024), size_t(a.E + 1) * 4, st, a);
+    if (!own)
+        e = launch_pdl(k_balance_count, dim3(kCountParts * kCountCluster), dim3(512), size_t(count_stride(a.E)) * 4, st, a);
     if (e != cudaSuccess) return e;
     const int nv = int(ceil_div(a.E, 128));
-    if (nv <= 2) e = pick<2>(a, grid, own, st);
-    else if (nv <= 4) e = pick<4>(a, grid, own, st);
-    else if (nv <= 7) e = pick<7>(a, grid, own, st);
-    else e = pick<16>(a, grid, own, st);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_balance_final, dim3(kFinalCtas), dim3(32 * kFinalWarps), 0, st, a, int(grid));
+    if (nv <= 2) e = pick<2>(a, grid, own, one, st);
+    else if (nv <= 4) e = pick<4>(a, grid, own, one, st);
+    else if (nv <= 7) e = pick<7>(a, grid, own, one, st);
+    else e = pick<16>(a, grid, own, one, st);
+    if (e != cudaSuccess || one) return e;
+    return launch_pdl(k_balance_final, dim3(kFinalCtas), dim3(kFinalCols * kStrands), 0, st, a, int(grid));
 }
 
 }  // namespace lmoe

@@ -212,10 +212,11 @@ cudaError_t launch_fwd(const LayerNormArgs &a, cudaStream_t st)
     }
     const bool many = a.T > 8 * 152;
     // Many bf16 rows: as many blocks as an SM holds with the registers of 1024 threads.
-    if (sizeof(R) == 2 && a.H <= 8192 && many) {
-        const unsigned threads = unsigned(round_up(ceil_div(nv, 2), 32));
-        return launch_pdl(k_layer_norm_walk<R, 2>, dim3(152 * 2 * (512 / threads)), dim3(threads), 0, st, a);
-    }
+    if constexpr (sizeof(R) == 2)
+        if (a.H <= 8192 && many) {
+            const unsigned threads = unsigned(round_up(ceil_div(nv, 2), 32));
+            return launch_pdl(k_layer_norm_walk<R, 2>, dim3(152 * 2 * (512 / threads)), dim3(threads), 0, st, a);
+        }
     // Else a block a row.  Few rows: eight elements a thread, the shortest way from load to
     // store.  Many fp32 rows, us, by eights a thread:
     //   8192 x 7168 (352 MB)  1: 78.5  2: 60.5  3: 60.7  4: 55.7 (6.3 TB/s)   walking 68.5
@@ -238,17 +239,6 @@ cudaError_t launch_fwd(const LayerNormArgs &a, cudaStream_t st)
 }
 
 // ---- backward ------------------------------------------------------------------------
-
-// Two sums over a warp at once, half a warp each from the first step on; the same in every lane.
-__device__ __forceinline__ float2 warp_sum2(float a, float b)
-{
-    const int which = (threadIdx.x >> 4) & 1;
-    float s = which ? b : a;
-    s += __shfl_xor_sync(0xFFFFFFFFu, which ? a : b, 16);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
-}
 
 // Rows of at most 512 columns: a warp walks over rows, the next row on its way while this
 // one is worked on.  SUMS: the column sums are kept, and written to part[block][2][H] at

@@ -89,6 +89,17 @@ __device__ __forceinline__ float row_sum(float s, float *part)
     return s;
 }
 
+// Two sums over a warp at once, half a warp each from the first step on; the same in every lane.
+__device__ __forceinline__ float2 warp_sum2(float a, float b)
+{
+    const int which = (threadIdx.x >> 4) & 1;
+    float s = which ? b : a;
+    s += __shfl_xor_sync(0xFFFFFFFFu, which ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
+}
+
 // Two fp32 values as one operand of the packed instructions (each rounded as by itself).
 struct F2 {
     uint64_t v;

@@ -347,6 +347,12 @@ __device__ __forceinline__ void cluster_store_i32(uint32_t addr, int32_t v)
 {
     asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ int32_t cluster_load_i32(uint32_t addr)
+{
+    int32_t v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 // Arrival on a barrier of either CTA that publishes no memory: it says that this
 // thread has read what it waited for (tensor memory after its wait, a shared
 // word).  Without the cluster-scope release it does not wait for the thread's
