@@ -31,7 +31,7 @@ constexpr int MAX_PARTS = 16;
 
 template <int NT, bool PAIR>
 struct LCfg {
-    static constexpr int EW = NT >= 128 ? 8 : 4;  // epilogue warps
+    static constexpr int EW = 8;  // epilogue warps, two per TMEM lane quarter (32 columns each in turn)
     static constexpr int THREADS = 32 * (2 + EW);
     static constexpr int CL = PAIR ? 2 : 1;  // CTAs a tile: a pair (cta_group::2) has 256 rows of A, each CTA half of B
     static constexpr int MT = 128 * CL;
@@ -97,29 +97,27 @@ __device__ __forceinline__ void row_load(uint32_t (&u)[32], const void *base, in
     }
 }
 template <bool F32>
-__device__ __forceinline__ void row_add(const uint32_t (&u)[32], float (&y)[32])
+__device__ __forceinline__ void row_add(const uint32_t (&u)[32], F2 (&y)[16])
 {
 #pragma unroll
-    for (int i = 0; i < WORDS<F32>; ++i) {
-        if (F32) {
-            y[i] += __uint_as_float(u[i]);
-        } else {
-            y[2 * i] += __uint_as_float(u[i] << 16);
-            y[2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
-        }
-    }
+    for (int i = 0; i < 16; ++i)
+        y[i] = y[i] + (F32 ? f2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))
+                           : f2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)));
 }
 // Rounded to nearest even.
 template <bool F32>
-__device__ __forceinline__ void row_store(const float (&y)[32], void *base, int64_t at, int n, int vec)
+__device__ __forceinline__ void row_store(const F2 (&y)[16], void *base, int64_t at, int n, int vec)
 {
     uint32_t u[WORDS<F32>];
 #pragma unroll
-    for (int i = 0; i < WORDS<F32>; ++i) {
-        if (F32) {
-            u[i] = __float_as_uint(y[i]);
+    for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        f2_get(y[i], lo, hi);
+        if constexpr (F32) {
+            u[2 * i] = __float_as_uint(lo);
+            u[2 * i + 1] = __float_as_uint(hi);
         } else {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
             u[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
     }
@@ -143,51 +141,6 @@ __device__ __forceinline__ void row_store(const float (&y)[32], void *base, int6
                 uint16_t *h = reinterpret_cast<uint16_t *>(p);
                 if (2 * i < n) h[2 * i] = uint16_t(u[i]);
                 if (2 * i + 1 < n) h[2 * i + 1] = uint16_t(u[i] >> 16);
-            }
-        }
-    }
-}
-
-// y[j] = fn(y[j]), the function chosen once.
-__device__ __forceinline__ void apply32(int fn, float (&y)[32])
-{
-    auto all = [&](auto f) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = f(y[j]);
-    };
-    switch (fn) {
-    case LMOE_FN_RELU: all([](float z) { return apply<LMOE_FN_RELU>(z); }); break;
-    case LMOE_FN_SILU: all([](float z) { return apply<LMOE_FN_SILU>(z); }); break;
-    case LMOE_FN_GELU: all([](float z) { return apply<LMOE_FN_GELU>(z); }); break;
-    case LMOE_FN_GELU_TANH: all([](float z) { return apply<LMOE_FN_GELU_TANH>(z); }); break;
-    default: break;
-    }
-}
-
-// y[j] += bias[n + j], j < cols <= 32; n % 32 == 0.
-__device__ __forceinline__ void add_bias(const void *bias, int f32, int n, int cols, float (&y)[32])
-{
-    const float *bf = static_cast<const float *>(bias) + n;
-    const uint16_t *bh = static_cast<const uint16_t *>(bias) + n;
-    if (cols < 32) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < cols) y[j] += f32 ? __ldg(bf + j) : bf16_bits_to_f32(__ldg(bh + j));
-    } else if (f32) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(bf + j));
-            y[j] += f.x, y[j + 1] += f.y, y[j + 2] += f.z, y[j + 3] += f.w;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            const uint4 f = __ldg(reinterpret_cast<const uint4 *>(bh + j));
-            const uint32_t w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                y[j + 2 * i] += __uint_as_float(w[i] << 16);
-                y[j + 2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
             }
         }
     }
@@ -343,43 +296,66 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
         }
     } else if (warp >= 2) {
         // ---------------- epilogue ----------------
+        __shared__ __align__(16) float s_bias[C::EW][32];
         const int q = warp & 3, half = (warp - 2) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int it = first; it < items; it += step) {
             const int64_t m = tile_m(it) + 32 * q + lane;
-            const int n0 = tile_n(it);
+            const int n0 = tile_n(it), limit = min(NT, p.N - n0);
+            const bool mine = m < p.M;
+            const int64_t row = (it / tiles * p.M + m) * p.N + n0;  // (parts: fp32 rows one after another)
+            const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
+            // what 32 columns need from memory, on its way a turn ahead: the residual, a column's bias a lane
+            uint32_t r[32];
+            float bias = 0.f;
+            auto fetch = [&](int c) {
+                if (c >= limit) return;
+                if (p.res && mine) {
+                    if (p.res_f32) row_load<true>(r, p.res, row + c, min(32, limit - c), p.vec);
+                    else row_load<false>(r, p.res, row + c, min(32, limit - c), p.vec);
+                }
+                if (p.bias && c + lane < limit)
+                    bias = p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + n0 + c + lane)
+                                      : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p.bias) + n0 + c + lane));
+            };
+            fetch(32 * half);
             if (!mbar_wait_warp(&acc_full[acc], acc_phase, p.limit)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                 break;
             }
             tc_fence_after();
-            const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
-            for (int c = 32 * half; c < NT && n0 + c < p.N; c += 8 * C::EW) {
+            for (int c = 32 * half; c < limit; c += 8 * C::EW) {
                 uint32_t v[32];
                 tmem_ld_cols<32>(tb + c, v);
-                const int n = n0 + c, cols = min(32, p.N - n);
-                const bool mine = m < p.M;
-                const int64_t at = (it / tiles * p.M + m) * p.N + n;  // (parts: fp32 rows one after another)
-                uint32_t r[32];  // the residual's words
-                if (p.res && mine) {
-                    if (p.res_f32) row_load<true>(r, p.res, at, cols, p.vec);
-                    else row_load<false>(r, p.res, at, cols, p.vec);
+                const int cols = min(32, limit - c);
+                F2 y[16];
+                if (p.bias) {
+                    s_bias[warp - 2][lane] = bias;
+                    __syncwarp();
                 }
-                float y[32];
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
-                if (p.bias) add_bias(p.bias, p.bias_f32, n, cols, y);
-                if (p.pre && mine) row_store<false>(y, p.pre, at, cols, p.vec);
-                apply32(p.fn, y);
+                for (int j = 0; j < 16; ++j) y[j] = f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                if (p.bias) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 b = *reinterpret_cast<const float4 *>(&s_bias[warp - 2][4 * j]);
+                        y[2 * j] = y[2 * j] + f2(b.x, b.y);
+                        y[2 * j + 1] = y[2 * j + 1] + f2(b.z, b.w);
+                    }
+                    __syncwarp();
+                }
+                if (p.pre && mine) row_store<false>(y, p.pre, row + c, cols, p.vec);
+                apply_fn(p.fn, y);
                 if (p.res) {
                     if (p.res_f32) row_add<true>(r, y);
                     else row_add<false>(r, y);
                 }
+                fetch(c + 8 * C::EW);
                 if (mine) {
-                    if (p.out_f32) row_store<true>(y, p.out, at, cols, p.vec);
-                    else row_store<false>(y, p.out, at, cols, p.vec);
+                    if (p.out_f32) row_store<true>(y, p.out, row + c, cols, p.vec);
+                    else row_store<false>(y, p.out, row + c, cols, p.vec);
                 }
                 __syncwarp();
             }
@@ -496,8 +472,15 @@ __global__ void __launch_bounds__(256) k_split_sum(const float *part, const LArg
         }
     };
     if (p.pre) put(p.pre, false);
+    F2 z[(W + 1) / 2];
 #pragma unroll
-    for (int j = 0; j < W; ++j) y[j] = apply_fn(p.fn, y[j]);
+    for (int j = 0; j < W; j += 2) z[j / 2] = f2(y[j], W > 1 ? y[(j + 1) % W] : 0.f);
+    apply_fn(p.fn, z);
+#pragma unroll
+    for (int j = 0; j < W; j += 2) {
+        float other;
+        f2_get(z[j / 2], y[j], W > 1 ? y[(j + 1) % W] : other);
+    }
     if (p.res) {
         float v[W];
         if constexpr (W == 8) {
@@ -621,49 +604,57 @@ struct DzArgs {
 // A block takes 256 columns and every gridDim.y-th group of eight rows, a warp a row
 // of it, a lane eight columns.  VEC: rows start on 16 bytes.
 template <bool F32, int FN, bool VEC>
-__global__ void __launch_bounds__(256) k_act_back(const DzArgs p)
+__global__ void __launch_bounds__(256, 4) k_act_back(const DzArgs p)
 {
     __shared__ float s_cols[8][256 + 8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (int(blockIdx.x) * 32 + lane) * 8;
     float sum[8] = {};
     pdl_enter();
+    const int64_t step = int64_t(gridDim.y) * 8;
     if (c < p.Np)
-        for (int64_t t = int64_t(blockIdx.y) * 8 + warp; t < p.rows; t += int64_t(gridDim.y) * 8) {
-            float d[8], z[8] = {};
-            const int64_t at = t * p.N + c;
-            if (VEC) {
-                if (F32) {
-                    Pack<float, 8> q;
-                    q.load(static_cast<const float *>(p.dout) + at);
-                    q.get(d);
+        for (int64_t t0 = int64_t(blockIdx.y) * 8 + warp; t0 < p.rows; t0 += 4 * step) {
+            // four rows' loads at once: one row at a time left the loads' latency open (4096 x 7168,
+            // silu, sums alone: 36 us)
+            Pack<float, 8> df[F32 && VEC ? 4 : 1];
+            Pack<uint16_t, 8> dh[!F32 && VEC ? 4 : 1], zh[FN != LMOE_FN_NONE && VEC ? 4 : 1];
+            if constexpr (VEC) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t at = min(t0 + i * step, p.rows - 1) * p.N + c;
+                    if constexpr (F32) df[i].load(static_cast<const float *>(p.dout) + at);
+                    else dh[i].load(static_cast<const uint16_t *>(p.dout) + at);
+                    if constexpr (FN != LMOE_FN_NONE) zh[i].load(p.pre + at);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t t = t0 + i * step, at = t * p.N + c;
+                if (t >= p.rows) break;
+                float d[8], z[8] = {};
+                if constexpr (VEC) {
+                    if constexpr (F32) df[i].get(d);
+                    else dh[i].get(d);
+                    if constexpr (FN != LMOE_FN_NONE) zh[i].get(z);
                 } else {
-                    Pack<uint16_t, 8> q;
-                    q.load(static_cast<const uint16_t *>(p.dout) + at);
-                    q.get(d);
-                }
-                if (FN != LMOE_FN_NONE) {
-                    Pack<uint16_t, 8> q;
-                    q.load(p.pre + at);
-                    q.get(z);
-                }
-            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const bool in = c + j < p.N;
-                    d[j] = !in ? 0.f : F32 ? static_cast<const float *>(p.dout)[at + j] : bf16_bits_to_f32(static_cast<const uint16_t *>(p.dout)[at + j]);
-                    if (FN != LMOE_FN_NONE && in) z[j] = bf16_bits_to_f32(p.pre[at + j]);
+                    for (int j = 0; j < 8; ++j) {
+                        const bool in = c + j < p.N;
+                        d[j] = !in ? 0.f : F32 ? static_cast<const float *>(p.dout)[at + j] : bf16_bits_to_f32(static_cast<const uint16_t *>(p.dout)[at + j]);
+                        if (FN != LMOE_FN_NONE && in) z[j] = bf16_bits_to_f32(p.pre[at + j]);
+                    }
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (FN != LMOE_FN_NONE) d[j] *= slope<FN>(z[j]);
-                sum[j] += d[j];
-            }
-            if (p.dz) {
-                Pack<uint16_t, 8> q;
-                q.set(d);
-                q.store(p.dz + t * p.Np + c);
+                for (int j = 0; j < 8; j += 2) {
+                    if (FN != LMOE_FN_NONE) f2_get(f2(d[j], d[j + 1]) * slope<FN>(f2(z[j], z[j + 1])), d[j], d[j + 1]);
+                    sum[j] += d[j];
+                    sum[j + 1] += d[j + 1];
+                }
+                if (p.dz) {
+                    Pack<uint16_t, 8> q;
+                    q.set(d);
+                    q.store(p.dz + t * p.Np + c);
+                }
             }
         }
     if (!p.part) return;
@@ -678,10 +669,11 @@ __global__ void __launch_bounds__(256) k_act_back(const DzArgs p)
     p.part[int64_t(blockIdx.y) * p.N + col] = v;
 }
 
-// Groups of rows of k_act_back: four blocks an SM, eight rows a block at least.
+// Groups of rows of k_act_back: as many blocks as fit at once, four an SM, and eight rows a
+// block at least.
 int64_t dz_splits(int64_t rows, int N)
 {
-    const int64_t want = ceil_div(152 * 4, ceil_div(N, 256)), most = ceil_div(rows, 8);
+    const int64_t strips = ceil_div(N, 256), want = strips < 152 * 4 ? 152 * 4 / strips : 1, most = ceil_div(rows, 8);
     return want < most ? want : most;
 }
 

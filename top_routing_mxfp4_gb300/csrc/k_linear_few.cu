@@ -83,11 +83,18 @@ __global__ void __launch_bounds__(192, FCfg<NT>::PER_SM)
     tc_fence_after();
     if (p.KS > 1) cluster_sync();  // the cluster's barriers are initialised
     const uint32_t tmem = *tmem_slot;
-    pdl_enter();
-
     const int rank = p.KS > 1 ? int(cluster_rank()) : 0, tile = int(blockIdx.x) / p.KS;
-    const int m0 = tile * 128, r0 = int(blockIdx.y) * NT, cols = min(NT, p.rows - r0);
+    const int m0 = tile * 128, cols = p.rows;
     const int k0 = rank * p.KC / p.KS, k1 = (rank + 1) * p.KC / p.KS;  // this rank's chunks
+    // The first weights on their way to L2 (which the kernel before may still write them to)
+    // while that kernel ends: 64 rows 3584 -> 7168 15.6 -> 14.8 us, one row 12.3 -> 11.9; twice
+    // as many took longer than none.
+    if (warp == 0) {
+        if (elect_one())
+            for (int kc = k0; kc < min(k1, k0 + S); ++kc) tma_prefetch_2d(&tmA, kc * 64, m0);
+        __syncwarp();
+    }
+    pdl_enter();
 
     if (warp == 0) {
         // ---------------- copies ----------------
@@ -104,8 +111,8 @@ __global__ void __launch_bounds__(192, FCfg<NT>::PER_SM)
             if (elect_one() && !(p.stall && kc == k0)) {
                 uint8_t *sb = stages + stage * C::STAGE;
                 mbar_arrive_expect_tx(&full[stage], C::STAGE);
-                tma_load_2d_hint(sb, &tmA, kc * 64, m0, &full[stage], gridDim.y > 1 ? keep : once);
-                tma_load_2d_hint(sb + A_TILE, &tmB, kc * 64, r0, &full[stage], keep);
+                tma_load_2d_hint(sb, &tmA, kc * 64, m0, &full[stage], once);
+                tma_load_2d_hint(sb + A_TILE, &tmB, kc * 64, 0, &full[stage], keep);
             }
             __syncwarp();
             ++fills;
@@ -159,25 +166,34 @@ __global__ void __launch_bounds__(192, FCfg<NT>::PER_SM)
             bias = p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + n) : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p.bias) + n));
         // rows [c0, c1) of the tile, at most 16
         auto finish = [&](int c0, int c1, const float (&y)[16]) {
-            const int64_t at = int64_t(r0 + c0) * p.N + n;
-            float r[16];
+            const int64_t at = int64_t(c0) * p.N + n;
+            float r[16] = {};
             if (p.res)
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (mine && c0 + j < c1)
                         r[j] = p.res_f32 ? static_cast<const float *>(p.res)[at + int64_t(j) * p.N]
                                          : bf16_bits_to_f32(static_cast<const uint16_t *>(p.res)[at + int64_t(j) * p.N]);
+            F2 z[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (!mine || c0 + j >= c1) continue;
-                const int64_t i = at + int64_t(j) * p.N;
-                float z = y[j] + bias;
-                if (p.pre) reinterpret_cast<__nv_bfloat16 *>(p.pre)[i] = __float2bfloat16_rn(z);
-                z = apply_fn(p.fn, z);
-                if (p.res) z += r[j];
-                if (p.out_f32) static_cast<float *>(p.out)[i] = z;
-                else static_cast<__nv_bfloat16 *>(p.out)[i] = __float2bfloat16_rn(z);
-            }
+            for (int j = 0; j < 8; ++j) z[j] = f2(y[2 * j], y[2 * j + 1]) + f2(bias);
+            auto store = [&](void *base, bool f32) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    if (!mine || c0 + j >= c1) continue;
+                    float lo, hi;
+                    f2_get(z[j / 2], lo, hi);
+                    const int64_t i = at + int64_t(j) * p.N;
+                    if (f32) static_cast<float *>(base)[i] = j & 1 ? hi : lo;
+                    else static_cast<__nv_bfloat16 *>(base)[i] = __float2bfloat16_rn(j & 1 ? hi : lo);
+                }
+            };
+            if (p.pre) store(p.pre, false);
+            apply_fn(p.fn, z);
+            if (p.res)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = z[j] + f2(r[2 * j], r[2 * j + 1]);
+            store(p.out, p.out_f32);
         };
         if (!mbar_wait_warp(acc_full, 0, p.limit)) {
             if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
@@ -231,19 +247,19 @@ cudaError_t launch(const LinearActArgs &a, FArgs g, cudaStream_t st)
     CUtensorMap ma, mb;
     if (!make_tensor_map(&ma, a.W, MapType::BF16, a.K, a.N, 128) || !make_tensor_map(&mb, a.x, MapType::BF16, a.K, a.rows, NT))
         return cudaErrorInvalidValue;
-    const int64_t tiles = ceil_div(a.N, 128), rts = ceil_div(a.rows, NT);
+    const int64_t tiles = ceil_div(a.N, 128);
     // K is shared so that the CTAs fill the GPU's slots, two an SM, once, each with four
     // chunks at least.  One an SM took 20.8 against 15.9 us at 64 rows of 3584 -> 7168 and
     // as long at one row (12.6 against 12.5 us).
     const int64_t slots = int64_t(device_sms()) * C::PER_SM;
     int ks = 8;
-    while (ks > 1 && (tiles * rts * ks > slots || g.KC < 4 * ks)) --ks;
+    while (ks > 1 && (tiles * ks > slots || g.KC < 4 * ks)) --ks;
     g.KS = ks;
     const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::RED + (2 * C::S + 3) * 8 + 8;
     const cudaError_t e = cudaFuncSetAttribute(k_linear_few<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(tiles * ks), unsigned(rts));
+    cfg.gridDim = dim3(unsigned(tiles * ks));
     cfg.blockDim = dim3(192);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
