@@ -44,17 +44,31 @@ struct LCfg {
     static constexpr uint32_t TMEM_COLS = ACC * NT;
 };
 
-struct LArgs {
+// A product: D [M][N], tiles row by row.
+struct LJob {
     int64_t M;
-    int N, KC;       // chunks of the reduction
-    int MTL, NTL;    // tiles
-    int KS;          // parts of the reduction; with more than one, part k's sums go to out + k M N (fp32)
+    int N, KC, NTL;  // KC: chunks of the reduction; NTL: tiles a row
+    int a_mn, b_mn;  // the operand's reduction runs over the rows of its matrix
     // epilogue
     const void *bias, *res;
     int bias_f32, res_f32, out_f32, fn;
-    int vec;         // outputs' and residual's rows take vectors of this many bytes (32, 16) or single elements (0)
+    int vec;  // outputs' and residual's rows take vectors of this many bytes (32, 16) or single elements (0)
     void *out;
     uint16_t *pre;
+};
+// Consecutive tiles of a product, whole (ks = 1) or each in ks parts of its reduction,
+// whose sums go to part [tile][ks][MT][NT] (fp32).
+struct LSeg {
+    int job, tile0, tiles, ks;
+    int item0;  // number of its first item
+    float *part;
+};
+constexpr int MAX_SEGS = 4;
+
+struct LArgs {
+    LJob job[2];
+    LSeg seg[MAX_SEGS];
+    int segs, whole, items;  // items [0, whole) are whole tiles
     int32_t *status;
     long long limit;
     int stall;
@@ -148,14 +162,17 @@ __device__ __forceinline__ void row_store(const F2 (&y)[16], void *base, int64_t
 
 // ---- the products ------------------------------------------------------------------------
 
-// A_MN, B_MN: the operand's reduction runs over the rows of its matrix.
-template <int NT, bool PAIR, bool A_MN, bool B_MN>
+// GRAD: one or two products whose operands may run either way; else one of K-major operands
+// (the choice between operands' orders cost 27.9 -> 29.6 us at 512 rows 7168 -> 3584).
+template <int NT, bool PAIR, bool GRAD>
 __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
-    k_linear_act(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const LArgs p)
+    k_linear_act(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+                 const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+                 const __grid_constant__ LArgs p)
 {
     using C = LCfg<NT, PAIR>;
     constexpr int S = C::S;
-    static_assert(!B_MN || C::BROWS % 64 == 0, "blocks of 64 elements");
+    static_assert(C::BROWS % 64 == 0, "blocks of 64 elements");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(stages + S * C::STAGE);
@@ -177,8 +194,8 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
         }
         mbar_init(drain, 1);
         mbar_init_fence();
-        prefetch_tensormap(&tmA);
-        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmA0);
+        prefetch_tensormap(&tmB0);
     }
     if (warp == 1) PAIR ? tmem_alloc_pair(tmem_slot, C::TMEM_COLS) : tmem_alloc(tmem_slot, C::TMEM_COLS);
     tc_fence_before();
@@ -190,20 +207,44 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
 
     const int rank = PAIR ? int(cluster_rank()) : 0;
     const int first = int(blockIdx.x) / C::CL, step = int(gridDim.x) / C::CL;
-    const int tiles = p.MTL * p.NTL, items = tiles * p.KS;
-    auto tile_m = [&](int it) { return int64_t(it % tiles / p.NTL) * C::MT + rank * 128; };  // this CTA's rows
-    auto tile_n = [&](int it) { return (it % tiles % p.NTL) * NT; };
-    auto chunk0 = [&](int it) { return it / tiles * p.KC / p.KS; };  // an item's chunks of the reduction
-    auto chunk1 = [&](int it) { return (it / tiles + 1) * p.KC / p.KS; };
+    // This CTA's items: whole tiles, every step-th, then parts, handed out from the other end (the
+    // first CTAs may have one whole tile more).
+    const int part0 = p.whole + step - 1 - first, begin = first < p.whole ? first : part0;
+    auto next = [&](int it) {
+        if (it >= p.whole || it + step < p.whole) return it + step;
+        return part0;
+    };
+    struct Item {
+        int job, m, n, k0, k1;  // m, n: first row and column of the tile
+        float *part;            // of its sums [MT][NT], or null
+    };
+    auto item = [&](int it) {
+        int s = 0;
+        while (s + 1 < p.segs && p.seg[s + 1].item0 <= it) ++s;
+        const LSeg &g = p.seg[s];
+        const LJob &j = p.job[GRAD ? g.job : 0];
+        const int l = it - g.item0, k = l / g.tiles, at = l - k * g.tiles, tile = g.tile0 + at;
+        Item r;
+        r.job = GRAD ? g.job : 0;
+        r.m = tile / j.NTL * C::MT;
+        r.n = tile % j.NTL * NT;
+        r.k0 = int(int64_t(k) * j.KC / g.ks);
+        r.k1 = int(int64_t(k + 1) * j.KC / g.ks);
+        r.part = g.ks > 1 ? g.part + (int64_t(at) * g.ks + k) * (C::MT * NT) : nullptr;
+        return r;
+    };
 
     if (warp == 0) {
         // ---------------- copies ----------------
         int stage = 0, fills = 0;
         uint32_t phase = 0;
         bool ok = true, at_start = true;  // (the failure-path test withholds a CTA's first stage)
-        for (int it = first; it < items && ok; it += step) {
-            const int m0 = int(tile_m(it)), n0 = tile_n(it) + rank * C::BROWS, k1 = chunk1(it);
-            for (int kc = chunk0(it); kc < k1; ++kc) {
+        for (int it = begin; it < p.items && ok; it = next(it)) {
+            const Item w = item(it);
+            const int m0 = w.m + rank * 128, n0 = w.n + rank * C::BROWS;
+            const CUtensorMap *tmA = GRAD && w.job ? &tmA1 : &tmA0, *tmB = GRAD && w.job ? &tmB1 : &tmB0;
+            const bool a_mn = GRAD && p.job[w.job].a_mn, b_mn = GRAD && p.job[w.job].b_mn;
+            for (int kc = w.k0; kc < w.k1; ++kc) {
                 ok = mbar_wait_warp(&empty[stage], phase ^ 1, p.limit);
                 if (!ok) {
                     if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
@@ -218,17 +259,17 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
                     auto load = [&](void *dst, const CUtensorMap *tm, int x, int y) {
                         PAIR ? tma_load_2d_pair(dst, tm, x, y, bar, policy) : tma_load_2d_hint(dst, tm, x, y, &full[stage], policy);
                     };
-                    if (A_MN) {
-                        load(sa, &tmA, m0, kc * 64);
-                        load(sa + 8192, &tmA, m0 + 64, kc * 64);
+                    if (a_mn) {
+                        load(sa, tmA, m0, kc * 64);
+                        load(sa + 8192, tmA, m0 + 64, kc * 64);
                     } else {
-                        load(sa, &tmA, kc * 64, m0);
+                        load(sa, tmA, kc * 64, m0);
                     }
-                    if (B_MN) {
+                    if (b_mn) {
 #pragma unroll
-                        for (int b = 0; b < C::BROWS / 64; ++b) load(sb + b * 8192, &tmB, n0 + 64 * b, kc * 64);
+                        for (int b = 0; b < C::BROWS / 64; ++b) load(sb + b * 8192, tmB, n0 + 64 * b, kc * 64);
                     } else {
-                        load(sb, &tmB, kc * 64, n0);
+                        load(sb, tmB, kc * 64, n0);
                     }
                 }
                 __syncwarp();
@@ -249,21 +290,24 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
-        const uint32_t id = (PAIR ? idesc_bf16_pair(NT) : idesc_bf16(NT)) | (A_MN ? IDESC_A_MN : 0) | (B_MN ? IDESC_B_MN : 0);
-        constexpr uint32_t a_step = A_MN ? 128 : 2, b_step = B_MN ? 128 : 2;  // 16 of the reduction, in 16-byte units
-        for (int it = first; it < items && ok; it += step) {
+        for (int it = begin; it < p.items && ok; it = next(it)) {
+            const Item w = item(it);
+            const bool a_mn = GRAD && p.job[w.job].a_mn, b_mn = GRAD && p.job[w.job].b_mn;
+            const uint32_t id = (PAIR ? idesc_bf16_pair(NT) : idesc_bf16(NT)) | (a_mn ? IDESC_A_MN : 0) | (b_mn ? IDESC_B_MN : 0);
+            const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;  // 16 of the reduction, in 16-byte units
+            const uint32_t base = smem_u32(stages);
+            const uint64_t ad0 = a_mn ? sdesc_mn128(base, 8192) : sdesc_k128(base);  // of stage 0
+            const uint64_t bd0 = b_mn ? sdesc_mn128(base + A_TILE, 8192) : sdesc_k128(base + A_TILE);
             ok = mbar_wait_warp(&acc_empty[acc], acc_phase ^ 1, p.limit);
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * NT);
-            const int k0 = chunk0(it), k1 = chunk1(it);
+            const int k0 = w.k0, k1 = w.k1;
             for (int kc = k0; kc < k1 && ok; ++kc) {
                 ok = mbar_wait_warp(&full[stage], phase, p.limit);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t sa = smem_u32(stages + stage * C::STAGE), sb = sa + A_TILE;
-                    const uint64_t ad = A_MN ? sdesc_mn128(sa, 8192) : sdesc_k128(sa);
-                    const uint64_t bd = B_MN ? sdesc_mn128(sb, 8192) : sdesc_k128(sb);
+                    const uint64_t ad = ad0 + uint32_t(stage) * (C::STAGE >> 4), bd = bd0 + uint32_t(stage) * (C::STAGE >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         if (PAIR)
@@ -300,62 +344,80 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
         const int q = warp & 3, half = (warp - 2) >> 2;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int it = first; it < items; it += step) {
-            const int64_t m = tile_m(it) + 32 * q + lane;
-            const int n0 = tile_n(it), limit = min(NT, p.N - n0);
-            const bool mine = m < p.M;
-            const int64_t row = (it / tiles * p.M + m) * p.N + n0;  // (parts: fp32 rows one after another)
+        for (int it = begin; it < p.items; it = next(it)) {
+            const Item w = item(it);
+            const LJob &j = p.job[GRAD ? w.job : 0];
+            const int64_t m = w.m + rank * 128 + 32 * q + lane;
+            const int n0 = w.n, limit = min(NT, j.N - n0);
+            const bool mine = m < j.M;
+            const int64_t row = m * j.N + n0;
             const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
             // what 32 columns need from memory, on its way a turn ahead: the residual, a column's bias a lane
             uint32_t r[32];
             float bias = 0.f;
             auto fetch = [&](int c) {
                 if (c >= limit) return;
-                if (p.res && mine) {
-                    if (p.res_f32) row_load<true>(r, p.res, row + c, min(32, limit - c), p.vec);
-                    else row_load<false>(r, p.res, row + c, min(32, limit - c), p.vec);
+                if (j.res && mine) {
+                    if (j.res_f32) row_load<true>(r, j.res, row + c, min(32, limit - c), j.vec);
+                    else row_load<false>(r, j.res, row + c, min(32, limit - c), j.vec);
                 }
-                if (p.bias && c + lane < limit)
-                    bias = p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + n0 + c + lane)
-                                      : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p.bias) + n0 + c + lane));
+                if (j.bias && c + lane < limit)
+                    bias = j.bias_f32 ? __ldg(static_cast<const float *>(j.bias) + n0 + c + lane)
+                                      : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(j.bias) + n0 + c + lane));
             };
-            fetch(32 * half);
+            if (!w.part) fetch(32 * half);
             if (!mbar_wait_warp(&acc_full[acc], acc_phase, p.limit)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                 break;
             }
             tc_fence_after();
-            for (int c = 32 * half; c < limit; c += 8 * C::EW) {
+            if (w.part) {
+                float *sums = w.part + int64_t(rank * 128 + 32 * q + lane) * NT;
+                for (int c = 32 * half; c < limit; c += 8 * C::EW) {
+                    uint32_t v[32];
+                    tmem_ld_cols<32>(tb + c, v);
+                    tmem_ld_wait();
+                    if (mine)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(sums + c + i), "r"(v[i]),
+                                         "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]),
+                                         "r"(v[i + 6]), "r"(v[i + 7])
+                                         : "memory");
+                    __syncwarp();
+                }
+            }
+            for (int c = 32 * half; c < limit && !w.part; c += 8 * C::EW) {
                 uint32_t v[32];
                 tmem_ld_cols<32>(tb + c, v);
                 const int cols = min(32, limit - c);
                 F2 y[16];
-                if (p.bias) {
+                if (j.bias) {
                     s_bias[warp - 2][lane] = bias;
                     __syncwarp();
                 }
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                if (p.bias) {
+                for (int i = 0; i < 16; ++i) y[i] = f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                if (j.bias) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 b = *reinterpret_cast<const float4 *>(&s_bias[warp - 2][4 * j]);
-                        y[2 * j] = y[2 * j] + f2(b.x, b.y);
-                        y[2 * j + 1] = y[2 * j + 1] + f2(b.z, b.w);
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 b = *reinterpret_cast<const float4 *>(&s_bias[warp - 2][4 * i]);
+                        y[2 * i] = y[2 * i] + f2(b.x, b.y);
+                        y[2 * i + 1] = y[2 * i + 1] + f2(b.z, b.w);
                     }
                     __syncwarp();
                 }
-                if (p.pre && mine) row_store<false>(y, p.pre, row + c, cols, p.vec);
-                apply_fn(p.fn, y);
-                if (p.res) {
-                    if (p.res_f32) row_add<true>(r, y);
+                if (j.pre && mine) row_store<false>(y, j.pre, row + c, cols, j.vec);
+                apply_fn(j.fn, y);
+                if (j.res) {
+                    if (j.res_f32) row_add<true>(r, y);
                     else row_add<false>(r, y);
                 }
                 fetch(c + 8 * C::EW);
                 if (mine) {
-                    if (p.out_f32) row_store<true>(y, p.out, row + c, cols, p.vec);
-                    else row_store<false>(y, p.out, row + c, cols, p.vec);
+                    if (j.out_f32) row_store<true>(y, j.out, row + c, cols, j.vec);
+                    else row_store<false>(y, j.out, row + c, cols, j.vec);
                 }
                 __syncwarp();
             }
@@ -375,131 +437,88 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
     if (warp == 1) PAIR ? tmem_dealloc_pair(tmem, C::TMEM_COLS) : tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
-// An operand: [rows][cols] bf16, rows `stride` elements apart.
-struct Operand {
-    const uint16_t *p;
-    int64_t rows, cols, stride;
-};
-
-template <int NT, bool PAIR, bool A_MN, bool B_MN>
-cudaError_t launch(const Operand &A, const Operand &B, LArgs g, cudaStream_t st)
-{
-    using C = LCfg<NT, PAIR>;
-    CUtensorMap ma, mb;
-    if (!make_tensor_map(&ma, A.p, MapType::BF16, A.cols, A.rows, A_MN ? 64 : 128, A.stride) ||
-        !make_tensor_map(&mb, B.p, MapType::BF16, B.cols, B.rows, B_MN ? 64 : C::BROWS, B.stride))
-        return cudaErrorInvalidValue;
-    g.MTL = int(ceil_div(g.M, C::MT));
-    g.NTL = int(ceil_div(g.N, NT));
-    const int64_t items = int64_t(g.MTL) * g.NTL * g.KS;
-    const size_t smem = 1024 + size_t(C::S) * C::STAGE + (2 * C::S + 2 * C::ACC + 1) * 8 + 8;
-    auto *kern = k_linear_act<NT, PAIR, A_MN, B_MN>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-    const int64_t slots = device_sms() / C::CL;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((items < slots ? items : slots) * C::CL));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = C::CL;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, g);
-}
-
-// Vectors of 32 or 16 bytes where every row of every tensor starts on one.
-int vector_bytes(const LArgs &g)
-{
-    auto fits = [&](const void *p, int bytes, int v) {
-        return !p || (reinterpret_cast<uintptr_t>(p) % v == 0 && int64_t(g.N) * bytes % v == 0);
-    };
-    for (int v : {32, 16})
-        if (fits(g.out, g.out_f32 ? 4 : 2, v) && fits(g.pre, 2, v) && fits(g.res, g.res_f32 ? 4 : 2, v)) return v;
-    return 0;
-}
-
 // ---- parts of the reduction ------------------------------------------------------------------
 
-// The parts' sums added in order, then the epilogue.  W columns a thread (8: rows of all
-// tensors start on 16 bytes).
-template <int W>
-__global__ void __launch_bounds__(256) k_split_sum(const float *part, const LArgs p)
+// The parts' sums added in order, then the epilogue: eight columns a thread, the blocks of
+// a tile one after another.
+template <int MT, int NT>
+__global__ void __launch_bounds__(256) k_split_sum(const __grid_constant__ LArgs p)
 {
-    const int64_t per_row = (p.N + W - 1) / W, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    pdl_enter();
-    if (i >= p.M * per_row) return;
-    const int64_t m = i / per_row, at = m * p.N + (i - m * per_row) * W;
-    const int n = int(i - m * per_row) * W;
-    float y[W] = {};
-    for (int k = 0; k < p.KS; ++k) {
-        const float *s = part + int64_t(k) * p.M * p.N + at;
-        if constexpr (W == 8) {
-            Pack<float, 8> q;
-            q.load(s);
-            float v[8];
-            q.get(v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] += v[j];
-        } else {
-            y[0] += *s;
-        }
+    constexpr int PER = MT * NT / 8 / 256;  // blocks a tile
+    int at = int(blockIdx.x) / PER, s = 0;
+    while (p.seg[s].ks == 1 || at >= p.seg[s].tiles) {
+        if (p.seg[s].ks > 1) at -= p.seg[s].tiles;
+        ++s;
     }
-    if (p.bias)
+    const LSeg &g = p.seg[s];
+    const LJob &j = p.job[g.job];
+    const int e = int(blockIdx.x) % PER * 256 + threadIdx.x, tile = g.tile0 + at;
+    const int64_t m = int64_t(tile / j.NTL) * MT + e / (NT / 8);
+    const int n = tile % j.NTL * NT + e % (NT / 8) * 8, left = j.N - n;
+    pdl_enter();
+    if (m >= j.M || left <= 0) return;
+    const float *sums = g.part + int64_t(at) * g.ks * (MT * NT) + e * 8;
+    F2 y[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)}, v[4];
+    for (int k = 0; k < g.ks; ++k) {
+        Pack<float, 8> q;
+        q.load(sums + int64_t(k) * (MT * NT));
+        pairs(q, v);
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            y[j] += p.bias_f32 ? __ldg(static_cast<const float *>(p.bias) + n + j)
-                               : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(p.bias) + n + j));
-    auto put = [&](void *base, bool f32) {
-        if constexpr (W == 8) {
+        for (int i = 0; i < 4; ++i) y[i] = y[i] + v[i];
+    }
+    const bool wide = j.N % 8 == 0;
+    const int64_t to = m * j.N + n;
+    auto add = [&](const void *base, bool f32, int64_t from) {  // eight elements of bias or residual
+        if (wide) {
             if (f32) {
                 Pack<float, 8> q;
-                q.set(y);
-                q.store(static_cast<float *>(base) + at);
+                q.load(static_cast<const float *>(base) + from);
+                pairs(q, v);
             } else {
                 Pack<uint16_t, 8> q;
-                q.set(y);
-                q.store(static_cast<uint16_t *>(base) + at);
+                q.load(static_cast<const uint16_t *>(base) + from);
+                pairs(q, v);
             }
         } else {
-            if (f32) static_cast<float *>(base)[at] = y[0];
-            else static_cast<__nv_bfloat16 *>(base)[at] = __float2bfloat16_rn(y[0]);
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                f[i] = i >= left ? 0.f : f32 ? static_cast<const float *>(base)[from + i]
+                                             : bf16_bits_to_f32(static_cast<const uint16_t *>(base)[from + i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = y[i] + v[i];
+    };
+    auto put = [&](void *base, bool f32) {
+        if (wide) {
+            if (f32) {
+                Pack<float, 8> q;
+                set_pairs(q, y);
+                q.store(static_cast<float *>(base) + to);
+            } else {
+                Pack<uint16_t, 8> q;
+                set_pairs(q, y);
+                q.store(static_cast<uint16_t *>(base) + to);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float lo, hi;
+            f2_get(y[i / 2], lo, hi);
+            const float f = i & 1 ? hi : lo;
+            if (i >= left) continue;
+            if (f32) static_cast<float *>(base)[to + i] = f;
+            else static_cast<__nv_bfloat16 *>(base)[to + i] = __float2bfloat16_rn(f);
         }
     };
-    if (p.pre) put(p.pre, false);
-    F2 z[(W + 1) / 2];
-#pragma unroll
-    for (int j = 0; j < W; j += 2) z[j / 2] = f2(y[j], W > 1 ? y[(j + 1) % W] : 0.f);
-    apply_fn(p.fn, z);
-#pragma unroll
-    for (int j = 0; j < W; j += 2) {
-        float other;
-        f2_get(z[j / 2], y[j], W > 1 ? y[(j + 1) % W] : other);
-    }
-    if (p.res) {
-        float v[W];
-        if constexpr (W == 8) {
-            if (p.res_f32) {
-                Pack<float, 8> q;
-                q.load(static_cast<const float *>(p.res) + at);
-                q.get(v);
-            } else {
-                Pack<uint16_t, 8> q;
-                q.load(static_cast<const uint16_t *>(p.res) + at);
-                q.get(v);
-            }
-        } else {
-            v[0] = p.res_f32 ? static_cast<const float *>(p.res)[at] : bf16_bits_to_f32(static_cast<const uint16_t *>(p.res)[at]);
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) y[j] += v[j];
-    }
-    put(p.out, p.out_f32);
+    if (j.bias) add(j.bias, j.bias_f32, n);
+    if (j.pre) put(j.pre, false);
+    apply_fn(j.fn, y);
+    if (j.res) add(j.res, j.res_f32, to);
+    put(j.out, j.out_f32);
 }
 
 // ---- the choice of tiles and parts -----------------------------------------------------------
@@ -512,39 +531,121 @@ struct Tile {
 constexpr Tile TILES[4] = {
     {256, 256, 2, 32768, 295}, {256, 128, 2, 24576, 175}, {128, 128, 1, 32768, 213}, {128, 64, 1, 24576, 190}};
 
+// What a product's sizes and epilogue say of its time.
+struct Size {
+    int64_t M, N, K;
+    int extra;  // residual and pre: 0 to 2
+};
+// The tile, and how many tiles of each product are split into how many parts (the last
+// ones; none: ks = 1).
 struct Plan {
-    int tile, KS;
+    int tile = 0;
+    int64_t split[2] = {0, 0};
+    int ks[2] = {1, 1};
 };
 
-// The tile and the number of parts of the reduction with the least time by this model: whole
-// waves of items, a chunk's time or that of its bytes at the 14 TB/s that all SMs' copies
-// together get out of L2, and for parts the second kernel and its traffic.  Measured, us:
+// The least time by a model of one or two products in one launch, the longer reduction
+// first: whole tiles in turns of the GPU's slots; a chunk's time, or that of its bytes at
+// the 14 TB/s that all SMs' copies together get out of L2; an epilogue that shows where
+// the reduction is short, and at the end; parts for what is left after whole turns (or for
+// all where that is less than a turn), or for the longer product where its tiles are few,
+// with the second kernel and its traffic.  Measured, us:
 //                          256x256  256x128  128x128  128x64   256x128, 2 parts   128x128, 2 / 3 / 4 parts
-//   512 rows 7168 -> 3584    39.1     28.1     34.2     54.2        -                 -
-//   200 rows 7168 -> 3584    38.5     24.7     28.8     29.8       20.5              23.2
-//   128 rows 7168 -> 3584    38.5     24.6     28.9     26.5       23.1              20.1 / 18.1 / 18.0
-//   600 rows 7168 -> 1024    38.4     24.4     28.4     26.8       19.5              20.4 / 18.8 / -
-//   331 rows 1056 -> 1000    14.1      9.6      9.9      9.2        8.2               8.4 / 8.2 / 8.7
-//   300 rows  512 -> 512     10.5      6.9      7.1      5.9        7.2               7.2
-//   1000 rows 1024 -> 2048   13.0      9.2      9.9     12.0        -                 -
-Plan plan(int64_t M, int64_t N, int64_t K)
+//   512 rows 7168 -> 3584    38.3     27.9     33.8     53.5        -                 -
+//   200 rows 7168 -> 3584    37.6     24.3     28.3     29.9       20.4              22.9
+//   128 rows 7168 -> 3584    37.6     24.2     28.5     26.2       23.3              19.9 / 17.9 / 18.0
+//   600 rows 7168 -> 1024    37.5     24.1     28.0     26.5       19.3              20.3 / 18.5 / -
+//   331 rows 1056 -> 1000    13.2      9.2      9.5      7.8        8.1               8.2 / 8.2 / 8.6
+//   300 rows  512 -> 512      9.5      6.4      6.6      5.3        7.2               7.2
+//   1000 rows 1024 -> 2048   12.0      8.6      9.4     11.0        -                 -
+Plan plan(const Size *size, int jobs)
 {
-    const int64_t KC = ceil_div(K, 64);
     const int sms = device_sms();
-    Plan best{0, 1};
-    double least = 1e30;
+    const int last = jobs - 1;
+    Plan best;
+    double least = 1e300;
     for (int t = 0; t < 4; ++t) {
         const Tile &T = TILES[t];
-        const int64_t tiles = ceil_div(M, T.M) * ceil_div(N, T.N), slots = sms / T.ctas;
-        for (int ks = 1; ks <= MAX_PARTS; ++ks) {
-            if (ks > 1 && (tiles * ks > slots || KC < 4 * ks)) break;
-            const int64_t items = tiles * ks, busy = items < slots ? items : slots;
-            const double from_l2 = double(busy * T.ctas) * T.bytes / 14000;
-            double ns = double(ceil_div(items, slots) * ceil_div(KC, ks)) * (from_l2 > T.chunk ? from_l2 : T.chunk);
-            if (ks > 1) ns += 1000 + double(ks) * double(M) * double(N) * 8 / 5000;
+        const int64_t slots = sms / T.ctas;
+        const int turns_n = T.N / 64;  // 32 columns at a time, of an epilogue warp
+        int64_t KC[2] = {0, 0}, tiles[2] = {0, 0}, total = 0;
+        double epi[2] = {0, 0}, tail = 0;
+        for (int j = 0; j < jobs; ++j) {
+            KC[j] = ceil_div(size[j].K, 64);
+            tiles[j] = ceil_div(size[j].M, T.M) * ceil_div(size[j].N, T.N);
+            epi[j] = 1500 + turns_n * (450 + 500 * size[j].extra);  // from tile to tile
+            tail = 500 + turns_n * (350 + 400 * size[j].extra);     // the last one's
+            total += tiles[j];
+        }
+        auto chunk = [&](int64_t items) {
+            const double from_l2 = double((items < slots ? items : slots) * T.ctas) * T.bytes / 14000;
+            return from_l2 > T.chunk ? from_l2 : double(T.chunk);
+        };
+        const double c = chunk(total);
+        // n whole tiles of a product, one after another
+        auto whole = [&](int j, double n) {
+            const double main = KC[j] * c;
+            return n <= 0 ? 0. : main > epi[j] ? n * main : main + (n - 1) * epi[j];
+        };
+        auto offer = [&](double ns, const Plan &p) {
             if (ns < least) {
                 least = ns;
-                best = {t, ks};
+                best = p;
+            }
+        };
+        auto traffic = [&](double parts_of_tiles) { return 1000 + parts_of_tiles * T.M * T.N * 8 / 3000; };
+        // when the slots end that have one tile of product 0 more than the others, and the others
+        double more, less;
+        auto turns = [&](int64_t n_last) {
+            const int64_t t0 = jobs > 1 ? tiles[0] : 0, all = t0 + n_last;
+            const int64_t q0 = t0 / slots, q = all / slots;
+            const bool extra = t0 % slots > 0, partial = all % slots > 0;
+            less = whole(0, double(q0)) + whole(last, double(q - q0 + partial));
+            more = extra ? whole(0, double(q0 + 1)) + whole(last, double(q - q0 + partial - 1)) : less;
+            if (more < less) more = less;
+        };
+        turns(tiles[last]);
+        Plan p;
+        p.tile = t;
+        offer(more + tail, p);
+        if (total < slots) {
+            for (int k0 = 2; k0 <= MAX_PARTS && KC[0] >= 4 * k0; ++k0) {
+                const int64_t len = ceil_div(KC[0], k0);
+                int64_t items = 0;
+                double bytes = 0;
+                for (int j = 0; j < jobs; ++j) {
+                    const int64_t k = ceil_div(KC[j], len);
+                    p.ks[j] = int(k > MAX_PARTS ? MAX_PARTS : k);
+                    p.split[j] = p.ks[j] > 1 ? tiles[j] : 0;
+                    items += tiles[j] * p.ks[j];
+                    if (p.ks[j] > 1) bytes += double(p.ks[j]) * double(size[j].M) * double(size[j].N) * 8;
+                }
+                if (items > slots) break;
+                offer(double(len) * chunk(items) + 1000 + bytes / 3000, p);
+            }
+            continue;
+        }
+        if (const int64_t r = total % slots; r > 0 && r <= tiles[last]) {
+            turns(tiles[last] - r);
+            const int64_t room = jobs > 1 ? slots - tiles[0] % slots : 0;  // slots that end early
+            for (int ks = 2; ks <= MAX_PARTS && KC[last] >= 4 * ks; ++ks) {
+                const double n = double(ceil_div(r * ks, slots) * ceil_div(KC[last], ks)) * c;
+                const double end = r * ks <= room ? (less + n < more ? more : less + n) : more + n;
+                p.split[last] = r;
+                p.ks[last] = ks;
+                offer(end + traffic(double(r * ks)), p);
+            }
+        }
+        if (jobs > 1 && tiles[0] < slots) {
+            p = Plan();
+            p.tile = t;
+            p.split[0] = tiles[0];
+            for (int ks = 2; ks <= MAX_PARTS && KC[0] >= 4 * ks; ++ks) {
+                const double len = double(ceil_div(KC[0], ks)) * c, one = KC[1] * c > epi[1] ? KC[1] * c : epi[1];
+                p.ks[0] = ks;
+                offer((double(tiles[0] * ks) * len + double(tiles[1]) * one) / double(slots) + (len > one ? len : one) +
+                          traffic(double(tiles[0] * ks)),
+                      p);
             }
         }
     }
@@ -552,42 +653,106 @@ Plan plan(int64_t M, int64_t N, int64_t K)
 }
 
 // Bytes of the parts.
-size_t part_bytes(int64_t M, int64_t N, int64_t K)
+size_t part_bytes(const Plan &p)
 {
-    const Plan pl = plan(M, N, K);
-    return pl.KS > 1 ? size_t(round_up(pl.KS * M * N * 4, 256)) : 0;
+    const Tile &T = TILES[p.tile];
+    return size_t(p.split[0] * p.ks[0] + p.split[1] * p.ks[1]) * T.M * T.N * 4;
 }
 
-template <bool A_MN, bool B_MN>
-cudaError_t product(const Operand &A, const Operand &B, LArgs g, int64_t K, const WaitArgs &wait, void *parts, cudaStream_t st)
+// An operand: [rows][cols] bf16, rows `stride` elements apart; mn: the reduction runs over its rows.
+struct Operand {
+    const uint16_t *p;
+    int64_t rows, cols, stride;
+    bool mn;
+};
+
+template <int NT, bool PAIR, bool GRAD>
+cudaError_t launch(const Operand (*ops)[2], int jobs, const LArgs &g, cudaStream_t st)
 {
-    const Plan pl = plan(g.M, g.N, K);
-    g.KC = int(ceil_div(K, 64));
-    g.KS = pl.KS;
-    g.vec = vector_bytes(g);
+    using C = LCfg<NT, PAIR>;
+    CUtensorMap maps[2][2];
+    for (int j = 0; j < 2; ++j) {
+        const Operand &A = ops[j < jobs ? j : 0][0], &B = ops[j < jobs ? j : 0][1];
+        if (!make_tensor_map(&maps[j][0], A.p, MapType::BF16, A.cols, A.rows, A.mn ? 64 : 128, A.stride) ||
+            !make_tensor_map(&maps[j][1], B.p, MapType::BF16, B.cols, B.rows, B.mn ? 64 : C::BROWS, B.stride))
+            return cudaErrorInvalidValue;
+    }
+    const size_t smem = 1024 + size_t(C::S) * C::STAGE + (2 * C::S + 2 * C::ACC + 1) * 8 + 8;
+    auto *kern = k_linear_act<NT, PAIR, GRAD>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    const int slots = device_sms() / C::CL;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((g.items < slots ? g.items : slots) * C::CL));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::CL;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, maps[0][0], maps[0][1], maps[1][0], maps[1][1], g);
+    if (e != cudaSuccess || g.items == g.whole) return e;
+    int split = 0;
+    for (int s = 0; s < g.segs; ++s) split += g.seg[s].ks > 1 ? g.seg[s].tiles : 0;
+    return launch_pdl(k_split_sum<C::MT, NT>, dim3(unsigned(split * (C::MT * NT / 8 / 256))), dim3(256), 0, st, g);
+}
+
+// Vectors of 32 or 16 bytes where every row of every tensor starts on one.
+int vector_bytes(const LJob &g)
+{
+    auto fits = [&](const void *p, int bytes, int v) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % v == 0 && int64_t(g.N) * bytes % v == 0);
+    };
+    for (int v : {32, 16})
+        if (fits(g.out, g.out_f32 ? 4 : 2, v) && fits(g.pre, 2, v) && fits(g.res, g.res_f32 ? 4 : 2, v)) return v;
+    return 0;
+}
+
+// One product or two, the longer reduction first; ops[j]: A and B of product j.
+template <bool GRAD>
+cudaError_t products(const Operand (*ops)[2], const Size *size, int jobs, const Plan &pl, LArgs g, const WaitArgs &wait,
+                     void *parts, cudaStream_t st)
+{
+    const Tile &T = TILES[pl.tile];
+    float *part = static_cast<float *>(parts);
+    int64_t tiles[2] = {0, 0}, items = 0;
+    for (int j = 0; j < jobs; ++j) {
+        LJob &b = g.job[j];
+        b.M = size[j].M;
+        b.N = int(size[j].N);
+        b.KC = int(ceil_div(size[j].K, 64));
+        b.NTL = int(ceil_div(size[j].N, T.N));
+        b.a_mn = ops[j][0].mn;
+        b.b_mn = ops[j][1].mn;
+        b.vec = vector_bytes(b);
+        tiles[j] = ceil_div(size[j].M, T.M) * b.NTL;
+    }
+    for (int parted = 0; parted < 2; ++parted) {  // whole tiles first
+        for (int j = 0; j < jobs; ++j) {
+            const int64_t n = parted ? pl.split[j] : tiles[j] - pl.split[j];
+            if (n == 0) continue;
+            const int ks = parted ? pl.ks[j] : 1;
+            g.seg[g.segs++] = {j, int(tiles[j] - n) * parted, int(n), ks, int(items), parted ? part : nullptr};
+            if (parted) part += n * ks * T.M * T.N;
+            items += n * ks;
+        }
+        if (!parted) g.whole = int(items);
+    }
+    if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
+    g.items = int(items);
     g.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
     g.stall = wait.stall_first_fill;
-    LArgs h = g;
-    if (pl.KS > 1) {
-        h.bias = h.res = nullptr;
-        h.pre = nullptr;
-        h.fn = LMOE_FN_NONE;
-        h.out = parts;
-        h.out_f32 = 1;
-        h.vec = vector_bytes(h);
-    }
-    cudaError_t e;
     switch (pl.tile) {
-    case 0: e = launch<256, true, A_MN, B_MN>(A, B, h, st); break;
-    case 1: e = launch<128, true, A_MN, B_MN>(A, B, h, st); break;
-    case 2: e = launch<128, false, A_MN, B_MN>(A, B, h, st); break;
-    default: e = launch<64, false, A_MN, B_MN>(A, B, h, st); break;
+    case 0: return launch<256, true, GRAD>(ops, jobs, g, st);
+    case 1: return launch<128, true, GRAD>(ops, jobs, g, st);
+    case 2: return launch<128, false, GRAD>(ops, jobs, g, st);
+    default: return launch<64, false, GRAD>(ops, jobs, g, st);
     }
-    if (e != cudaSuccess || pl.KS == 1) return e;
-    const bool wide = g.vec && g.N % 8 == 0;
-    const dim3 grid(unsigned(ceil_div(g.M * ceil_div(g.N, wide ? 8 : 1), 256)));
-    const float *part = static_cast<const float *>(parts);
-    return wide ? launch_pdl(k_split_sum<8>, grid, dim3(256), 0, st, part, g) : launch_pdl(k_split_sum<1>, grid, dim3(256), 0, st, part, g);
 }
 
 // ---- dz and its column sums ----------------------------------------------------------------
@@ -611,16 +776,17 @@ __global__ void __launch_bounds__(256, 4) k_act_back(const DzArgs p)
     const int c = (int(blockIdx.x) * 32 + lane) * 8;
     float sum[8] = {};
     pdl_enter();
+    constexpr int B = FN == LMOE_FN_NONE && !F32 ? 8 : 4;
     const int64_t step = int64_t(gridDim.y) * 8;
     if (c < p.Np)
-        for (int64_t t0 = int64_t(blockIdx.y) * 8 + warp; t0 < p.rows; t0 += 4 * step) {
-            // four rows' loads at once: one row at a time left the loads' latency open (4096 x 7168,
-            // silu, sums alone: 36 us)
-            Pack<float, 8> df[F32 && VEC ? 4 : 1];
-            Pack<uint16_t, 8> dh[!F32 && VEC ? 4 : 1], zh[FN != LMOE_FN_NONE && VEC ? 4 : 1];
+        for (int64_t t0 = int64_t(blockIdx.y) * 8 + warp; t0 < p.rows; t0 += B * step) {
+            // several rows' loads at once: one row at a time left the loads' latency open (4096 x 7168,
+            // silu, dz and sums: 36 against 26 us)
+            Pack<float, 8> df[F32 && VEC ? B : 1];
+            Pack<uint16_t, 8> dh[!F32 && VEC ? B : 1], zh[FN != LMOE_FN_NONE && VEC ? B : 1];
             if constexpr (VEC) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < B; ++i) {
                     const int64_t at = min(t0 + i * step, p.rows - 1) * p.N + c;
                     if constexpr (F32) df[i].load(static_cast<const float *>(p.dout) + at);
                     else dh[i].load(static_cast<const uint16_t *>(p.dout) + at);
@@ -628,7 +794,7 @@ __global__ void __launch_bounds__(256, 4) k_act_back(const DzArgs p)
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < B; ++i) {
                 const int64_t t = t0 + i * step, at = t * p.N + c;
                 if (t >= p.rows) break;
                 float d[8], z[8] = {};
@@ -695,33 +861,70 @@ cudaError_t dz_fn(const DzArgs &g, int fn, dim3 grid, cudaStream_t st)
 // it took 23.4 and 21.1 us (3584 -> 7168, 7168 -> 3584) against 18.0 and 18.0 here.
 constexpr int64_t FEW = 64;
 
-size_t linear_act_scratch_bytes(int64_t rows, int K, int N) { return rows <= FEW ? 0 : part_bytes(rows, N, K); }
+// The plan may differ with what the epilogue reads and writes: room for any.
+size_t linear_act_scratch_bytes(int64_t rows, int K, int N)
+{
+    size_t most = 0;
+    if (rows > FEW)
+        for (int extra = 0; extra <= 2; ++extra) {
+            const Size size{rows, N, K, extra};
+            const size_t n = part_bytes(plan(&size, 1));
+            most = n > most ? n : most;
+        }
+    return most;
+}
 
 cudaError_t launch_linear_act(const LinearActArgs &a, void *scratch, cudaStream_t st)
 {
-    if (a.rows <= FEW) return launch_linear_few(a, st);
+    if (a.rows <= FEW) {
+        FewArgs f{};
+        f.x = a.x;
+        f.x_stride = a.K;
+        f.rows = a.rows;
+        f.W = a.W;
+        f.K = a.K;
+        f.N = a.N;
+        f.bias = a.bias;
+        f.res = a.res;
+        f.bias_fmt = a.bias_fmt;
+        f.res_fmt = a.res_fmt;
+        f.out_fmt = a.out_fmt;
+        f.fn = a.fn;
+        f.out = a.out;
+        f.pre = a.pre;
+        f.status = a.status;
+        f.wait = a.wait;
+        return launch_linear_few(f, st);
+    }
     LArgs g{};
-    g.M = a.rows;
-    g.N = a.N;
-    g.bias = a.bias;
-    g.bias_f32 = a.bias_fmt == LMOE_F32;
-    g.res = a.res;
-    g.res_f32 = a.res_fmt == LMOE_F32;
-    g.out_f32 = a.out_fmt == LMOE_F32;
-    g.fn = a.fn;
-    g.out = a.out;
-    g.pre = a.pre;
+    LJob &j = g.job[0];
+    j.bias = a.bias;
+    j.bias_f32 = a.bias_fmt == LMOE_F32;
+    j.res = a.res;
+    j.res_f32 = a.res_fmt == LMOE_F32;
+    j.out_f32 = a.out_fmt == LMOE_F32;
+    j.fn = a.fn;
+    j.out = a.out;
+    j.pre = a.pre;
     g.status = a.status;
-    return product<false, false>({a.x, a.rows, a.K, a.K}, {a.W, a.N, a.K, a.K}, g, a.K, a.wait, scratch, st);
+    const Size size{a.rows, a.N, a.K, (a.res != nullptr) + (a.pre != nullptr)};
+    const Operand ops[1][2] = {{{a.x, a.rows, a.K, a.K, false}, {a.W, a.N, a.K, a.K, false}}};
+    return products<false>(ops, &size, 1, plan(&size, 1), g, a.wait, scratch, st);
 }
 
-// dz [rows][Np] bf16 | column sums | parts of a product's reduction
+// dz [rows][Np] bf16 | column sums | parts of the products' reductions
 size_t linear_act_back_scratch_bytes(int64_t rows, int K, int N)
 {
     if (rows == 0) return 0;
     const int64_t Np = round_up(N, 8);
-    const size_t dx = part_bytes(rows, K, N), dW = part_bytes(N, K, rows);
-    return size_t(round_up(rows * Np * 2, 256)) + size_t(round_up(dz_splits(rows, N) * N * 4, 256)) + (dx > dW ? dx : dW);
+    const Size dx{rows, K, N, 0}, dW{N, K, rows, 0}, both[2] = {N >= rows ? dx : dW, N >= rows ? dW : dx};
+    size_t most = rows > FEW ? part_bytes(plan(both, 2)) : 0;
+    for (const Size *one : {&dx, &dW}) {
+        if (one == &dx && rows <= FEW) continue;
+        const size_t n = part_bytes(plan(one, 1));
+        most = n > most ? n : most;
+    }
+    return size_t(round_up(rows * Np * 2, 256)) + size_t(round_up(dz_splits(rows, N) * N * 4, 256)) + most;
 }
 
 cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cudaStream_t st)
@@ -748,24 +951,52 @@ cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cu
         if (e == cudaSuccess && a.dbias) e = launch_col_sums(part, grid.y, a.N, 1, a.dbias, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    const Operand d{as_is ? static_cast<const uint16_t *>(a.dout) : dz, a.rows, a.N, Np};
+    // both products in one launch, the longer reduction first
+    const Operand d{as_is ? static_cast<const uint16_t *>(a.dout) : dz, a.rows, a.N, Np, false};
+    Operand ops[2][2];
+    Size size[2];
     LArgs g{};
     g.status = a.status;
-    if (a.dx) {
-        g.M = a.rows;
-        g.N = a.K;
-        g.out = a.dx;
-        e = product<false, true>(d, {a.W, a.N, a.K, a.K}, g, a.N, a.wait, parts, st);
+    int jobs = 0;
+    auto dx = [&] {
+        if (!a.dx) return;
+        g.job[jobs].out = a.dx;
+        size[jobs] = {a.rows, a.K, a.N, 0};
+        ops[jobs][0] = d;
+        ops[jobs++][1] = {a.W, a.N, a.K, a.K, true};
+    };
+    auto dW = [&] {
+        if (!a.dW) return;
+        g.job[jobs].out = a.dW;
+        g.job[jobs].out_f32 = a.dW_fmt == LMOE_F32;
+        size[jobs] = {a.N, a.K, a.rows, 0};
+        ops[jobs][0] = d;
+        ops[jobs][0].mn = true;
+        ops[jobs++][1] = {a.x, a.rows, a.K, a.K, true};
+    };
+    if (a.dx && a.rows <= FEW) {  // the weights' stream is the bound
+        FewArgs f{};
+        f.x = d.p;
+        f.x_stride = Np;
+        f.rows = a.rows;
+        f.W = a.W;
+        f.across = true;
+        f.K = a.N;
+        f.N = a.K;
+        f.out = a.dx;
+        f.status = a.status;
+        f.wait = a.wait;
+        e = launch_linear_few(f, st);
         if (e != cudaSuccess) return e;
+        dW();
+    } else if (a.N >= a.rows) {
+        dx();
+        dW();
+    } else {
+        dW();
+        dx();
     }
-    if (a.dW) {
-        g.M = a.N;
-        g.N = a.K;
-        g.out = a.dW;
-        g.out_f32 = a.dW_fmt == LMOE_F32;
-        e = product<true, true>(d, {a.x, a.rows, a.K, a.K}, g, a.rows, a.wait, parts, st);
-    }
-    return e;
+    return jobs ? products<true>(ops, size, jobs, plan(size, jobs), g, a.wait, parts, st) : e;
 }
 
 }  // namespace lmoe

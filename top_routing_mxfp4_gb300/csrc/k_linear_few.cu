@@ -1,9 +1,12 @@
 // Linear layer with bias, function and residual for few rows (decode batches):
 //   z = x W^T + bias,  out = fn(z) + res,  pre = bf16(z)
+// and the gradient by x of few rows, dx = dz W (`across`: the reduction runs over the
+// weights' rows).
 //
-// The weight stream bounds it, so the weights are the M = 128 operand (A) and the
-// rows the N operand (B, 16 to 64 of them, so that one token costs no 128 rows of
-// copies), both K-major, 64 columns a chunk.  An output tile's K is shared by a
+// The weight stream bounds it, so the weights are the M = 128 operand (A, K-major or,
+// across, MN-major: two blocks of 64 elements) and the rows the N operand (B, K-major, 16
+// to 64 of them, so that one token costs no 128 rows of copies), 64 of the reduction a
+// chunk.  An output tile's K is shared by a
 // cluster of KS CTAs, so that few tiles stream with the whole GPU; the ranks' sums
 // are added in rank order (cluster_sum.cuh), each rank finishing a share of the rows.
 //
@@ -41,6 +44,7 @@ struct FArgs {
     const void *bias, *res;
     int bias_f32, res_f32, out_f32, fn;
     int rows, N, KC, KS;
+    int across;
     void *out;
     uint16_t *pre;
     int32_t *status;
@@ -91,7 +95,14 @@ __global__ void __launch_bounds__(192, FCfg<NT>::PER_SM)
     // as many took longer than none.
     if (warp == 0) {
         if (elect_one())
-            for (int kc = k0; kc < min(k1, k0 + S); ++kc) tma_prefetch_2d(&tmA, kc * 64, m0);
+            for (int kc = k0; kc < min(k1, k0 + S); ++kc) {
+                if (p.across) {
+                    tma_prefetch_2d(&tmA, m0, kc * 64);
+                    tma_prefetch_2d(&tmA, m0 + 64, kc * 64);
+                } else {
+                    tma_prefetch_2d(&tmA, kc * 64, m0);
+                }
+            }
         __syncwarp();
     }
     pdl_enter();
@@ -111,7 +122,12 @@ __global__ void __launch_bounds__(192, FCfg<NT>::PER_SM)
             if (elect_one() && !(p.stall && kc == k0)) {
                 uint8_t *sb = stages + stage * C::STAGE;
                 mbar_arrive_expect_tx(&full[stage], C::STAGE);
-                tma_load_2d_hint(sb, &tmA, kc * 64, m0, &full[stage], once);
+                if (p.across) {
+                    tma_load_2d_hint(sb, &tmA, m0, kc * 64, &full[stage], once);
+                    tma_load_2d_hint(sb + 8192, &tmA, m0 + 64, kc * 64, &full[stage], once);
+                } else {
+                    tma_load_2d_hint(sb, &tmA, kc * 64, m0, &full[stage], once);
+                }
                 tma_load_2d_hint(sb + A_TILE, &tmB, kc * 64, 0, &full[stage], keep);
             }
             __syncwarp();
@@ -128,17 +144,18 @@ __global__ void __launch_bounds__(192, FCfg<NT>::PER_SM)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        const uint32_t id = idesc_bf16(uint32_t((cols + 15) & ~15));
+        const uint32_t id = idesc_bf16(uint32_t((cols + 15) & ~15)) | (p.across ? IDESC_A_MN : 0);
+        const uint32_t base = smem_u32(stages), a_step = p.across ? 128 : 2;
+        const uint64_t ad0 = p.across ? sdesc_mn128(base, 8192) : sdesc_k128(base), bd0 = sdesc_k128(base + A_TILE);
         for (int kc = k0; kc < k1; ++kc) {
             ok = mbar_wait_warp(&full[stage], phase, p.limit);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t sa = smem_u32(stages + stage * C::STAGE);
-                const uint64_t ad = sdesc_k128(sa), bd = sdesc_k128(sa + A_TILE);
+                const uint64_t ad = ad0 + uint32_t(stage) * (C::STAGE >> 4), bd = bd0 + uint32_t(stage) * (C::STAGE >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)  // 4 x K = 16 per 128-byte row
-                    mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)  // 4 x K = 16
+                    mma_bf16(tmem, ad + a_step * kk, bd + 2 * kk, id, (kc > k0 || kk > 0) ? 1u : 0u);
                 tc_commit(&empty[stage]);
             }
             __syncwarp();
@@ -241,11 +258,12 @@ __global__ void __launch_bounds__(192, FCfg<NT>::PER_SM)
 }
 
 template <int NT>
-cudaError_t launch(const LinearActArgs &a, FArgs g, cudaStream_t st)
+cudaError_t launch(const FewArgs &a, FArgs g, cudaStream_t st)
 {
     using C = FCfg<NT>;
     CUtensorMap ma, mb;
-    if (!make_tensor_map(&ma, a.W, MapType::BF16, a.K, a.N, 128) || !make_tensor_map(&mb, a.x, MapType::BF16, a.K, a.rows, NT))
+    if (!(a.across ? make_tensor_map(&ma, a.W, MapType::BF16, a.N, a.K, 64) : make_tensor_map(&ma, a.W, MapType::BF16, a.K, a.N, 128)) ||
+        !make_tensor_map(&mb, a.x, MapType::BF16, a.K, a.rows, NT, a.x_stride))
         return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(a.N, 128);
     // K is shared so that the CTAs fill the GPU's slots, two an SM, once, each with four
@@ -276,7 +294,7 @@ cudaError_t launch(const LinearActArgs &a, FArgs g, cudaStream_t st)
 
 }  // namespace
 
-cudaError_t launch_linear_few(const LinearActArgs &a, cudaStream_t st)
+cudaError_t launch_linear_few(const FewArgs &a, cudaStream_t st)
 {
     FArgs g{};
     g.bias = a.bias;
@@ -288,6 +306,7 @@ cudaError_t launch_linear_few(const LinearActArgs &a, cudaStream_t st)
     g.rows = int(a.rows);
     g.N = a.N;
     g.KC = int(ceil_div(a.K, 64));
+    g.across = a.across;
     g.out = a.out;
     g.pre = a.pre;
     g.status = a.status;

@@ -450,8 +450,22 @@ struct LinearActArgs {
 };
 size_t linear_act_scratch_bytes(int64_t rows, int K, int N);
 cudaError_t launch_linear_act(const LinearActArgs &a, void *scratch, cudaStream_t st);
-// the same for few rows (k_linear_few.cu)
-cudaError_t launch_linear_few(const LinearActArgs &a, cudaStream_t st);
+// At most 64 rows (k_linear_few.cu): x [rows][K], its rows x_stride elements apart, times W [N][K] transposed or,
+// across, W [K][N].
+struct FewArgs {
+    const uint16_t *x;
+    int64_t x_stride, rows;
+    const uint16_t *W;
+    bool across;
+    int K, N;
+    const void *bias, *res;
+    int bias_fmt, res_fmt, fn, out_fmt;
+    void *out;
+    uint16_t *pre;
+    int32_t *status;
+    WaitArgs wait;
+};
+cudaError_t launch_linear_few(const FewArgs &a, cudaStream_t st);
 struct LinearActBackArgs {
     const void *dout;
     int dout_fmt;
