@@ -10,7 +10,7 @@
 //
 // Persistent CTAs: warp 0 copies (TMA), warp 1 issues the MMAs, the others are the
 // epilogue (TMEM lane quarter = warp % 4), which adds bias, applies the function,
-// adds the residual and stores, a row a lane, while the next tile's MMAs run in the
+// adds the residual and hands the outputs to TMA, while the next tile's MMAs run in the
 // other accumulator.  Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -38,7 +38,8 @@ struct LCfg {
     static constexpr int BROWS = NT / CL;
     static constexpr uint32_t B_TILE = BROWS * 128;
     static constexpr uint32_t STAGE = A_TILE + B_TILE;
-    static constexpr int S_RAW = int(200 * 1024 / STAGE);
+    static constexpr uint32_t BUF = 4096, BUFS = EW * BUF;  // a chunk of 32 x 32 fp32, or two of bf16, an epilogue warp
+    static constexpr int S_RAW = int((225 * 1024 - BUFS) / STAGE);
     static constexpr int S = S_RAW > 8 ? 8 : S_RAW;
     static constexpr int ACC = 2;  // accumulators: a tile's epilogue overlaps the next one's MMAs
     static constexpr uint32_t TMEM_COLS = ACC * NT;
@@ -52,7 +53,6 @@ struct LJob {
     // epilogue
     const void *bias, *res;
     int bias_f32, res_f32, out_f32, fn;
-    int vec;  // outputs' and residual's rows take vectors of this many bytes (32, 16) or single elements (0)
     void *out;
     uint16_t *pre;
 };
@@ -76,53 +76,19 @@ struct LArgs {
 
 // ---- rows of outputs ---------------------------------------------------------------------
 
-// 32 consecutive elements of a row, fp32 or bf16, as 32-bit words.
+// A chunk of 32 x 32 elements in shared memory: row r's 16-byte pieces, swizzled as the
+// tensor maps of outputs have it, so that lanes that each write or read their own row, and
+// lanes that hold pieces of one row, meet no bank conflicts.
 template <bool F32>
-constexpr int WORDS = F32 ? 32 : 16;
-
-template <bool F32>
-__device__ __forceinline__ void row_load(uint32_t (&u)[32], const void *base, int64_t at, int n, int vec)
+__device__ __forceinline__ uint4 *piece(uint8_t *buf, int r, int i)
 {
-    const char *p = static_cast<const char *>(base) + at * (F32 ? 4 : 2);
-    if (n == 32 && vec == 32) {
-#pragma unroll
-        for (int i = 0; i < WORDS<F32>; i += 8)
-            asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                         : "=r"(u[i]), "=r"(u[i + 1]), "=r"(u[i + 2]), "=r"(u[i + 3]), "=r"(u[i + 4]), "=r"(u[i + 5]),
-                           "=r"(u[i + 6]), "=r"(u[i + 7])
-                         : "l"(p + 4 * i)
-                         : "memory");
-    } else if (n == 32 && vec == 16) {
-#pragma unroll
-        for (int i = 0; i < WORDS<F32>; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
-            u[i] = v.x, u[i + 1] = v.y, u[i + 2] = v.z, u[i + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < WORDS<F32>; ++i) {
-            if (F32) {
-                u[i] = i < n ? reinterpret_cast<const uint32_t *>(p)[i] : 0u;
-            } else {
-                const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-                u[i] = (2 * i < n ? uint32_t(h[2 * i]) : 0u) | (2 * i + 1 < n ? uint32_t(h[2 * i + 1]) << 16 : 0u);
-            }
-        }
-    }
+    return reinterpret_cast<uint4 *>(buf) + (F32 ? r * 8 + (i ^ (r & 7)) : r * 4 + (i ^ ((r >> 1) & 3)));
 }
+// The lane's row into the chunk, rounded to nearest even.
 template <bool F32>
-__device__ __forceinline__ void row_add(const uint32_t (&u)[32], F2 (&y)[16])
+__device__ __forceinline__ void put_row(uint8_t *buf, int lane, const F2 (&y)[16])
 {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        y[i] = y[i] + (F32 ? f2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]))
-                           : f2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)));
-}
-// Rounded to nearest even.
-template <bool F32>
-__device__ __forceinline__ void row_store(const F2 (&y)[16], void *base, int64_t at, int n, int vec)
-{
-    uint32_t u[WORDS<F32>];
+    uint32_t u[F32 ? 32 : 16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         float lo, hi;
@@ -135,28 +101,65 @@ __device__ __forceinline__ void row_store(const F2 (&y)[16], void *base, int64_t
             u[i] = *reinterpret_cast<const uint32_t *>(&b);
         }
     }
-    char *p = static_cast<char *>(base) + at * (F32 ? 4 : 2);
-    if (n == 32 && vec == 32) {
 #pragma unroll
-        for (int i = 0; i < WORDS<F32>; i += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + 4 * i), "r"(u[i]), "r"(u[i + 1]),
-                         "r"(u[i + 2]), "r"(u[i + 3]), "r"(u[i + 4]), "r"(u[i + 5]), "r"(u[i + 6]), "r"(u[i + 7])
-                         : "memory");
-    } else if (n == 32 && vec == 16) {
+    for (int i = 0; i < (F32 ? 8 : 4); ++i)
+        *piece<F32>(buf, lane, i) = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+}
+// The lane's row of the chunk added.
+template <bool F32>
+__device__ __forceinline__ void add_row(uint8_t *buf, int lane, F2 (&y)[16])
+{
 #pragma unroll
-        for (int i = 0; i < WORDS<F32>; i += 4)
-            *reinterpret_cast<uint4 *>(p + 4 * i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
-    } else {
+    for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+        const uint4 q = *piece<F32>(buf, lane, i);
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        if constexpr (F32) {
+            y[2 * i] = y[2 * i] + f2(__uint_as_float(u[0]), __uint_as_float(u[1]));
+            y[2 * i + 1] = y[2 * i + 1] + f2(__uint_as_float(u[2]), __uint_as_float(u[3]));
+        } else {
 #pragma unroll
-        for (int i = 0; i < WORDS<F32>; ++i) {
-            if (F32) {
-                if (i < n) reinterpret_cast<uint32_t *>(p)[i] = u[i];
-            } else {
-                uint16_t *h = reinterpret_cast<uint16_t *>(p);
-                if (2 * i < n) h[2 * i] = uint16_t(u[i]);
-                if (2 * i + 1 < n) h[2 * i + 1] = uint16_t(u[i] >> 16);
-            }
+            for (int j = 0; j < 4; ++j)
+                y[4 * i + j] = y[4 * i + j] + f2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xFFFF0000u));
         }
+    }
+}
+// A chunk of a matrix, a few rows' pieces an access, in registers; and from there into the
+// buffer.  rows, cols: how many of the 32 there are.
+template <bool F32>
+__device__ __forceinline__ void load_chunk(uint4 (&r)[8], const void *at, int64_t N, int lane, int rows, int cols)
+{
+    constexpr int L = F32 ? 8 : 4, E = F32 ? 4 : 8;  // lanes a row, elements a piece
+    const int row = lane / L, col = lane % L * E;
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+        if (row + i * (32 / L) < rows && col < cols)
+            r[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(at) +
+                                                    ((row + i * (32 / L)) * N + col) * (F32 ? 4 : 2));
+}
+template <bool F32>
+__device__ __forceinline__ void put_chunk(uint8_t *buf, const uint4 (&r)[8], int lane)
+{
+    constexpr int L = F32 ? 8 : 4;
+#pragma unroll
+    for (int i = 0; i < L; ++i) *piece<F32>(buf, lane / L + i * (32 / L), lane % L) = r[i];
+}
+
+// The chunk (fp32) stored a column a lane, n rows of it, N elements apart; with the residual
+// added.
+__device__ __forceinline__ float read1(const float *p) { return *p; }
+__device__ __forceinline__ float read1(const uint16_t *p) { return bf16_bits_to_f32(*p); }
+template <bool F32, typename Out, typename Res = float>
+__device__ __forceinline__ void put_columns(uint8_t *buf, int lane, int n, int64_t N, Out *out, const Res *res = nullptr)
+{
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = res && i < n ? read1(res + i * N) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        v[i] += reinterpret_cast<const float *>(piece<true>(buf, i, lane >> 2))[lane & 3];
+        if (i >= n) continue;
+        if constexpr (F32) out[i * N] = v[i];
+        else reinterpret_cast<__nv_bfloat16 *>(out)[i * N] = __float2bfloat16_rn(v[i]);
     }
 }
 
@@ -164,18 +167,22 @@ __device__ __forceinline__ void row_store(const F2 (&y)[16], void *base, int64_t
 
 // GRAD: one or two products whose operands may run either way; else one of K-major operands
 // (the choice between operands' orders cost 27.9 -> 29.6 us at 512 rows 7168 -> 3584).
-template <int NT, bool PAIR, bool GRAD>
+// COPIED: all rows of outputs and residual start on 16 bytes, so whole pieces are copied; else
+// single elements (a gradient's rows always do: K % 8 == 0).
+template <int NT, bool PAIR, bool GRAD, bool COPIED>
 __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
     k_linear_act(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                  const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
-                 const __grid_constant__ LArgs p)
+                 const __grid_constant__ CUtensorMap tmOut0, const __grid_constant__ CUtensorMap tmOut1,
+                 const __grid_constant__ CUtensorMap tmPre, const __grid_constant__ LArgs p)
 {
     using C = LCfg<NT, PAIR>;
     constexpr int S = C::S;
     static_assert(C::BROWS % 64 == 0, "blocks of 64 elements");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(stages + S * C::STAGE);
+    uint8_t *bufs = stages + S * C::STAGE;
+    uint64_t *full = reinterpret_cast<uint64_t *>(bufs + C::BUFS);
     uint64_t *empty = full + S;
     uint64_t *acc_full = empty + S;
     uint64_t *acc_empty = acc_full + C::ACC;
@@ -340,32 +347,36 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
         }
     } else if (warp >= 2) {
         // ---------------- epilogue ----------------
+        // 32 rows x 32 columns at a time.  Outputs go through shared memory and are copied from there
+        // by TMA, the residual comes the other way round in whole pieces of rows: stored from the
+        // lanes' registers, a row a lane, every 16 or 32 bytes were a request to L2 of their own
+        // (6000 rows 128 -> 3000, fp32 residual and output, pre: 57 us, 10.5 million requests).
         __shared__ __align__(16) float s_bias[C::EW][32];
         const int q = warp & 3, half = (warp - 2) >> 2;
+        uint8_t *buf = bufs + (warp - 2) * C::BUF, *pre_buf = buf + C::BUF / 2;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int it = begin; it < p.items; it = next(it)) {
             const Item w = item(it);
             const LJob &j = p.job[GRAD ? w.job : 0];
-            const int64_t m = w.m + rank * 128 + 32 * q + lane;
-            const int n0 = w.n, limit = min(NT, j.N - n0);
-            const bool mine = m < j.M;
-            const int64_t row = m * j.N + n0;
+            const int64_t m = w.m + rank * 128 + 32 * q;  // the warp's first row
+            const int n0 = w.n, limit = min(NT, j.N - n0), rows = int(min(int64_t(32), j.M - m));
             const uint32_t tb = tmem + (uint32_t(32 * q) << 16) + uint32_t(acc * NT);
             // what 32 columns need from memory, on its way a turn ahead: the residual, a column's bias a lane
-            uint32_t r[32];
+            uint4 r[8];
             float bias = 0.f;
             auto fetch = [&](int c) {
-                if (c >= limit) return;
-                if (j.res && mine) {
-                    if (j.res_f32) row_load<true>(r, j.res, row + c, min(32, limit - c), j.vec);
-                    else row_load<false>(r, j.res, row + c, min(32, limit - c), j.vec);
+                if (c >= limit || w.part) return;
+                if (COPIED && j.res) {
+                    const int64_t at = m * j.N + n0 + c;
+                    if (j.res_f32) load_chunk<true>(r, static_cast<const float *>(j.res) + at, j.N, lane, rows, limit - c);
+                    else load_chunk<false>(r, static_cast<const uint16_t *>(j.res) + at, j.N, lane, rows, limit - c);
                 }
                 if (j.bias && c + lane < limit)
                     bias = j.bias_f32 ? __ldg(static_cast<const float *>(j.bias) + n0 + c + lane)
                                       : bf16_bits_to_f32(__ldg(static_cast<const uint16_t *>(j.bias) + n0 + c + lane));
             };
-            if (!w.part) fetch(32 * half);
+            fetch(32 * half);
             if (!mbar_wait_warp(&acc_full[acc], acc_phase, p.limit)) {
                 if (lane == 0) set_status(p.status, LMOE_ERR_TIMEOUT);
                 break;
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
                     uint32_t v[32];
                     tmem_ld_cols<32>(tb + c, v);
                     tmem_ld_wait();
-                    if (mine)
+                    if (lane < rows)
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(sums + c + i), "r"(v[i]),
@@ -390,12 +401,10 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
             for (int c = 32 * half; c < limit && !w.part; c += 8 * C::EW) {
                 uint32_t v[32];
                 tmem_ld_cols<32>(tb + c, v);
-                const int cols = min(32, limit - c);
                 F2 y[16];
-                if (j.bias) {
-                    s_bias[warp - 2][lane] = bias;
-                    __syncwarp();
-                }
+                if (j.bias) s_bias[warp - 2][lane] = bias;
+                if (COPIED && elect_one()) bulk_wait_read<0>();  // the copies of the chunk before have read the buffers
+                __syncwarp();
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) y[i] = f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
@@ -408,16 +417,70 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
                     }
                     __syncwarp();
                 }
-                if (j.pre && mine) row_store<false>(y, j.pre, row + c, cols, j.vec);
-                apply_fn(j.fn, y);
-                if (j.res) {
-                    if (j.res_f32) row_add<true>(r, y);
-                    else row_add<false>(r, y);
-                }
-                fetch(c + 8 * C::EW);
-                if (mine) {
-                    if (j.out_f32) row_store<true>(y, j.out, row + c, cols, j.vec);
-                    else row_store<false>(y, j.out, row + c, cols, j.vec);
+                if constexpr (!COPIED) {
+                    // Rows that start anywhere: turned round, so that a lane has a column and an access is a
+                    // piece of one row.
+                    const int n_rows = c + lane < limit ? rows : 0;
+                    const int64_t at = m * j.N + n0 + c + lane;
+                    if (j.pre) {
+                        put_row<true>(buf, lane, y);
+                        __syncwarp();
+                        put_columns<false>(buf, lane, n_rows, j.N, j.pre + at);
+                        __syncwarp();
+                    }
+                    apply_fn(j.fn, y);
+                    put_row<true>(buf, lane, y);
+                    __syncwarp();
+                    if (j.out_f32) {
+                        float *o = static_cast<float *>(j.out) + at;
+                        if (!j.res) put_columns<true>(buf, lane, n_rows, j.N, o);
+                        else if (j.res_f32) put_columns<true>(buf, lane, n_rows, j.N, o, static_cast<const float *>(j.res) + at);
+                        else put_columns<true>(buf, lane, n_rows, j.N, o, static_cast<const uint16_t *>(j.res) + at);
+                    } else {
+                        uint16_t *o = static_cast<uint16_t *>(j.out) + at;
+                        if (!j.res) put_columns<false>(buf, lane, n_rows, j.N, o);
+                        else if (j.res_f32) put_columns<false>(buf, lane, n_rows, j.N, o, static_cast<const float *>(j.res) + at);
+                        else put_columns<false>(buf, lane, n_rows, j.N, o, static_cast<const uint16_t *>(j.res) + at);
+                    }
+                    __syncwarp();
+                    fetch(c + 8 * C::EW);
+                } else {
+                    if (j.pre) {
+                        put_row<false>(pre_buf, lane, y);
+                        fence_async_shared();
+                        __syncwarp();
+                        if (rows > 0 && elect_one()) {
+                            tma_store_2d(&tmPre, n0 + c, int(m), pre_buf);
+                            bulk_commit();
+                        }
+                        __syncwarp();
+                    }
+                    apply_fn(j.fn, y);
+                    if (j.pre && (j.out_f32 || (j.res && j.res_f32))) {  // which take pre's half of the buffer too
+                        if (elect_one()) bulk_wait_read<0>();
+                        __syncwarp();
+                    }
+                    if (j.res) {
+                        if (j.res_f32) {
+                            put_chunk<true>(buf, r, lane);
+                            __syncwarp();
+                            add_row<true>(buf, lane, y);
+                        } else {
+                            put_chunk<false>(buf, r, lane);
+                            __syncwarp();
+                            add_row<false>(buf, lane, y);
+                        }
+                        __syncwarp();
+                    }
+                    fetch(c + 8 * C::EW);
+                    if (j.out_f32) put_row<true>(buf, lane, y);
+                    else put_row<false>(buf, lane, y);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (rows > 0 && elect_one()) {
+                        tma_store_2d(GRAD && w.job ? &tmOut1 : &tmOut0, n0 + c, int(m), buf);
+                        bulk_commit();
+                    }
                 }
                 __syncwarp();
             }
@@ -428,6 +491,8 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
                 acc_phase ^= 1;
             }
         }
+        if (elect_one()) bulk_wait_read<0>();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -666,7 +731,7 @@ struct Operand {
     bool mn;
 };
 
-template <int NT, bool PAIR, bool GRAD>
+template <int NT, bool PAIR, bool GRAD, bool COPIED>
 cudaError_t launch(const Operand (*ops)[2], int jobs, const LArgs &g, cudaStream_t st)
 {
     using C = LCfg<NT, PAIR>;
@@ -677,8 +742,17 @@ cudaError_t launch(const Operand (*ops)[2], int jobs, const LArgs &g, cudaStream
             !make_tensor_map(&maps[j][1], B.p, MapType::BF16, B.cols, B.rows, B.mn ? 64 : C::BROWS, B.stride))
             return cudaErrorInvalidValue;
     }
-    const size_t smem = 1024 + size_t(C::S) * C::STAGE + (2 * C::S + 2 * C::ACC + 1) * 8 + 8;
-    auto *kern = k_linear_act<NT, PAIR, GRAD>;
+    CUtensorMap out[2], pre;
+    for (int j = 0; j < 2; ++j) {
+        const LJob &b = g.job[j < jobs ? j : 0];
+        if (!COPIED) out[j] = maps[0][0];  // (not used)
+        else if (!make_store_map(&out[j], b.out, b.out_f32, b.N, b.M)) return cudaErrorInvalidValue;
+    }
+    pre = out[0];
+    if (COPIED && g.job[0].pre && !make_store_map(&pre, g.job[0].pre, false, g.job[0].N, g.job[0].M))
+        return cudaErrorInvalidValue;
+    const size_t smem = 1024 + size_t(C::S) * C::STAGE + C::BUFS + (2 * C::S + 2 * C::ACC + 1) * 8 + 8;
+    auto *kern = k_linear_act<NT, PAIR, GRAD, COPIED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     const int slots = device_sms() / C::CL;
@@ -695,22 +769,29 @@ cudaError_t launch(const Operand (*ops)[2], int jobs, const LArgs &g, cudaStream
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, maps[0][0], maps[0][1], maps[1][0], maps[1][1], g);
+    e = cudaLaunchKernelEx(&cfg, kern, maps[0][0], maps[0][1], maps[1][0], maps[1][1], out[0], out[1], pre, g);
     if (e != cudaSuccess || g.items == g.whole) return e;
     int split = 0;
     for (int s = 0; s < g.segs; ++s) split += g.seg[s].ks > 1 ? g.seg[s].tiles : 0;
     return launch_pdl(k_split_sum<C::MT, NT>, dim3(unsigned(split * (C::MT * NT / 8 / 256))), dim3(256), 0, st, g);
 }
 
-// Vectors of 32 or 16 bytes where every row of every tensor starts on one.
-int vector_bytes(const LJob &g)
+// Whether every row of every tensor starts on 16 bytes.
+bool rows_on_16(const LJob &g)
 {
-    auto fits = [&](const void *p, int bytes, int v) {
-        return !p || (reinterpret_cast<uintptr_t>(p) % v == 0 && int64_t(g.N) * bytes % v == 0);
-    };
-    for (int v : {32, 16})
-        if (fits(g.out, g.out_f32 ? 4 : 2, v) && fits(g.pre, 2, v) && fits(g.res, g.res_f32 ? 4 : 2, v)) return v;
-    return 0;
+    auto fits = [&](const void *p, int bytes) { return !p || int64_t(g.N) * bytes % 16 == 0; };
+    return fits(g.out, g.out_f32 ? 4 : 2) && fits(g.pre, 2) && fits(g.res, g.res_f32 ? 4 : 2);
+}
+
+template <bool GRAD, bool COPIED>
+cudaError_t on_tile(int tile, const Operand (*ops)[2], int jobs, const LArgs &g, cudaStream_t st)
+{
+    switch (tile) {
+    case 0: return launch<256, true, GRAD, COPIED>(ops, jobs, g, st);
+    case 1: return launch<128, true, GRAD, COPIED>(ops, jobs, g, st);
+    case 2: return launch<128, false, GRAD, COPIED>(ops, jobs, g, st);
+    default: return launch<64, false, GRAD, COPIED>(ops, jobs, g, st);
+    }
 }
 
 // One product or two, the longer reduction first; ops[j]: A and B of product j.
@@ -729,7 +810,6 @@ cudaError_t products(const Operand (*ops)[2], const Size *size, int jobs, const 
         b.NTL = int(ceil_div(size[j].N, T.N));
         b.a_mn = ops[j][0].mn;
         b.b_mn = ops[j][1].mn;
-        b.vec = vector_bytes(b);
         tiles[j] = ceil_div(size[j].M, T.M) * b.NTL;
     }
     for (int parted = 0; parted < 2; ++parted) {  // whole tiles first
@@ -747,12 +827,9 @@ cudaError_t products(const Operand (*ops)[2], const Size *size, int jobs, const 
     g.items = int(items);
     g.limit = wait.limit > 0 ? wait.limit : 4000000000LL;  // about 2 s of SM clocks
     g.stall = wait.stall_first_fill;
-    switch (pl.tile) {
-    case 0: return launch<256, true, GRAD>(ops, jobs, g, st);
-    case 1: return launch<128, true, GRAD>(ops, jobs, g, st);
-    case 2: return launch<128, false, GRAD>(ops, jobs, g, st);
-    default: return launch<64, false, GRAD>(ops, jobs, g, st);
-    }
+    if constexpr (!GRAD)
+        if (!rows_on_16(g.job[0])) return on_tile<GRAD, false>(pl.tile, ops, jobs, g, st);
+    return on_tile<GRAD, true>(pl.tile, ops, jobs, g, st);
 }
 
 // ---- dz and its column sums ----------------------------------------------------------------

@@ -13,22 +13,28 @@ enum class MapType {
     FP4  // packed, two a byte in memory; 128 columns, a byte each in shared memory
 };
 
-// A map of [rows][K] elements (rows K elements apart, or `stride` where given) in boxes of box_rows rows.
-inline bool make_tensor_map(CUtensorMap *m, const void *base, MapType type, int64_t K, int64_t rows, int box_rows,
-                            int64_t stride = 0)
+typedef CUresult (*TensorMapEncode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline TensorMapEncode tensor_map_encode()  // null where the driver has none
 {
-    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode encode = [] {
+    static const TensorMapEncode encode = [] {
         cudaDriverEntryPointQueryResult q;
         void *f = nullptr;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
                 cudaSuccess ||
             q != cudaDriverEntryPointSuccess)
             f = nullptr;
-        return reinterpret_cast<Encode>(f);
+        return reinterpret_cast<TensorMapEncode>(f);
     }();
+    return encode;
+}
+
+// A map of [rows][K] elements (rows K elements apart, or `stride` where given) in boxes of box_rows rows.
+inline bool make_tensor_map(CUtensorMap *m, const void *base, MapType type, int64_t K, int64_t rows, int box_rows,
+                            int64_t stride = 0)
+{
+    const TensorMapEncode encode = tensor_map_encode();
     if (!encode) return false;
     const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
     if (!stride) stride = K;
@@ -40,6 +46,19 @@ inline bool make_tensor_map(CUtensorMap *m, const void *base, MapType type, int6
     return encode(m, t, 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A map of [rows][cols] outputs, fp32 or bf16, in boxes of 32 x 32 whose rows in shared memory (128 or 64 bytes) are
+// swizzled by as much.  Rows start on 16 bytes.
+inline bool make_store_map(CUtensorMap *m, void *base, bool f32, int64_t cols, int64_t rows)
+{
+    const TensorMapEncode encode = tensor_map_encode();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(cols * (f32 ? 4 : 2))};
+    const cuuint32_t box[2] = {32, 32}, step[2] = {1, 1};
+    return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
+                  step, CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline int device_sms()
