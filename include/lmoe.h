@@ -407,7 +407,7 @@ typedef struct {
  * out[r][n] = fn(z) + res[r][n], rounded once to out_fmt;  pre[r][n] = bf16(z)
  * x bf16 [rows][K], W bf16 [N][K], products accumulated in fp32 by the tensor
  * core, the rest in fp32.  pre may be NULL; out may be res where they have one
- * type; otherwise outputs overlap no input.  act NULL: no bias, no function, no
+ * type; otherwise outputs overlap no input and not one another.  act NULL: no bias, no function, no
  * residual.  K % 8 == 0, any N >= 1, rows <= 2^29, no matrix
  * of more than 2^40 elements.  The status word is used as
  * by lmoe_linear_mxfp4: cleared by the caller once, before the workspace's first
@@ -439,7 +439,8 @@ lmoe_status lmoe_linear_act_bf16_backward(const void *dout, int32_t dout_fmt, co
  * out[t][c] = bf16( (x[t][c] - m) * s * w[c] + b[c] );  mean[t] = m, rstd[t] = s
  * x [T][H] of type x_fmt; w, b fp32 [H], either may be NULL (1 and 0); mean and
  * rstd fp32 [T], both or neither.  fp32 arithmetic, the squares of the centred
- * values; limits as for lmoe_rms_norm.  out overlaps no input. */
+ * values (a row's sum of them stays below 2^128); limits as for lmoe_rms_norm.
+ * out overlaps no input. */
 lmoe_status lmoe_layer_norm(const void *x, int32_t x_fmt, const float *w, const float *b, float eps, int64_t T, int32_t H,
                             uint16_t *out, float *mean, float *rstd, void *stream);
 

@@ -425,7 +425,8 @@ def picks(g, T, E, k):
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 896, 16), (2, 7, 7), (5, 32, 32), (64, 896, 16), (333, 130, 3),
                                    (151, 384, 8), (1000, 257, 4), (1100, 896, 16), (2100, 60, 8), (700, 2048, 32),
-                                   (513, 1023, 5), (3000, 4, 2)])
+                                   (513, 1023, 5), (3000, 4, 2),
+                                   (73, 1149, 20), (125, 1032, 25)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_balance_loss(cuda_lib, T, E, k, masked):
     g = gen(T + E + k)
@@ -631,3 +632,142 @@ def test_balance_loss_rows_of_extreme_logits(cuda_lib, E):
     f = counts.to(D) / (k * T) * E
     within(probs, p.mean(0), 800 * U * p.mean(0))
     within(d, p * (f - (p * f).sum(1, keepdim=True)) / T, 400 * U / T * p * (f + (p * f).sum(1, keepdim=True)) + TINY)
+
+
+# ---- offsets beyond 32 bits ------------------------------------------------------------------
+
+def test_linear_act_backward_beyond_2_31_elements(cuda_lib):
+    rows, K, N = 66000, 8, 33000
+    g = gen(5)
+    x, W, pre = randn(g, rows, K), randn(g, N, K), randn(g, rows, N)
+    dout = randn(g, rows, N, scale=0.01)
+    dx, dW, db = cuda_lib.linear_act_bf16_backward(dout, x, W, "relu", pre)
+    assert cuda_lib.last_call_status() == cuda_lib.OK
+    for r0 in (0, rows - 33):
+        dz = dout[r0:r0 + 33].to(D) * (pre[r0:r0 + 33] > 0)  # bf16 as it is: relu's slope rounds nothing
+        ref = dz @ W.to(D)
+        tol = (N + 2) * U * (dz.abs() @ W.to(D).abs())
+        within(dx[r0:r0 + 33], ref, tol + (ref.abs() + tol) * HALF)
+    for n0 in (0, N - 9):
+        dz = dout[:, n0:n0 + 9].to(D) * (pre[:, n0:n0 + 9] > 0)
+        ref = dz.t() @ x.to(D)
+        tol = (rows + 2) * U * (dz.abs().t() @ x.to(D).abs())
+        within(dW[n0:n0 + 9], ref, tol + (ref.abs() + tol) * HALF)
+        within(db[n0:n0 + 9], dz.sum(0), (rows + 2) * U * dz.abs().sum(0))
+
+
+def test_layer_norm_beyond_2_31_elements(cuda_lib):
+    T, H = 263000, 8192
+    x = torch.empty(T, H, device=DEV, dtype=torch.bfloat16).normal_(generator=gen(6))
+    out, mean, rstd = cuda_lib.layer_norm(x, stats=True)
+    dx, _, _ = cuda_lib.layer_norm_backward(out, x, mean, rstd, want_params=False)
+    for t0 in (0, T - 5):
+        v = x[t0:t0 + 5].to(D)
+        m, var = v.mean(1, keepdim=True), v.var(1, unbiased=False, keepdim=True)
+        ref = (v - m) / (var + 1e-5).sqrt()
+        within(out[t0:t0 + 5], ref, ref.abs() * (HALF + 80 * U) + 100 * U)
+        small = cuda_lib.layer_norm_backward(out[t0:t0 + 5].contiguous(), x[t0:t0 + 5].contiguous(), mean[t0:t0 + 5].contiguous(),
+                                             rstd[t0:t0 + 5].contiguous(), want_params=False)[0]
+        assert torch.equal(dx[t0:t0 + 5], small)
+
+
+def test_balance_loss_beyond_2_31_logits(cuda_lib):
+    T, E, k = 1_060_000, 2048, 1
+    l = torch.empty(T, E, device=DEV).normal_(generator=gen(7))
+    first, last = l[:3].clone(), l[-3:].clone()
+    idx = torch.randint(0, E, (T, k), device=DEV, generator=gen(8)).to(torch.int32)
+    loss, counts, probs, d = cuda_lib.balance_loss(l, idx, coef=(1.0, 0.5), grad=True, dlogits=l)
+    assert d is l and torch.equal(counts.long(), torch.bincount(idx[:, 0].long(), minlength=E))
+    f = counts.to(D) * E / (k * T)
+    for rows, got in ((first, d[:3]), (last, d[-3:])):
+        lse = torch.logsumexp(rows.to(D), 1, keepdim=True)
+        p = torch.exp(rows.to(D) - lse)
+        sf = (p * f).sum(1, keepdim=True)
+        ref = p * ((f - sf) + lse) / T
+        within(got, ref, 400 * U * p * (f + sf + lse.abs() + 1) / T + TINY)
+    assert abs(float(probs.sum()) - 1) < 1e-4 and abs(float(loss[0]) - 1) < 1e-2
+
+
+# ---- edges ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,N", [(5, 45), (200, 45), (700, 1001), (300, 1004), (64, 264), (65, 264)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_linear_act_in_place_where_rows_start_anywhere(cuda_lib, rows, N, dt):
+    g = gen(rows + N)
+    x, W, b = randn(g, rows, 200), randn(g, N, 200, scale=0.07), randn(g, N, dtype=torch.float32)
+    res = randn(g, rows, N, dtype=dt)
+    want = cuda_lib.linear_act_bf16(x, W, b, "gelu_tanh", res, pre=True)
+    r2 = res.clone()
+    got = cuda_lib.linear_act_bf16(x, W, b, "gelu_tanh", r2, out=r2, pre=True)
+    assert torch.equal(want[0], r2) and torch.equal(want[1], got[1])
+
+
+def test_workspaces_may_hold_anything_behind_the_status(cuda_lib):
+    """One workspace for all the calls, full of NaN patterns: each writes what it reads of it, and none touches the
+    status word."""
+    lmoe = cuda_lib
+    g = gen(21)
+    x, W, d = randn(g, 128, 7168), randn(g, 200, 7168, scale=0.01), randn(g, 128, 200)
+    l, idx = torch.randn(9000, 64, device=DEV, generator=g), picks(g, 9000, 64, 4)
+    mean, rstd = torch.randn(128, device=DEV, generator=g), torch.rand(128, device=DEV, generator=g)
+    calls = [(lambda ws: lmoe.linear_act_bf16(x, W, act="silu", pre=True, ws=ws), lmoe.linear_act_workspace_size(128, 7168, 200)),
+             (lambda ws: lmoe.linear_act_bf16_backward(d, x, W, "gelu", d, ws=ws),
+              lmoe.linear_act_backward_workspace_size(128, 7168, 200)),
+             (lambda ws: lmoe.layer_norm_backward(x, x, mean, rstd, ws=ws), lmoe.layer_norm_backward_workspace_size(128, 7168)),
+             (lambda ws: lmoe.balance_loss(l, idx, grad=True, ws=ws), lmoe.balance_loss_workspace_size(9000, 64, 4))]
+    ws = torch.full((max(n for _, n in calls),), 0xFF, dtype=torch.uint8, device=DEV)
+    ws[:256] = 0
+    for call, n in calls:
+        want = [t.clone() for t in call(torch.zeros(n, dtype=torch.uint8, device=DEV))]
+        got = call(ws)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert lmoe.last_device_status(ws) == lmoe.OK
+        ws[256:] = 0xFF
+
+
+def test_calls_at_once_on_two_streams(cuda_lib):
+    """Calls that overlap on the GPU, each on a workspace of its own."""
+    a, b = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
+    calls = _calls(cuda_lib, gen(31), T=700, H=1032, N=1000, E=96, k=4)
+    want = [[t.clone() for t in c()] for c in calls]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        with torch.cuda.stream(a):
+            got.append([c() for c in calls])
+        with torch.cuda.stream(b):
+            got.append([c() for c in reversed(calls)][::-1])
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(x, y) for w, o in zip(want, g) for x, y in zip(w, o))
+
+
+def test_the_binding_refuses_strides_types_and_shapes(cuda_lib):
+    lmoe = cuda_lib
+    g = gen(41)
+    x, W, f = randn(g, 6, 64), randn(g, 16, 64), torch.zeros(6, 64, device=DEV)
+    d, i = randn(g, 6, 16), torch.zeros(6, 2, dtype=torch.int32, device=DEV)
+    s = torch.zeros(6, device=DEV)
+    wide = randn(g, 6, 128)[:, :64]
+    bad = [lambda: lmoe.linear_act_bf16(wide, W), lambda: lmoe.linear_act_bf16(f, W), lambda: lmoe.linear_act_bf16(x, W[:, :32]),
+           lambda: lmoe.linear_act_bf16(x, W, bias=torch.zeros(8, device=DEV)), lambda: lmoe.linear_act_bf16(x, W, res=f),
+           lambda: lmoe.linear_act_bf16(x, W, out=torch.zeros(6, 16, device=DEV, dtype=torch.float16)),
+           lambda: lmoe.linear_act_bf16(x, W, pre=f), lambda: lmoe.linear_act_bf16(x, W, ws=f),
+           lambda: lmoe.linear_act_bf16(x.cpu(), W), lambda: lmoe.linear_act_bf16(x, W.cpu()),
+           lambda: lmoe.linear_act_bf16_backward(d, x, W, "silu"), lambda: lmoe.linear_act_bf16_backward(d, x, W, "none", d),
+           lambda: lmoe.linear_act_bf16_backward(d.t().contiguous(), x, W), lambda: lmoe.layer_norm(wide),
+           lambda: lmoe.layer_norm(x, w=x[0]), lambda: lmoe.layer_norm(x, mean=s[:3], rstd=s),
+           lambda: lmoe.layer_norm_backward(f, f, s, s), lambda: lmoe.layer_norm_backward(x, f, s, s, add=x),
+           lambda: lmoe.layer_norm_backward(x, f, s[:5], s), lambda: lmoe.balance_loss(x, i), lambda: lmoe.balance_loss(f, i.long()),
+           lambda: lmoe.balance_loss(f, i, mask=s), lambda: lmoe.balance_loss(f, i, grad=True, topk_w=torch.zeros(6, 2, device=DEV)),
+           lambda: lmoe.balance_loss(f, i, scale=s[:1]), lambda: lmoe.balance_loss(f, i, grad=True, scale=s),
+           lambda: lmoe.balance_loss(f[:5], i)]
+    for n, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {n} was not refused")
+    for call in (lambda: lmoe.linear_act_bf16(randn(g, 6, 60), randn(g, 16, 60)), lambda: lmoe.layer_norm(randn(g, 6, 60)),
+                 lambda: lmoe.balance_loss(f, torch.zeros(6, 33, dtype=torch.int32, device=DEV)),
+                 lambda: lmoe.linear_act_bf16(x, W, ws=torch.zeros(16, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(lmoe.LmoeError):
+            call()

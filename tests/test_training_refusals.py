@@ -38,7 +38,8 @@ def test_linear_act_refusals(lmoe):
 
     for bad in BAD_SIZES + (dict(x=NULL), dict(W=NULL), dict(out=NULL), dict(x=ODD), dict(W=ODD), dict(out=ODD), dict(pre=ODD),
                             dict(bias=4104), dict(res=4104), dict(fn=-1), dict(fn=5), dict(fmt=2), dict(fmt=-1),
-                            dict(bias_fmt=2), dict(res_fmt=-1), dict(res=4096, res_fmt=1)):
+                            dict(bias_fmt=2), dict(res_fmt=-1), dict(res=4096, res_fmt=1), dict(pre=P),
+                            dict(pre=vp(8192), res=8192)):
         assert call(**bad) == lmoe.ERR_INVALID_ARG, bad
     for bad in (dict(ws=NULL), dict(n=need - 1), dict(ws=vp(4096 + 64))):
         assert call(**bad) == lmoe.ERR_WORKSPACE, bad

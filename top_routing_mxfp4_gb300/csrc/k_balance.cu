@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(ROW_THREADS<NV>, ROW_BLOCKS<NV>) k_balance_row
         const F2 inv2 = f2(inv), base = f2(fmaf(cz, lse, -sf * inv));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const F2 p0 = v[2 * i] * inv2, p1 = v[2 * i + 1] * inv2;
-            acc[2 * i] = acc[2 * i] + p0;
-            acc[2 * i + 1] = acc[2 * i + 1] + p1;
+            acc[2 * i] = fma2(v[2 * i], inv2, acc[2 * i]);
+            acc[2 * i + 1] = fma2(v[2 * i + 1], inv2, acc[2 * i + 1]);
             if (!GRAD) continue;
+            const F2 p0 = v[2 * i] * inv2, p1 = v[2 * i + 1] * inv2;
             float f[4], q[4] = {};
             get4(s_f, i, 0.f, f);
             if (gate) get4(mine, i, 0.f, q);

@@ -650,7 +650,7 @@ lmoe_status lmoe_linear_act_bf16(const uint16_t *x, const uint16_t *W, const lmo
     if (!x || !W || !out) return LMOE_ERR_INVALID_ARG;
     for (const void *p : {(const void *)x, (const void *)W, (const void *)out, (const void *)pre, f.bias, f.res})
         if (!aligned(p, 16)) return LMOE_ERR_INVALID_ARG;
-    if (f.res == out && f.res_fmt != out_fmt) return LMOE_ERR_INVALID_ARG;
+    if ((f.res == out && f.res_fmt != out_fmt) || (pre && (pre == out || pre == f.res))) return LMOE_ERR_INVALID_ARG;
     if (!workspace || ws_bytes < lmoe_linear_act_workspace_size(rows, K, N) || !aligned(workspace, 256))
         return LMOE_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);

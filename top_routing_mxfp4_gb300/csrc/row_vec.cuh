@@ -100,7 +100,9 @@ __device__ __forceinline__ float2 warp_sum2(float a, float b)
     return make_float2(__shfl_sync(0xFFFFFFFFu, s, 0), __shfl_sync(0xFFFFFFFFu, s, 16));
 }
 
-// Two fp32 values as one operand of the packed instructions (each rounded as by itself).
+// Two fp32 values as one operand of the packed instructions.  (The assembler may join a
+// product and a sum into one rounding: where two instances have to agree bit for bit, they
+// say fma2.)
 struct F2 {
     uint64_t v;
 };
