@@ -615,13 +615,14 @@ lmoe_status lmoe_forward_workspace_views(const lmoe_dims *dims, lmoe_ffn_views *
 lmoe_status lmoe_set_h_capture(float *h_f32, size_t bytes);
 
 /* Failure-path test of the bounded waits of the expert GEMMs, the MXFP4
- * linear and the grouped products.  Every wait on an mbarrier there gives up after a limit of SM clocks (about
+ * linear, the grouped products and the linear layer with functions.  Every
+ * wait on an mbarrier there gives up after a limit of SM clocks (about
  * 2 s by default), records LMOE_ERR_TIMEOUT in the status word, and the
  * kernel winds down (an MMA issuer first waits, again bounded, for its MMAs
  * in flight) and returns; so does the wait of a down item, in the kernel
  * that runs both GEMMs, for its token tile's h.  With stall_first_fill set, the first pipeline
  * stage of every CTA of the following lmoe_forward / lmoe_expert_ffn /
- * lmoe_linear_mxfp4 / lmoe_grouped_* calls is never filled, so those waits run out after wait_limit_cycles; the host
+ * lmoe_linear_mxfp4 / lmoe_grouped_* / lmoe_linear_act_* calls is never filled, so those waits run out after wait_limit_cycles; the host
  * then reads LMOE_ERR_TIMEOUT with lmoe_last_device_status.  (0, 0) restores
  * the normal behaviour; wait_limit_cycles alone (stall 0) only changes the
  * limit.  After LMOE_ERR_TIMEOUT the outputs of that call are undefined and

@@ -3,8 +3,8 @@
 // By one quick exponential (2 u of itself and of its argument) and one quick reciprocal
 // each, two elements at a time in packed fp32 arithmetic: 7 instructions an element for
 // silu and gelu by tanh, 12 for gelu.  The epilogue of a tile is bound by them where K is
-// short (8192 rows 512 -> 3584, us: no function 25; silu 39, gelu 55 with expf's quick form
-// and __fdividef one element at a time).
+// short (8192 rows 512 -> 3584, us: silu 36, gelu 40; 39 and 55 with expf's quick form and
+// __fdividef one element at a time).
 //
 // With a = |z|, the logistic function's and the normal distribution's left tails go
 // into max(z, 0) - a tail(a), right for both signs, and exact far out.

@@ -1,5 +1,5 @@
-// Binding of the short calls (norms, MXFP4 linear, grouped products) on torch
-// tensors: the same marshalling as the ctypes functions of lmoe.py (checks of
+// Binding of the short calls (norms, MXFP4 linear, grouped products, the linear layer
+// with functions, layer norm and balance loss with their gradients) on torch tensors: the same marshalling as the ctypes functions of lmoe.py (checks of
 // types, shapes and devices, outputs allocated in the call's stream, then the C
 // entry point of the same name), in C++.  These calls run for a few
 // microseconds; through ctypes a call with two outputs cost 12 us of host time,

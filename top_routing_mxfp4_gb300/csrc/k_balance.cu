@@ -8,7 +8,10 @@
 // The counts depend on the picks alone, which are a few percent of the logits'
 // bytes: they are counted first, and then one pass over the logits gives the
 // probabilities' sums and the whole gradient, each logit read once and each
-// gradient written once.  HBM bounds it.
+// gradient written once.  HBM bounds it (32768 tokens of 896 experts, top 16, all outputs:
+// 54 us of the 36 that the bytes take; the counting and the last cluster's sums, which
+// take 7 and 8 us alone, lie mostly under it), and at few tokens the start and end of its
+// launches (64 tokens 7.2).
 //
 // A warp takes a row: a lane holds the same columns in every row it meets, so the
 // sums over the tokens stay in its registers (fp32) until the end; each block
