@@ -21,6 +21,8 @@
 // 122 us; a ring of cp.async copies 118; w, h and g kept and packed arithmetic 113;
 // four rows of ring 81, 5.9 TB/s, 86% of HBM; fp32 rows 143, 85%).  At few rows the two
 // kernels' starts and ends are most of the time (64 rows of 7168: 8 us).
+#include <algorithm>
+
 #include "lmoe_internal.cuh"
 #include "row_vec.cuh"
 
@@ -605,10 +607,14 @@ int blocks_per_sm(int H)
     const int n = 512 / int(round_up(ceil_div(H, 16), 32));
     return n < 1 ? 1 : n > 6 ? 6 : n;  // (1024 columns, 8192 rows: two 26.0, four 19.8, six 19.6, eight 21.5 us)
 }
+// A block costs a row of partial sums, so it takes two rows from 304 blocks on, four from
+// 608 on (fp32 rows, us: 1001 x 1024 8.3, 2000 x 1024 12.0, 500 x 2048 7.2, 1001 x 2048 12.7;
+// a block a row up to the most: 12.4, 15.4, 8.5, 11.2).
 int64_t fused_blocks(int64_t T, int H)
 {
-    const int64_t most = int64_t(152) * blocks_per_sm(H), rows = H <= kMaxWarpH ? ceil_div(T, 8) : T;
-    return rows < most ? rows : most;
+    const int64_t most = int64_t(152) * blocks_per_sm(H);
+    if (H <= kMaxWarpH) return std::min(ceil_div(T, 8), most);
+    return std::min(std::max({std::min<int64_t>(T, 304), std::min<int64_t>(T / 2, 608), T / 4}), most);
 }
 
 template <typename R, int E8>
