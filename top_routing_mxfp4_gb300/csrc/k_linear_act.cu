@@ -76,6 +76,10 @@ struct LArgs {
     LJob job[2];
     LSeg seg[MAX_SEGS];
     int segs, whole, items;  // items [0, whole) are whole tiles
+    // GRAD: dbias [col_n], the sums of col_part's [col_parts][col_n], or null
+    float *dbias;
+    const float *col_part;
+    int col_n, col_parts;
     int32_t *status;
     long long limit;
     int stall;
@@ -171,6 +175,13 @@ __device__ __forceinline__ void put_columns(uint8_t *buf, int lane, int n, int64
 }
 
 // ---- the products ------------------------------------------------------------------------
+
+// Between the epilogue warps alone.
+template <int WARPS>
+__device__ __forceinline__ void epilogue_sync()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
+}
 
 // GRAD: one or two products whose operands may run either way; else one of K-major operands
 // (the choice between operands' orders cost 27.9 -> 29.6 us at 512 rows 7168 -> 3584).
@@ -361,6 +372,37 @@ __global__ void __launch_bounds__((LCfg<NT, PAIR>::THREADS), 1)
         __shared__ __align__(16) float s_bias[C::EW][32];
         const int q = warp & 3, half = (warp - 2) >> 2;
         uint8_t *buf = bufs + (warp - 2) * C::BUF, *pre_buf = buf + C::BUF / 2;
+        // These warps wait for the first tile anyway: the column sums of dz, in k_col_sums' order (16
+        // strands), here two of them a warp.  A launch of its own for them took 1.5 to 3.5 us (333 x 1056 x 1000
+        // 12.4 against 10.9, one row 3584 -> 7168 40.0 against 36.5, 8192 x 512 x 256 25.8 against 22.5).
+        if (GRAD && p.dbias) {
+            constexpr int STRANDS = 16;
+            float(*s_cols)[32] = reinterpret_cast<float(*)[32]>(bufs);  // [STRANDS]
+            for (int64_t c0 = int64_t(blockIdx.x) * 32; c0 < p.col_n; c0 += int64_t(gridDim.x) * 32) {
+                const int64_t c = c0 + lane;
+                for (int strand = warp - 2; strand < STRANDS; strand += C::EW) {
+                    float v = 0.f;
+                    if (c < p.col_n)
+                        for (int g = strand; g < p.col_parts; g += 8 * STRANDS) {
+                            float r[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                r[i] = g + i * STRANDS < p.col_parts ? p.col_part[int64_t(g + i * STRANDS) * p.col_n + c] : 0.f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v += r[i];
+                        }
+                    s_cols[strand][lane] = v;
+                }
+                epilogue_sync<C::EW>();
+                if (warp == 2 && c < p.col_n) {
+                    float v = s_cols[0][lane];
+#pragma unroll
+                    for (int i = 1; i < STRANDS; ++i) v += s_cols[i][lane];
+                    p.dbias[c] = v;
+                }
+                epilogue_sync<C::EW>();
+            }
+        }
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int it = begin; it < p.items; it = next(it)) {
@@ -1032,7 +1074,9 @@ cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cu
         const bool f32 = a.dout_fmt == LMOE_F32, vec = Np == a.N;
         e = f32 ? (vec ? dz_fn<true, true>(g, a.fn, grid, st) : dz_fn<true, false>(g, a.fn, grid, st))
                 : (vec ? dz_fn<false, true>(g, a.fn, grid, st) : dz_fn<false, false>(g, a.fn, grid, st));
-        if (e == cudaSuccess && a.dbias) e = launch_col_sums(part, grid.y, a.N, 1, a.dbias, nullptr, st);
+        // the products' kernel adds the groups' sums up on the way, where there is one
+        if (e == cudaSuccess && a.dbias && !a.dW && (!a.dx || a.rows <= FEW))
+            e = launch_col_sums(part, grid.y, a.N, 1, a.dbias, nullptr, st);
         if (e != cudaSuccess) return e;
     }
     // both products in one launch, the longer reduction first
@@ -1041,6 +1085,10 @@ cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cu
     Size size[2];
     LArgs g{};
     g.status = a.status;
+    g.dbias = a.dbias;
+    g.col_part = part;
+    g.col_n = a.N;
+    g.col_parts = int(dz_splits(a.rows, a.N));
     int jobs = 0;
     auto dx = [&] {
         if (!a.dx) return;
