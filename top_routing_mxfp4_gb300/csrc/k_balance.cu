@@ -9,9 +9,8 @@
 // bytes: they are counted first, and then one pass over the logits gives the
 // probabilities' sums and the whole gradient, each logit read once and each
 // gradient written once.  HBM bounds it (32768 tokens of 896 experts, top 16, all outputs:
-// 54 us of the 36 that the bytes take; the counting and the last cluster's sums, which
-// take 7 and 8 us alone, lie mostly under it), and at few tokens the start and end of its
-// launches (64 tokens 7.2).
+// 50 us of the 36 that the bytes take, 37 of them the pass over the logits; of 64 experts
+// 17.6), and at few tokens the start and end of its launches (64 tokens 7.1).
 //
 // A warp takes a row: a lane holds the same columns in every row it meets, so the
 // sums over the tokens stay in its registers (fp32) until the end; each block
@@ -105,17 +104,17 @@ __global__ void __cluster_dims__(kCountCluster, 1, 1) __launch_bounds__(512) k_b
     tc::cluster_sync_end();  // no CTA's counts go while another reads them
 }
 
-// A row's logits and the column sums in registers: half the warps beyond 1024 columns.
+// A row's logits, the next row's and the column sums in registers: fewer warps for wider rows
+// (32768 tokens of 256 experts, 512, 768, 1024 threads, two blocks of 512: 21.8, 21.1, 22.7, 25.1 us;
+// of 384 experts, 512, 640, 768 threads: 26.7, 28.6, 29.4).
 template <int NV>
-constexpr int ROW_THREADS = NV <= 8 ? 512 : 256;
-template <int NV>
-constexpr int ROW_BLOCKS = NV <= 2 ? 2 : 1;  // an SM
+constexpr int ROW_THREADS = NV <= 2 ? 768 : NV <= 8 ? 512 : 256;
 
 // NV: 128 columns each; VEC: E % 4 == 0, a lane's columns are fours of them.
 // own: the block counts the picks itself.  one: the grid is one cluster, which adds up its
 // blocks' sums itself.
 template <int NV, bool VEC, bool GRAD>
-__global__ void __launch_bounds__(ROW_THREADS<NV>, ROW_BLOCKS<NV>) k_balance_rows(const BalanceArgs a, bool own, bool one)
+__global__ void __launch_bounds__(ROW_THREADS<NV>, 1) k_balance_rows(const BalanceArgs a, bool own, bool one)
 {
     constexpr int kBlock = ROW_THREADS<NV>, kWarps = kBlock / 32;
     extern __shared__ __align__(16) float s_mem[];
@@ -130,6 +129,53 @@ __global__ void __launch_bounds__(ROW_THREADS<NV>, ROW_BLOCKS<NV>) k_balance_row
     if (GRAD && a.topk_w)
         for (int e = threadIdx.x; e < kWarps * Ep; e += kBlock) s_row[e] = 0.f;
     pdl_enter();
+    // a lane's columns: fours of consecutive ones, or (E % 4) single ones, 32 lanes apart
+    auto col = [&](int i) { return VEC ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane; };
+    auto get4 = [&](const float *p, int i, float none, float (&q)[4]) {  // the lane's i-th four of a row
+        if (VEC) {
+            float4 r = make_float4(none, none, none, none);
+            if (col(4 * i) < a.E) r = *reinterpret_cast<const float4 *>(p + col(4 * i));
+            q[0] = r.x, q[1] = r.y, q[2] = r.z, q[3] = r.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = col(4 * i + j) < a.E ? p[col(4 * i + j)] : none;
+        }
+    };
+    auto put4 = [&](float *p, int i, const float (&q)[4]) {
+        if (VEC) {
+            if (col(4 * i) < a.E) *reinterpret_cast<float4 *>(p + col(4 * i)) = make_float4(q[0], q[1], q[2], q[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col(4 * i + j) < a.E) p[col(4 * i + j)] = q[j];
+        }
+    };
+    const int64_t step = int64_t(gridDim.x) * kWarps;
+    auto counts_in = [&](int64_t t) { return t >= a.T ? 0u : a.mask ? uint32_t(__ldg(a.mask + t)) : 1u; };
+    // what a row needs, on its way while the row before is worked on (and not looked at before:
+    // with the ids checked and the mask compared where they are loaded a warp waited for them)
+    float next[NV * 4];
+    int ne = -1;
+    float nw = 0.f, ng = 0.f;
+    auto load = [&](int64_t t) {
+        const float *l = a.logits + t * a.E;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float q[4];
+            get4(l, i, -INFINITY, q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) next[4 * i + j] = q[j];
+        }
+        if (GRAD && a.topk_w && lane < a.k) {
+            ne = __ldg(a.idx + t * a.k + lane);
+            nw = __ldg(a.topk_w + t * a.k + lane);
+            ng = __ldg(a.dtopk_w + t * a.k + lane);
+        }
+    };
+    // the first row, before the counts
+    int64_t t = int64_t(warp) * gridDim.x + blockIdx.x;
+    uint32_t in = counts_in(t), in_next = counts_in(t + step);
+    if (in) load(t);
     __syncthreads();
     if (own) {
         count_picks(a, threadIdx.x, kBlock, s_counts, s_counts + a.E);
@@ -163,59 +209,13 @@ __global__ void __launch_bounds__(ROW_THREADS<NV>, ROW_BLOCKS<NV>) k_balance_row
     }
     __syncthreads();
 
-    // a lane's columns: fours of consecutive ones, or (E % 4) single ones, 32 lanes apart
-    auto col = [&](int i) { return VEC ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane; };
-    auto get4 = [&](const float *p, int i, float none, float (&q)[4]) {  // the lane's i-th four of a row
-        if (VEC) {
-            float4 r = make_float4(none, none, none, none);
-            if (col(4 * i) < a.E) r = *reinterpret_cast<const float4 *>(p + col(4 * i));
-            q[0] = r.x, q[1] = r.y, q[2] = r.z, q[3] = r.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = col(4 * i + j) < a.E ? p[col(4 * i + j)] : none;
-        }
-    };
-    auto put4 = [&](float *p, int i, const float (&q)[4]) {
-        if (VEC) {
-            if (col(4 * i) < a.E) *reinterpret_cast<float4 *>(p + col(4 * i)) = make_float4(q[0], q[1], q[2], q[3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (col(4 * i + j) < a.E) p[col(4 * i + j)] = q[j];
-        }
-    };
-    const int64_t step = int64_t(gridDim.x) * kWarps;
-    auto counts_in = [&](int64_t t) { return t < a.T && (!a.mask || __ldg(a.mask + t)); };
-    // what a row needs, on its way while the row before is worked on
-    float next[NV * 4];
-    int ne = -1;
-    float nw = 0.f, ng = 0.f;
-    auto load = [&](int64_t t) {
-        const float *l = a.logits + t * a.E;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float q[4];
-            get4(l, i, -INFINITY, q);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) next[4 * i + j] = q[j];
-        }
-        if (GRAD && a.topk_w && lane < a.k) {
-            ne = __ldg(a.idx + t * a.k + lane);
-            nw = __ldg(a.topk_w + t * a.k + lane);
-            ng = __ldg(a.dtopk_w + t * a.k + lane);
-            if (uint32_t(ne) >= uint32_t(a.E)) ne = -1;
-        }
-    };
     F2 acc[NV * 2];
 #pragma unroll
     for (int i = 0; i < NV * 2; ++i) acc[i] = f2(0.f);
     float z = 0.f;
-    int64_t t = int64_t(warp) * gridDim.x + blockIdx.x;
-    bool in = counts_in(t), in_next = counts_in(t + step);
-    if (in) load(t);
     for (; t < a.T; t += step) {
         float *d = GRAD ? a.dlogits + t * a.E : nullptr;
-        const bool in_after = counts_in(t + 2 * step);
+        const uint32_t in_after = counts_in(t + 2 * step);
         F2 v[NV * 2];
         float m = -INFINITY;
         int e = -1;
@@ -226,10 +226,10 @@ __global__ void __launch_bounds__(ROW_THREADS<NV>, ROW_BLOCKS<NV>) k_balance_row
                 v[i] = f2(next[2 * i], next[2 * i + 1]);
                 m = fmaxf(m, fmaxf(next[2 * i], next[2 * i + 1]));
             }
-            e = ne, w = nw, g = ng;
+            e = uint32_t(ne) < uint32_t(a.E) ? ne : -1, w = nw, g = ng;
         }
         if (in_next) load(t + step);
-        const bool here = in;
+        const bool here = in != 0;
         in = in_next;
         in_next = in_after;
         if (!here) {
@@ -363,16 +363,18 @@ __global__ void __launch_bounds__(ROW_THREADS<NV>, ROW_BLOCKS<NV>) k_balance_row
     }
 }
 
-// The blocks' sums added in order (within eight strands, added in order), probs, and the
-// losses.  One cluster: each CTA takes 128 columns at a time, rank 0 adds the CTAs'
-// shares of the loss.
-constexpr int kFinalCols = 128, kStrands = 8;
-__global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalCols *kStrands)
-    k_balance_final(const BalanceArgs a, int blocks)
+// The blocks' sums added in order (within strands, added in order), probs, and the losses.
+// One cluster: each CTA takes COLS columns at a time, L of a strand's loads in flight; rank
+// 0 adds the CTAs' shares of the loss.  Few columns are shared by all the CTAs, with more
+// strands (5000 tokens of 200 experts 11.5 against 13.9 us).
+constexpr int kFinalThreads = 1024;
+template <int COLS, int L>
+__global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThreads) k_balance_final(const BalanceArgs a, int blocks)
 {
-    __shared__ float s[kStrands][kFinalCols];
-    __shared__ float s_warp[kFinalCols / 32], s_loss[kFinalCtas];
-    const int at = threadIdx.x % kFinalCols, strand = threadIdx.x / kFinalCols;
+    constexpr int STRANDS = kFinalThreads / COLS;
+    __shared__ float s[STRANDS][COLS + 1];
+    __shared__ float s_warp[COLS / 32], s_loss[kFinalCtas];
+    const int at = threadIdx.x % COLS, strand = threadIdx.x / COLS;
     const int rank = int(tc::cluster_rank());
     pdl_enter();
     const int tokens = *a.tokens;
@@ -380,23 +382,22 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalCols 
     const float scale = float(a.E) / float(a.k) * inv_n;
     float loss = 0.f;
     // column E holds the sums of lse^2
-    for (int c = rank * kFinalCols + at; c - at <= a.E; c += kFinalCtas * kFinalCols) {
+    for (int c = rank * COLS + at; c - at <= a.E; c += kFinalCtas * COLS) {
+        const int n = strand == 0 && c < a.E ? a.counts[c] : 0;
         float v = 0.f;
         if (c <= a.E)
-            for (int b = strand; b < blocks; b += 10 * kStrands) {
-                float q[10];
+            for (int b = strand; b < blocks; b += L * STRANDS) {
+                float q[L];
 #pragma unroll
-                for (int i = 0; i < 10; ++i)
-                    q[i] = b + i * kStrands < blocks ? a.part[int64_t(b + i * kStrands) * (a.E + 1) + c] : 0.f;
+                for (int i = 0; i < L; ++i) q[i] = b + i * STRANDS < blocks ? a.part[int64_t(b + i * STRANDS) * (a.E + 1) + c] : 0.f;
 #pragma unroll
-                for (int i = 0; i < 10; ++i) v += q[i];
+                for (int i = 0; i < L; ++i) v += q[i];
             }
-        const int n = strand == 0 && c < a.E ? a.counts[c] : 0;
         s[strand][at] = v;
         __syncthreads();
         if (strand == 0) {
 #pragma unroll
-            for (int q = 1; q < kStrands; ++q) v += s[q][at];
+            for (int q = 1; q < STRANDS; ++q) v += s[q][at];
             v *= inv_n;
             if (c < a.E) {
                 a.probs[c] = v;
@@ -414,7 +415,7 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalCols 
     __syncthreads();
     if (threadIdx.x == 0) {
         loss = 0.f;
-        for (int q = 0; q < kFinalCols / 32; ++q) loss += s_warp[q];
+        for (int q = 0; q < COLS / 32; ++q) loss += s_warp[q];
         tc::cluster_store_i32(tc::cluster_map(tc::smem_u32(&s_loss[rank]), 0), __float_as_int(loss));
     }
     __syncthreads();
@@ -463,10 +464,9 @@ cudaError_t pick(const BalanceArgs &a, unsigned grid, bool own, bool one, cudaSt
 // Few rows are the work of one cluster, which needs no second kernel.
 bool one_cluster(int64_t T) { return T <= kOneCluster; }
 
-unsigned row_blocks(int64_t T, int E)
+unsigned row_blocks(int64_t T)
 {
-    const int64_t most = 152 * (E <= 256 ? ROW_BLOCKS<2> : 1);
-    return one_cluster(T) ? unsigned(kFinalCtas) : unsigned(T < most ? T : most);
+    return one_cluster(T) ? unsigned(kFinalCtas) : unsigned(T < 152 ? T : 152);
 }
 
 size_t count_bytes(int64_t T, int E, int k)
@@ -479,7 +479,7 @@ size_t count_bytes(int64_t T, int E, int k)
 // tokens (256 bytes) | counts of k_balance_count's parts | sums of the row blocks
 size_t balance_scratch_bytes(int64_t T, int E, int k)
 {
-    return 256 + count_bytes(T, E, k) + size_t(row_blocks(T, E)) * size_t(E + 1) * 4;
+    return 256 + count_bytes(T, E, k) + size_t(row_blocks(T)) * size_t(E + 1) * 4;
 }
 
 cudaError_t launch_balance(BalanceArgs a, void *scratch, cudaStream_t st)
@@ -489,18 +489,20 @@ cudaError_t launch_balance(BalanceArgs a, void *scratch, cudaStream_t st)
     a.count_part = reinterpret_cast<int32_t *>(s + 256);
     a.part = reinterpret_cast<float *>(s + 256 + count_bytes(a.T, a.E, a.k));
     const bool own = a.T * a.k <= kOwnCount, one = one_cluster(a.T);
-    const unsigned grid = row_blocks(a.T, a.E);
+    const unsigned grid = row_blocks(a.T);
     cudaError_t e = cudaSuccess;
     if (!own)
         e = launch_pdl(k_balance_count, dim3(kCountParts * kCountCluster), dim3(512), size_t(count_stride(a.E)) * 4, st, a);
     if (e != cudaSuccess) return e;
     const int nv = int(ceil_div(a.E, 128));
-    if (nv <= 2) e = pick<2>(a, grid, own, one, st);
+    if (nv <= 1) e = pick<1>(a, grid, own, one, st);
+    else if (nv <= 2) e = pick<2>(a, grid, own, one, st);
     else if (nv <= 4) e = pick<4>(a, grid, own, one, st);
     else if (nv <= 7) e = pick<7>(a, grid, own, one, st);
     else e = pick<16>(a, grid, own, one, st);
     if (e != cudaSuccess || one) return e;
-    return launch_pdl(k_balance_final, dim3(kFinalCtas), dim3(kFinalCols * kStrands), 0, st, a, int(grid));
+    return launch_pdl(a.E < 256 ? k_balance_final<32, 10> : k_balance_final<128, 20>, dim3(kFinalCtas), dim3(kFinalThreads), 0, st, a,
+                      int(grid));
 }
 
 }  // namespace lmoe
