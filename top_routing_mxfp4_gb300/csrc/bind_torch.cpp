@@ -1,9 +1,9 @@
 // Binding of the short calls (norms, MXFP4 linear, grouped products, the linear layer
-// with functions, layer norm and balance loss with their gradients) on torch tensors: the same marshalling as the ctypes functions of lmoe.py (checks of
-// types, shapes and devices, outputs allocated in the call's stream, then the C
-// entry point of the same name), in C++.  These calls run for a few
-// microseconds; through ctypes a call with two outputs cost 12 us of host time,
-// here about 4.
+// with functions, layer norm and balance loss with their gradients) on torch tensors: the
+// same marshalling as the ctypes functions of lmoe.py (checks of types, shapes and
+// devices, outputs allocated in the call's stream, then the C entry point of the same
+// name), in C++.  These calls run for a few microseconds; through ctypes a call with two
+// outputs cost 12 us of host time, here about 4.
 //
 // The module is not linked to the library: lmoe.py hands it the addresses of the
 // entry points of the library it loaded (bind).
@@ -443,7 +443,7 @@ PyObject *linear_act(PyObject *const *a)
     Out out(a[5], x, {rows, N}, fmt == LMOE_F32 ? at::kFloat : at::kBFloat16, "out", dev);
     MaybeOut pre;
     if (want_pre) pre.make(pre_given ? a[6] : Py_None, x, {rows, N}, at::kBFloat16, "pre", dev);
-    Ws ws(a[7], a[7] == Py_None ? TE.linear_act_ws(rows, K, N) : 0, x, dev);
+    Ws ws(a[7], a[7] == Py_None ? TE.linear_act_ws(rows, K, N) : 0, x, dev, 256);
     check(TE.linear_act(static_cast<const uint16_t *>(xp), static_cast<const uint16_t *>(wp), &f, rows, K, N, fmt, out.ptr,
                         static_cast<uint16_t *>(pre.ptr), ws.ptr, ws.bytes, on.stream),
           "lmoe_linear_act_bf16");
