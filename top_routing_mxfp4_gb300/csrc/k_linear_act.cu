@@ -784,18 +784,19 @@ template <int NT, bool PAIR, bool GRAD, bool COPIED>
 cudaError_t launch(const Operand (*ops)[2], int jobs, const LArgs &g, cudaStream_t st)
 {
     using C = LCfg<NT, PAIR>;
-    CUtensorMap maps[2][2];
-    for (int j = 0; j < 2; ++j) {
-        const Operand &A = ops[j < jobs ? j : 0][0], &B = ops[j < jobs ? j : 0][1];
+    CUtensorMap maps[2][2], out[2], pre;
+    for (int j = 0; j < jobs; ++j) {
+        const Operand &A = ops[j][0], &B = ops[j][1];
         if (!make_tensor_map(&maps[j][0], A.p, MapType::BF16, A.cols, A.rows, A.mn ? 64 : 128, A.stride) ||
             !make_tensor_map(&maps[j][1], B.p, MapType::BF16, B.cols, B.rows, B.mn ? 64 : C::BROWS, B.stride))
             return cudaErrorInvalidValue;
-    }
-    CUtensorMap out[2], pre;
-    for (int j = 0; j < 2; ++j) {
-        const LJob &b = g.job[j < jobs ? j : 0];
+        const LJob &b = g.job[j];
         if (!COPIED) out[j] = maps[0][0];  // (not used)
         else if (!make_store_map(&out[j], b.out, b.out_f32, b.N, b.M)) return cudaErrorInvalidValue;
+    }
+    if (jobs == 1) {  // (not used)
+        maps[1][0] = maps[1][1] = maps[0][0];
+        out[1] = out[0];
     }
     pre = out[0];
     if (COPIED && g.job[0].pre && !make_store_map(&pre, g.job[0].pre, false, g.job[0].N, g.job[0].M))
