@@ -247,6 +247,21 @@ def test_linear_act_backward_parts(cuda_lib):
     assert cuda_lib.linear_act_bf16_backward(dout, x, W, "gelu", pre, False, False, False) == (None, None, None)
 
 
+@pytest.mark.parametrize("rows,K,N", [(1, 8, 33), (65, 16, 20011), (300, 8, 9000), (6000, 72, 40), (8192, 64, 257),
+                                      (2048, 512, 1024)])
+def test_dbias_of_many_groups(cuda_lib, rows, K, N):
+    """dbias has the same bits whether it comes by itself or on the way of one product or both."""
+    g = gen(rows + N)
+    x, W = randn(g, rows, K), randn(g, N, K, scale=K ** -0.5)
+    dout, pre = randn(g, rows, N, scale=0.1), randn(g, rows, N)
+    dx, dW, db = check_back(cuda_lib, dout, x, W, "silu", pre, torch.float32)
+    for want in ((False, False), (True, False), (False, True)):
+        part = cuda_lib.linear_act_bf16_backward(dout, x, W, "silu", pre, *want)
+        assert torch.equal(part[2], db)
+        assert not want[0] or torch.equal(part[0], dx)
+        assert cuda_lib.last_call_status() == cuda_lib.OK
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_slopes_far_out(cuda_lib, act):
     """dbias of one row is dout times the slope: finite and right for every pre-activation."""
@@ -356,6 +371,16 @@ def test_layer_norm_backward(cuda_lib, T, H, dt, weighted, added, params):
         assert not params or (torch.equal(inplace[1], r[1]) and torch.equal(inplace[2], r[2]))
 
 
+@pytest.mark.parametrize("T,H", [(303, 1024), (305, 1024), (609, 640), (1216, 520), (1217, 2048), (2431, 640), (2433, 1024),
+                                 (3649, 1000)])
+def test_layer_norm_backward_by_blocks(cuda_lib, T, H):
+    """Row counts about those where a block takes one row, two or four."""
+    g = gen(T + H)
+    x, dy, w = stream_rows(g, T, H, torch.float32), randn(g, T, H, scale=0.1), randn(g, H, dtype=torch.float32)
+    _, mean, rstd = cuda_lib.layer_norm(x, w, stats=True)
+    check_norm_back(cuda_lib, T, H, torch.float32, w, randn(g, T, H, dtype=torch.float32), dy, x, mean, rstd)
+
+
 def test_layer_norm_backward_without_rows(cuda_lib):
     z = torch.zeros(0, 256, device=DEV, dtype=torch.bfloat16)
     s = torch.zeros(0, device=DEV)
@@ -426,7 +451,8 @@ def picks(g, T, E, k):
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 896, 16), (2, 7, 7), (5, 32, 32), (64, 896, 16), (333, 130, 3),
                                    (151, 384, 8), (1000, 257, 4), (1100, 896, 16), (2100, 60, 8), (700, 2048, 32),
                                    (513, 1023, 5), (3000, 4, 2),
-                                   (73, 1149, 20), (125, 1032, 25)])
+                                   (73, 1149, 20), (125, 1032, 25), (2000, 128, 8), (2000, 129, 8), (1500, 256, 4),
+                                   (1500, 255, 4), (128, 128, 32), (129, 16, 4), (20000, 8, 2)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_balance_loss(cuda_lib, T, E, k, masked):
     g = gen(T + E + k)
