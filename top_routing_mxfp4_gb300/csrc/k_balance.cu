@@ -9,8 +9,8 @@
 // bytes: they are counted first, and then one pass over the logits gives the
 // probabilities' sums and the whole gradient, each logit read once and each
 // gradient written once.  HBM bounds it (32768 tokens of 896 experts, top 16, all outputs:
-// 50 us of the 36 that the bytes take, 37 of them the pass over the logits; of 64 experts
-// 17.6), and at few tokens the start and end of its launches (64 tokens 7.1).
+// 48.7 us of the 36 that the bytes take, 36 of them the pass over the logits; of 64 experts
+// 17.6), and at few tokens the start and end of its launches (64 tokens 6.6).
 //
 // A warp takes a row: a lane holds the same columns in every row it meets, so the
 // sums over the tokens stay in its registers (fp32) until the end; each block
@@ -31,7 +31,8 @@ constexpr int kFinalCtas = 8;  // of the cluster that adds up the blocks' sums
 // kernel of their own (1000 tokens of 16: 12.9 against 15.4 us).
 constexpr int64_t kOwnCount = 4096;
 // Up to this many tokens are the work of one cluster, which needs no second kernel (64
-// tokens of 896 experts 7.2 against 9.0 us, 128: 8.0 against 9.7, 256: 13 against 10.5).
+// tokens of 896 experts 7.2 against 9.0 us, 128: 8.0 against 9.7, 256: 13 against 10.5, with
+// blocks of 512 threads).
 constexpr int64_t kOneCluster = 128;
 
 __device__ __forceinline__ float warp_max(float v)
@@ -104,11 +105,12 @@ __global__ void __cluster_dims__(kCountCluster, 1, 1) __launch_bounds__(512) k_b
     tc::cluster_sync_end();  // no CTA's counts go while another reads them
 }
 
-// A row's logits, the next row's and the column sums in registers: fewer warps for wider rows
-// (32768 tokens of 256 experts, 512, 768, 1024 threads, two blocks of 512: 21.8, 21.1, 22.7, 25.1 us;
-// of 384 experts, 512, 640, 768 threads: 26.7, 28.6, 29.4).
+// A row's logits, the next row's and the column sums in registers: fewer warps for wider rows.
+// 32768 tokens, us: of 256 experts, 512, 768, 1024 threads 21.8, 21.1, 22.7; of 384, 512, 640, 768
+// threads 26.7, 28.6, 29.4; of 896, 320, 384, 448, 512, 576 threads 49.9, 48.1, 49.1, 50.2, 68.7
+// (which spills); 14000 of 2048, 192, 256, 320 threads 54.0, 52.5, 90 (spills).
 template <int NV>
-constexpr int ROW_THREADS = NV <= 2 ? 768 : NV <= 8 ? 512 : 256;
+constexpr int ROW_THREADS = NV <= 2 ? 768 : NV <= 4 ? 512 : NV <= 8 ? 384 : 256;
 
 // NV: 128 columns each; VEC: E % 4 == 0, a lane's columns are fours of them.
 // own: the block counts the picks itself.  one: the grid is one cluster, which adds up its
@@ -499,6 +501,7 @@ cudaError_t launch_balance(BalanceArgs a, void *scratch, cudaStream_t st)
     else if (nv <= 2) e = pick<2>(a, grid, own, one, st);
     else if (nv <= 4) e = pick<4>(a, grid, own, one, st);
     else if (nv <= 7) e = pick<7>(a, grid, own, one, st);
+    else if (nv <= 8) e = pick<8>(a, grid, own, one, st);
     else e = pick<16>(a, grid, own, one, st);
     if (e != cudaSuccess || one) return e;
     return launch_pdl(a.E < 256 ? k_balance_final<32, 10> : k_balance_final<128, 20>, dim3(kFinalCtas), dim3(kFinalThreads), 0, st, a,
