@@ -378,6 +378,7 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
     __shared__ float s_warp[COLS / 32], s_loss[kFinalCtas];
     const int at = threadIdx.x % COLS, strand = threadIdx.x / COLS;
     const int rank = int(tc::cluster_rank());
+    tc::cluster_sync();  // rank 0 runs before another rank stores into its shared memory; while the kernel before ends
     pdl_enter();
     const int tokens = *a.tokens;
     const float inv_n = tokens > 0 ? 1.f / float(tokens) : 0.f;
