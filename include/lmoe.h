@@ -411,7 +411,9 @@ typedef struct {
  * residual.  K % 8 == 0, any N >= 1, rows <= 2^29, no matrix
  * of more than 2^40 elements.  The status word is used as
  * by lmoe_linear_mxfp4: cleared by the caller once, before the workspace's first
- * use; calls that may overlap on the GPU need a workspace each. */
+ * use; calls that may overlap on the GPU need a workspace each.  The size never
+ * falls as rows grow: a workspace for the most rows serves all calls of this K and
+ * N with fewer. */
 size_t lmoe_linear_act_workspace_size(int64_t rows, int32_t K, int32_t N);
 lmoe_status lmoe_linear_act_bf16(const uint16_t *x, const uint16_t *W, const lmoe_linear_act *act, int64_t rows, int32_t K,
                                  int32_t N, int32_t out_fmt, void *out, uint16_t *pre, void *workspace, size_t ws_bytes,
@@ -452,7 +454,8 @@ lmoe_status lmoe_layer_norm(const void *x, int32_t x_fmt, const float *w, const 
  * residual stream's own).  dx may be add.  w may be NULL (1); dw and db may be
  * NULL, each by itself.  Without rows dw and db are zero.  One order of sums.
  * Limits as for lmoe_rms_norm.  The workspace holds partial sums of dw and db; it
- * need not be cleared.  Calls that may overlap need a workspace each. */
+ * need not be cleared, and its size never falls as T grows.  Calls that may overlap
+ * need a workspace each. */
 size_t lmoe_layer_norm_backward_workspace_size(int64_t T, int32_t H);
 lmoe_status lmoe_layer_norm_backward(const uint16_t *dy, const void *x, int32_t x_fmt, const float *mean,
                                      const float *rstd, const float *w, const void *add, int64_t T, int32_t H, void *dx,
@@ -491,7 +494,7 @@ typedef struct {
  * loss fp32 [2], counts int32 [E], probs fp32 [E].  1 <= E <= 2048,
  * 1 <= k <= min(E, 32), T * k <= INT32_MAX / 2, coefficients finite.  Outputs
  * overlap no input and one another, but dlogits may be logits.  The status word
- * as for lmoe_linear_mxfp4. */
+ * as for lmoe_linear_mxfp4; the workspace's size never falls as T grows. */
 size_t lmoe_balance_loss_workspace_size(int64_t T, int32_t E, int32_t k);
 lmoe_status lmoe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t *mask, int64_t T, int32_t E,
                               int32_t k, float *loss, int32_t *counts, float *probs, const lmoe_balance_grad *grad,

@@ -35,6 +35,7 @@ using namespace tc;
 
 constexpr uint32_t A_TILE = 128 * 128;  // 128 x 64 bf16
 constexpr int MAX_PARTS = 16;
+constexpr int MAX_TURNS = 4;  // of parts: they take at most so many turns of the GPU's slots
 
 template <int NT, bool PAIR>
 struct LCfg {
@@ -742,7 +743,7 @@ Plan plan(const Size *size, int jobs)
         if (const int64_t r = total % slots; r > 0 && r <= tiles[last]) {
             turns(tiles[last] - r);
             const int64_t room = jobs > 1 ? slots - tiles[0] % slots : 0;  // slots that end early
-            for (int ks = 2; ks <= MAX_PARTS && KC[last] >= 4 * ks; ++ks) {
+            for (int ks = 2; ks <= MAX_PARTS && KC[last] >= 4 * ks && r * ks <= MAX_TURNS * slots; ++ks) {
                 const double n = double(ceil_div(r * ks, slots) * ceil_div(KC[last], ks)) * c;
                 const double end = r * ks <= room ? (less + n < more ? more : less + n) : more + n;
                 p.split[last] = r;
@@ -754,7 +755,7 @@ Plan plan(const Size *size, int jobs)
             p = Plan();
             p.tile = t;
             p.split[0] = tiles[0];
-            for (int ks = 2; ks <= MAX_PARTS && KC[0] >= 4 * ks; ++ks) {
+            for (int ks = 2; ks <= MAX_PARTS && KC[0] >= 4 * ks && tiles[0] * ks <= MAX_TURNS * slots; ++ks) {
                 const double len = double(ceil_div(KC[0], ks)) * c, one = KC[1] * c > epi[1] ? KC[1] * c : epi[1];
                 p.ks[0] = ks;
                 offer((double(tiles[0] * ks) * len + double(tiles[1]) * one) / double(slots) + (len > one ? len : one) +
@@ -766,11 +767,25 @@ Plan plan(const Size *size, int jobs)
     return best;
 }
 
-// Bytes of the parts.
-size_t part_bytes(const Plan &p)
+// Room for the parts of any plan of these products, of each by itself, and of any with fewer
+// rows: no plan has more parts than MAX_TURNS allow, nor a product more than one for every
+// four chunks of its reduction.  (What one plan needs does not grow with the rows: none at
+// 8192 rows 7168 -> 3584, 15 MB at 333.)
+size_t part_room(const Size *size, int jobs)
 {
-    const Tile &T = TILES[p.tile];
-    return size_t(p.split[0] * p.ks[0] + p.split[1] * p.ks[1]) * T.M * T.N * 4;
+    const int64_t sms = device_sms();
+    size_t most = 0;
+    for (const Tile &T : TILES) {
+        int64_t parts = 0;
+        for (int j = 0; j < jobs; ++j) {
+            const int64_t ks = ceil_div(ceil_div(size[j].K, 64), 4);
+            if (ks > 1) parts += ceil_div(size[j].M, T.M) * ceil_div(size[j].N, T.N) * (ks < MAX_PARTS ? ks : MAX_PARTS);
+        }
+        const int64_t cap = sms / T.ctas * MAX_TURNS;
+        const size_t n = size_t(parts < cap ? parts : cap) * T.M * T.N * 4;
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 // An operand: [rows][cols] bf16, rows `stride` elements apart; mn: the reduction runs over its rows.
@@ -988,17 +1003,10 @@ cudaError_t dz_fn(const DzArgs &g, int fn, dim3 grid, cudaStream_t st)
 // it took 23.4 and 21.1 us (3584 -> 7168, 7168 -> 3584) against 18.0 and 18.0 here.
 constexpr int64_t FEW = 64;
 
-// The plan may differ with what the epilogue reads and writes: room for any.
 size_t linear_act_scratch_bytes(int64_t rows, int K, int N)
 {
-    size_t most = 0;
-    if (rows > FEW)
-        for (int extra = 0; extra <= 2; ++extra) {
-            const Size size{rows, N, K, extra};
-            const size_t n = part_bytes(plan(&size, 1));
-            most = n > most ? n : most;
-        }
-    return most;
+    const Size size{rows, N, K, 0};
+    return rows > FEW ? part_room(&size, 1) : 0;
 }
 
 cudaError_t launch_linear_act(const LinearActArgs &a, void *scratch, cudaStream_t st)
@@ -1044,14 +1052,9 @@ size_t linear_act_back_scratch_bytes(int64_t rows, int K, int N)
 {
     if (rows == 0) return 0;
     const int64_t Np = round_up(N, 8);
-    const Size dx{rows, K, N, 0}, dW{N, K, rows, 0}, both[2] = {N >= rows ? dx : dW, N >= rows ? dW : dx};
-    size_t most = rows > FEW ? part_bytes(plan(both, 2)) : 0;
-    for (const Size *one : {&dx, &dW}) {
-        if (one == &dx && rows <= FEW) continue;
-        const size_t n = part_bytes(plan(one, 1));
-        most = n > most ? n : most;
-    }
-    return size_t(round_up(rows * Np * 2, 256)) + size_t(round_up(dz_splits(rows, N) * N * 4, 256)) + most;
+    const Size products[2] = {{N, K, rows, 0}, {rows, K, N, 0}};  // dW, dx (few rows' goes another way)
+    return size_t(round_up(rows * Np * 2, 256)) + size_t(round_up(dz_splits(rows, N) * N * 4, 256)) +
+           part_room(products, rows > FEW ? 2 : 1);
 }
 
 cudaError_t launch_linear_act_back(const LinearActBackArgs &a, void *scratch, cudaStream_t st)

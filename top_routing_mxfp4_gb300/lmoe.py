@@ -728,6 +728,7 @@ def _function(act: str) -> int:
 
 
 def linear_act_workspace_size(rows: int, K: int, N: int) -> int:
+    """Bytes for linear_act_bf16 with up to `rows` rows."""
     return int(_linear_act_ws(rows, K, N))
 
 
@@ -743,6 +744,7 @@ def linear_act_bf16(x, W, bias=None, act: str = "none", res=None, out=None, pre=
 
 
 def linear_act_backward_workspace_size(rows: int, K: int, N: int) -> int:
+    """Bytes for linear_act_bf16_backward with up to `rows` rows."""
     return int(_linear_act_back_ws(rows, K, N))
 
 
