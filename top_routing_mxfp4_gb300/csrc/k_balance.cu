@@ -434,11 +434,12 @@ __global__ void __cluster_dims__(kFinalCtas, 1, 1) __launch_bounds__(kFinalThrea
 template <int NV, bool VEC, bool GRAD>
 cudaError_t rows(const BalanceArgs &a, unsigned grid, bool own, bool one, cudaStream_t st)
 {
-    const int Ep = (a.E + 3) & ~3;
     constexpr int kBlock = ROW_THREADS<NV>;
-    const size_t smem = size_t(1 + kBlock / 32) * Ep * 4 + size_t(count_stride(a.E)) * 4;
+    constexpr auto bytes = [](int E) { return size_t(1 + kBlock / 32) * ((E + 3) & ~3) * 4 + size_t(count_stride(E)) * 4; };
+    const size_t smem = bytes(a.E);
     auto *kern = k_balance_rows<NV, VEC, GRAD>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // the most of any width: another host thread's narrower call does not lower it before this launch
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes(NV * 128)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);

@@ -629,6 +629,7 @@ cudaError_t warps(const LayerNormBackArgs &a, unsigned grid, cudaStream_t st)
     return launch_pdl(kern, dim3(grid), dim3(256), smem, st, a);
 }
 
+constexpr int64_t kRingBytes = 220 * 1024;  // of an SM's shared memory for the rings of its blocks
 template <typename R, int S>
 cudaError_t ring(const LayerNormBackArgs &a, unsigned grid, cudaStream_t st)
 {
@@ -636,7 +637,8 @@ cudaError_t ring(const LayerNormBackArgs &a, unsigned grid, cudaStream_t st)
     const bool sums = a.dw || a.db;
     auto *kern = sums ? (a.add ? k_layer_norm_ring<R, S, true, true> : k_layer_norm_ring<R, S, true, false>)
                       : (a.add ? k_layer_norm_ring<R, S, false, true> : k_layer_norm_ring<R, S, false, false>);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // the most of any width: another host thread's narrower call does not lower it before this launch
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingBytes));
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(unsigned(round_up(ceil_div(a.H / 8, 2), 32))), smem, st, a);
 }
@@ -656,7 +658,7 @@ cudaError_t launch_back(const LayerNormBackArgs &a, cudaStream_t st)
         else {
             // stages of the ring: what the blocks of an SM have room for
             const int64_t row = int64_t(a.H) * (sizeof(R) * (a.add ? 2 : 1) + 2);
-            const int64_t stages = 220 * 1024 / (row * blocks_per_sm(a.H));
+            const int64_t stages = kRingBytes / (row * blocks_per_sm(a.H));
             e = stages >= 4 ? ring<R, 4>(a, grid, st) : stages == 3 ? ring<R, 3>(a, grid, st) : ring<R, 2>(a, grid, st);
         }
     } else {
