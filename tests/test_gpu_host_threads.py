@@ -73,3 +73,24 @@ def test_balance_losses_of_other_widths(cuda_lib):
     torch.cuda.synchronize()
     at_once(calls)
     assert all(torch.equal(a, b) for want, got in outs for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("T", [64, 2000])
+def test_permutes_of_other_expert_counts(cuda_lib, T):
+    lmoe = cuda_lib
+    g = gen(T)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    calls, outs, keep = [], [], []
+    for E in (896, 1600, 2048):
+        idx = torch.rand(T, E, device=DEV, generator=g).topk(4, 1).indices.to(torch.int32).contiguous()
+        want = lmoe.permute(idx, E)[:4]
+        got = [torch.empty_like(t) for t in want]
+        n = lmoe.permute_workspace_size(T, E, 4)
+        ws, s, dims = torch.zeros(n, dtype=torch.uint8, device=DEV), torch.cuda.Stream(DEV), lmoe.dims(T, 128, E, 4, 32)
+        args = (p(idx), ctypes.byref(dims), *map(p, got), p(ws), n, ctypes.c_void_p(s.cuda_stream))
+        calls.append(lambda args=args: lmoe._permute(*args))
+        outs.append((want, got))
+        keep.append((idx, ws, s, dims))
+    torch.cuda.synchronize()
+    at_once(calls)
+    assert all(torch.equal(a, b) for want, got in outs for a, b in zip(want, got))

@@ -1089,9 +1089,9 @@ int num_sms()
 }
 
 // Deepest pipeline that fits the per-block shared-memory limit (dynamic part
-// after the kernel's static shared memory) and the TMEM column budget.
+// after the kernel's static shared memory, `most`) and the TMEM column budget.
 template <int MODE, int NT, bool SPLIT>
-int gemm_stages(int E, size_t &smem)
+int gemm_stages(int E, size_t &smem, int &most)
 {
     using C = Cfg<MODE, NT>;
     int dev = 0, optin = 0;
@@ -1100,7 +1100,8 @@ int gemm_stages(int E, size_t &smem)
     cudaFuncAttributes fa{};
     cudaFuncGetAttributes(&fa, k_moe_gemm<MODE, NT, SPLIT>);
     const size_t fixed = 1024 + C::EPI_BYTES + (2 * 16 + 2 * C::ACC_STAGES + 2) * 8 + 16 + size_t(2) * (E + 1) * 4;
-    const long avail = long(optin) - long(fa.sharedSizeBytes) - long(fixed);
+    most = optin - int(fa.sharedSizeBytes);
+    const long avail = long(most) - long(fixed);
     int st = int(avail / long(C::STAGE_BYTES));
     if (st > C::MAX_STAGES) st = C::MAX_STAGES;
     smem = fixed + size_t(st > 0 ? st : 0) * C::STAGE_BYTES;
@@ -1116,11 +1117,12 @@ cudaError_t launch_gemm(const CUtensorMap &a0, const CUtensorMap &a1, const CUte
                         const GemmArgs *args2 = nullptr)
 {
     size_t smem = 0;
-    args.stages = gemm_stages<MODE, NT, SPLIT>(args.E, smem);
+    int most = 0;
+    args.stages = gemm_stages<MODE, NT, SPLIT>(args.E, smem, most);
     if (args.stages < 2) return cudaErrorInvalidConfiguration;
     if (MODE == FUSED && (!d || !h || !args2)) return cudaErrorInvalidValue;
-    cudaError_t e =
-        cudaFuncSetAttribute(k_moe_gemm<MODE, NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // one limit for all sizes: another host thread's smaller call does not lower it before this launch
+    cudaError_t e = cudaFuncSetAttribute(k_moe_gemm<MODE, NT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     GemmArgs q = args2 ? *args2 : args;
     q.stages = args.stages;
@@ -1243,7 +1245,7 @@ cudaError_t launch_quant_scatter_pad(const uint16_t *x, int T, int d, int k, int
         const size_t smem = size_t(2) * d;
         if (smem > 48 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(k_quant_scatter_rows, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 int(smem));
+                                                 224 * 1024);  // one limit for all widths
             if (e != cudaSuccess) return e;
         }
         const cudaError_t le_ = launch_pdl(

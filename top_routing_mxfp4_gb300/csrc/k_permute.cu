@@ -297,9 +297,11 @@ cudaError_t launch_permute(const int32_t *idx, int64_t P, int E, int32_t *counts
     int32_t *blockhist = static_cast<int32_t *>(scratch);
     if (nblk == 1) {
         // dynamic part; the kernel also has ~16 KB of static shared memory, so
-        // the limit is raised explicitly
+        // the limit is raised explicitly, to one value for all sizes (another host
+        // thread's smaller call does not lower it before this launch)
         const size_t smem = size_t(WARPS + 1) * E * sizeof(int32_t) + 16;
-        cudaError_t e = cudaFuncSetAttribute(k_perm_single, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        const cudaError_t e = cudaFuncSetAttribute(k_perm_single, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (WARPS + 1) * MAXE * int(sizeof(int32_t)) + 16);
         if (e != cudaSuccess) return e;
         {
             const cudaError_t le_ = launch_pdl(k_perm_single, dim3(1), dim3(256), smem, st, idx, int(P), E, counts, offsets, perm, inv, status, sched);
@@ -320,7 +322,8 @@ cudaError_t launch_permute(const int32_t *idx, int64_t P, int E, int32_t *counts
     if (nblk > 0) {
         const size_t smem = size_t(WARPS) * E * sizeof(int32_t);
         if (smem > 48 * 1024) {  // above the default dynamic shared-memory limit (E > 1536)
-            cudaError_t e = cudaFuncSetAttribute(k_perm_scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+            const cudaError_t e = cudaFuncSetAttribute(k_perm_scatter, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       WARPS * MAXE * int(sizeof(int32_t)));
             if (e != cudaSuccess) return e;
         }
         {

@@ -253,10 +253,12 @@ cudaError_t launch_topk_softmax(const float *logits, int T, int E, int k, int32_
         const size_t smem = size_t(2) * TOPK_GROUP * E * 4;
         const int ngroups = int(ceil_div(T, TOPK_GROUP));
         const int grid = ngroups < 2 * 152 ? ngroups : 2 * 152;
+        // one limit for all E of an instance: another host thread's smaller call does not lower it before this launch
+        const auto limit = [](int most_E) { return 2 * TOPK_GROUP * most_E * 4; };
         cudaError_t e = E <= 256 ? cudaFuncSetAttribute(k_topk_softmax_staged<8>,
-                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))
+                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, limit(256))
                                  : cudaFuncSetAttribute(k_topk_softmax_staged<28>,
-                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, limit(896));
         if (e != cudaSuccess) return e;
         e = E <= 256 ? launch_pdl(k_topk_softmax_staged<8>, dim3(grid), dim3(256), smem, st, logits, T, E, k, idx, w,
                                   status)

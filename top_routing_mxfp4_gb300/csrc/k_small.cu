@@ -832,10 +832,11 @@ int down_group(int P, int d, int I)
 }
 size_t down_smem(int P, int d, int I, int gp) { return down_fixed_smem(P, I) + 2 * size_t(gp) * down_pair_bytes(d, I); }
 
+// One limit for all sizes: another host thread's smaller call does not lower it before this launch.
 template <typename K>
-cudaError_t smem_attr(K kernel, size_t bytes)
+cudaError_t smem_attr(K kernel)
 {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemLimit));
 }
 
 }  // namespace
@@ -861,19 +862,19 @@ cudaError_t launch_small_t(const uint16_t *x, const uint16_t *Wr3, const float *
     const size_t rs = route_smem(T, d, E);
     const int rgrid = int(ceil_div(2 * E, R_WARPS));
     if (T <= 1) {
-        if ((e = smem_attr(k_small_route<1, FP4>, rs)) != cudaSuccess) return e;
+        if ((e = smem_attr(k_small_route<1, FP4>)) != cudaSuccess) return e;
         e = launch_pdl(k_small_route<1, FP4>, dim3(rgrid), dim3(32 * R_WARPS), rs, st, x, Wr3, bias, T, d, E, k,
                        logits, idx, w, sp);
     } else if (T <= 2) {
-        if ((e = smem_attr(k_small_route<2, FP4>, rs)) != cudaSuccess) return e;
+        if ((e = smem_attr(k_small_route<2, FP4>)) != cudaSuccess) return e;
         e = launch_pdl(k_small_route<2, FP4>, dim3(rgrid), dim3(32 * R_WARPS), rs, st, x, Wr3, bias, T, d, E, k,
                        logits, idx, w, sp);
     } else if (T <= 4) {
-        if ((e = smem_attr(k_small_route<4, FP4>, rs)) != cudaSuccess) return e;
+        if ((e = smem_attr(k_small_route<4, FP4>)) != cudaSuccess) return e;
         e = launch_pdl(k_small_route<4, FP4>, dim3(rgrid), dim3(32 * R_WARPS), rs, st, x, Wr3, bias, T, d, E, k,
                        logits, idx, w, sp);
     } else {
-        if ((e = smem_attr(k_small_route<SMALL_MAX_TOKENS, FP4>, rs)) != cudaSuccess) return e;
+        if ((e = smem_attr(k_small_route<SMALL_MAX_TOKENS, FP4>)) != cudaSuccess) return e;
         e = launch_pdl(k_small_route<SMALL_MAX_TOKENS, FP4>, dim3(rgrid), dim3(32 * R_WARPS), rs, st, x, Wr3, bias,
                        T, d, E, k, logits, idx, w, sp);
     }
@@ -883,7 +884,7 @@ cudaError_t launch_small_t(const uint16_t *x, const uint16_t *Wr3, const float *
         if ((e = cudaEventRecord(stage_events[i], st)) != cudaSuccess) return e;
     const int npair_max = T < G_PAIRS ? T : G_PAIRS;
     const size_t gs = gateup_smem(T, d);
-    if ((e = smem_attr(k_small_gateup<FP4>, gs)) != cudaSuccess) return e;
+    if ((e = smem_attr(k_small_gateup<FP4>)) != cudaSuccess) return e;
     const int max_units = P * (I / 32);
     const int ggrid = max_units < 152 ? max_units : 152;
     e = launch_pdl(k_small_gateup<FP4>, dim3(ggrid), dim3(32 * G_WARPS), gs, st, W->gate_q, W->gate_s, W->up_q,
@@ -892,7 +893,7 @@ cudaError_t launch_small_t(const uint16_t *x, const uint16_t *Wr3, const float *
     if (stage_events && (e = cudaEventRecord(stage_events[4], st)) != cudaSuccess) return e;
     const int gp = down_group(P, d, I);
     const size_t ds = down_smem(P, d, I, gp);
-    if ((e = smem_attr(k_small_down<FP4>, ds)) != cudaSuccess) return e;
+    if ((e = smem_attr(k_small_down<FP4>)) != cudaSuccess) return e;
     const int rpc = down_rows_per_cta(d);
     const int dgrid = int(ceil_div(d, rpc));
     e = launch_pdl(k_small_down<FP4>, dim3(dgrid), dim3(32 * D_WARPS), ds, st, W->down_q, W->down_s, idx, w, T, d, I,
