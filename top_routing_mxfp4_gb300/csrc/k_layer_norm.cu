@@ -228,12 +228,14 @@ cudaError_t launch_fwd(const LayerNormArgs &a, cudaStream_t st)
     // and of bf16 rows      8192 x 7168  1: 82.5  2: 56.1  3: 56.1  4: 55.1  walking 44.2 (5.3 TB/s)
     //                       8192 x 2048  1: 20.2  2: 16.1  3: 16.0  4: 16.5  walking 15.2
     const dim3 grid{unsigned(a.T)};
-    int e8 = !many ? 1 : nv > 300 ? 4 : 2;
-    if (nv > (e8 == 1 ? 1024 : 512 * e8)) e8 = nv <= 1024 ? 2 : nv <= 1536 ? 3 : nv <= 2048 ? 4 : 8;
+    int e8 = !many ? 1 : nv > 300 ? 4 : 2;  // (2: fp32 alone, such bf16 rows are walked over)
+    if (e8 == 1 && nv > 1024) e8 = nv <= 1536 ? 3 : 4;
+    if (nv > 2048) e8 = 8;
     const dim3 block(unsigned(round_up(ceil_div(nv, e8), 32)));
+    if constexpr (sizeof(R) == 4)
+        if (e8 == 2) return launch_pdl(k_layer_norm<R, 2, false>, grid, block, 0, st, a);
     switch (e8) {
     case 1: return launch_pdl(k_layer_norm<R, 1, false>, grid, block, 0, st, a);
-    case 2: return launch_pdl(k_layer_norm<R, 2, false>, grid, block, 0, st, a);
     case 3: return launch_pdl(k_layer_norm<R, 3, false>, grid, block, 0, st, a);
     case 4: return launch_pdl(k_layer_norm<R, 4, false>, grid, block, 0, st, a);
     default: return launch_pdl(k_layer_norm<R, 8, false>, grid, block, 0, st, a);
@@ -635,8 +637,9 @@ cudaError_t ring(const LayerNormBackArgs &a, unsigned grid, cudaStream_t st)
 {
     const size_t smem = size_t(S) * a.H * (sizeof(R) * (a.add ? 2 : 1) + 2);
     const bool sums = a.dw || a.db;
-    auto *kern = sums ? (a.add ? k_layer_norm_ring<R, S, true, true> : k_layer_norm_ring<R, S, true, false>)
-                      : (a.add ? k_layer_norm_ring<R, S, false, true> : k_layer_norm_ring<R, S, false, false>);
+    auto *kern = sums ? k_layer_norm_ring<R, S, true, true> : k_layer_norm_ring<R, S, false, true>;
+    if constexpr (S == 4)  // (without add four stages always fit)
+        if (!a.add) kern = sums ? k_layer_norm_ring<R, S, true, false> : k_layer_norm_ring<R, S, false, false>;
     // the most of any width: another host thread's narrower call does not lower it before this launch
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kRingBytes));
     if (e != cudaSuccess) return e;
@@ -656,10 +659,11 @@ cudaError_t launch_back(const LayerNormBackArgs &a, cudaStream_t st)
         if (nv <= 32) e = warps<R, 1>(a, grid, st);
         else if (nv <= 64) e = warps<R, 2>(a, grid, st);
         else {
-            // stages of the ring: what the blocks of an SM have room for
-            const int64_t row = int64_t(a.H) * (sizeof(R) * (a.add ? 2 : 1) + 2);
-            const int64_t stages = kRingBytes / (row * blocks_per_sm(a.H));
-            e = stages >= 4 ? ring<R, 4>(a, grid, st) : stages == 3 ? ring<R, 3>(a, grid, st) : ring<R, 2>(a, grid, st);
+            // stages of the ring: what the blocks of an SM have room for, four but for fp32 rows with add (the
+            // blocks' rows have at most 8192 elements together: 10 bytes each there, else 6)
+            const int64_t stages = kRingBytes / (int64_t(a.H) * 10 * blocks_per_sm(a.H));
+            if (sizeof(R) == 2 || !a.add || stages >= 4) e = ring<R, 4>(a, grid, st);
+            else if constexpr (sizeof(R) == 4) e = stages == 3 ? ring<R, 3>(a, grid, st) : ring<R, 2>(a, grid, st);
         }
     } else {
         const unsigned grid = unsigned(a.T < 152 * 2 ? a.T : 152 * 2);
