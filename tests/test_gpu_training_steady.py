@@ -38,6 +38,16 @@ def test_balance_loss_of_several_rows_a_warp(cuda_lib, T, E, k, mask):
     assert all(torch.equal(x, y) for x, y in zip(a, c))
 
 
+@pytest.mark.parametrize("T,E,k", [(256, 896, 16), (257, 896, 16), (767, 300, 16), (768, 896, 16), (769, 896, 16), (768, 61, 16),
+                                   (769, 61, 16), (384, 2048, 32), (385, 2048, 32)])
+def test_balance_loss_about_the_picks_that_a_block_counts(cuda_lib, T, E, k):
+    """4096 and 12288 picks: counted by every block or by a kernel of their own."""
+    g = gen(T + E)
+    l, idx = torch.randn(T, E, device=DEV, generator=g), ops.picks(g, T, E, k)
+    w, dw = torch.rand(T, k, device=DEV, generator=g), torch.randn(T, k, device=DEV, generator=g)
+    ops.check_balance(cuda_lib, l, idx, torch.rand(T, device=DEV, generator=g) < 0.8, w=w, dw=dw)
+
+
 @pytest.mark.parametrize("T,E,k", [(6000, 896, 16), (9000, 130, 32), (4000, 2048, 8)])
 def test_balance_loss_of_several_rows_with_experts_twice(cuda_lib, T, E, k):
     """A row that names an expert twice, then one that does not, in one warp: the gate weights' share of one row does

@@ -27,12 +27,15 @@ namespace {
 
 constexpr int kCountCluster = 8, kCountParts = 16;
 constexpr int kFinalCtas = 8;  // of the cluster that adds up the blocks' sums
-// Up to this many picks every block counts them all by itself; more are counted by a
-// kernel of their own (1000 tokens of 16: 12.9 against 15.4 us).
-constexpr int64_t kOwnCount = 4096;
-// Up to this many tokens are the work of one cluster, which needs no second kernel (64
-// tokens of 896 experts 7.2 against 9.0 us, 128: 8.0 against 9.7, 256: 13 against 10.5, with
-// blocks of 512 threads).
+// Up to this many picks every block counts them all by itself; more are counted by a kernel
+// of their own.  us, by itself and by the kernel: 4096 picks of 896 experts 8.9 and 11.4, 8192
+// 9.7 and 11.3, 12288 10.8 and 11.6, 16384 12.4 and 11.8; of 64 experts 12288 8.3 and 8.7,
+// 16384 9.6 and 8.8; of 2048 experts 12288 16.3 and 17.4, 16384 17.8 and 17.4.
+constexpr int64_t kOwnCount = 12288;
+// Up to this many tokens are the work of one cluster, which needs no second kernel.  us, one
+// cluster and two kernels: of 896 experts 64 tokens 6.2 and 7.5, 128 7.5 and 7.8, 192 8.3 and
+// 7.9, 256 10.3 and 8.9; of 2048 experts 128 11.1 and 12.9, 192 17.3 and 17.4, 256 19.4 and 17.3;
+// of 64 experts 128 5.4 and 6.6, 256 6.2 and 6.8.
 constexpr int64_t kOneCluster = 128;
 
 __device__ __forceinline__ float warp_max(float v)
