@@ -699,6 +699,9 @@ def grouped_swiglu_bf16(x, Wg, Wu, offsets, perm=None, k: int = 1, gather=None, 
 
 
 # ---- the layer's dense, trained neighbours: linear with bias, function and residual, layer norm, balance loss ----
+#
+# As with every call of this module, autograd records nothing: outputs have no graph, also where inputs require a
+# gradient.  A torch.autograd.Function that trains makes the forward and the _backward call itself.
 
 class _TrainBinding:
     """The entry points of these calls, handed to the compiled binding at the first of them."""
