@@ -29,8 +29,11 @@
 namespace lmoe {
 namespace {
 
-constexpr int kMaxWarpH = 512;    // columns up to which a warp takes a row backward (at 1024 its sums spill: 47 against 29 us
-                                  // at 8192 rows)
+// Columns up to which a warp takes a row backward.  At 1024 its sums spill (8192 rows: 47 us, a
+// block a row 29).  At 257 to 512 fp32 rows with add spill a little too (192 bytes at 128
+// registers), and are ahead all the same: 8192 x 512 16.5 us, a block a row 25.4; 50000 x 512
+// 74 and 82; bf16 rows 10.5 and 18.5, 46 and 51.
+constexpr int kMaxWarpH = 512;
 constexpr int kMaxFusedH = 8192;  // columns up to which one pass makes dx and the column sums
 
 // Sum over a block of at most 16 warps, the same in every thread and in a fixed order.

@@ -898,6 +898,12 @@ cudaError_t products(const Operand (*ops)[2], const Size *size, int jobs, const 
 }
 
 // ---- dz and its column sums ----------------------------------------------------------------
+//
+// dz is fp32 until the column sums have it, and is rounded to bf16 for the two products: the
+// tensor cores take operands of one type, and the other operand, x or W, is bf16.  Half a step
+// of every term leaves dx and dW 2.3e-3 of their size from 64 bits, where rounding bf16 results
+// alone leaves 1.7e-3.  dz as two bf16 pieces would keep it, at twice the products' time (214 of
+// the 256 us at 4096 rows 3584 -> 7168).
 
 struct DzArgs {
     const void *dout;
@@ -909,7 +915,9 @@ struct DzArgs {
 };
 
 // A block takes 256 columns and every gridDim.y-th group of eight rows, a warp a row
-// of it, a lane eight columns.  VEC: rows start on 16 bytes.
+// of it, a lane eight columns.  VEC: rows start on 16 bytes.  (fp32 gradients through a
+// function spill 60 to 90 bytes at the 64 registers that four blocks an SM leave; the sums
+// alone of 4096 x 7168, silu, read 5.2 TB/s all the same, 33.8 us, bf16 ones 4.9 TB/s, 23.8.)
 template <bool F32, int FN, bool VEC>
 __global__ void __launch_bounds__(256, 4) k_act_back(const DzArgs p)
 {
@@ -999,8 +1007,10 @@ cudaError_t dz_fn(const DzArgs &g, int fn, dim3 grid, cudaStream_t st)
 
 }  // namespace
 
-// Up to this many rows the weights' stream is the bound (k_linear_few.cu); at 96 and 128
-// it took 23.4 and 21.1 us (3584 -> 7168, 7168 -> 3584) against 18.0 and 18.0 here.
+// Up to this many rows the weights' stream is the bound (k_linear_few.cu).  us there and here,
+// 64 rows: 3584 -> 7168 13.2 and 15.9, 7168 -> 3584 14.6 and 16.7, 7168 -> 28672 64 and 73,
+// 1024 -> 1024 6.0 and 6.6, 512 -> 512 6.7 and 6.2; dx of 3584 -> 7168 12.5 and 15.1.  96 and 128
+// rows took it 23.4 and 21.1 (3584 -> 7168, 7168 -> 3584) against 18.6 and 17.5 here.
 constexpr int64_t FEW = 64;
 
 size_t linear_act_scratch_bytes(int64_t rows, int K, int N)

@@ -11,7 +11,7 @@
 // are added in rank order (cluster_sum.cuh), each rank finishing a share of the rows.
 // One row 3584 -> 7168 11.7 us, 64 rows 13.2 (weights that lie in L2: 7.6 us at HBM speed
 // and about 4 of start, cluster sum and end); 7168 -> 28672, from HBM, 70 (5.9 TB/s, 87%).
-// At 128 rows the tiles of k_linear_act win (21.1 against 18.0 us).
+// At 128 rows the tiles of k_linear_act win (21.1 against 17.5 us).
 //
 // One tile a cluster, up to two CTAs an SM: warp 0 copies, warp 1 issues the MMAs,
 // four epilogue warps.  Every wait is bounded (LMOE_ERR_TIMEOUT in the status word).
