@@ -124,3 +124,35 @@ def test_linear_act_far_values_by_their_tails(cuda_lib, act, rows):
     factor = torch.where(tail > 0, (16 + 8 * arg) * U, torch.zeros_like(arg))
     ref = z.clamp_min(0) - tail
     within(out, ref, 2 * U * ref.abs() + factor * tail + ops.TINY)
+
+
+@pytest.mark.parametrize("act", ops.ACTS)
+@pytest.mark.parametrize("N", [16, 13])
+def test_values_and_slopes_at_infinity(cuda_lib, act, N):
+    """A column whose bias is -infinity (masked) or infinity: the function's limit, and 0 or 1 for its slope, so that the
+    gradients of a masked column are zero and no other column's change.  A NaN stays a NaN."""
+    g = gen(N)
+    rows, K = 70, 24
+    x, W, bias = randn(g, rows, K), randn(g, N, K), randn(g, N, dtype=torch.float32)
+    dout = randn(g, rows, N)
+    want = cuda_lib.linear_act_bf16(x, W, bias, act, pre=True)
+    bias[3], bias[7], bias[9] = -float("inf"), float("inf"), float("nan")
+    out, pre = cuda_lib.linear_act_bf16(x, W, bias, act, pre=True)
+    rest = [n for n in range(N) if n not in (3, 7, 9)]
+    assert torch.equal(out[:, rest], want[0][:, rest])
+    assert bool((out[:, 3] == (-float("inf") if act == "none" else 0)).all()) and bool((out[:, 7] == float("inf")).all())
+    assert bool(out[:, 9].isnan().all())
+    saved = None if act == "none" else pre
+    _, _, db = cuda_lib.linear_act_bf16_backward(dout, x, W, act, saved)
+    low = 1.0 if act == "none" else 0.0
+    within(db[[3]], low * dout[:, 3].to(D).sum()[None], (rows + 2) * U * dout[:, 3].to(D).abs().sum()[None])
+    within(db[[7]], dout[:, 7].to(D).sum()[None], (rows + 2) * U * dout[:, 7].to(D).abs().sum()[None])
+    if act == "none":
+        return
+    assert bool(db[9].isnan())
+    pre[:, 9] = 0  # without the NaN: masked columns add nothing to dx, and their dW is zero
+    dx, dW, _ = cuda_lib.linear_act_bf16_backward(dout, x, W, act, pre)
+    pre[:, 3], masked = -200.0, W.clone()
+    masked[3] = 0
+    also = cuda_lib.linear_act_bf16_backward(dout, x, masked, act, pre)
+    assert torch.equal(dx, also[0]) and not bool(dW[3].any()) and bool(torch.isfinite(dW).all())

@@ -108,6 +108,9 @@ __device__ __forceinline__ void apply_fn(int fn, F2 (&y)[N])
     }
 }
 
+// The factor of a term that fades out: infinity times zero is none.  (A NaN of z's comes back with the other factor.)
+__device__ __forceinline__ F2 finite(F2 z) { return each(z, [](float v) { return fminf(fmaxf(v, -1e30f), 1e30f); }); }
+
 template <int FN>
 __device__ __forceinline__ F2 slope(F2 z)
 {
@@ -119,10 +122,10 @@ __device__ __forceinline__ F2 slope(F2 z)
         float z0, z1, q0, q1;
         f2_get(z, z0, z1);
         f2_get(q, q0, q1);
-        return fma2(z * f2(0.39894228f), e, f2(z0 < 0.f ? q0 : 1.f - q0, z1 < 0.f ? q1 : 1.f - q1));
+        return fma2(finite(z) * f2(0.39894228f), e, f2(z0 < 0.f ? q0 : 1.f - q0, z1 < 0.f ? q1 : 1.f - q1));
     } else if constexpr (FN == LMOE_FN_SILU || FN == LMOE_FN_GELU_TANH) {
         const F2 u = FN == LMOE_FN_SILU ? z : tanh_arg(z);
-        const F2 du = FN == LMOE_FN_SILU ? f2(1.f) : fma2(z * z, f2(3 * 0.044715f * TANH_C), f2(TANH_C));
+        const F2 du = fma2(z * z, f2(3 * 0.044715f * TANH_C), f2(TANH_C));  // of gelu by tanh
         const F2 e = each(u * f2(LOG2E), [](float v) { return exp2_quick(-fabsf(v)); });
         const F2 r = each(e + f2(1.f), [](float v) { return rcp_quick(v); });
         const F2 er = e * r;  // the logistic function of u is r or er, by u's sign, and 1 - it the other
@@ -130,9 +133,8 @@ __device__ __forceinline__ F2 slope(F2 z)
         f2_get(u, u0, u1);
         f2_get(r, r0, r1);
         f2_get(er, s0, s1);
-        F2 zd = z * du;
-        if constexpr (FN == LMOE_FN_GELU_TANH)  // infinite far out, where r er is 0
-            zd = each(zd, [](float v) { return fminf(fmaxf(v, -1e30f), 1e30f); });
+        // (far out z du is infinite, where r er is 0)
+        const F2 zd = FN == LMOE_FN_SILU ? finite(z) : finite(z * du);
         return fma2(zd, r * er, f2(u0 < 0.f ? s0 : r0, u1 < 0.f ? s1 : r1));
     } else {
         return f2(1.f);

@@ -917,7 +917,7 @@ struct DzArgs {
 // A block takes 256 columns and every gridDim.y-th group of eight rows, a warp a row
 // of it, a lane eight columns.  VEC: rows start on 16 bytes.  (fp32 gradients through a
 // function spill 60 to 90 bytes at the 64 registers that four blocks an SM leave; the sums
-// alone of 4096 x 7168, silu, read 5.2 TB/s all the same, 33.8 us, bf16 ones 4.9 TB/s, 23.8.)
+// alone of 4096 x 7168, silu, read 5.1 TB/s all the same, 34.7 us, bf16 ones 4.7 TB/s, 24.9.)
 template <bool F32, int FN, bool VEC>
 __global__ void __launch_bounds__(256, 4) k_act_back(const DzArgs p)
 {
